@@ -199,7 +199,8 @@ def _pick(values, rows):
 
 
 def _scale(amax):
-    return torch.clamp(amax / 448.0, min=TINY)
+    # (a tensor of 448: dividing by a number multiplies by its rounded reciprocal on the GPU)
+    return torch.clamp(amax / torch.full_like(amax, 448.0), min=TINY)
 
 
 def _codes(x, inv):
@@ -450,7 +451,7 @@ def _e4m3_64(v):
 def _block_64(v):
     """One block: (values of its codes, scale); the scale and the scaled values are fp32 numbers by definition."""
     m = v.abs().amax()
-    s = torch.clamp(m.float() / 448.0, min=TINY)
+    s = torch.clamp((m.float().double() / 448.0).float(), min=TINY)
     return _e4m3_64((v.float() * (1.0 / s)).double()), s.double()
 
 
@@ -459,7 +460,7 @@ def _rows_64(x):
     q, s = torch.empty_like(x, dtype=torch.float64), []
     for c0 in range(0, x.shape[1], 128):
         v = x[:, c0:c0 + 128]
-        sc = torch.clamp(v.abs().amax(1).float() / 448.0, min=TINY)
+        sc = torch.clamp((v.abs().amax(1).float().double() / 448.0).float(), min=TINY)
         q[:, c0:c0 + 128] = _e4m3_64((v.float() * (1.0 / sc)[:, None]).double())
         s.append(sc.double())
     return q, torch.stack(s, 1)
