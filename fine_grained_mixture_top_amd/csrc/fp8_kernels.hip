@@ -1,0 +1,340 @@
+// Quantizers to E4M3 with a scale per block of 128, and the SwiGLU kernels
+// between the experts' two products (include/moe_ops.h).  All of them are
+// bound by memory: every value is read once and its code written once.
+#include <algorithm>
+
+#include "fp8_block.h"
+#include "ops_launch.h"
+
+namespace moe {
+
+namespace {
+
+// A plan's rows as a kernel over row numbers sees them: every row without one.
+struct RowFilter {
+  const int32_t* offsets;    // null: every row
+  const int32_t* row_token;
+  int E;
+  __device__ __forceinline__ bool operator()(int64_t r) const {
+    return !offsets || (r < offsets[E] && row_token[r] >= 0);
+  }
+};
+
+constexpr int64_t MAX_GRID = 1 << 22;  // workgroups; the kernels stride over what is left
+
+unsigned grid_for(int64_t threads) { return (unsigned)std::min<int64_t>((threads + 255) / 256, MAX_GRID); }
+
+// rows [R][C] -> codes and scales, eight lanes per block of 128
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_quant_rows_128(const T* __restrict__ src, int64_t R, int C, RowFilter rows, uint8_t* __restrict__ q,
+                 float* __restrict__ s) {
+  const int nb = (C + 127) / 128;
+  const int64_t blocks = R * nb;
+  for (int64_t b = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 3; b < blocks; b += (int64_t)gridDim.x * 32) {
+    const int64_t r = b >> 32 ? b / nb : (int64_t)((uint32_t)b / (uint32_t)nb);
+    const int cb = (int)(b - r * nb), col = cb * 128 + (threadIdx.x & 7) * 16;
+    const bool on = rows(r);
+    float v[16];
+    if (on && col < C) {
+      load16(src + r * C + col, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    }
+    float sc;
+    const uint4 code = quant_block8(v, sc);
+    if (!on) continue;
+    if (col < C) *reinterpret_cast<uint4*>(q + r * C + col) = code;
+    if ((threadIdx.x & 7) == 0) s[b] = sc;
+  }
+}
+
+// logistic sigmoid to about half a step more than correct rounding: the
+// exponential's argument in two parts, the reciprocal with a Newton step.
+// (device_common.h's sigmoidf_ is off by |g| steps, and a value near the border
+// of two codes then falls on the other side more often than it needs to.)
+__device__ __forceinline__ float sigmoid_(float g) {
+  constexpr float L = 1.44269502f, L_LO = 1.92596299e-8f;  // log2(e) = L + L_LO
+  const float hi = -g * L;
+  const float lo = fmaf(-g, L, -hi) - g * L_LO;
+  const float p = __builtin_amdgcn_exp2f(hi);
+  const float e = fabsf(hi) < 126.f ? fmaf(p, lo * 0.693147181f, p) : p;
+  const float d = fminf(1.f + e, 0x1p127f);  // (finite: the Newton step of an infinite d would be NaN)
+  const float r = __builtin_amdgcn_rcpf(d);
+  return fmaf(r, fmaf(-d, r, 1.f), r);
+}
+
+// A = silu(G) U of rows h [R][2n], quantized; A itself too when `a` is set
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_swiglu_fp8(const T* __restrict__ h, int64_t R, int n, RowFilter rows, uint8_t* __restrict__ q,
+             float* __restrict__ s, T* __restrict__ a) {
+  const int nb = (n + 127) / 128;
+  const int64_t blocks = R * nb;
+  for (int64_t b = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 3; b < blocks; b += (int64_t)gridDim.x * 32) {
+    const int64_t r = b >> 32 ? b / nb : (int64_t)((uint32_t)b / (uint32_t)nb);
+    const int cb = (int)(b - r * nb), col = cb * 128 + (threadIdx.x & 7) * 16;
+    const bool on = rows(r);
+    float v[16];
+    if (on && col < n) {
+      float g[16], u[16];
+      load16(h + r * 2 * n + col, g);
+      load16(h + r * 2 * n + n + col, u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = g[i] * sigmoid_(g[i]) * u[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    }
+    float sc;
+    const uint4 code = quant_block8(v, sc);
+    if (!on) continue;
+    if (col < n) {
+      *reinterpret_cast<uint4*>(q + r * n + col) = code;
+      if (a) store16(a + r * n + col, v);
+    }
+    if ((threadIdx.x & 7) == 0) s[b] = sc;
+  }
+}
+
+// dh = (da U s (1 + G (1 - s)), da silu(G)), s = sigmoid(G); 16 columns per thread
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_swiglu_bwd_rows(const T* __restrict__ da, const T* __restrict__ h, int64_t R, int n, RowFilter rows,
+                  T* __restrict__ dh) {
+  const int per = n / 16;
+  const int64_t total = R * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i >> 32 ? i / per : (int64_t)((uint32_t)i / (uint32_t)per);
+    const int col = (int)(i - r * per) * 16;
+    if (!rows(r)) continue;
+    float d[16], g[16], u[16];
+    load16(da + r * n + col, d);
+    load16(h + r * 2 * n + col, g);
+    load16(h + r * 2 * n + n + col, u);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float sg = sigmoid_(g[j]), dj = d[j];
+      d[j] = dj * u[j] * sg * (1.f + g[j] * (1.f - sg));
+      u[j] = dj * g[j] * sg;
+    }
+    store16(dh + r * 2 * n + col, d);
+    store16(dh + r * 2 * n + n + col, u);
+  }
+}
+
+// ---- 128 x 128 tiles ----
+// 256 threads; thread t holds the 8 x 8 values at rows 8 (t / 16), columns
+// 8 (t % 16), so that both a row's codes and a column's are eight bytes of it.
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+// byte j of each of eight rows (two words a row) -> eight bytes of column j
+__device__ __forceinline__ uint2 column_bytes(const uint32_t (&w)[8][2], int j) {
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo |= ((w[i][j >> 2] >> (8 * (j & 3))) & 0xffu) << (8 * i);
+    hi |= ((w[4 + i][j >> 2] >> (8 * (j & 3))) & 0xffu) << (8 * i);
+  }
+  return make_uint2(lo, hi);
+}
+
+constexpr int TP = 128 + 16;  // LDS pitch of a transposed tile's row (bytes)
+
+// weights [K][N] of expert blockIdx.z, tile (blockIdx.y, blockIdx.x)
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_quant_weights_128(const T* __restrict__ w, int K, int N, uint8_t* __restrict__ q, uint8_t* __restrict__ qt,
+                    float* __restrict__ s) {
+  __shared__ uint32_t wmax[4];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * TP];
+  const int tid = threadIdx.x;
+  const int k0 = blockIdx.y * 128, n0 = blockIdx.x * 128;
+  const int rk = (tid >> 4) * 8, cn = (tid & 15) * 8;
+  const size_t base = (size_t)blockIdx.z * K * N;
+  float v[8][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int k = k0 + rk + i, n = n0 + cn;
+    if (k < K && n < N) {
+      load8(w + base + (size_t)k * N + n, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, mag_bits(v[i][j]));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+  if ((tid & 63) == 0) wmax[tid >> 6] = m;
+  __syncthreads();
+  m = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
+  const float sc = block_scale(m), inv = __fdiv_rn(1.f, sc);
+  if (tid == 0) s[((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = sc;
+  uint32_t c[8][2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i][0] = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+    c[i][1] = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+  }
+  if (q) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = k0 + rk + i, n = n0 + cn;
+      if (k < K && n < N) *reinterpret_cast<uint2*>(q + base + (size_t)k * N + n) = make_uint2(c[i][0], c[i][1]);
+    }
+  }
+  if (qt) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(tile + (cn + j) * TP + rk) = column_bytes(c, j);
+    __syncthreads();
+    // 16 bytes per thread: eight threads per column's 128 rows
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = i * 32 + (tid >> 3), k = (tid & 7) * 16;
+      if (n0 + n < N && k0 + k < K)
+        *reinterpret_cast<uint4*>(qt + base + (size_t)(n0 + n) * K + k0 + k) =
+            *reinterpret_cast<const uint4*>(tile + n * TP + k);
+    }
+  }
+}
+
+// columns of the segments: one workgroup per block of 128 rows and 128 columns
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_quant_cols_128(const T* __restrict__ src, int C, int Tn, bool gather, PlanArgs p, uint8_t* __restrict__ q,
+                 float* __restrict__ s) {
+  __shared__ uint32_t cmax[16][128];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * TP];
+  const int tid = threadIdx.x;
+  const int ct = (C + 127) / 128;
+  const int64_t blk = blockIdx.x / ct;
+  const int r0 = (int)(blk * 128), c0 = (int)(blockIdx.x % ct) * 128;
+  if (r0 >= p.offsets[p.E]) return;
+  const int rk = (tid >> 4) * 8, cn = (tid & 15) * 8;
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + rk + i, col = c0 + cn;
+    const int tok = p.row_token[r];
+    if ((unsigned)tok < (unsigned)Tn && col < C) {
+      load8(src + (size_t)(gather ? tok : r) * C + col, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, mag_bits(v[i][j]));
+    cmax[tid >> 4][cn + j] = m;
+  }
+  __syncthreads();
+  float inv[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) m = max(m, cmax[g][cn + j]);
+    const float sc = block_scale(m);
+    inv[j] = __fdiv_rn(1.f, sc);
+    if (tid < 16 && c0 + cn + j < C) s[blk * C + c0 + cn + j] = sc;
+  }
+  uint32_t c[8][2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i][0] = e4m3x4(v[i][0] * inv[0], v[i][1] * inv[1], v[i][2] * inv[2], v[i][3] * inv[3]);
+    c[i][1] = e4m3x4(v[i][4] * inv[4], v[i][5] * inv[5], v[i][6] * inv[6], v[i][7] * inv[7]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(tile + (cn + j) * TP + rk) = column_bytes(c, j);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = i * 32 + (tid >> 3), k = (tid & 7) * 16;
+    if (c0 + n < C)
+      *reinterpret_cast<uint4*>(q + (blk * C + c0 + n) * 128 + k) = *reinterpret_cast<const uint4*>(tile + n * TP + k);
+  }
+}
+
+RowFilter filter_of(const PlanArgs& p) { return RowFilter{p.offsets, p.row_token, p.E}; }
+
+}  // namespace
+
+hipError_t launch_quant_rows_128(const PlanArgs& p, int dtype, int64_t R, int C, const void* src, uint8_t* q,
+                                 float* s, hipStream_t st) {
+  const dim3 grid(grid_for(R * ((C + 127) / 128) * 8));
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(k_quant_rows_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)src, R, C, filter_of(p), q, s);
+  else
+    hipLaunchKernelGGL(k_quant_rows_128<float>, grid, dim3(256), 0, st, (const float*)src, R, C, filter_of(p), q, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_fp8(const PlanArgs& p, int dtype, int64_t R, int n, const void* h, uint8_t* q, float* s,
+                             void* a, hipStream_t st) {
+  const dim3 grid(grid_for(R * ((n + 127) / 128) * 8));
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(k_swiglu_fp8<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)h, R, n, filter_of(p), q, s,
+                       (bf16_t*)a);
+  else
+    hipLaunchKernelGGL(k_swiglu_fp8<float>, grid, dim3(256), 0, st, (const float*)h, R, n, filter_of(p), q, s,
+                       (float*)a);
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_bwd_rows(const PlanArgs& p, int dtype, int64_t R, int n, const void* da, const void* h,
+                                  void* dh, hipStream_t st) {
+  const dim3 grid(grid_for(R * (n / 16)));
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(k_swiglu_bwd_rows<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)da, (const bf16_t*)h, R, n,
+                       filter_of(p), (bf16_t*)dh);
+  else
+    hipLaunchKernelGGL(k_swiglu_bwd_rows<float>, grid, dim3(256), 0, st, (const float*)da, (const float*)h, R, n,
+                       filter_of(p), (float*)dh);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_weights_128(int dtype, int E, int K, int N, const void* w, uint8_t* q, uint8_t* qt, float* s,
+                                    hipStream_t st) {
+  const dim3 grid((N + 127) / 128, (K + 127) / 128, E);
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(k_quant_weights_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)w, K, N, q, qt, s);
+  else
+    hipLaunchKernelGGL(k_quant_weights_128<float>, grid, dim3(256), 0, st, (const float*)w, K, N, q, qt, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_cols_128(const PlanArgs& p, int dtype, int C, bool gather, const void* src, uint8_t* q,
+                                 float* s, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)(p.cap / 128) * ((C + 127) / 128)));
+  if (grid.x == 0) return hipSuccess;
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(k_quant_cols_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)src, C, p.T, gather, p, q, s);
+  else
+    hipLaunchKernelGGL(k_quant_cols_128<float>, grid, dim3(256), 0, st, (const float*)src, C, p.T, gather, p, q, s);
+  return hipGetLastError();
+}
+
+}  // namespace moe

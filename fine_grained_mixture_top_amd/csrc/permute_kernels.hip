@@ -1,0 +1,411 @@
+// Tokens sorted by expert and back (moe_sort, moe_permute, moe_unpermute and
+// their gradients).
+//
+// Sort: a stable counting sort of the T*K expert choices.  A choice's row is
+//   offsets[e] + (choices of e in earlier chunks) + (earlier in its chunk),
+// and each of the three terms is an integer count, so the result does not
+// depend on the order in which workgroups run.
+//
+// Moving rows: bandwidth is all there is.  The permutation walks tokens, not
+// rows: a token's row is read once and written to its K places.  The way back
+// walks tokens too, with the K rows' loads in flight together.
+#include <algorithm>
+
+#include "device_common.h"
+#include "fp8_block.h"
+#include "ops_launch.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int SORT_NT = 1024;      // threads of a sort workgroup = slots per step
+constexpr int SORT_WAVES = SORT_NT / 64;
+constexpr int SORT_MAX_CHUNKS = 256;
+constexpr int SORT_MAX_E = 1024;
+
+// Rank of every lane among the lanes of its wave with the same key (ascending
+// lane), and how many those are.  keys < 2^bits.
+__device__ __forceinline__ void wave_rank(int key, int bits, int lane, int& rank, int& count) {
+  uint64_t same = ~0ull;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (key >> b) & 1;
+    const uint64_t m = __ballot(one);
+    same &= one ? m : ~m;
+  }
+  rank = __popcll(same & ((1ull << lane) - 1));
+  count = __popcll(same);
+}
+
+// Choices per expert and chunk of `chunk` slots: cnt [chunks][E]
+__global__ void __launch_bounds__(SORT_NT)
+k_sort_count(const int32_t* __restrict__ idx, int slots, int E, int chunk, int32_t* __restrict__ cnt) {
+  __shared__ int h[SORT_MAX_E];
+  for (int e = threadIdx.x; e < E; e += SORT_NT) h[e] = 0;
+  __syncthreads();
+  const int s0 = blockIdx.x * chunk, s1 = min(slots - s0, chunk) + s0;
+  for (int s = s0 + (int)threadIdx.x; s < s1; s += SORT_NT) {
+    const int e = idx[s];
+    if ((unsigned)e < (unsigned)E) atomicAdd(&h[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += SORT_NT) cnt[(size_t)blockIdx.x * E + e] = h[e];
+}
+
+// Rows of one chunk's choices.  With `cnt` null the launch is one workgroup
+// that counts all slots itself.
+__global__ void __launch_bounds__(SORT_NT)
+k_sort_place(const int32_t* __restrict__ idx, int slots, int K, int E, int align, int chunk,
+             const int32_t* __restrict__ cnt, int32_t* __restrict__ offsets, int32_t* __restrict__ counts,
+             int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row) {
+  __shared__ int total[SORT_MAX_E];                 // choices of each expert, then its segment's first row
+  __shared__ int before[SORT_MAX_E];                // of those, in earlier chunks; then the next free row
+  __shared__ int wcount[SORT_WAVES][SORT_MAX_E];    // this step's choices per wave and expert
+  __shared__ int wsum[SORT_WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int chunks = gridDim.x, me = blockIdx.x;
+
+  for (int e = tid; e < E; e += SORT_NT) total[e] = before[e] = 0;
+  __syncthreads();
+  if (cnt) {
+    // thread groups of E take the chunks in turn; integer sums
+    const int groups = max(1, SORT_NT / E);
+    const int g = tid / E, e = tid % E;
+    if (g < groups) {
+      int t = 0, b = 0;
+      for (int c = g; c < chunks; c += groups) {
+        const int v = cnt[(size_t)c * E + e];
+        t += v;
+        if (c < me) b += v;
+      }
+      atomicAdd(&total[e], t);
+      atomicAdd(&before[e], b);
+    }
+  } else {
+    for (int s = tid; s < slots; s += SORT_NT) {
+      const int e = idx[s];
+      if ((unsigned)e < (unsigned)E) atomicAdd(&total[e], 1);
+    }
+  }
+  __syncthreads();
+
+  // exclusive scan of the padded lengths (thread e = expert e)
+  const int n = tid < E ? total[tid] : 0;
+  const int padded = (n + align - 1) / align * align;
+  int incl = padded;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 63) wsum[wave] = incl;
+  __syncthreads();
+  int first = incl - padded;
+  for (int w = 0; w < wave; ++w) first += wsum[w];
+  if (tid < E) {
+    if (me == 0) {
+      offsets[tid] = first;
+      counts[tid] = n;
+      if (tid == E - 1) offsets[E] = first + padded;
+    }
+    // the rows that fill up a segment, dealt to the workgroups by expert
+    if (tid % chunks == me)
+      for (int r = first + n; r < first + padded; ++r) row_token[r] = -1;
+    before[tid] += first;
+  }
+  const int bits = 32 - __clz(E);  // E itself marks a dropped choice
+
+  const int s0 = me * chunk, s1 = min(slots - s0, chunk) + s0;
+  for (int base = s0; base < s1; base += SORT_NT) {
+    for (int i = tid; i < SORT_WAVES * E; i += SORT_NT) wcount[i / E][i % E] = 0;
+    __syncthreads();  // (also: `before` is complete)
+    const int s = base + tid;
+    const int id = s < s1 ? idx[s] : -1;
+    const bool kept = (unsigned)id < (unsigned)E;
+    const int e = kept ? id : E;
+    int rank, same;
+    wave_rank(e, bits, lane, rank, same);
+    if (kept && rank == 0) wcount[wave][e] = same;
+    __syncthreads();
+    int row = -1;
+    if (kept) {
+      row = before[e] + rank;
+      for (int w = 0; w < wave; ++w) row += wcount[w][e];
+      row_token[row] = s / K;
+    }
+    if (s < s1) slot_row[s] = row;
+    __syncthreads();
+    if (tid < E)
+      for (int w = 0; w < SORT_WAVES; ++w) before[tid] += wcount[w][tid];
+    __syncthreads();  // wcount is cleared next
+  }
+}
+
+int sort_chunk(int64_t slots) {
+  const int64_t per = (slots + SORT_MAX_CHUNKS - 1) / SORT_MAX_CHUNKS;
+  return (int)((std::max<int64_t>(per, 1) + SORT_NT - 1) / SORT_NT * SORT_NT);
+}
+
+// Up to this many slots one workgroup counts and places them itself.
+constexpr int SORT_ONE = 4096;
+
+// xp[slot_row[t,k]] = x[t], 16-byte pieces; `splits` waves share a token's row
+__global__ void __launch_bounds__(256)
+k_permute(const uint4* __restrict__ x, const int32_t* __restrict__ slot_row, int T, int K, int cap, int pieces,
+          int splits, uint4* __restrict__ xp) {
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (int)(w / splits);
+  if (t >= T) return;
+  const int32_t* rows = slot_row + (size_t)t * K;
+  for (int c = (int)(w % splits) * 64 + lane; c < pieces; c += splits * 64) {
+    const uint4 v = x[(size_t)t * pieces + c];
+    for (int k = 0; k < K; ++k) {
+      const int r = rows[k];
+      if ((unsigned)r < (unsigned)cap) xp[(size_t)r * pieces + c] = v;
+    }
+  }
+}
+
+// The same with the row quantized on the way: eight lanes per block of 128.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_permute_fp8(const T* __restrict__ x, const int32_t* __restrict__ slot_row, int Tn, int K, int cap, int d,
+              int splits, uint8_t* __restrict__ q, float* __restrict__ s) {
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (int)(w / splits);
+  if (t >= Tn) return;
+  const int32_t* rows = slot_row + (size_t)t * K;
+  const int nb = (d + 127) / 128;
+  for (int b0 = (int)(w % splits) * 8; b0 < nb; b0 += splits * 8) {
+    const int b = b0 + (lane >> 3), col = b * 128 + (lane & 7) * 16;
+    float v[16];
+    if (col < d) {
+      load16(x + (size_t)t * d + col, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    }
+    float sc;
+    const uint4 code = quant_block8(v, sc);
+    for (int k = 0; k < K; ++k) {
+      const int r = rows[k];
+      if ((unsigned)r >= (unsigned)cap) continue;
+      if (col < d) *reinterpret_cast<uint4*>(q + (size_t)r * d + col) = code;
+      if ((lane & 7) == 0 && b < nb) s[(size_t)r * nb + b] = sc;
+    }
+  }
+}
+
+template <typename T> constexpr int VEC = 16 / (int)sizeof(T);
+
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4 u, float (&v)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float (&v)[16 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 2)
+    return make_uint4(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]), f2bf2(v[4], v[5]), f2bf2(v[6], v[7]));
+  else
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+constexpr int ROWS_UNR = 8;  // rows of a token in flight
+
+// o[t] = sum over k of w[t,k] y[slot_row[t,k]] in ascending k (w null: ones)
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_unpermute(const uint4* __restrict__ y, const float* __restrict__ wt, const int32_t* __restrict__ slot_row, int Tn,
+            int K, int cap, int pieces, int splits, uint4* __restrict__ o) {
+  constexpr int V = VEC<T>;
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (int)(w / splits);
+  if (t >= Tn) return;
+  const int32_t* rows = slot_row + (size_t)t * K;
+  for (int c = (int)(w % splits) * 64 + lane; c < pieces; c += splits * 64) {
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int k0 = 0; k0 < K; k0 += ROWS_UNR) {
+      uint4 raw[ROWS_UNR];
+      bool ok[ROWS_UNR];
+#pragma unroll
+      for (int j = 0; j < ROWS_UNR; ++j) {
+        const int r = k0 + j < K ? rows[k0 + j] : -1;
+        ok[j] = (unsigned)r < (unsigned)cap;
+        raw[j] = ok[j] ? y[(size_t)r * pieces + c] : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < ROWS_UNR; ++j) {
+        if (!ok[j]) continue;
+        const float g = wt ? wt[(size_t)t * K + k0 + j] : 1.f;
+        float v[V];
+        unpack16<T>(raw[j], v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+      }
+    }
+    o[(size_t)t * pieces + c] = pack16<T>(acc);
+  }
+}
+
+// dy[r] = w[t,k] d_o[t] and dw[t,k] = <d_o[t], y[r]>, r = slot_row[t,k]: one
+// workgroup per token; the dot products end in a fixed tree over lanes and waves
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_unpermute_bwd(const uint4* __restrict__ d_o, const uint4* __restrict__ y, const float* __restrict__ wt,
+                const int32_t* __restrict__ slot_row, int K, int cap, int pieces, uint4* __restrict__ dy,
+                float* __restrict__ dw) {
+  constexpr int V = VEC<T>;
+  constexpr int KG = ROWS_UNR;
+  __shared__ float part[4][KG];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int t = blockIdx.x;
+  const int32_t* rows = slot_row + (size_t)t * K;
+  for (int k0 = 0; k0 < K; k0 += KG) {
+    int r[KG];
+    float g[KG], dot[KG];
+#pragma unroll
+    for (int j = 0; j < KG; ++j) {
+      r[j] = k0 + j < K ? rows[k0 + j] : -1;
+      if ((unsigned)r[j] >= (unsigned)cap) r[j] = -1;
+      g[j] = dy && r[j] >= 0 ? wt[(size_t)t * K + k0 + j] : 0.f;
+      dot[j] = 0.f;
+    }
+    for (int c = tid; c < pieces; c += 256) {
+      float a[V];
+      unpack16<T>(d_o[(size_t)t * pieces + c], a);
+      if (dw) {
+        uint4 raw[KG];
+#pragma unroll
+        for (int j = 0; j < KG; ++j)
+          raw[j] = r[j] >= 0 ? y[(size_t)r[j] * pieces + c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < KG; ++j) {
+          if (r[j] < 0) continue;
+          float v[V];
+          unpack16<T>(raw[j], v);
+#pragma unroll
+          for (int i = 0; i < V; ++i) dot[j] = fmaf(a[i], v[i], dot[j]);
+        }
+      }
+      if (dy) {
+#pragma unroll
+        for (int j = 0; j < KG; ++j) {
+          if (r[j] < 0) continue;
+          float v[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] = g[j] * a[i];
+          dy[(size_t)r[j] * pieces + c] = pack16<T>(v);
+        }
+      }
+    }
+    if (dw) {
+#pragma unroll
+      for (int j = 0; j < KG; ++j) {
+        const float s = wave_sum(dot[j]);
+        if (lane == 0) part[wave][j] = s;
+      }
+      __syncthreads();
+      if (tid < KG && k0 + tid < K)
+        dw[(size_t)t * K + k0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+      __syncthreads();
+    }
+  }
+}
+
+// Waves per token: rows of one token are split until there are about eight
+// waves per SIMD's share of the card, and no finer than one pass of 64 lanes.
+int row_splits(int T, int passes) {
+  const int want = (4096 + T - 1) / std::max(T, 1);
+  return std::max(1, std::min(want, passes));
+}
+
+unsigned wave_blocks(int T, int splits) { return (unsigned)(((int64_t)T * splits + 3) / 4); }
+
+}  // namespace
+
+size_t sort_ws_bytes(int64_t slots, int E) {
+  if (slots <= SORT_ONE) return 0;
+  const int chunk = sort_chunk(slots);
+  return (size_t)((slots + chunk - 1) / chunk) * E * sizeof(int32_t);
+}
+
+hipError_t launch_sort(const PlanArgs& p, const int32_t* expert_idx, const moe_plan& out, void* ws, hipStream_t st) {
+  const int slots = p.T * p.K;
+  if (slots <= SORT_ONE) {
+    hipLaunchKernelGGL(k_sort_place, dim3(1), dim3(SORT_NT), 0, st, expert_idx, slots, p.K, p.E, p.align,
+                       SORT_ONE, nullptr, out.offsets, out.counts, out.row_token, out.slot_row);
+    return hipGetLastError();
+  }
+  const int chunk = sort_chunk(slots);
+  const unsigned chunks = (unsigned)(((int64_t)slots + chunk - 1) / chunk);
+  hipLaunchKernelGGL(k_sort_count, dim3(chunks), dim3(SORT_NT), 0, st, expert_idx, slots, p.E, chunk, (int32_t*)ws);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_sort_place, dim3(chunks), dim3(SORT_NT), 0, st, expert_idx, slots, p.K, p.E, p.align, chunk,
+                     (const int32_t*)ws, out.offsets, out.counts, out.row_token, out.slot_row);
+  return hipGetLastError();
+}
+
+hipError_t launch_permute(const PlanArgs& p, int dtype, int d, const void* x, void* xp, hipStream_t st) {
+  const int pieces = (int)((int64_t)d * (dtype == MOE_BF16 ? 2 : 4) / 16);
+  const int splits = row_splits(p.T, (pieces + 63) / 64);
+  hipLaunchKernelGGL(k_permute, dim3(wave_blocks(p.T, splits)), dim3(256), 0, st, (const uint4*)x, p.slot_row, p.T,
+                     p.K, p.cap, pieces, splits, (uint4*)xp);
+  return hipGetLastError();
+}
+
+hipError_t launch_permute_fp8(const PlanArgs& p, int dtype, int d, const void* x, uint8_t* q, float* s,
+                              hipStream_t st) {
+  const int splits = row_splits(p.T, (d + 1023) / 1024);
+  const dim3 grid(wave_blocks(p.T, splits));
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(k_permute_fp8<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)x, p.slot_row, p.T, p.K, p.cap,
+                       d, splits, q, s);
+  else
+    hipLaunchKernelGGL(k_permute_fp8<float>, grid, dim3(256), 0, st, (const float*)x, p.slot_row, p.T, p.K, p.cap, d,
+                       splits, q, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_unpermute(const PlanArgs& p, int dtype, int d, const void* y, const float* w, void* o,
+                            hipStream_t st) {
+  const int pieces = (int)((int64_t)d * (dtype == MOE_BF16 ? 2 : 4) / 16);
+  const int splits = row_splits(p.T, (pieces + 63) / 64);
+  const dim3 grid(wave_blocks(p.T, splits));
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(k_unpermute<bf16_t>, grid, dim3(256), 0, st, (const uint4*)y, w, p.slot_row, p.T, p.K, p.cap,
+                       pieces, splits, (uint4*)o);
+  else
+    hipLaunchKernelGGL(k_unpermute<float>, grid, dim3(256), 0, st, (const uint4*)y, w, p.slot_row, p.T, p.K, p.cap,
+                       pieces, splits, (uint4*)o);
+  return hipGetLastError();
+}
+
+hipError_t launch_unpermute_bwd(const PlanArgs& p, int dtype, int d, const void* d_o, const void* y, const float* w,
+                                void* dy, float* dw, hipStream_t st) {
+  const int pieces = (int)((int64_t)d * (dtype == MOE_BF16 ? 2 : 4) / 16);
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(k_unpermute_bwd<bf16_t>, dim3(p.T), dim3(256), 0, st, (const uint4*)d_o, (const uint4*)y, w,
+                       p.slot_row, p.K, p.cap, pieces, (uint4*)dy, dw);
+  else
+    hipLaunchKernelGGL(k_unpermute_bwd<float>, dim3(p.T), dim3(256), 0, st, (const uint4*)d_o, (const uint4*)y, w,
+                       p.slot_row, p.K, p.cap, pieces, (uint4*)dy, dw);
+  return hipGetLastError();
+}
+
+}  // namespace moe
