@@ -20,15 +20,18 @@
 //
 //  * Both operands are lines of 128 codes: a row's block (moe_fp8_mm: rows of
 //    a, gathered or not, and rows of b) or a column's block of 128 rows
-//    (moe_fp8_wgrad).  A stage goes straight into LDS, 16 bytes per lane; the
-//    16-byte chunk c of line r sits in slot c ^ (r & 7), so that the eight
-//    lanes of an LDS access meet eight different slots.  Two stages: one
-//    computed, one in flight.
+//    (moe_fp8_wgrad).  A stage goes straight into LDS, 16 bytes per lane.  Two
+//    stage buffers: a stage's fragments are all in registers before its last
+//    row piece is multiplied, so the one barrier of a stage stands there, the
+//    stage after next starts loading into the same buffer, and the next
+//    stage's fragments are read beside that piece's matrix instructions.
 //  * The N-side operand is the MFMA's first: lane l then holds, for the row
-//    l % 16 of a piece, the four columns 4 (l / 16) .. +3.
+//    l % 16 of a piece, four columns.
 //  * Persistent workgroups walk the tiles expert by expert, neighbouring tiles
-//    on one XCD, and load the next tile's first stage during a tile's last.
+//    on one XCD; loading runs two stages ahead across the tiles' borders.
 #pragma once
+
+#include <type_traits>
 
 #include "device_common.h"
 #include "ops_launch.h"
@@ -51,9 +54,13 @@ __device__ __forceinline__ void load16_lds(__amdgpu_buffer_rsrc_t r, char* lds, 
 __device__ __forceinline__ void load4_lds(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t voff, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds, 4, voff, soff, 0, 0);
 }
-__device__ __forceinline__ void wait_vm0() {
+// all but the newest N vector memory operations of this wave are complete
+// (loads and stores complete in the order they were issued)
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N < 64, "vmcnt has six bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0); lgkmcnt, expcnt at their maximum
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));  // lgkmcnt, expcnt at their maximum
   asm volatile("" ::: "memory");
 }
 
@@ -64,24 +71,23 @@ __device__ __forceinline__ f32x4_v mfma128(i32x8_v a, i32x8_v b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
 }
 
-// A lane's 32 of the 128 codes of a line, as the matrix cores take them.  Both
-// operands place equal k in equal lanes and bytes, so any split of the 128 does.
+// A lane's 32 of the 128 codes of a line, as read, and as the matrix cores take
+// them.  Both operands place equal k in equal lanes and bytes, so any split of
+// the 128 does.
 template <bool EXACT> struct Frag;
 template <> struct Frag<false> {
   i32x8_v v;
   __device__ __forceinline__ Frag() {}
-  __device__ __forceinline__ Frag(const uint4 lo, const uint4 hi)
-      : v{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w} {}
+  __device__ __forceinline__ explicit Frag(const i32x8_v r) : v(r) {}
 };
 template <> struct Frag<true> {
   bf16x8_v v[4];
   __device__ __forceinline__ Frag() {}
-  __device__ __forceinline__ Frag(const uint4 lo, const uint4 hi) {
-    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  __device__ __forceinline__ explicit Frag(const i32x8_v r) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const bf16x2_v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.f, false);
-      const bf16x2_v b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.f, true);
+      const bf16x2_v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[i], 1.f, false);
+      const bf16x2_v b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[i], 1.f, true);
       v[i >> 1][4 * (i & 1)] = a[0];
       v[i >> 1][4 * (i & 1) + 1] = a[1];
       v[i >> 1][4 * (i & 1) + 2] = b[0];
@@ -99,11 +105,26 @@ __device__ __forceinline__ f32x4_v dot(const Frag<true>& a, const Frag<true>& b)
   return d;
 }
 
-// this lane's codes of line rb + l % 16: chunks l / 16 and l / 16 + 4
-template <bool EXACT>
-__device__ __forceinline__ Frag<EXACT> frag(const char* op, int rb, int lane) {
-  const int r = rb + (lane & 15), h = lane >> 4;
-  return Frag<EXACT>(lds_ld16(op + r * 128 + ((h ^ r) & 7) * 16), lds_ld16(op + r * 128 + (((h + 4) ^ r) & 7) * 16));
+__device__ __forceinline__ i32x8_v join(const uint4 lo, const uint4 hi) {
+  return i32x8_v{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+
+// Chunk c of line r of an operand's stage sits in slot c ^ key(r); the lines
+// that eight neighbouring lanes read at once have eight different keys.
+__device__ __forceinline__ int key_a(int r) { return r & 7; }
+// N side: a lane's results are to be neighbouring columns, 16 bytes of them at
+// once, so with 2-byte results the position p of piece i takes the column
+// 32 (i / 2) + 8 (p / 4) + 4 (i % 2) + p % 4 of the wave's 64.
+// (its lines 4 (i % 2) apart share the low bits, hence another key)
+template <bool WIDE> __device__ __forceinline__ int key_b(int r) { return WIDE ? r & 7 : (r & 3) | ((r >> 1) & 4); }
+template <bool WIDE> __device__ __forceinline__ int column(int i, int p) {
+  return WIDE ? 16 * i + p : 32 * (i >> 1) + 8 * (p >> 2) + 4 * (i & 1) + (p & 3);
+}
+
+// this lane's codes of line r: chunks l / 16 and l / 16 + 4
+__device__ __forceinline__ i32x8_v line_codes(const char* op, int r, int key, int lane) {
+  const int h = lane >> 4;
+  return join(lds_ld16(op + r * 128 + (h ^ key) * 16), lds_ld16(op + r * 128 + ((h + 4) ^ key) * 16));
 }
 
 struct Args {
@@ -121,12 +142,6 @@ struct Args {
   int sb_k, sb_n;            // strides of sb in (reduction block, column block)
 };
 
-template <typename O>
-__device__ __forceinline__ void store4(O* p, f32x4_v v) {
-  if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(p) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
-  else *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-
 // BM x BN tiles, WM x WN waves.  WG: weight gradient (tiles of dw over the
 // segment's blocks), else rows of c.
 template <int BM, int BN, int WM, int WN, bool WG>
@@ -140,10 +155,17 @@ struct Cfg {
   static constexpr int SBN = WG ? BN : 64;                  // scale words of b per stage
   static constexpr int STAGE = SB_OFF + SBN * 4;
   static constexpr int SMEM = 2 * STAGE;
-  static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0 && TM % 16 == 0 && TN % 16 == 0, "tile split");
+  static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0 && TM % 32 == 0 && TN % 32 == 0, "tile split");
   static_assert(WG || 128 % TN == 0, "a wave's columns lie in one block of 128");
   static_assert(WG ? BM / 64 + BN / 64 <= W : BM / 64 + 1 <= W, "one scale load per wave");
   static_assert(STAGE % 256 == 0, "alignment");
+};
+
+// One tile: expert, first row in its segment (weight gradient: first column of
+// a), first column, stages; first row and rows of the segment from there on
+// (weight gradient: of the segment).
+struct Tile {
+  int e, m0, n0, nk, row0, rows;
 };
 
 template <int BM, int BN, int WM, int WN, bool WG, typename O>
@@ -151,10 +173,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
 k_fp8_gemm(Args g) {
   using C = Cfg<BM, BN, WM, WN, WG>;
   constexpr bool EX = sizeof(O) == 4;  // fp32 results on the bf16 matrix cores
+  constexpr int FM = C::FM, FN = C::FN;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   __shared__ int seg0[MAX_E];         // first row of each segment
   __shared__ int segn[MAX_E];         // its rows
   __shared__ int tprefix[MAX_E + 1];  // row tiles before it
+  __shared__ int tok[2][WG ? 1 : BM];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = w / WN, wn = w % WN;
@@ -197,33 +221,53 @@ k_fp8_gemm(Args g) {
     if (tid == 0) tprefix[g.E] = carry;
     __syncthreads();
   }
-  const int64_t total = (int64_t)tprefix[g.E] * NT;
+  // (a result that fits the memory has far fewer than 2^31 tiles)
+  const int total = __builtin_amdgcn_readfirstlane(tprefix[g.E]) * NT;
   const int G = gridDim.x;
+  const int t0 = xcd_virtual_id(blockIdx.x, G);
+  if (t0 >= total) return;
 
-  struct Tile {
-    int e, m0, n0;   // expert, first row (column of a) in its segment, first column
-    int nk;          // stages
+  // tile t, at or behind expert e
+  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  auto uniform_ptr = [&](const char* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    return reinterpret_cast<const char*>((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
   };
-  auto tile_at = [&](int64_t t) {
+  auto tile_at = [&](int t, int e) {
     Tile q;
-    const int mg = (int)(t / NT);
-    q.n0 = (int)(t % NT) * BN;
-    q.e = upper_index(tprefix, g.E + 1, mg);
-    q.m0 = (mg - tprefix[q.e]) * BM;
+    const int mg = (int)((unsigned)t / (unsigned)NT);
+    q.n0 = (t - mg * NT) * BN;
+    while (uniform(tprefix[e + 1]) <= mg) ++e;
+    q.e = e;
+    q.m0 = (mg - uniform(tprefix[e])) * BM;
+    q.row0 = uniform(seg0[e]) + (WG ? 0 : q.m0);
+    q.rows = uniform(segn[e]) - (WG ? 0 : q.m0);
     // (a segment never reaches past the last whole block of the buffers)
-    q.nk = WG ? max(0, min((segn[q.e] + 127) >> 7, (g.rows >> 7) - (seg0[q.e] >> 7))) : g.kb;
+    q.nk = WG ? max(0, min((q.rows + 127) >> 7, (g.rows >> 7) - (q.row0 >> 7))) : g.kb;
     return q;
   };
 
-  const int sub = lane >> 3;                          // line of a 1 KB load
-  const uint32_t chunk = (uint32_t)((lane & 7) ^ sub) * 16u;
-  uint32_t oa[C::IA], ob[C::IB], os;                  // lane offsets of this tile's loads
+  // ---- loading: a cursor over the stages of this workgroup's tiles ----
+  const int sub = lane >> 3;  // line of a 1 KB load
+  const uint32_t cha = (uint32_t)((lane & 7) ^ key_a(sub)) * 16u;
+  auto chb = [&](int i) { return (uint32_t)((lane & 7) ^ key_b<EX>((C::IB * w + i) * 8 + sub)) * 16u; };
+  uint32_t oa[C::IA], ob[C::IB], os;  // lane offsets of the cursor's tile
   const char *pa, *pb, *psa, *psb;
-  uint32_t na, nb, nsa, nsb;                          // record counts
-
-  auto setup = [&](const Tile& q) {
+  uint32_t na, nb, nsa, nsb;          // record counts
+  int lt = t0;                        // the cursor's tile, -1 behind the last one
+  int lk = 0;                         // and stage
+  Tile lq = tile_at(t0, 0);
+  // gathered rows: the tokens of the cursor's next tile go into LDS one tile
+  // ahead, into one buffer while other waves may still read the other
+  int tp = 0;
+  auto fetch_tokens = [&](const Tile& q) {
+    if (!WG && g.row_token && w < BM / 64)
+      load4_lds(rsrc(g.row_token + q.row0, (uint32_t)min(q.rows, BM) * 4u), reinterpret_cast<char*>(tok[tp] + 64 * w),
+                (uint32_t)(64 * w + lane) * 4u, 0);
+  };
+  auto setup = [&](const Tile& q, const int* tok) {
     if constexpr (WG) {
-      const int64_t blk = seg0[q.e] >> 7;
+      const int64_t blk = q.row0 >> 7;
       pa = (const char*)g.a + blk * g.M * 128;
       pb = (const char*)g.b + blk * g.N * 128;
       psa = (const char*)(g.sa + blk * g.M);
@@ -233,21 +277,20 @@ k_fp8_gemm(Args g) {
       nsa = (uint32_t)g.M * 4u;
       nsb = (uint32_t)g.N * 4u;
 #pragma unroll
-      for (int i = 0; i < C::IA; ++i) oa[i] = (uint32_t)(q.m0 + (C::IA * w + i) * 8 + sub) * 128u + chunk;
+      for (int i = 0; i < C::IA; ++i) oa[i] = (uint32_t)(q.m0 + (C::IA * w + i) * 8 + sub) * 128u + cha;
 #pragma unroll
-      for (int i = 0; i < C::IB; ++i) ob[i] = (uint32_t)(q.n0 + (C::IB * w + i) * 8 + sub) * 128u + chunk;
+      for (int i = 0; i < C::IB; ++i) ob[i] = (uint32_t)(q.n0 + (C::IB * w + i) * 8 + sub) * 128u + chb(i);
       os = w < BM / 64 ? (uint32_t)(q.m0 + 64 * w + lane) * 4u : (uint32_t)(q.n0 + 64 * (w - BM / 64) + lane) * 4u;
     } else {
-      const int row0 = seg0[q.e] + q.m0, left = segn[q.e] - q.m0;
+      const bool gather = g.row_token != nullptr;
       // line of a for row i of the tile, relative to pa; OOB for none
       auto arow = [&](int i) -> uint32_t {
-        if (i >= left) return OOB;
-        if (!g.row_token) return (uint32_t)i;
-        const int t = g.row_token[row0 + i];
-        return (unsigned)t < (unsigned)g.a_rows ? (uint32_t)t : OOB;
+        if (i >= q.rows) return OOB;
+        if (!gather) return (uint32_t)i;
+        return (unsigned)tok[i] < (unsigned)g.a_rows ? (uint32_t)tok[i] : OOB;
       };
-      const int64_t abase = g.row_token ? 0 : row0;
-      const uint32_t alines = g.row_token ? (uint32_t)g.a_rows : (uint32_t)min(left, BM);
+      const int64_t abase = gather ? 0 : q.row0;
+      const uint32_t alines = gather ? (uint32_t)g.a_rows : (uint32_t)min(q.rows, BM);
       pa = (const char*)g.a + abase * g.K;
       na = alines * (uint32_t)g.K;
       psa = (const char*)(g.sa + abase * g.kb);
@@ -260,12 +303,12 @@ k_fp8_gemm(Args g) {
 #pragma unroll
       for (int i = 0; i < C::IA; ++i) {
         const uint32_t r = arow((C::IA * w + i) * 8 + sub);
-        oa[i] = r == OOB ? OOB : r * (uint32_t)g.K + chunk;
+        oa[i] = r == OOB ? OOB : r * (uint32_t)g.K + cha;
       }
 #pragma unroll
       for (int i = 0; i < C::IB; ++i) {
         const int n = q.n0 + (C::IB * w + i) * 8 + sub;
-        ob[i] = n < g.N ? (uint32_t)n * (uint32_t)g.K + chunk : OOB;
+        ob[i] = n < g.N ? (uint32_t)n * (uint32_t)g.K + chb(i) : OOB;
       }
       if (w < BM / 64) {
         const uint32_t r = arow(64 * w + lane);
@@ -276,119 +319,221 @@ k_fp8_gemm(Args g) {
       }
     }
   };
-  int parity = 0;
-  auto issue = [&](int k, int par) {
+  // The loads of a stage come in PARTS: every wave's load instructions in one
+  // burst would keep the matrix cores waiting for their issue.  part 0 starts
+  // the cursor's stage in buffer `par`, the last one moves the cursor on.  On
+  // entry lq is the cursor's tile (lk == 0: not set up yet) or, for lk > 0, the
+  // next one.
+  constexpr int PARTS = FN;
+  int lnk = 0;
+  auto load_part = [&](int part, int par) {
+    if (lt < 0) return;
+    if (part == 0 && lk == 0) {
+      // the next tile with stages (a weight gradient may have none)
+      while (WG && lq.nk == 0) {
+        lt += G;
+        if (lt >= total) {
+          lt = -1;
+          return;
+        }
+        lq = tile_at(lt, lq.e);
+      }
+      setup(lq, tok[tp]);
+      tp ^= 1;
+      lnk = lq.nk;
+      if (lt + G < total) {
+        lq = tile_at(lt + G, lq.e);
+        fetch_tokens(lq);
+      }
+    }
     char* st = smem + par * C::STAGE;
+    // (a descriptor shared by the parts would travel through vector registers)
+    const char *ua = uniform_ptr(pa), *ub = uniform_ptr(pb);
+    const __amdgpu_buffer_rsrc_t ra = rsrc(ua, (uint32_t)uniform((int)na)), rb = rsrc(ub, (uint32_t)uniform((int)nb));
+    const uint32_t k0 = WG ? 0u : (uint32_t)lk * 128u;
+    // a shorter last block: its missing codes are zeros on both sides
+    const bool tail = !WG && k0 + 128u > (uint32_t)g.K;
+    const uint32_t end = (uint32_t)g.K - k0;
+#pragma unroll
+    for (int i = 0; i < C::IA; ++i)
+      if (part == i * PARTS / (C::IA + C::IB))
+        load16_lds(ra, st + (C::IA * w + i) * 1024, !tail || cha < end ? oa[i] : OOB, k0);
+#pragma unroll
+    for (int i = 0; i < C::IB; ++i)
+      if (part == (C::IA + i) * PARTS / (C::IA + C::IB))
+        load16_lds(rb, st + BM * 128 + (C::IB * w + i) * 1024, !tail || chb(i) < end ? ob[i] : OOB, k0);
+    if (part != PARTS - 1) return;
     if constexpr (WG) {
-      const __amdgpu_buffer_rsrc_t ra = rsrc(pa, na), rb = rsrc(pb, nb);
-#pragma unroll
-      for (int i = 0; i < C::IA; ++i) load16_lds(ra, st + (C::IA * w + i) * 1024, oa[i], 0);
-#pragma unroll
-      for (int i = 0; i < C::IB; ++i) load16_lds(rb, st + BM * 128 + (C::IB * w + i) * 1024, ob[i], 0);
-      if (w < BM / 64) load4_lds(rsrc(psa, nsa), st + C::SA_OFF + w * 256, os, 0);
-      else if (w < BM / 64 + BN / 64) load4_lds(rsrc(psb, nsb), st + C::SB_OFF + (w - BM / 64) * 256, os, 0);
+      if (w < BM / 64) load4_lds(rsrc(uniform_ptr(psa), (uint32_t)uniform((int)nsa)), st + C::SA_OFF + w * 256, os, 0);
+      else if (w < BM / 64 + BN / 64) load4_lds(rsrc(uniform_ptr(psb), (uint32_t)uniform((int)nsb)), st + C::SB_OFF + (w - BM / 64) * 256, os, 0);
       pa += na; pb += nb; psa += nsa; psb += nsb;  // the next block's
     } else {
-      const uint32_t k0 = (uint32_t)k * 128u;
-      const __amdgpu_buffer_rsrc_t ra = rsrc(pa, na), rb = rsrc(pb, nb);
-      // a shorter last block: its missing codes are zeros on both sides
-      const bool in = k0 + chunk < (uint32_t)g.K;
-#pragma unroll
-      for (int i = 0; i < C::IA; ++i) load16_lds(ra, st + (C::IA * w + i) * 1024, in ? oa[i] : OOB, k0);
-#pragma unroll
-      for (int i = 0; i < C::IB; ++i) load16_lds(rb, st + BM * 128 + (C::IB * w + i) * 1024, in ? ob[i] : OOB, k0);
-      if (w < BM / 64) load4_lds(rsrc(psa, nsa), st + C::SA_OFF + w * 256, os, (uint32_t)k * 4u);
-      else if (w == BM / 64) load4_lds(rsrc(psb, nsb), st + C::SB_OFF, os, (uint32_t)(k * g.sb_k) * 4u);
+      if (w < BM / 64) load4_lds(rsrc(uniform_ptr(psa), (uint32_t)uniform((int)nsa)), st + C::SA_OFF + w * 256, os, (uint32_t)lk * 4u);
+      else if (w == BM / 64) load4_lds(rsrc(uniform_ptr(psb), (uint32_t)uniform((int)nsb)), st + C::SB_OFF, os, (uint32_t)(lk * g.sb_k) * 4u);
     }
+    if (++lk == lnk) {
+      lk = 0;
+      lt = lt + G < total ? lt + G : -1;
+    }
+    lt = uniform(lt);
+    lk = uniform(lk);
+  };
+  auto load_stage = [&](int par) {
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) load_part(part, par);
   };
 
-  int64_t t = xcd_virtual_id(blockIdx.x, G);
-  if (t >= total) return;
-  Tile q = tile_at(t);
-  setup(q);
-  if (q.nk > 0) issue(0, 0);
-  while (t < total) {
-    f32x4_v acc[C::FN][C::FM];
+  // ---- computing: row pieces j of a stage in turn.  The sums of a piece run
+  // beside the matrix instructions of the next one.  The last two pieces go
+  // column by column, so that a column's codes of the next stage can be read as
+  // soon as its last two instructions are out. ----
+  const int la = wm * C::TM + (lane & 15);                 // line of a's piece 0
+  const int lb = wn * C::TN + column<EX>(0, lane & 15);    // of b's piece 0
+  // addresses of the two chunks of a line and of the scales, in stage buffer 0
+  auto slot = [&](int c, int key) { return (c ^ key) * 16; };
+  const int h = lane >> 4, ka = key_a(lane & 15), kbl = key_b<EX>(column<EX>(0, lane & 15));
+  int al = la * 128 + slot(h, ka), ah = la * 128 + slot(h + 4, ka);
+  int bl = (BM + lb) * 128 + slot(h, kbl), bh = (BM + lb) * 128 + slot(h + 4, kbl);
+  int sal = C::SA_OFF + la * 4;
+  int sbl = C::SB_OFF + (WG ? wn * C::TN + column<EX>(0, 4 * h) : (wn * C::TN) >> 7) * 4;
+  int step = C::STAGE;  // to the other buffer
+  auto other_buffer = [&] {
+    al += step; ah += step; bl += step; bh += step; sal += step; sbl += step;
+    step = -step;
+  };
+  i32x8_v nr[FN];   // codes of the next stage's columns
+  auto read_cols = [&](int i) {
+    nr[i] = join(lds_ld16(smem + bl + column<EX>(i, 0) * 128), lds_ld16(smem + bh + column<EX>(i, 0) * 128));
+  };
+  auto read_row = [&](int j, i32x8_v& m, float& sc) {
+    m = join(lds_ld16(smem + al + j * 2048), lds_ld16(smem + ah + j * 2048));
+    sc = *reinterpret_cast<const float*>(smem + sal + j * 64);
+  };
+
+  fetch_tokens(lq);
+  wait_vm<0>();
+  lds_sync();
+  load_stage(0);
+  wait_vm<0>();  // (the second stage may be the next tile's: its tokens)
+  lds_sync();
+  load_stage(1);
+  wait_vm<0>();
+  lds_sync();
+  i32x8_v mr;        // codes and scale of the next row piece
+  float sm, sbn = 0.f;
+  f32x4_v sn[WG ? FN : 1];
 #pragma unroll
-    for (int i = 0; i < C::FN; ++i)
+  for (int i = 0; i < FN; ++i) read_cols(i);
+  read_row(0, mr, sm);
+  if constexpr (!WG) sbn = *reinterpret_cast<const float*>(smem + sbl);
+
+  // A whole tile's stores are issued unconditionally, so their number is known
+  // and the wait for the next stage's loads, which are older, can leave them be.
+  constexpr int STORES = FM * FN / (EX ? 1 : 2);
+  bool stores = false;
+  int par = 0;
+  Tile q = tile_at(t0, 0);
+  for (int t = t0; t < total; t += G) {
+    if (t != t0) q = tile_at(t, q.e);
+    f32x4_v acc[FN][FM], d[FN];
+    float sp = 0.f;  // scale of the piece whose sums are due
 #pragma unroll
-      for (int j = 0; j < C::FM; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
-    const Tile cur = q;
-    const int64_t tn = t + G;
-    auto next_tile = [&] {
-      if (tn >= total) return;
-      q = tile_at(tn);
-      setup(q);
+    for (int i = 0; i < FN; ++i) {
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+      d[i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+      if constexpr (WG) sn[i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+    }
+    auto add = [&](const f32x4_v& v, float sc, int i, int j) {  // piece (i, j) joins the sums
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(v[x], WG ? sc * sn[i][x] : sc, acc[i][j][x]);
+      // stays here: the compiler would gather the sums behind the branch of
+      // the next loads, and their summands with them
+      asm volatile("" : "+v"(acc[i][j]));
     };
-    if (cur.nk == 0) {
-      next_tile();
-      if (tn < total && q.nk > 0) {
-        lds_sync();  // every wave is done with the stage that is written next
-        issue(0, parity);
-      }
-    }
 #pragma unroll 1
-    for (int k = 0; k < cur.nk; ++k) {
-      wait_vm0();
-      lds_sync();  // stage k is there; the other stage's readers are done
-      if (k + 1 < cur.nk) {
-        issue(k + 1, parity ^ 1);
-      } else {
-        next_tile();
-        if (tn < total && q.nk > 0) issue(0, parity ^ 1);
-      }
-      const char* st = smem + parity * C::STAGE;
-      const float* sa = reinterpret_cast<const float*>(st + C::SA_OFF);
-      const float* sb = reinterpret_cast<const float*>(st + C::SB_OFF);
-      Frag<EX> nf[C::FN];
+    for (int k = 0; k < q.nk; ++k) {
+      Frag<EX> nf[FN];
 #pragma unroll
-      for (int i = 0; i < C::FN; ++i) nf[i] = frag<EX>(st + BM * 128, wn * C::TN + 16 * i, lane);
-      if constexpr (WG) {
-        f32x4_v sn[C::FN];
+      for (int i = 0; i < FN; ++i) nf[i] = Frag<EX>(nr[i]);
+      const float sbk = WG ? 1.f : sbn;
+      i32x8_v mx;
+      float sx = 0.f;
 #pragma unroll
-        for (int i = 0; i < C::FN; ++i) sn[i] = lds_ld_f4(sb + wn * C::TN + 16 * i + 4 * (lane >> 4));
+      for (int j = 0; j < FM - 2; ++j) {
+        const Frag<EX> mf(mr);
+        const float sj = sm;
+        read_row(j + 1, mr, sm);
+        if (j == FM - 3) read_row(FM - 1, mx, sx);
 #pragma unroll
-        for (int j = 0; j < C::FM; ++j) {
-          const Frag<EX> mf = frag<EX>(st, wm * C::TM + 16 * j, lane);
-          const float sm = sa[wm * C::TM + 16 * j + (lane & 15)];
-#pragma unroll
-          for (int i = 0; i < C::FN; ++i) {
-            const f32x4_v d = dot(nf[i], mf);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(d[x], sm * sn[i][x], acc[i][j][x]);
+        for (int i = 0; i < FN; ++i) {
+          add(d[i], sp, i, (j + FM - 1) % FM);
+          d[i] = dot(nf[i], mf);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (WG) {
+            if (j == 0) sn[i] = lds_ld_f4(smem + sbl + column<EX>(i, 0) * 4);
           }
         }
-      } else {
-        const float sn = sb[(wn * C::TN) >> 7];
+        sp = sj * sbk;
+      }
+      const Frag<EX> m0(mr), m1(mx);
+      const float s0 = sm * sbk, s1 = sx * sbk;
+      // this stage is read; the next one is there once everybody's loads are
+      if (stores) wait_vm<STORES>();
+      else wait_vm<0>();
+      stores = false;
+      lds_sync();
+      other_buffer();
+      read_row(0, mr, sm);
+      if constexpr (!WG) sbn = *reinterpret_cast<const float*>(smem + sbl);
+      f32x4_v last;
 #pragma unroll
-        for (int j = 0; j < C::FM; ++j) {
-          const Frag<EX> mf = frag<EX>(st, wm * C::TM + 16 * j, lane);
-          const float sm = sa[wm * C::TM + 16 * j + (lane & 15)] * sn;
+      for (int i = 0; i < FN; ++i) {
+        load_part(i, par);
+        add(d[i], sp, i, FM - 3);
+        const f32x4_v v = dot(nf[i], m0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i > 0) add(last, s0, i - 1, FM - 2);
+        last = v;
+        d[i] = dot(nf[i], m1);
+        __builtin_amdgcn_sched_barrier(0);
+        read_cols(i);
+      }
+      add(last, s0, FN - 1, FM - 2);
+      sp = s1;
+      par ^= 1;
+    }
 #pragma unroll
-          for (int i = 0; i < C::FN; ++i) {
-            const f32x4_v d = dot(nf[i], mf);
+    for (int i = 0; i < FN; ++i) add(d[i], sp, i, FM - 1);
+
+    // results: lane l holds the row l % 16 of a piece
+    const int left = WG ? g.M - q.m0 : q.rows;
+    const int64_t crow0 = WG ? (int64_t)q.e * g.M + q.m0 : (int64_t)q.row0;
+    const int c0 = q.n0 + wn * C::TN + column<EX>(0, 4 * (lane >> 4));
+    O* const out = reinterpret_cast<O*>(g.c) + (crow0 + la) * g.N + c0;
+    auto store = [&](auto whole) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(d[x], sm, acc[i][j][x]);
+      for (int j = 0; j < FM; ++j) {
+        O* row = out + (int64_t)(16 * j) * g.N;
+        if (!whole && la + 16 * j >= left) continue;
+#pragma unroll
+        for (int i = 0; i < FN; i += EX ? 1 : 2) {
+          const int n = column<EX>(i, 0);
+          if (!whole && c0 + n >= g.N) continue;
+          const f32x4_v u = acc[i][j];
+          if constexpr (EX) {
+            *reinterpret_cast<float4*>(row + n) = make_float4(u[0], u[1], u[2], u[3]);
+          } else {
+            const f32x4_v v = acc[i + 1][j];
+            *reinterpret_cast<uint4*>(row + n) =
+                make_uint4(f2bf2(u[0], u[1]), f2bf2(u[2], u[3]), f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
           }
         }
       }
-      parity ^= 1;
-    }
-    // results: lane l holds row l % 16 of a piece, columns 4 (l / 16) .. +3
-    const int left = WG ? g.M - cur.m0 : segn[cur.e] - cur.m0;
-    const int64_t crow0 = WG ? (int64_t)cur.e * g.M + cur.m0 : (int64_t)seg0[cur.e] + cur.m0;
-#pragma unroll
-    for (int j = 0; j < C::FM; ++j) {
-      const int m = wm * C::TM + 16 * j + (lane & 15);
-      if (m >= left) continue;
-      O* row = reinterpret_cast<O*>(g.c) + (crow0 + m) * g.N;
-#pragma unroll
-      for (int i = 0; i < C::FN; ++i) {
-        const int n = cur.n0 + wn * C::TN + 16 * i + 4 * (lane >> 4);
-        if (n < g.N) store4(row + n, acc[i][j]);
-      }
-    }
-    t = tn;
+    };
+    stores = left >= BM && q.n0 + BN <= g.N;
+    if (stores) store(std::true_type());
+    else store(std::false_type());
   }
 }
 

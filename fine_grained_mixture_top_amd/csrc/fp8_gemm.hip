@@ -47,13 +47,13 @@ hipError_t launch_tiles(const f8::Args& a, int64_t tiles, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, bool WG>
-hipError_t launch_out(int out, const f8::Args& a, int64_t tiles, hipStream_t st) {
-  return out == MOE_BF16 ? launch_tiles<BM, BN, WM, WN, WG, bf16_t>(a, tiles, st)
-                         : launch_tiles<BM, BN, WM, WN, WG, float>(a, tiles, st);
-}
-
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// tiles of a row product, at most (every segment may end inside one)
+int64_t row_tiles(const f8::Args& a, int BM, int BN) {
+  return (div_up(a.rows, BM) + std::min(a.E, a.rows)) * div_up(a.N, BN);
+}
+int64_t wgrad_tiles(const f8::Args& a, int BM, int BN) { return a.E * div_up(a.M, BM) * div_up(a.N, BN); }
 
 }  // namespace
 
@@ -68,8 +68,11 @@ hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) 
   const int nbn = (m.N + 127) / 128;
   a.sb_k = m.sb_out_major ? 1 : nbn;
   a.sb_n = m.sb_out_major ? a.kb : 1;
-  const int64_t bound = div_up(m.rows, 128) + std::min(m.E, m.rows);
-  return launch_out<128, 128, 2, 2, false>(m.out, a, bound * div_up(m.N, 128), st);
+  if (m.out == MOE_F32) return launch_tiles<128, 64, 2, 2, false, float>(a, row_tiles(a, 128, 64), st);
+  static const char* v = getenv("F8V");
+  if (v && v[0] == '1') return launch_tiles<128, 128, 2, 2, false, bf16_t>(a, row_tiles(a, 128, 128), st);
+  if (v && v[0] == '2') return launch_tiles<256, 128, 4, 2, false, bf16_t>(a, row_tiles(a, 256, 128), st);
+  return launch_tiles<256, 256, 2, 4, false, bf16_t>(a, row_tiles(a, 256, 256), st);
 }
 
 hipError_t launch_fp8_wgrad(const PlanArgs& p, int M, int N, int out, const uint8_t* qa, const float* sa,
@@ -79,7 +82,12 @@ hipError_t launch_fp8_wgrad(const PlanArgs& p, int M, int N, int out, const uint
   a.offsets = p.offsets; a.counts = p.counts;
   a.rows = p.cap; a.E = p.E;
   a.M = M; a.N = N;
-  return launch_out<128, 128, 2, 2, true>(out, a, (int64_t)p.E * div_up(M, 128) * div_up(N, 128), st);
+  if (out == MOE_F32) return launch_tiles<128, 64, 2, 2, true, float>(a, wgrad_tiles(a, 128, 64), st);
+  static const char* v = getenv("F8V");
+  if (v && v[0] == '1') return launch_tiles<128, 128, 2, 2, true, bf16_t>(a, wgrad_tiles(a, 128, 128), st);
+  if (v && v[0] == '2') return launch_tiles<256, 128, 4, 2, true, bf16_t>(a, wgrad_tiles(a, 256, 128), st);
+  if (v && v[0] == '3') return launch_tiles<128, 256, 2, 4, true, bf16_t>(a, wgrad_tiles(a, 128, 256), st);
+  return launch_tiles<256, 256, 2, 4, true, bf16_t>(a, wgrad_tiles(a, 256, 256), st);
 }
 
 }  // namespace moe
