@@ -142,6 +142,13 @@ struct Args {
   int sb_k, sb_n;            // strides of sb in (reduction block, column block)
 };
 
+// rows of segment e that lie in the buffers (rows past them are never touched)
+__device__ __forceinline__ int seg_rows(const Args& g, int e) {
+  if (!g.offsets) return g.rows;
+  const int o = g.offsets[e];
+  return o < 0 || o >= g.rows ? 0 : max(0, min(g.counts[e], g.rows - o));
+}
+
 // BM x BN tiles, WM x WN waves.  WG: weight gradient (tiles of dw over the
 // segment's blocks), else rows of c.
 template <int BM, int BN, int WM, int WN, bool WG>
@@ -195,9 +202,7 @@ k_fp8_gemm(Args g) {
       int o = 0, n = 0;
       if (e < g.E) {
         o = g.offsets ? g.offsets[e] : 0;
-        n = g.offsets ? g.counts[e] : g.rows;
-        if (o < 0 || o >= g.rows) n = 0;  // rows past the buffers are never touched
-        n = max(0, min(n, g.rows - o));
+        n = seg_rows(g, e);
         seg0[e] = o;
         segn[e] = n;
       }
@@ -410,12 +415,17 @@ k_fp8_gemm(Args g) {
     sc = *reinterpret_cast<const float*>(smem + sal + j * 64);
   };
 
+  const bool gathered = !WG && g.row_token != nullptr;
   fetch_tokens(lq);
-  wait_vm<0>();
-  lds_sync();
+  if (gathered) {
+    wait_vm<0>();
+    lds_sync();
+  }
   load_stage(0);
-  wait_vm<0>();  // (the second stage may be the next tile's: its tokens)
-  lds_sync();
+  if (gathered && lk == 0) {  // the second stage is the next tile's: its tokens
+    wait_vm<0>();
+    lds_sync();
+  }
   load_stage(1);
   wait_vm<0>();
   lds_sync();
@@ -534,6 +544,162 @@ k_fp8_gemm(Args g) {
     stores = left >= BM && q.n0 + BN <= g.N;
     if (stores) store(std::true_type());
     else store(std::false_type());
+  }
+}
+
+// Row product for segments of few rows (decode): the weights' bytes are all the
+// work, and every touched expert's are read once, straight into registers.  A
+// workgroup takes 16 RT rows of a segment and 32 columns; its four waves split
+// the reduction's blocks (wave w: blocks w, w + 4, ...), load UNR of theirs at a
+// time, and add up their sums in wave order.  The matrix work is small, so it
+// runs on the bf16 matrix cores whatever the result's type.
+template <int RT, int FN, int UNR, typename O>
+__global__ void __launch_bounds__(256)
+k_fp8_thin(Args g) {
+  constexpr int BN = 16 * FN, BM = 16 * RT;
+  __shared__ float part[3][RT][FN][64][4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int NT = (g.N + BN - 1) / BN;
+  const int mg = (int)(blockIdx.x / (unsigned)NT), n0 = (int)(blockIdx.x % (unsigned)NT) * BN;
+
+  // the row tile's segment: lanes scan `per` experts each
+  const int per = (g.E + 63) >> 6;
+  int mine = 0;
+  for (int x = 0; x < per; ++x) {
+    const int e = lane * per + x;
+    if (e < g.E) mine += (seg_rows(g, e) + BM - 1) / BM;
+  }
+  int incl = mine;
+  for (int s = 1; s < 64; s <<= 1) {
+    const int y = __shfl_up(incl, s, 64);
+    if (lane >= s) incl += y;
+  }
+  const uint64_t past = __ballot(incl > mg);
+  if (past == 0) return;  // no such tile
+  const int src = __builtin_ctzll(past);
+  int left = mg - (__shfl(incl, src, 64) - __shfl(mine, src, 64));
+  int e = src * per, n = 0;
+  for (;; ++e) {
+    n = seg_rows(g, e);
+    const int tiles = (n + BM - 1) / BM;
+    if (left < tiles) break;
+    left -= tiles;
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int m0 = __builtin_amdgcn_readfirstlane(left) * BM;
+  const int rows = min(__builtin_amdgcn_readfirstlane(n) - m0, BM);
+  const int row0 = (g.offsets ? g.offsets[e] : 0) + m0;
+
+  const int p = lane & 15, h = lane >> 4;
+  // rows and columns past the end repeat the last one (their results are dropped)
+  const uint8_t* pa[RT];
+  const float* psa[RT];
+  bool real[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    int64_t row = row0 + min(16 * r + p, rows - 1);
+    if (g.row_token) row = g.row_token[row];
+    real[r] = (uint64_t)row < (uint64_t)g.a_rows;  // a token that does not exist counts as zeros
+    if (!real[r]) row = 0;
+    pa[r] = g.a + row * g.K + 16 * h;
+    psa[r] = g.sa + row * g.kb;
+  }
+  const uint8_t* pb[FN];
+#pragma unroll
+  for (int i = 0; i < FN; ++i) pb[i] = g.b + ((int64_t)e * g.N + min(n0 + 16 * i + p, g.N - 1)) * g.K + 16 * h;
+  const float* psb = g.sb + (int64_t)e * g.kb * ((g.N + 127) >> 7) + (int64_t)(n0 >> 7) * g.sb_n;
+
+  f32x4_v acc[RT][FN];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int i = 0; i < FN; ++i) acc[r][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = w; k0 < g.kb; k0 += 4 * UNR) {
+    // All loads first, none of them under a condition: past the reduction they
+    // read its first codes, and both sides' become zeros afterwards.
+    uint4 ra[UNR][RT][2], rb[UNR][FN][2];
+    float sa[UNR][RT], sb[UNR];
+    bool in[UNR][2];
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+      const int k = k0 + 4 * u;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int at = k * 128 + 64 * c;  // this lane's chunk: 16 h further on
+        in[u][c] = at + 16 * h < g.K;
+        const int from = in[u][c] ? at : -16 * h;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) rb[u][i][c] = *reinterpret_cast<const uint4*>(pb[i] + from);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) ra[u][r][c] = *reinterpret_cast<const uint4*>(pa[r] + from);
+      }
+      const int ks = min(k, g.kb - 1);
+      sb[u] = psb[(int64_t)ks * g.sb_k];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) sa[u][r] = psa[r][ks];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const bool whole = (k0 + 4 * (UNR - 1) + 1) * 128 <= g.K;
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+      if (!whole) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (!in[u][c]) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) rb[u][i][c] = z;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) ra[u][r][c] = z;
+          }
+        }
+        if (k0 + 4 * u >= g.kb) sb[u] = 0.f;  // (a scale that is not finite would spoil the zeros)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          if (k0 + 4 * u >= g.kb) sa[u][r] = 0.f;
+      }
+      Frag<true> mf[RT];
+      float sc[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        mf[r] = Frag<true>(join(ra[u][r][0], ra[u][r][1]));
+        sc[r] = real[r] ? sa[u][r] * sb[u] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        const Frag<true> nf(join(rb[u][i][0], rb[u][i][1]));
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const f32x4_v d = dot(nf, mf[r]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[r][i][x] = fmaf(d[x], sc[r], acc[r][i][x]);
+        }
+      }
+    }
+  }
+  if (w > 0)
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < FN; ++i) *reinterpret_cast<f32x4_v*>(part[w - 1][r][i][lane]) = acc[r][i];
+  __syncthreads();
+  if (w > 0) return;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int m = 16 * r + p;
+    if (m >= rows) continue;
+    O* row = reinterpret_cast<O*>(g.c) + ((int64_t)row0 + m) * g.N;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      f32x4_v v = acc[r][i];
+#pragma unroll
+      for (int x = 0; x < 3; ++x) v += *reinterpret_cast<const f32x4_v*>(part[x][r][i][lane]);
+      const int c = n0 + 16 * i + 4 * h;
+      if (c >= g.N) continue;
+      if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(row + c) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
+      else *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
+    }
   }
 }
 

@@ -49,14 +49,35 @@ hipError_t launch_tiles(const f8::Args& a, int64_t tiles, hipStream_t st) {
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// tiles of a row product, at most (every segment may end inside one)
-int64_t row_tiles(const f8::Args& a, int BM, int BN) {
-  return (div_up(a.rows, BM) + std::min(a.E, a.rows)) * div_up(a.N, BN);
+// Row tiles at most: every segment with rows may end inside one.
+int64_t row_tiles(const f8::Args& a, int64_t used, int BM) { return div_up(used, BM) + std::min<int64_t>(a.E, used); }
+
+template <int RT, int FN, int UNR>
+hipError_t launch_thin(int out, const f8::Args& a, int64_t used, hipStream_t st) {
+  const int64_t tiles = row_tiles(a, used, 16 * RT) * div_up(a.N, 16 * FN);
+  if (out == MOE_BF16)
+    hipLaunchKernelGGL((f8::k_fp8_thin<RT, FN, UNR, bf16_t>), dim3((unsigned)tiles), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((f8::k_fp8_thin<RT, FN, UNR, float>), dim3((unsigned)tiles), dim3(256), 0, st, a);
+  return hipGetLastError();
 }
-int64_t wgrad_tiles(const f8::Args& a, int BM, int BN) { return a.E * div_up(a.M, BM) * div_up(a.N, BN); }
 
 }  // namespace
 
+// Which kernel, by the rows per expert (avg; the host knows no segment's own).
+// Times in us at E = 64, K = N = 2048 and at E = 128, K = 1536, N = 512:
+//   avg                          4          8          12         16         24         32
+//   bf16, 16 rows, 64 columns    45 / -     47 / 20.5  50 / -     63 / 28    82 / -     - / 41
+//         32 rows, 64 columns    48 / -     50 / 23.8  51 / -     54 / 25    60 / -     - / 34
+//         128 x 128 tiles        52 / -     50 / 29.6  53 / -     53 / 30    54 / -     - / 31
+//   fp32, 16 rows, 64 columns    45 / -     48 / 20.7  52 / -     65 / 28    85 / -     - / 42
+//         32 rows, 64 columns    50 / -     50 / 23.8  53 / -     56 / 25    63 / -     - / 34
+//         128 x 64 tiles         95 / -     92 / 46    92 / -     92 / 46    93 / -     - / 47
+// and at avg 48: 32 rows 106, 128 x 64 tiles 97.  Below one row per expert, 32
+// columns give twice the workgroups (E = 256, K = 2048, N = 512, 128 rows: 22.9
+// against 24.3; 8 rows: 6.5 against 9.4).  256 x 256 tiles need enough rows and
+// tiles (E = 64, K = N = 2048: avg 64 69 against 60 with 128 x 128, avg 128 82
+// against 99, avg 4096 1210 against 1572).
 hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) {
   f8::Args a{};
   a.a = m.a; a.sa = m.sa; a.b = m.b; a.sb = m.sb; a.c = m.c;
@@ -68,11 +89,17 @@ hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) 
   const int nbn = (m.N + 127) / 128;
   a.sb_k = m.sb_out_major ? 1 : nbn;
   a.sb_n = m.sb_out_major ? a.kb : 1;
-  if (m.out == MOE_F32) return launch_tiles<128, 64, 2, 2, false, float>(a, row_tiles(a, 128, 64), st);
-  static const char* v = getenv("F8V");
-  if (v && v[0] == '1') return launch_tiles<128, 128, 2, 2, false, bf16_t>(a, row_tiles(a, 128, 128), st);
-  if (v && v[0] == '2') return launch_tiles<256, 128, 4, 2, false, bf16_t>(a, row_tiles(a, 256, 128), st);
-  return launch_tiles<256, 256, 2, 4, false, bf16_t>(a, row_tiles(a, 256, 256), st);
+  const int64_t used = m.rows_used, E = m.E;
+  const bool wide = m.out == MOE_F32;
+  // (their grids, one workgroup per tile, stay below 2^32 threads)
+  const bool thin = row_tiles(a, used, 16) * div_up(a.N, 32) < (1 << 24);
+  if (thin && used < E) return launch_thin<1, 2, 1>(m.out, a, used, st);
+  if (thin && used <= 12 * E) return launch_thin<1, 4, 1>(m.out, a, used, st);
+  if (thin && used <= (wide ? 40 : 18) * E) return launch_thin<2, 4, 1>(m.out, a, used, st);
+  if (wide) return launch_tiles<128, 64, 2, 2, false, float>(a, row_tiles(a, used, 128) * div_up(a.N, 64), st);
+  if (used >= 96 * E && a.N > 128 && (used / 256 + 1) * div_up(a.N, 256) >= cu_count(device()))
+    return launch_tiles<256, 256, 2, 4, false, bf16_t>(a, row_tiles(a, used, 256) * div_up(a.N, 256), st);
+  return launch_tiles<128, 128, 2, 2, false, bf16_t>(a, row_tiles(a, used, 128) * div_up(a.N, 128), st);
 }
 
 hipError_t launch_fp8_wgrad(const PlanArgs& p, int M, int N, int out, const uint8_t* qa, const float* sa,
@@ -82,12 +109,9 @@ hipError_t launch_fp8_wgrad(const PlanArgs& p, int M, int N, int out, const uint
   a.offsets = p.offsets; a.counts = p.counts;
   a.rows = p.cap; a.E = p.E;
   a.M = M; a.N = N;
-  if (out == MOE_F32) return launch_tiles<128, 64, 2, 2, true, float>(a, wgrad_tiles(a, 128, 64), st);
-  static const char* v = getenv("F8V");
-  if (v && v[0] == '1') return launch_tiles<128, 128, 2, 2, true, bf16_t>(a, wgrad_tiles(a, 128, 128), st);
-  if (v && v[0] == '2') return launch_tiles<256, 128, 4, 2, true, bf16_t>(a, wgrad_tiles(a, 256, 128), st);
-  if (v && v[0] == '3') return launch_tiles<128, 256, 2, 4, true, bf16_t>(a, wgrad_tiles(a, 128, 256), st);
-  return launch_tiles<256, 256, 2, 4, true, bf16_t>(a, wgrad_tiles(a, 256, 256), st);
+  auto tiles = [&](int BM, int BN) { return a.E * div_up(M, BM) * div_up(N, BN); };
+  if (out == MOE_F32) return launch_tiles<128, 64, 2, 2, true, float>(a, tiles(128, 64), st);
+  return launch_tiles<128, 128, 2, 2, true, bf16_t>(a, tiles(128, 128), st);
 }
 
 }  // namespace moe

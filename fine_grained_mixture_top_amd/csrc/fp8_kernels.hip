@@ -128,32 +128,84 @@ k_swiglu_bwd_rows(const T* __restrict__ da, const T* __restrict__ h, int64_t R, 
 // 256 threads; thread t holds the 8 x 8 values at rows 8 (t / 16), columns
 // 8 (t % 16), so that both a row's codes and a column's are eight bytes of it.
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
+// The 8 x 8 values as loaded, their largest magnitudes and their codes.
+// fp32: magnitudes as the value's bits, a word per column.
+template <typename T> struct Tile8;
+template <> struct Tile8<float> {
+  float v[8][8];
+  typedef uint32_t Mag[8];  // per column
+  __device__ __forceinline__ void load(int i, const float* p) {
     const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+    v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
   }
+  __device__ __forceinline__ void zero(int i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+  }
+  __device__ __forceinline__ void column_mags(Mag& m) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[j] = max(m[j], mag_bits(v[i][j]));
+    }
+  }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t bits(const Mag& m, int j) { return m[j]; }
+  __device__ __forceinline__ float value(int i, int j) const { return v[i][j]; }
+};
+// bf16: two columns in a word, which an integer maximum of 16-bit halves
+// orders just as well
+template <> struct Tile8<bf16_t> {
+  uint4 w[8];
+  typedef uint32_t Mag[4];
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  __device__ __forceinline__ void load(int i, const bf16_t* p) { w[i] = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero(int i) { w[i] = make_uint4(0, 0, 0, 0); }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+  }
+  __device__ __forceinline__ uint32_t word(int i, int c) const {
+    return c == 0 ? w[i].x : c == 1 ? w[i].y : c == 2 ? w[i].z : w[i].w;
+  }
+  __device__ __forceinline__ void column_mags(Mag& m) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      m[c] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[c] = larger(m[c], word(i, c) & 0x7fff7fffu);
+    }
+  }
+  static __device__ __forceinline__ uint32_t bits(const Mag& m, int j) {
+    return j & 1 ? m[j >> 1] & 0xffff0000u : m[j >> 1] << 16;
+  }
+  __device__ __forceinline__ float value(int i, int j) const {
+    return __uint_as_float(j & 1 ? word(i, j >> 1) & 0xffff0000u : word(i, j >> 1) << 16);
+  }
+};
+
+// 4 x 4 bytes transposed: word i's byte j -> word j's byte i
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602);
+  w[0] = __builtin_amdgcn_perm(c, a, 0x05040100);
+  w[1] = __builtin_amdgcn_perm(c, a, 0x07060302);
+  w[2] = __builtin_amdgcn_perm(d, b, 0x05040100);
+  w[3] = __builtin_amdgcn_perm(d, b, 0x07060302);
 }
 
-// byte j of each of eight rows (two words a row) -> eight bytes of column j
-__device__ __forceinline__ uint2 column_bytes(const uint32_t (&w)[8][2], int j) {
-  uint32_t lo = 0, hi = 0;
+// codes c [8 rows][2 words] as eight bytes of each column: t [8 columns][2 words]
+__device__ __forceinline__ void transpose8(const uint32_t (&c)[8][2], uint32_t (&t)[8][2]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo |= ((w[i][j >> 2] >> (8 * (j & 3))) & 0xffu) << (8 * i);
-    hi |= ((w[4 + i][j >> 2] >> (8 * (j & 3))) & 0xffu) << (8 * i);
-  }
-  return make_uint2(lo, hi);
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[4] = {c[4 * r][h], c[4 * r + 1][h], c[4 * r + 2][h], c[4 * r + 3][h]};
+      transpose4(w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[4 * h + j][r] = w[j];
+    }
 }
 
 constexpr int TP = 128 + 16;  // LDS pitch of a transposed tile's row (bytes)
@@ -169,19 +221,19 @@ k_quant_weights_128(const T* __restrict__ w, int K, int N, uint8_t* __restrict__
   const int k0 = blockIdx.y * 128, n0 = blockIdx.x * 128;
   const int rk = (tid >> 4) * 8, cn = (tid & 15) * 8;
   const size_t base = (size_t)blockIdx.z * K * N;
-  float v[8][8];
-  uint32_t m = 0;
+  Tile8<T> v;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int k = k0 + rk + i, n = n0 + cn;
-    if (k < K && n < N) {
-      load8(w + base + (size_t)k * N + n, v[i]);
-    } else {
+    if (k < K && n < N) v.load(i, w + base + (size_t)k * N + n);
+    else v.zero(i);
+  }
+  uint32_t m = 0;
+  {
+    typename Tile8<T>::Mag cm;
+    v.column_mags(cm);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, mag_bits(v[i][j]));
+    for (int j = 0; j < 8; ++j) m = max(m, Tile8<T>::bits(cm, j));
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
@@ -193,8 +245,8 @@ k_quant_weights_128(const T* __restrict__ w, int K, int N, uint8_t* __restrict__
   uint32_t c[8][2];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    c[i][0] = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-    c[i][1] = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+    c[i][0] = e4m3x4(v.value(i, 0) * inv, v.value(i, 1) * inv, v.value(i, 2) * inv, v.value(i, 3) * inv);
+    c[i][1] = e4m3x4(v.value(i, 4) * inv, v.value(i, 5) * inv, v.value(i, 6) * inv, v.value(i, 7) * inv);
   }
   if (q) {
 #pragma unroll
@@ -204,8 +256,10 @@ k_quant_weights_128(const T* __restrict__ w, int K, int N, uint8_t* __restrict__
     }
   }
   if (qt) {
+    uint32_t ct[8][2];
+    transpose8(c, ct);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(tile + (cn + j) * TP + rk) = column_bytes(c, j);
+    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(tile + (cn + j) * TP + rk) = make_uint2(ct[j][0], ct[j][1]);
     __syncthreads();
     // 16 bytes per thread: eight threads per column's 128 rows
 #pragma unroll
@@ -223,7 +277,9 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 k_quant_cols_128(const T* __restrict__ src, int C, int Tn, bool gather, PlanArgs p, uint8_t* __restrict__ q,
                  float* __restrict__ s) {
-  __shared__ uint32_t cmax[16][128];
+  typedef Tile8<T> V;
+  constexpr int MW = sizeof(typename V::Mag) / 4;
+  __shared__ typename V::Mag cmax[4][16];
   __shared__ __attribute__((aligned(16))) uint8_t tile[128 * TP];
   const int tid = threadIdx.x;
   const int ct = (C + 127) / 128;
@@ -231,44 +287,49 @@ k_quant_cols_128(const T* __restrict__ src, int C, int Tn, bool gather, PlanArgs
   const int r0 = (int)(blk * 128), c0 = (int)(blockIdx.x % ct) * 128;
   if (r0 >= p.offsets[p.E]) return;
   const int rk = (tid >> 4) * 8, cn = (tid & 15) * 8;
-  float v[8][8];
+  int tok[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) tok[i] = p.row_token[r0 + rk + i];
+  V v;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int r = r0 + rk + i, col = c0 + cn;
-    const int tok = p.row_token[r];
-    if ((unsigned)tok < (unsigned)Tn && col < C) {
-      load8(src + (size_t)(gather ? tok : r) * C + col, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
+    if ((unsigned)tok[i] < (unsigned)Tn && c0 + cn < C)
+      v.load(i, src + (size_t)(gather ? tok[i] : r0 + rk + i) * C + c0 + cn);
+    else
+      v.zero(i);
   }
+  // the columns' magnitudes: over this thread's rows, the wave's, the block's
+  typename V::Mag m;
+  v.column_mags(m);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, mag_bits(v[i][j]));
-    cmax[tid >> 4][cn + j] = m;
+  for (int j = 0; j < MW; ++j) {
+    m[j] = V::larger(m[j], (uint32_t)__shfl_xor((int)m[j], 16, 64));
+    m[j] = V::larger(m[j], (uint32_t)__shfl_xor((int)m[j], 32, 64));
   }
+  if ((tid & 63) < 16)
+#pragma unroll
+    for (int j = 0; j < MW; ++j) cmax[tid >> 6][tid & 15][j] = m[j];
   __syncthreads();
+#pragma unroll
+  for (int j = 0; j < MW; ++j)
+    m[j] = V::larger(V::larger(cmax[0][tid & 15][j], cmax[1][tid & 15][j]),
+                     V::larger(cmax[2][tid & 15][j], cmax[3][tid & 15][j]));
   float inv[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int g = 0; g < 16; ++g) m = max(m, cmax[g][cn + j]);
-    const float sc = block_scale(m);
+    const float sc = block_scale(V::bits(m, j));
     inv[j] = __fdiv_rn(1.f, sc);
     if (tid < 16 && c0 + cn + j < C) s[blk * C + c0 + cn + j] = sc;
   }
-  uint32_t c[8][2];
+  uint32_t c[8][2], t[8][2];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    c[i][0] = e4m3x4(v[i][0] * inv[0], v[i][1] * inv[1], v[i][2] * inv[2], v[i][3] * inv[3]);
-    c[i][1] = e4m3x4(v[i][4] * inv[4], v[i][5] * inv[5], v[i][6] * inv[6], v[i][7] * inv[7]);
+    c[i][0] = e4m3x4(v.value(i, 0) * inv[0], v.value(i, 1) * inv[1], v.value(i, 2) * inv[2], v.value(i, 3) * inv[3]);
+    c[i][1] = e4m3x4(v.value(i, 4) * inv[4], v.value(i, 5) * inv[5], v.value(i, 6) * inv[6], v.value(i, 7) * inv[7]);
   }
+  transpose8(c, t);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(tile + (cn + j) * TP + rk) = column_bytes(c, j);
+  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(tile + (cn + j) * TP + rk) = make_uint2(t[j][0], t[j][1]);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

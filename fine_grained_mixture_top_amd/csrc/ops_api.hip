@@ -220,6 +220,7 @@ int moe_fp8_mm(const moe_mm_desc* desc, const void* a, const float* sa, const vo
   if (!desc || desc->reserved || (desc->flags & ~(MOE_MM_GATHER | MOE_MM_SB_OUT_MAJOR))) return MOE_EINVAL;
   const bool gather = (desc->flags & MOE_MM_GATHER) != 0;
   if (desc->a_rows < 0 || desc->rows < 0 || desc->E < 1) return MOE_EINVAL;
+  if (desc->rows_used < 0 || desc->rows_used > desc->rows) return MOE_EINVAL;
   int e = check_dtype(desc->out);
   if (e == MOE_OK) e = check_width(desc->K);
   if (e == MOE_OK) e = check_width(desc->N);
@@ -235,13 +236,14 @@ int moe_fp8_mm(const moe_mm_desc* desc, const void* a, const float* sa, const vo
   if (plan && (!plan->offsets || !plan->counts || (gather && !plan->row_token))) return MOE_EINVAL;
   if (!a || !sa || !b || !sb || !c) return MOE_EINVAL;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(c, 16) || !aligned(sa, 4) || !aligned(sb, 4)) return MOE_EINVAL;
+  const int used = desc->rows_used > 0 ? desc->rows_used : desc->rows;
   PlanArgs p{};
   if (plan) {
     p.offsets = plan->offsets;
     p.counts = plan->counts;
     p.row_token = plan->row_token;
   }
-  const Fp8MmArgs g{(const uint8_t*)a, sa, (const uint8_t*)b, sb, c, desc->a_rows, desc->rows, desc->E, desc->K,
+  const Fp8MmArgs g{(const uint8_t*)a, sa, (const uint8_t*)b, sb, c, desc->a_rows, desc->rows, used, desc->E, desc->K,
                     desc->N, desc->out, gather, (desc->flags & MOE_MM_SB_OUT_MAJOR) != 0};
   return timed(desc->profile, stream, MOE_OPS_K_FP8_MM, [&](hipStream_t st) { return launch_fp8_mm(p, g, st); });
 }

@@ -51,7 +51,7 @@ struct Fp8MmArgs {
   const uint8_t* b;
   const float* sb;
   void* c;
-  int a_rows, rows, E, K, N;
+  int a_rows, rows, rows_used, E, K, N;
   int out;
   bool gather, sb_out_major;
 };

@@ -73,6 +73,7 @@ k_sort_place(const int32_t* __restrict__ idx, int slots, int K, int E, int align
     const int g = tid / E, e = tid % E;
     if (g < groups) {
       int t = 0, b = 0;
+#pragma unroll 8
       for (int c = g; c < chunks; c += groups) {
         const int v = cnt[(size_t)c * E + e];
         t += v;

@@ -48,8 +48,8 @@ class MoePlan(ctypes.Structure):
 
 
 class MoeMmDesc(ctypes.Structure):
-    _fields_ = [("a_rows", ctypes.c_int32), ("rows", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
-                ("N", ctypes.c_int32), ("out", ctypes.c_int32), ("flags", ctypes.c_uint32),
+    _fields_ = [("a_rows", ctypes.c_int32), ("rows", ctypes.c_int32), ("rows_used", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("out", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32), ("profile", ctypes.POINTER(B.MoeProfile))]
 
 
@@ -121,6 +121,11 @@ def _matrix(name, t, dtypes=_VALUES, dims=2):
     return t
 
 
+# the current stream's handle without building a Stream object (2 us a call),
+# where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _call(fn, device, stream, *args):
     """fn(*args, stream) with `device` current; raises on a non-zero status."""
     index = device.index
@@ -128,7 +133,7 @@ def _call(fn, device, stream, *args):
         with torch.cuda.device(device):
             return _call(fn, device, stream, *args)
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = _raw_stream(index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
     else:
         if stream.device != device:
             raise ValueError(f"stream on {stream.device}, the call is on {device}")
@@ -305,7 +310,8 @@ def moe_fp8_mm(plan, a, sa, b, sb, c, gather: bool = False, sb_out_major: bool =
     psb = _need("sb", sb, _F32, (E, nb, kb) if sb_out_major else (E, kb, nb), dev)
     pc = _need("c", c, _VALUES, (rows, N), dev)
     flags = (MOE_MM_GATHER if gather else 0) | (MOE_MM_SB_OUT_MAJOR if sb_out_major else 0)
-    d = MoeMmDesc(rows_a, rows, E, K, N, _DTYPE[c.dtype], flags, 0, _profile(plan))
+    used = 0 if plan is None else plan.T * plan.K
+    d = MoeMmDesc(rows_a, rows, used, E, K, N, _DTYPE[c.dtype], flags, 0, _profile(plan))
     _call("moe_fp8_mm", dev, stream, ctypes.byref(d), pa, psa, pb, psb, None if plan is None else plan._p, pc)
 
 

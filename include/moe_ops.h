@@ -158,7 +158,9 @@ int moe_fp8_quant_cols(const moe_plan_desc* desc, const moe_plan* plan, int dtyp
  *   c  [rows, N] (dtype `out`); rows of no segment are left as they were.
  * With a plan, rows = the plan's capacity and a_rows = rows, or T with
  * MOE_MM_GATHER.  Without one (plan NULL) the product is dense: E = 1 and
- * a_rows = rows.  rows = 0 does nothing.
+ * a_rows = rows.  rows = 0 does nothing.  rows_used: at most so many of the rows
+ * belong to segments, T*K for a plan (all segments' rows together; results of
+ * further ones are not computed); 0: rows.
  *
  * For weights w [E,K,N] quantized by moe_fp8_quant_weights: x w takes b = qt,
  * sb = s; its input gradient, dy w^T, takes b = q (a product with K and N
@@ -169,7 +171,7 @@ int moe_fp8_quant_cols(const moe_plan_desc* desc, const moe_plan* plan, int dtyp
  *   through moe_permute_fp8).
  */
 typedef struct moe_mm_desc {
-    int32_t  a_rows, rows, E, K, N;
+    int32_t  a_rows, rows, rows_used, E, K, N;
     int32_t  out;           /* MOE_F32 or MOE_BF16 */
     uint32_t flags;         /* MOE_MM_* */
     uint32_t reserved;      /* must be 0 */

@@ -153,13 +153,13 @@ def test_quantizers_refused():
     assert b(None, None, bf, 0, 128, None, None, None) == B.MOE_OK
 
 
-def mm(a_rows=8, rows=8, E=2, K=128, N=128, out=B.MOE_BF16, flags=0, reserved=0):
-    return ops.MoeMmDesc(a_rows, rows, E, K, N, out, flags, reserved, None)
+def mm(a_rows=8, rows=8, rows_used=0, E=2, K=128, N=128, out=B.MOE_BF16, flags=0, reserved=0):
+    return ops.MoeMmDesc(a_rows, rows, rows_used, E, K, N, out, flags, reserved, None)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(flags=4), B.MOE_EINVAL), (dict(reserved=1), B.MOE_EINVAL), (dict(a_rows=-1), B.MOE_EINVAL),
-    (dict(rows=-1, a_rows=-1), B.MOE_EINVAL), (dict(E=0), B.MOE_EINVAL), (dict(out=3), B.MOE_EDTYPE),
+    (dict(rows=-1, a_rows=-1), B.MOE_EINVAL), (dict(rows_used=-1), B.MOE_EINVAL), (dict(rows_used=9), B.MOE_EINVAL), (dict(E=0), B.MOE_EINVAL), (dict(out=3), B.MOE_EDTYPE),
     (dict(K=0), B.MOE_EINVAL), (dict(K=72), B.MOE_ESHAPE), (dict(N=24), B.MOE_ESHAPE),
     (dict(K=(1 << 20) + 16), B.MOE_ESHAPE), (dict(E=1025), B.MOE_ESHAPE), (dict(K=1 << 16, N=1 << 15), B.MOE_ESHAPE),
     (dict(a_rows=9), B.MOE_EINVAL), (dict(a_rows=1 << 24, K=128, flags=ops.MOE_MM_GATHER), B.MOE_ESHAPE),
