@@ -27,8 +27,8 @@ unsigned grid_for(int64_t threads) { return (unsigned)std::min<int64_t>((threads
 // rows [R][C] -> codes and scales, eight lanes per block of 128
 template <typename T>
 __global__ void __launch_bounds__(256)
-k_quant_rows_128(const T* __restrict__ src, int64_t R, int C, RowFilter rows, uint8_t* __restrict__ q,
-                 float* __restrict__ s) {
+k_quant_rows_128(const T* __restrict__ src, int64_t R, int C, RowFilter rows, bool stream,
+                 uint8_t* __restrict__ q, float* __restrict__ s) {
   const int nb = (C + 127) / 128;
   const int64_t blocks = R * nb;
   for (int64_t b = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 3; b < blocks; b += (int64_t)gridDim.x * 32) {
@@ -45,7 +45,7 @@ k_quant_rows_128(const T* __restrict__ src, int64_t R, int C, RowFilter rows, ui
     float sc;
     const uint4 code = quant_block8(v, sc);
     if (!on) continue;
-    if (col < C) *reinterpret_cast<uint4*>(q + r * C + col) = code;
+    if (col < C) store_as(reinterpret_cast<uint4*>(q + r * C + col), code, stream);
     if ((threadIdx.x & 7) == 0) s[b] = sc;
   }
 }
@@ -68,7 +68,7 @@ __device__ __forceinline__ float sigmoid_(float g) {
 // A = silu(G) U of rows h [R][2n], quantized; A itself too when `a` is set
 template <typename T>
 __global__ void __launch_bounds__(256)
-k_swiglu_fp8(const T* __restrict__ h, int64_t R, int n, RowFilter rows, uint8_t* __restrict__ q,
+k_swiglu_fp8(const T* __restrict__ h, int64_t R, int n, RowFilter rows, bool stream, uint8_t* __restrict__ q,
              float* __restrict__ s, T* __restrict__ a) {
   const int nb = (n + 127) / 128;
   const int64_t blocks = R * nb;
@@ -91,8 +91,8 @@ k_swiglu_fp8(const T* __restrict__ h, int64_t R, int n, RowFilter rows, uint8_t*
     const uint4 code = quant_block8(v, sc);
     if (!on) continue;
     if (col < n) {
-      *reinterpret_cast<uint4*>(q + r * n + col) = code;
-      if (a) store16(a + r * n + col, v);
+      store_as(reinterpret_cast<uint4*>(q + r * n + col), code, stream);
+      if (a) store16(a + r * n + col, v, stream);
     }
     if ((threadIdx.x & 7) == 0) s[b] = sc;
   }
@@ -101,7 +101,7 @@ k_swiglu_fp8(const T* __restrict__ h, int64_t R, int n, RowFilter rows, uint8_t*
 // dh = (da U s (1 + G (1 - s)), da silu(G)), s = sigmoid(G); 16 columns per thread
 template <typename T>
 __global__ void __launch_bounds__(256)
-k_swiglu_bwd_rows(const T* __restrict__ da, const T* __restrict__ h, int64_t R, int n, RowFilter rows,
+k_swiglu_bwd_rows(const T* __restrict__ da, const T* __restrict__ h, int64_t R, int n, RowFilter rows, bool stream,
                   T* __restrict__ dh) {
   const int per = n / 16;
   const int64_t total = R * per;
@@ -119,8 +119,8 @@ k_swiglu_bwd_rows(const T* __restrict__ da, const T* __restrict__ h, int64_t R, 
       d[j] = dj * u[j] * sg * (1.f + g[j] * (1.f - sg));
       u[j] = dj * g[j] * sg;
     }
-    store16(dh + r * 2 * n + col, d);
-    store16(dh + r * 2 * n + n + col, u);
+    store16(dh + r * 2 * n + col, d, stream);
+    store16(dh + r * 2 * n + n + col, u, stream);
   }
 }
 
@@ -213,8 +213,8 @@ constexpr int TP = 128 + 16;  // LDS pitch of a transposed tile's row (bytes)
 // weights [K][N] of expert blockIdx.z, tile (blockIdx.y, blockIdx.x)
 template <typename T>
 __global__ void __launch_bounds__(256)
-k_quant_weights_128(const T* __restrict__ w, int K, int N, uint8_t* __restrict__ q, uint8_t* __restrict__ qt,
-                    float* __restrict__ s) {
+k_quant_weights_128(const T* __restrict__ w, int K, int N, bool stream, uint8_t* __restrict__ q,
+                    uint8_t* __restrict__ qt, float* __restrict__ s) {
   __shared__ uint32_t wmax[4];
   __shared__ __attribute__((aligned(16))) uint8_t tile[128 * TP];
   const int tid = threadIdx.x;
@@ -252,7 +252,8 @@ k_quant_weights_128(const T* __restrict__ w, int K, int N, uint8_t* __restrict__
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int k = k0 + rk + i, n = n0 + cn;
-      if (k < K && n < N) *reinterpret_cast<uint2*>(q + base + (size_t)k * N + n) = make_uint2(c[i][0], c[i][1]);
+      if (k < K && n < N)
+        store_as(reinterpret_cast<uint2*>(q + base + (size_t)k * N + n), make_uint2(c[i][0], c[i][1]), stream);
     }
   }
   if (qt) {
@@ -266,8 +267,8 @@ k_quant_weights_128(const T* __restrict__ w, int K, int N, uint8_t* __restrict__
     for (int i = 0; i < 4; ++i) {
       const int n = i * 32 + (tid >> 3), k = (tid & 7) * 16;
       if (n0 + n < N && k0 + k < K)
-        *reinterpret_cast<uint4*>(qt + base + (size_t)(n0 + n) * K + k0 + k) =
-            *reinterpret_cast<const uint4*>(tile + n * TP + k);
+        store_as(reinterpret_cast<uint4*>(qt + base + (size_t)(n0 + n) * K + k0 + k),
+                 *reinterpret_cast<const uint4*>(tile + n * TP + k), stream);
     }
   }
 }
@@ -275,8 +276,8 @@ k_quant_weights_128(const T* __restrict__ w, int K, int N, uint8_t* __restrict__
 // columns of the segments: one workgroup per block of 128 rows and 128 columns
 template <typename T>
 __global__ void __launch_bounds__(256)
-k_quant_cols_128(const T* __restrict__ src, int C, int Tn, bool gather, PlanArgs p, uint8_t* __restrict__ q,
-                 float* __restrict__ s) {
+k_quant_cols_128(const T* __restrict__ src, int C, int Tn, bool gather, PlanArgs p, bool stream,
+                 uint8_t* __restrict__ q, float* __restrict__ s) {
   typedef Tile8<T> V;
   constexpr int MW = sizeof(typename V::Mag) / 4;
   __shared__ typename V::Mag cmax[4][16];
@@ -335,9 +336,12 @@ k_quant_cols_128(const T* __restrict__ src, int C, int Tn, bool gather, PlanArgs
   for (int i = 0; i < 4; ++i) {
     const int n = i * 32 + (tid >> 3), k = (tid & 7) * 16;
     if (c0 + n < C)
-      *reinterpret_cast<uint4*>(q + (blk * C + c0 + n) * 128 + k) = *reinterpret_cast<const uint4*>(tile + n * TP + k);
+      store_as(reinterpret_cast<uint4*>(q + (blk * C + c0 + n) * 128 + k),
+               *reinterpret_cast<const uint4*>(tile + n * TP + k), stream);
   }
 }
+
+int64_t bytes_of(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
 RowFilter filter_of(const PlanArgs& p) { return RowFilter{p.offsets, p.row_token, p.E}; }
 
@@ -346,21 +350,25 @@ RowFilter filter_of(const PlanArgs& p) { return RowFilter{p.offsets, p.row_token
 hipError_t launch_quant_rows_128(const PlanArgs& p, int dtype, int64_t R, int C, const void* src, uint8_t* q,
                                  float* s, hipStream_t st) {
   const dim3 grid(grid_for(R * ((C + 127) / 128) * 8));
+  const bool stream = streams(R * C * (bytes_of(dtype) + 1));
   if (dtype == MOE_BF16)
-    hipLaunchKernelGGL(k_quant_rows_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)src, R, C, filter_of(p), q, s);
+    hipLaunchKernelGGL(k_quant_rows_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)src, R, C, filter_of(p), stream,
+                       q, s);
   else
-    hipLaunchKernelGGL(k_quant_rows_128<float>, grid, dim3(256), 0, st, (const float*)src, R, C, filter_of(p), q, s);
+    hipLaunchKernelGGL(k_quant_rows_128<float>, grid, dim3(256), 0, st, (const float*)src, R, C, filter_of(p), stream,
+                       q, s);
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_fp8(const PlanArgs& p, int dtype, int64_t R, int n, const void* h, uint8_t* q, float* s,
                              void* a, hipStream_t st) {
   const dim3 grid(grid_for(R * ((n + 127) / 128) * 8));
+  const bool stream = streams(R * n * ((a ? 3 : 2) * bytes_of(dtype) + 1));
   if (dtype == MOE_BF16)
-    hipLaunchKernelGGL(k_swiglu_fp8<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)h, R, n, filter_of(p), q, s,
+    hipLaunchKernelGGL(k_swiglu_fp8<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)h, R, n, filter_of(p), stream, q, s,
                        (bf16_t*)a);
   else
-    hipLaunchKernelGGL(k_swiglu_fp8<float>, grid, dim3(256), 0, st, (const float*)h, R, n, filter_of(p), q, s,
+    hipLaunchKernelGGL(k_swiglu_fp8<float>, grid, dim3(256), 0, st, (const float*)h, R, n, filter_of(p), stream, q, s,
                        (float*)a);
   return hipGetLastError();
 }
@@ -368,22 +376,26 @@ hipError_t launch_swiglu_fp8(const PlanArgs& p, int dtype, int64_t R, int n, con
 hipError_t launch_swiglu_bwd_rows(const PlanArgs& p, int dtype, int64_t R, int n, const void* da, const void* h,
                                   void* dh, hipStream_t st) {
   const dim3 grid(grid_for(R * (n / 16)));
+  const bool stream = streams(R * n * 5 * bytes_of(dtype));
   if (dtype == MOE_BF16)
     hipLaunchKernelGGL(k_swiglu_bwd_rows<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)da, (const bf16_t*)h, R, n,
-                       filter_of(p), (bf16_t*)dh);
+                       filter_of(p), stream, (bf16_t*)dh);
   else
     hipLaunchKernelGGL(k_swiglu_bwd_rows<float>, grid, dim3(256), 0, st, (const float*)da, (const float*)h, R, n,
-                       filter_of(p), (float*)dh);
+                       filter_of(p), stream, (float*)dh);
   return hipGetLastError();
 }
 
 hipError_t launch_quant_weights_128(int dtype, int E, int K, int N, const void* w, uint8_t* q, uint8_t* qt, float* s,
                                     hipStream_t st) {
   const dim3 grid((N + 127) / 128, (K + 127) / 128, E);
+  const bool stream = streams((int64_t)E * K * N * (bytes_of(dtype) + (q ? 1 : 0) + (qt ? 1 : 0)));
   if (dtype == MOE_BF16)
-    hipLaunchKernelGGL(k_quant_weights_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)w, K, N, q, qt, s);
+    hipLaunchKernelGGL(k_quant_weights_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)w, K, N, stream, q,
+                       qt, s);
   else
-    hipLaunchKernelGGL(k_quant_weights_128<float>, grid, dim3(256), 0, st, (const float*)w, K, N, q, qt, s);
+    hipLaunchKernelGGL(k_quant_weights_128<float>, grid, dim3(256), 0, st, (const float*)w, K, N, stream, q,
+                       qt, s);
   return hipGetLastError();
 }
 
@@ -391,10 +403,13 @@ hipError_t launch_quant_cols_128(const PlanArgs& p, int dtype, int C, bool gathe
                                  float* s, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)(p.cap / 128) * ((C + 127) / 128)));
   if (grid.x == 0) return hipSuccess;
+  const bool stream = streams((int64_t)p.cap * C * (bytes_of(dtype) + 1));
   if (dtype == MOE_BF16)
-    hipLaunchKernelGGL(k_quant_cols_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)src, C, p.T, gather, p, q, s);
+    hipLaunchKernelGGL(k_quant_cols_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)src, C, p.T, gather,
+                       p, stream, q, s);
   else
-    hipLaunchKernelGGL(k_quant_cols_128<float>, grid, dim3(256), 0, st, (const float*)src, C, p.T, gather, p, q, s);
+    hipLaunchKernelGGL(k_quant_cols_128<float>, grid, dim3(256), 0, st, (const float*)src, C, p.T, gather, p,
+                       stream, q, s);
   return hipGetLastError();
 }
 

@@ -152,7 +152,7 @@ constexpr int SORT_ONE = 4096;
 // xp[slot_row[t,k]] = x[t], 16-byte pieces; `splits` waves share a token's row
 __global__ void __launch_bounds__(256)
 k_permute(const uint4* __restrict__ x, const int32_t* __restrict__ slot_row, int T, int K, int cap, int pieces,
-          int splits, uint4* __restrict__ xp) {
+          int splits, bool stream, uint4* __restrict__ xp) {
   const int lane = threadIdx.x & 63;
   const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = (int)(w / splits);
@@ -162,7 +162,7 @@ k_permute(const uint4* __restrict__ x, const int32_t* __restrict__ slot_row, int
     const uint4 v = x[(size_t)t * pieces + c];
     for (int k = 0; k < K; ++k) {
       const int r = rows[k];
-      if ((unsigned)r < (unsigned)cap) xp[(size_t)r * pieces + c] = v;
+      if ((unsigned)r < (unsigned)cap) store_as(xp + (size_t)r * pieces + c, v, stream);
     }
   }
 }
@@ -171,7 +171,7 @@ k_permute(const uint4* __restrict__ x, const int32_t* __restrict__ slot_row, int
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_permute_fp8(const T* __restrict__ x, const int32_t* __restrict__ slot_row, int Tn, int K, int cap, int d,
-              int splits, uint8_t* __restrict__ q, float* __restrict__ s) {
+              int splits, bool stream, uint8_t* __restrict__ q, float* __restrict__ s) {
   const int lane = threadIdx.x & 63;
   const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = (int)(w / splits);
@@ -192,7 +192,7 @@ k_permute_fp8(const T* __restrict__ x, const int32_t* __restrict__ slot_row, int
     for (int k = 0; k < K; ++k) {
       const int r = rows[k];
       if ((unsigned)r >= (unsigned)cap) continue;
-      if (col < d) *reinterpret_cast<uint4*>(q + (size_t)r * d + col) = code;
+      if (col < d) store_as(reinterpret_cast<uint4*>(q + (size_t)r * d + col), code, stream);
       if ((lane & 7) == 0 && b < nb) s[(size_t)r * nb + b] = sc;
     }
   }
@@ -247,7 +247,7 @@ k_unpermute(const uint4* __restrict__ y, const float* __restrict__ wt, const int
       for (int j = 0; j < ROWS_UNR; ++j) {
         const int r = k0 + j < K ? rows[k0 + j] : -1;
         ok[j] = (unsigned)r < (unsigned)cap;
-        raw[j] = ok[j] ? y[(size_t)r * pieces + c] : make_uint4(0, 0, 0, 0);
+        raw[j] = ok[j] ? load_stream(y + (size_t)r * pieces + c) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int j = 0; j < ROWS_UNR; ++j) {
@@ -268,8 +268,8 @@ k_unpermute(const uint4* __restrict__ y, const float* __restrict__ wt, const int
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_unpermute_bwd(const uint4* __restrict__ d_o, const uint4* __restrict__ y, const float* __restrict__ wt,
-                const int32_t* __restrict__ slot_row, int K, int cap, int pieces, uint4* __restrict__ dy,
-                float* __restrict__ dw) {
+                const int32_t* __restrict__ slot_row, int K, int cap, int pieces, bool stream,
+                uint4* __restrict__ dy, float* __restrict__ dw) {
   constexpr int V = VEC<T>;
   constexpr int KG = ROWS_UNR;
   __shared__ float part[4][KG];
@@ -293,7 +293,7 @@ k_unpermute_bwd(const uint4* __restrict__ d_o, const uint4* __restrict__ y, cons
         uint4 raw[KG];
 #pragma unroll
         for (int j = 0; j < KG; ++j)
-          raw[j] = r[j] >= 0 ? y[(size_t)r[j] * pieces + c] : make_uint4(0, 0, 0, 0);
+          raw[j] = r[j] >= 0 ? load_stream(y + (size_t)r[j] * pieces + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < KG; ++j) {
           if (r[j] < 0) continue;
@@ -310,7 +310,7 @@ k_unpermute_bwd(const uint4* __restrict__ d_o, const uint4* __restrict__ y, cons
           float v[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) v[i] = g[j] * a[i];
-          dy[(size_t)r[j] * pieces + c] = pack16<T>(v);
+          store_as(dy + (size_t)r[j] * pieces + c, pack16<T>(v), stream);
         }
       }
     }
@@ -334,6 +334,9 @@ int row_splits(int T, int passes) {
   const int want = (4096 + T - 1) / std::max(T, 1);
   return std::max(1, std::min(want, passes));
 }
+
+// T rows read and T*K written of so many bytes
+bool streamed(const PlanArgs& p, int64_t row_bytes) { return streams((int64_t)p.T * (p.K + 1) * row_bytes); }
 
 unsigned wave_blocks(int T, int splits) { return (unsigned)(((int64_t)T * splits + 3) / 4); }
 
@@ -366,7 +369,7 @@ hipError_t launch_permute(const PlanArgs& p, int dtype, int d, const void* x, vo
   const int pieces = (int)((int64_t)d * (dtype == MOE_BF16 ? 2 : 4) / 16);
   const int splits = row_splits(p.T, (pieces + 63) / 64);
   hipLaunchKernelGGL(k_permute, dim3(wave_blocks(p.T, splits)), dim3(256), 0, st, (const uint4*)x, p.slot_row, p.T,
-                     p.K, p.cap, pieces, splits, (uint4*)xp);
+                     p.K, p.cap, pieces, splits, streamed(p, (int64_t)pieces * 16), (uint4*)xp);
   return hipGetLastError();
 }
 
@@ -376,10 +379,10 @@ hipError_t launch_permute_fp8(const PlanArgs& p, int dtype, int d, const void* x
   const dim3 grid(wave_blocks(p.T, splits));
   if (dtype == MOE_BF16)
     hipLaunchKernelGGL(k_permute_fp8<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)x, p.slot_row, p.T, p.K, p.cap,
-                       d, splits, q, s);
+                       d, splits, streamed(p, d), q, s);
   else
     hipLaunchKernelGGL(k_permute_fp8<float>, grid, dim3(256), 0, st, (const float*)x, p.slot_row, p.T, p.K, p.cap, d,
-                       splits, q, s);
+                       splits, streamed(p, d), q, s);
   return hipGetLastError();
 }
 
@@ -402,10 +405,10 @@ hipError_t launch_unpermute_bwd(const PlanArgs& p, int dtype, int d, const void*
   const int pieces = (int)((int64_t)d * (dtype == MOE_BF16 ? 2 : 4) / 16);
   if (dtype == MOE_BF16)
     hipLaunchKernelGGL(k_unpermute_bwd<bf16_t>, dim3(p.T), dim3(256), 0, st, (const uint4*)d_o, (const uint4*)y, w,
-                       p.slot_row, p.K, p.cap, pieces, (uint4*)dy, dw);
+                       p.slot_row, p.K, p.cap, pieces, streamed(p, (int64_t)pieces * 16), (uint4*)dy, dw);
   else
     hipLaunchKernelGGL(k_unpermute_bwd<float>, dim3(p.T), dim3(256), 0, st, (const uint4*)d_o, (const uint4*)y, w,
-                       p.slot_row, p.K, p.cap, pieces, (uint4*)dy, dw);
+                       p.slot_row, p.K, p.cap, pieces, streamed(p, (int64_t)pieces * 16), (uint4*)dy, dw);
   return hipGetLastError();
 }
 
