@@ -52,14 +52,78 @@ k_sort_count(const int32_t* __restrict__ idx, int slots, int E, int chunk, int32
   for (int e = threadIdx.x; e < E; e += SORT_NT) cnt[(size_t)blockIdx.x * E + e] = h[e];
 }
 
-// Rows of one chunk's choices.  With `cnt` null the launch is one workgroup
-// that counts all slots itself.
+// Exclusive scan over the workgroup's threads; wsum: one word per wave
+__device__ __forceinline__ int block_scan(int v, int lane, int wave, int* wsum) {
+  int incl = v;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 63) wsum[wave] = incl;
+  __syncthreads();
+  int before = incl - v;
+#pragma unroll
+  for (int w = 0; w < SORT_WAVES; ++w) before += w < wave ? wsum[w] : 0;
+  return before;
+}
+
+// The choices of the waves before wave `wave` (of WAVES) for expert e
+__device__ __forceinline__ int waves_before(const int (*wcount)[SORT_MAX_E], int e, int wave) {
+  int n = 0;
+#pragma unroll
+  for (int w = 0; w < SORT_WAVES; ++w) n += w < wave ? wcount[w][e] : 0;
+  return n;
+}
+
+// Up to 1024 choices (one per thread) and experts: one workgroup, each choice
+// read once.  Launched with at least E threads.
+__global__ void __launch_bounds__(SORT_NT)
+k_sort_small(const int32_t* __restrict__ idx, int slots, int K, int E, int align, int32_t* __restrict__ offsets,
+             int32_t* __restrict__ counts, int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row) {
+  __shared__ int wcount[SORT_WAVES][SORT_MAX_E];
+  __shared__ int seg[SORT_MAX_E];
+  __shared__ int wsum[SORT_WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int waves = (slots + 63) >> 6;  // with choices
+  const int id = tid < slots ? idx[tid] : -1;
+  for (int w = 0; w < waves; ++w)
+    if (tid < E) wcount[w][tid] = 0;
+  if (tid < SORT_WAVES) wsum[tid] = 0;
+  const bool kept = (unsigned)id < (unsigned)E;
+  int rank, same;
+  wave_rank(kept ? id : E, 32 - __clz(E), lane, rank, same);
+  __syncthreads();
+  if (kept && rank == 0) wcount[wave][id] = same;
+  __syncthreads();
+  int n = 0;
+  if (tid < E)
+    for (int w = 0; w < waves; ++w) n += wcount[w][tid];
+  const int padded = (n + align - 1) / align * align;
+  const int first = block_scan(padded, lane, wave, wsum);
+  if (tid < E) {
+    seg[tid] = first;
+    offsets[tid] = first;
+    counts[tid] = n;
+    if (tid == E - 1) offsets[E] = first + padded;
+    for (int r = first + n; r < first + padded; ++r) row_token[r] = -1;
+  }
+  __syncthreads();
+  int row = -1;
+  if (kept) {
+    row = seg[id] + rank + waves_before(wcount, id, wave);
+    row_token[row] = tid / K;
+  }
+  if (tid < slots) slot_row[tid] = row;
+}
+
+// Rows of one chunk's choices, cnt [chunks][E] from k_sort_count.
 __global__ void __launch_bounds__(SORT_NT)
 k_sort_place(const int32_t* __restrict__ idx, int slots, int K, int E, int align, int chunk,
              const int32_t* __restrict__ cnt, int32_t* __restrict__ offsets, int32_t* __restrict__ counts,
              int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row) {
-  __shared__ int total[SORT_MAX_E];                 // choices of each expert, then its segment's first row
-  __shared__ int before[SORT_MAX_E];                // of those, in earlier chunks; then the next free row
+  __shared__ int total[SORT_MAX_E];                 // choices of each expert
+  __shared__ int seg[SORT_MAX_E];                   // its segment's first row
+  __shared__ int before[SORT_MAX_E];                // choices in earlier chunks, then the next free row
   __shared__ int wcount[SORT_WAVES][SORT_MAX_E];    // this step's choices per wave and expert
   __shared__ int wsum[SORT_WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -67,13 +131,13 @@ k_sort_place(const int32_t* __restrict__ idx, int slots, int K, int E, int align
 
   for (int e = tid; e < E; e += SORT_NT) total[e] = before[e] = 0;
   __syncthreads();
-  if (cnt) {
+  {
     // thread groups of E take the chunks in turn; integer sums
     const int groups = max(1, SORT_NT / E);
     const int g = tid / E, e = tid % E;
     if (g < groups) {
       int t = 0, b = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int c = g; c < chunks; c += groups) {
         const int v = cnt[(size_t)c * E + e];
         t += v;
@@ -82,63 +146,55 @@ k_sort_place(const int32_t* __restrict__ idx, int slots, int K, int E, int align
       atomicAdd(&total[e], t);
       atomicAdd(&before[e], b);
     }
-  } else {
-    for (int s = tid; s < slots; s += SORT_NT) {
-      const int e = idx[s];
-      if ((unsigned)e < (unsigned)E) atomicAdd(&total[e], 1);
-    }
   }
   __syncthreads();
 
   // exclusive scan of the padded lengths (thread e = expert e)
   const int n = tid < E ? total[tid] : 0;
   const int padded = (n + align - 1) / align * align;
-  int incl = padded;
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(incl, o, 64);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 63) wsum[wave] = incl;
-  __syncthreads();
-  int first = incl - padded;
-  for (int w = 0; w < wave; ++w) first += wsum[w];
+  const int first = block_scan(padded, lane, wave, wsum);
   if (tid < E) {
+    seg[tid] = first;
+    before[tid] += first;
     if (me == 0) {
       offsets[tid] = first;
       counts[tid] = n;
       if (tid == E - 1) offsets[E] = first + padded;
     }
-    // the rows that fill up a segment, dealt to the workgroups by expert
-    if (tid % chunks == me)
-      for (int r = first + n; r < first + padded; ++r) row_token[r] = -1;
-    before[tid] += first;
   }
   const int bits = 32 - __clz(E);  // E itself marks a dropped choice
 
   const int s0 = me * chunk, s1 = min(slots - s0, chunk) + s0;
   for (int base = s0; base < s1; base += SORT_NT) {
-    for (int i = tid; i < SORT_WAVES * E; i += SORT_NT) wcount[i / E][i % E] = 0;
-    __syncthreads();  // (also: `before` is complete)
     const int s = base + tid;
     const int id = s < s1 ? idx[s] : -1;
+    for (int i = tid; i < SORT_WAVES * SORT_MAX_E; i += SORT_NT)
+      if ((i & (SORT_MAX_E - 1)) < E) wcount[i / SORT_MAX_E][i & (SORT_MAX_E - 1)] = 0;
     const bool kept = (unsigned)id < (unsigned)E;
     const int e = kept ? id : E;
     int rank, same;
     wave_rank(e, bits, lane, rank, same);
+    __syncthreads();  // (also: seg and before are complete)
     if (kept && rank == 0) wcount[wave][e] = same;
     __syncthreads();
     int row = -1;
     if (kept) {
-      row = before[e] + rank;
-      for (int w = 0; w < wave; ++w) row += wcount[w][e];
+      row = before[e] + rank + waves_before(wcount, e, wave);
       row_token[row] = s / K;
     }
     if (s < s1) slot_row[s] = row;
     __syncthreads();
-    if (tid < E)
-      for (int w = 0; w < SORT_WAVES; ++w) before[tid] += wcount[w][tid];
+    if (tid < E) before[tid] += waves_before(wcount, tid, SORT_WAVES);
     __syncthreads();  // wcount is cleared next
   }
+
+  // the rows that fill up the segments, dealt to the workgroups by expert
+  if (align > 1)
+    for (int e = me; e < E; e += chunks) {
+      const int end = total[e] + seg[e];
+      const int fill = (total[e] + align - 1) / align * align - total[e];
+      if (tid < fill) row_token[end + tid] = -1;
+    }
 }
 
 int sort_chunk(int64_t slots) {
@@ -146,8 +202,8 @@ int sort_chunk(int64_t slots) {
   return (int)((std::max<int64_t>(per, 1) + SORT_NT - 1) / SORT_NT * SORT_NT);
 }
 
-// Up to this many slots one workgroup counts and places them itself.
-constexpr int SORT_ONE = 4096;
+// Up to this many slots one workgroup sorts them, a choice per thread.
+constexpr int SORT_ONE = SORT_NT;
 
 // xp[slot_row[t,k]] = x[t], 16-byte pieces; `splits` waves share a token's row
 __global__ void __launch_bounds__(256)
@@ -242,21 +298,22 @@ k_unpermute(const uint4* __restrict__ y, const float* __restrict__ wt, const int
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     for (int k0 = 0; k0 < K; k0 += ROWS_UNR) {
       uint4 raw[ROWS_UNR];
+      float g[ROWS_UNR];
       bool ok[ROWS_UNR];
 #pragma unroll
       for (int j = 0; j < ROWS_UNR; ++j) {
         const int r = k0 + j < K ? rows[k0 + j] : -1;
         ok[j] = (unsigned)r < (unsigned)cap;
+        g[j] = wt ? wt[(size_t)t * K + min(k0 + j, K - 1)] : 1.f;
         raw[j] = ok[j] ? load_stream(y + (size_t)r * pieces + c) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int j = 0; j < ROWS_UNR; ++j) {
         if (!ok[j]) continue;
-        const float g = wt ? wt[(size_t)t * K + k0 + j] : 1.f;
         float v[V];
         unpack16<T>(raw[j], v);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(g[j], v[i], acc[i]);
       }
     }
     o[(size_t)t * pieces + c] = pack16<T>(acc);
@@ -351,8 +408,9 @@ size_t sort_ws_bytes(int64_t slots, int E) {
 hipError_t launch_sort(const PlanArgs& p, const int32_t* expert_idx, const moe_plan& out, void* ws, hipStream_t st) {
   const int slots = p.T * p.K;
   if (slots <= SORT_ONE) {
-    hipLaunchKernelGGL(k_sort_place, dim3(1), dim3(SORT_NT), 0, st, expert_idx, slots, p.K, p.E, p.align,
-                       SORT_ONE, nullptr, out.offsets, out.counts, out.row_token, out.slot_row);
+    const int nt = (std::max(std::max(slots, p.E), 64) + 63) / 64 * 64;
+    hipLaunchKernelGGL(k_sort_small, dim3(1), dim3(nt), 0, st, expert_idx, slots, p.K, p.E, p.align, out.offsets,
+                       out.counts, out.row_token, out.slot_row);
     return hipGetLastError();
   }
   const int chunk = sort_chunk(slots);

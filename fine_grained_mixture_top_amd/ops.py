@@ -94,7 +94,9 @@ def blocks(n: int) -> int:
 
 
 def _need(name, t, dtypes, shape, device):
-    """A contiguous tensor of one of the types, of the shape, on the device; its address."""
+    """The address of a contiguous tensor of one of the types, of the shape, on the device."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.device == device:
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
     if t.dtype not in dtypes:
@@ -103,9 +105,7 @@ def _need(name, t, dtypes, shape, device):
         raise ValueError(f"{name}: shape {tuple(t.shape)} where {tuple(shape)} is needed")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on {t.device}, the call is on {device}")
 
 
 _VALUES = (torch.float32, torch.bfloat16)
@@ -113,12 +113,12 @@ _F32 = (torch.float32,)
 
 
 def _matrix(name, t, dtypes=_VALUES, dims=2):
-    """A tensor of `dims` dimensions to take sizes from."""
+    """A GPU tensor of `dims` dimensions to take sizes from."""
+    if isinstance(t, torch.Tensor) and t.dim() == dims and t.dtype in dtypes and t.is_cuda:
+        return t
     if not isinstance(t, torch.Tensor) or t.dim() != dims or t.dtype not in dtypes:
         raise ValueError(f"{name}: a {dims}-dimensional tensor of {', '.join(str(d) for d in dtypes)} is needed")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name}: on {t.device}, a GPU tensor is needed")
-    return t
+    raise ValueError(f"{name}: on {t.device}, a GPU tensor is needed")
 
 
 # the current stream's handle without building a Stream object (2 us a call),
@@ -138,8 +138,8 @@ def _call(fn, device, stream, *args):
         if stream.device != device:
             raise ValueError(f"stream on {stream.device}, the call is on {device}")
         handle = stream.cuda_stream
-    status = getattr(lib(), fn)(*args, handle)
-    if status != B.MOE_OK:
+    status = getattr(_lib or lib(), fn)(*args, handle)
+    if status:
         raise B.MoEError(fn, status)
 
 
