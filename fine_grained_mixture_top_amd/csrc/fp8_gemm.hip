@@ -69,15 +69,22 @@ hipError_t launch_thin(int out, const f8::Args& a, int64_t used, hipStream_t st)
 //   avg                          4          8          12         16         24         32
 //   bf16, 16 rows, 64 columns    45 / -     47 / 20.5  50 / -     63 / 28    82 / -     - / 41
 //         32 rows, 64 columns    48 / -     50 / 23.8  51 / -     54 / 25    60 / -     - / 34
+//         64 x 128 tiles                                                                - / 28
 //         128 x 128 tiles        52 / -     50 / 29.6  53 / -     53 / 30    54 / -     - / 31
 //   fp32, 16 rows, 64 columns    45 / -     48 / 20.7  52 / -     65 / 28    85 / -     - / 42
 //         32 rows, 64 columns    50 / -     50 / 23.8  53 / -     56 / 25    63 / -     - / 34
-//         128 x 64 tiles         95 / -     92 / 46    92 / -     92 / 46    93 / -     - / 47
-// and at avg 48: 32 rows 106, 128 x 64 tiles 97.  Below one row per expert, 32
-// columns give twice the workgroups (E = 256, K = 2048, N = 512, 128 rows: 22.9
-// against 24.3; 8 rows: 6.5 against 9.4).  256 x 256 tiles need enough rows and
-// tiles (E = 64, K = N = 2048: avg 64 69 against 60 with 128 x 128, avg 128 82
-// against 99, avg 4096 1210 against 1572).
+//   avg                          64         128        256        512
+//   bf16, 64 x 128 tiles         71 / -     112 / -    - / 67     295 / -
+//         128 x 128 tiles        64 / -     100 / -    - / 61     225 / -
+//         256 x 256 tiles        69 / -     81 / -     - / 62     193 / -
+//   fp32, 32 rows, 64 columns    (avg 48: 106, avg 64: 127)
+//         64 x 128 tiles         90 / -     145 / -    - / 96     396 / -
+//         128 x 256 tiles        85 / -     152 / -    - / 93     331 / -
+// Below one row per expert 32 columns give twice the workgroups (E = 256,
+// K = 2048, N = 512, 128 rows: 22.9 against 24.3; 8 rows: 6.5 against 9.4).
+// Large tiles need enough of them: 3003 rows, E = 24, K = 720, N = 1040 take
+// 21 (fp32) and 16.4 (bf16) with 64 x 128 tiles, 25 with 128 x 256, 17.5 with
+// 128 x 128.
 hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) {
   f8::Args a{};
   a.a = m.a; a.sa = m.sa; a.b = m.b; a.sb = m.sb; a.c = m.c;
@@ -96,10 +103,19 @@ hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) 
   if (thin && used < E) return launch_thin<1, 2, 1>(m.out, a, used, st);
   if (thin && used <= 12 * E) return launch_thin<1, 4, 1>(m.out, a, used, st);
   if (thin && used <= (wide ? 40 : 18) * E) return launch_thin<2, 4, 1>(m.out, a, used, st);
-  if (wide) return launch_tiles<128, 64, 2, 2, false, float>(a, row_tiles(a, used, 128) * div_up(a.N, 64), st);
-  if (used >= 96 * E && a.N > 128 && (used / 256 + 1) * div_up(a.N, 256) >= cu_count(device()))
-    return launch_tiles<256, 256, 2, 4, false, bf16_t>(a, row_tiles(a, used, 256) * div_up(a.N, 256), st);
-  return launch_tiles<128, 128, 2, 2, false, bf16_t>(a, row_tiles(a, used, 128) * div_up(a.N, 128), st);
+  // tiles of a size, about
+  auto full = [&](int BM, int BN) { return (used / BM + 1) * div_up(m.N, BN); };
+  auto bound = [&](int BM, int BN) { return row_tiles(a, used, BM) * div_up(m.N, BN); };
+  const int cus = cu_count(device());
+  if (wide) {
+    if (m.N > 128 && full(128, 256) >= cus) return launch_tiles<128, 256, 2, 4, false, float>(a, bound(128, 256), st);
+    return launch_tiles<64, 128, 1, 4, false, float>(a, bound(64, 128), st);
+  }
+  if (used >= 96 * E && m.N > 128 && full(256, 256) >= cus)
+    return launch_tiles<256, 256, 2, 4, false, bf16_t>(a, bound(256, 256), st);
+  if (used < 48 * E || full(128, 128) < cus)
+    return launch_tiles<64, 128, 1, 4, false, bf16_t>(a, bound(64, 128), st);
+  return launch_tiles<128, 128, 2, 2, false, bf16_t>(a, bound(128, 128), st);
 }
 
 hipError_t launch_fp8_wgrad(const PlanArgs& p, int M, int N, int out, const uint8_t* qa, const float* sa,

@@ -353,6 +353,13 @@ PRODUCTS = [  # T, K choices, E, reduction, columns, align, dropped, type, gathe
     (200, 2, 5, 400, 128, 128, 0.0, "f32", True), (700, 4, 8, 1024, 512, 1, 0.0, "bf16", False),
     (3001, 2, 9, 656, 336, 1, 0.4, "f32", True), (4096, 2, 4, 256, 768, 128, 0.0, "bf16", True),
     (900, 1, 1, 384, 256, 1, 0.0, "bf16", False), (64, 1, 1000, 144, 48, 1, 0.0, "f32", False),
+    # every workgroup walks several tiles: one block of the reduction a tile, a ragged one, several
+    (4111, 2, 4, 128, 2064, 1, 0.1, "bf16", True), (4111, 2, 4, 272, 2064, 1, 0.1, "bf16", True),
+    (4111, 2, 3, 16, 2304, 128, 0.0, "bf16", False), (5003, 2, 8, 640, 4096, 1, 0.3, "bf16", False),
+    (4111, 2, 4, 128, 1040, 1, 0.1, "f32", True), (4111, 2, 4, 400, 1040, 1, 0.1, "f32", False),
+    (6007, 2, 40, 384, 1296, 1, 0.2, "bf16", True), (6007, 2, 40, 112, 1296, 1, 0.2, "bf16", True),
+    (400, 2, 20, 1040, 2064, 1, 0.0, "bf16", True), (300, 2, 20, 1040, 400, 1, 0.0, "f32", True),
+    (150, 1, 10, 528, 272, 1, 0.0, "bf16", False),
 ]
 
 
@@ -434,6 +441,9 @@ WGRADS = [  # T, K, E, M, N, align, dropped, type, gathered
     (1, 1, 4, 16, 16, 128, 0.0, "f32", True), (5, 2, 3, 144, 272, 128, 0.0, "bf16", True),
     (300, 3, 9, 272, 144, 128, 0.2, "f32", False), (300, 2, 5, 256, 512, 256, 0.0, "bf16", True),
     (3000, 2, 3, 528, 400, 128, 0.0, "f32", True), (0, 2, 3, 128, 128, 128, 0.0, "bf16", False),
+    # more tiles than workgroups, several experts without rows
+    (90, 1, 80, 512, 528, 128, 0.3, "bf16", True), (90, 1, 80, 512, 528, 256, 0.3, "f32", True),
+    (2000, 3, 40, 528, 512, 128, 0.0, "bf16", False), (6000, 3, 2, 2064, 2048, 128, 0.0, "bf16", True),
 ]
 
 
