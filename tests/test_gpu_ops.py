@@ -444,6 +444,7 @@ WGRADS = [  # T, K, E, M, N, align, dropped, type, gathered
     # more tiles than workgroups, several experts without rows
     (90, 1, 80, 512, 528, 128, 0.3, "bf16", True), (90, 1, 80, 512, 528, 256, 0.3, "f32", True),
     (2000, 3, 40, 528, 512, 128, 0.0, "bf16", False), (6000, 3, 2, 2064, 2048, 128, 0.0, "bf16", True),
+    (900, 2, 40, 752, 512, 128, 0.1, "bf16", True), (60, 1, 90, 384, 512, 128, 0.2, "bf16", False),
 ]
 
 
