@@ -142,11 +142,9 @@ struct Args {
   int sb_k, sb_n;            // strides of sb in (reduction block, column block)
 };
 
-// rows of segment e that lie in the buffers (rows past them are never touched)
-__device__ __forceinline__ int seg_rows(const Args& g, int e) {
-  if (!g.offsets) return g.rows;
-  const int o = g.offsets[e];
-  return o < 0 || o >= g.rows ? 0 : max(0, min(g.counts[e], g.rows - o));
+// n rows from row o on, as far as they lie in the buffers (rows past them are never touched)
+__device__ __forceinline__ int rows_in(const Args& g, int o, int n) {
+  return o < 0 || o >= g.rows ? 0 : max(0, min(n, g.rows - o));
 }
 
 // BM x BN tiles, WM x WN waves.  WG: weight gradient (tiles of dw over the
@@ -202,7 +200,7 @@ k_fp8_gemm(Args g) {
       int o = 0, n = 0;
       if (e < g.E) {
         o = g.offsets ? g.offsets[e] : 0;
-        n = seg_rows(g, e);
+        n = rows_in(g, o, g.offsets ? g.counts[e] : g.rows);
         seg0[e] = o;
         segn[e] = n;
       }
@@ -563,12 +561,24 @@ k_fp8_thin(Args g) {
   const int NT = (g.N + BN - 1) / BN;
   const int mg = (int)(blockIdx.x / (unsigned)NT), n0 = (int)(blockIdx.x % (unsigned)NT) * BN;
 
-  // the row tile's segment: lanes scan `per` experts each
+  // The row tile's segment: lanes scan `per` experts each, four at a time
+  // (loads of four in flight; up to 256 experts they stay in registers).
   const int per = (g.E + 63) >> 6;
+  int first[4], rws[4];
   int mine = 0;
-  for (int x = 0; x < per; ++x) {
-    const int e = lane * per + x;
-    if (e < g.E) mine += (seg_rows(g, e) + BM - 1) / BM;
+  for (int x0 = 0; x0 < per; x0 += 4) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int e = lane * per + x0 + x;
+      const bool is = x0 + x < per && e < g.E;
+      first[x] = is && g.offsets ? g.offsets[e] : 0;
+      rws[x] = is ? (g.offsets ? g.counts[e] : g.rows) : 0;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      rws[x] = rows_in(g, first[x], rws[x]);
+      mine += (rws[x] + BM - 1) / BM;
+    }
   }
   int incl = mine;
   for (int s = 1; s < 64; s <<= 1) {
@@ -577,38 +587,92 @@ k_fp8_thin(Args g) {
   }
   const uint64_t past = __ballot(incl > mg);
   if (past == 0) return;  // no such tile
-  const int src = __builtin_ctzll(past);
-  int left = mg - (__shfl(incl, src, 64) - __shfl(mine, src, 64));
-  int e = src * per, n = 0;
-  for (;; ++e) {
-    n = seg_rows(g, e);
-    const int tiles = (n + BM - 1) / BM;
-    if (left < tiles) break;
-    left -= tiles;
+  const int src = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
+  int left = mg - (__builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(mine, src));
+  int e = src * per, n = 0, row0 = 0;
+  if (per <= 4) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int nx = __builtin_amdgcn_readlane(rws[x], src), tiles = (nx + BM - 1) / BM;
+      if (left >= 0 && left < tiles) {
+        e = src * per + x;
+        n = nx;
+        row0 = __builtin_amdgcn_readlane(first[x], src) + left * BM;
+        n -= left * BM;
+        left = -1;
+      }
+      if (left >= 0) left -= tiles;
+    }
+  } else {
+    for (;; ++e) {
+      row0 = __builtin_amdgcn_readfirstlane(g.offsets[e]);
+      n = rows_in(g, row0, __builtin_amdgcn_readfirstlane(g.counts[e]));
+      const int tiles = (n + BM - 1) / BM;
+      if (left < tiles) break;
+      left -= tiles;
+    }
+    row0 += left * BM;
+    n -= left * BM;
   }
   e = __builtin_amdgcn_readfirstlane(e);
-  const int m0 = __builtin_amdgcn_readfirstlane(left) * BM;
-  const int rows = min(__builtin_amdgcn_readfirstlane(n) - m0, BM);
-  const int row0 = (g.offsets ? g.offsets[e] : 0) + m0;
+  row0 = __builtin_amdgcn_readfirstlane(row0);
+  const int rows = min(__builtin_amdgcn_readfirstlane(n), BM);
 
   const int p = lane & 15, h = lane >> 4;
   // rows and columns past the end repeat the last one (their results are dropped)
   const uint8_t* pa[RT];
   const float* psa[RT];
   bool real[RT];
+  int64_t row[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    int64_t row = row0 + min(16 * r + p, rows - 1);
-    if (g.row_token) row = g.row_token[row];
-    real[r] = (uint64_t)row < (uint64_t)g.a_rows;  // a token that does not exist counts as zeros
-    if (!real[r]) row = 0;
-    pa[r] = g.a + row * g.K + 16 * h;
-    psa[r] = g.sa + row * g.kb;
+    row[r] = row0 + min(16 * r + p, rows - 1);
+    if (g.row_token) row[r] = g.row_token[row[r]];
   }
   const uint8_t* pb[FN];
 #pragma unroll
   for (int i = 0; i < FN; ++i) pb[i] = g.b + ((int64_t)e * g.N + min(n0 + 16 * i + p, g.N - 1)) * g.K + 16 * h;
   const float* psb = g.sb + (int64_t)e * g.kb * ((g.N + 127) >> 7) + (int64_t)(n0 >> 7) * g.sb_n;
+
+  // Loads of the blocks k0, k0 + 4, ..: none under a condition; past the
+  // reduction they read its first codes, and both sides' become zeros later.
+  uint4 ra[UNR][RT][2], rb[UNR][FN][2];
+  float sa[UNR][RT], sb[UNR];
+  auto from = [&](int k, int c) {  // this lane's chunk: 16 h further on
+    const int at = k * 128 + 64 * c;
+    return at + 16 * h < g.K ? at : -16 * h;
+  };
+  auto load_b = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < FN; ++i) rb[u][i][c] = *reinterpret_cast<const uint4*>(pb[i] + from(k0 + 4 * u, c));
+      sb[u] = psb[(int64_t)min(k0 + 4 * u, g.kb - 1) * g.sb_k];
+    }
+  };
+  auto load_a = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) ra[u][r][c] = *reinterpret_cast<const uint4*>(pa[r] + from(k0 + 4 * u, c));
+#pragma unroll
+      for (int r = 0; r < RT; ++r) sa[u][r] = psa[r][min(k0 + 4 * u, g.kb - 1)];
+    }
+  };
+  load_b(w);  // (on the way while the tokens arrive)
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    real[r] = (uint64_t)row[r] < (uint64_t)g.a_rows;  // a token that does not exist counts as zeros
+    if (!real[r]) row[r] = 0;
+    pa[r] = g.a + row[r] * g.K + 16 * h;
+    psa[r] = g.sa + row[r] * g.kb;
+  }
+  load_a(w);
 
   f32x4_v acc[RT][FN];
 #pragma unroll
@@ -616,28 +680,9 @@ k_fp8_thin(Args g) {
 #pragma unroll
     for (int i = 0; i < FN; ++i) acc[r][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
   for (int k0 = w; k0 < g.kb; k0 += 4 * UNR) {
-    // All loads first, none of them under a condition: past the reduction they
-    // read its first codes, and both sides' become zeros afterwards.
-    uint4 ra[UNR][RT][2], rb[UNR][FN][2];
-    float sa[UNR][RT], sb[UNR];
-    bool in[UNR][2];
-#pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-      const int k = k0 + 4 * u;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int at = k * 128 + 64 * c;  // this lane's chunk: 16 h further on
-        in[u][c] = at + 16 * h < g.K;
-        const int from = in[u][c] ? at : -16 * h;
-#pragma unroll
-        for (int i = 0; i < FN; ++i) rb[u][i][c] = *reinterpret_cast<const uint4*>(pb[i] + from);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) ra[u][r][c] = *reinterpret_cast<const uint4*>(pa[r] + from);
-      }
-      const int ks = min(k, g.kb - 1);
-      sb[u] = psb[(int64_t)ks * g.sb_k];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) sa[u][r] = psa[r][ks];
+    if (k0 > w) {
+      load_b(k0);
+      load_a(k0);
     }
     __builtin_amdgcn_sched_barrier(0);
     const bool whole = (k0 + 4 * (UNR - 1) + 1) * 128 <= g.K;
@@ -647,7 +692,7 @@ k_fp8_thin(Args g) {
         const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if (!in[u][c]) {
+          if ((k0 + 4 * u) * 128 + 64 * c + 16 * h >= g.K) {
 #pragma unroll
             for (int i = 0; i < FN; ++i) rb[u][i][c] = z;
 #pragma unroll
@@ -689,7 +734,7 @@ k_fp8_thin(Args g) {
   for (int r = 0; r < RT; ++r) {
     const int m = 16 * r + p;
     if (m >= rows) continue;
-    O* row = reinterpret_cast<O*>(g.c) + ((int64_t)row0 + m) * g.N;
+    O* out = reinterpret_cast<O*>(g.c) + ((int64_t)row0 + m) * g.N;
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
       f32x4_v v = acc[r][i];
@@ -697,8 +742,8 @@ k_fp8_thin(Args g) {
       for (int x = 0; x < 3; ++x) v += *reinterpret_cast<const f32x4_v*>(part[x][r][i][lane]);
       const int c = n0 + 16 * i + 4 * h;
       if (c >= g.N) continue;
-      if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(row + c) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
-      else *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
+      if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(out + c) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
+      else *reinterpret_cast<float4*>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
     }
   }
 }
