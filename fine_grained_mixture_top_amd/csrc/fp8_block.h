@@ -32,9 +32,10 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 // 16-byte accesses that a cache does not keep.  The result of a call that moves
 // more than the memory-side cache holds is not there any more when its reader
-// comes, and written past the caches it takes less: 262144 rows of SwiGLU with
-// n = 256 (337 MB) 60.9 -> 51.6 us, 262144 permuted rows of 1536 bf16 values
-// (905 MB) 192 -> 170 us.  Below that size a result stays where it is read next.
+// comes, and written past the caches it takes less.  With inputs that are not
+// in the caches either: combination gradient, 1.1 GB, 220 -> 201 us; weights,
+// 0.54 GB, 106 -> 102; permutation, 0.9 GB, 189 -> 185; SwiGLU, 0.34 GB, 64 -> 62.
+// Below that size a result stays where it is read next.
 typedef uint32_t u32x4_m __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void store_stream(uint4* p, uint4 v) {
   __builtin_nontemporal_store(u32x4_m{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4_m*>(p));
@@ -78,20 +79,44 @@ __device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
   }
 }
 
+// (two or four stores with gaps between the lanes: through the caches, which
+// put the lines together)
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&v)[16], bool stream) {
-  uint4* o = reinterpret_cast<uint4*>(p);
+__device__ __forceinline__ void store16(T* p, const float (&v)[16]) {
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      store_as(o + h, make_uint4(f2bf2(v[8 * h], v[8 * h + 1]), f2bf2(v[8 * h + 2], v[8 * h + 3]),
-                                 f2bf2(v[8 * h + 4], v[8 * h + 5]), f2bf2(v[8 * h + 6], v[8 * h + 7])), stream);
+      reinterpret_cast<uint4*>(p)[h] = make_uint4(f2bf2(v[8 * h], v[8 * h + 1]), f2bf2(v[8 * h + 2], v[8 * h + 3]),
+                                                  f2bf2(v[8 * h + 4], v[8 * h + 5]), f2bf2(v[8 * h + 6], v[8 * h + 7]));
   } else {
 #pragma unroll
     for (int h = 0; h < 4; ++h)
-      store_as(o + h, make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
-                                 __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])), stream);
+      reinterpret_cast<float4*>(p)[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
   }
+}
+
+// 16 bytes as fp32 values and back
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4 u, float (&v)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float (&v)[16 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 2)
+    return make_uint4(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]), f2bf2(v[4], v[5]), f2bf2(v[6], v[7]));
+  else
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
 
 // Eight lanes hold a block of 128 values, 16 each (zeros past the row's end):

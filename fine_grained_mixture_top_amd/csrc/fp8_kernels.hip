@@ -92,35 +92,38 @@ k_swiglu_fp8(const T* __restrict__ h, int64_t R, int n, RowFilter rows, bool str
     if (!on) continue;
     if (col < n) {
       store_as(reinterpret_cast<uint4*>(q + r * n + col), code, stream);
-      if (a) store16(a + r * n + col, v, stream);
+      if (a) store16(a + r * n + col, v);
     }
     if ((threadIdx.x & 7) == 0) s[b] = sc;
   }
 }
 
-// dh = (da U s (1 + G (1 - s)), da silu(G)), s = sigmoid(G); 16 columns per thread
+// dh = (da U s (1 + G (1 - s)), da silu(G)), s = sigmoid(G); 16 bytes of each
+// matrix per thread, so that every store instruction writes whole lines (32
+// bytes in two stores, past the caches: 3.2 instead of 5.4 TB/s)
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_swiglu_bwd_rows(const T* __restrict__ da, const T* __restrict__ h, int64_t R, int n, RowFilter rows, bool stream,
                   T* __restrict__ dh) {
-  const int per = n / 16;
+  constexpr int V = 16 / (int)sizeof(T);
+  const int per = n / V;
   const int64_t total = R * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i >> 32 ? i / per : (int64_t)((uint32_t)i / (uint32_t)per);
-    const int col = (int)(i - r * per) * 16;
+    const int64_t r = total >> 32 ? i / per : (int64_t)((uint32_t)i / (uint32_t)per);
+    const int col = (int)(i - r * per) * V;
     if (!rows(r)) continue;
-    float d[16], g[16], u[16];
-    load16(da + r * n + col, d);
-    load16(h + r * 2 * n + col, g);
-    load16(h + r * 2 * n + n + col, u);
+    float d[V], g[V], u[V];
+    unpack16<T>(*reinterpret_cast<const uint4*>(da + r * n + col), d);
+    unpack16<T>(*reinterpret_cast<const uint4*>(h + r * 2 * n + col), g);
+    unpack16<T>(*reinterpret_cast<const uint4*>(h + r * 2 * n + n + col), u);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < V; ++j) {
       const float sg = sigmoid_(g[j]), dj = d[j];
       d[j] = dj * u[j] * sg * (1.f + g[j] * (1.f - sg));
       u[j] = dj * g[j] * sg;
     }
-    store16(dh + r * 2 * n + col, d, stream);
-    store16(dh + r * 2 * n + n + col, u, stream);
+    store_as(reinterpret_cast<uint4*>(dh + r * 2 * n + col), pack16<T>(d), stream);
+    store_as(reinterpret_cast<uint4*>(dh + r * 2 * n + n + col), pack16<T>(u), stream);
   }
 }
 
@@ -375,7 +378,7 @@ hipError_t launch_swiglu_fp8(const PlanArgs& p, int dtype, int64_t R, int n, con
 
 hipError_t launch_swiglu_bwd_rows(const PlanArgs& p, int dtype, int64_t R, int n, const void* da, const void* h,
                                   void* dh, hipStream_t st) {
-  const dim3 grid(grid_for(R * (n / 16)));
+  const dim3 grid(grid_for(R * (n / (16 / bytes_of(dtype)))));
   const bool stream = streams(R * n * 5 * bytes_of(dtype));
   if (dtype == MOE_BF16)
     hipLaunchKernelGGL(k_swiglu_bwd_rows<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)da, (const bf16_t*)h, R, n,

@@ -256,29 +256,6 @@ k_permute_fp8(const T* __restrict__ x, const int32_t* __restrict__ slot_row, int
 
 template <typename T> constexpr int VEC = 16 / (int)sizeof(T);
 
-template <typename T>
-__device__ __forceinline__ void unpack16(const uint4 u, float (&v)[16 / sizeof(T)]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 pack16(const float (&v)[16 / sizeof(T)]) {
-  if constexpr (sizeof(T) == 2)
-    return make_uint4(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]), f2bf2(v[4], v[5]), f2bf2(v[6], v[7]));
-  else
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-}
-
 constexpr int ROWS_UNR = 8;  // rows of a token in flight
 
 // o[t] = sum over k of w[t,k] y[slot_row[t,k]] in ascending k (w null: ones)
