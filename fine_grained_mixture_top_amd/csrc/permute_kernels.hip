@@ -6,9 +6,14 @@
 // and each of the three terms is an integer count, so the result does not
 // depend on the order in which workgroups run.
 //
-// Moving rows: bandwidth is all there is.  The permutation walks tokens, not
-// rows: a token's row is read once and written to its K places.  The way back
-// walks tokens too, with the K rows' loads in flight together.
+// Moving rows: bandwidth is all there is (device copy of 1 GiB: 5.2 TB/s).  The
+// permutation walks tokens, not rows: a token's row is read once and written to
+// its K places, where a walk over rows would read it K times.  The way back
+// walks tokens too, with the K rows' loads in flight together.  At T = 16384,
+// K = 8, d = 2048, bf16: permute 106 us (5.7 TB/s), to 8 bits 54 us (6.3),
+// weighted sum 115 us (5.3), its two gradients 212 us (5.4).  Few tokens are
+// bound by launch and latency: a token's row is split over waves then (T = 1,
+// d = 7168: 2.7 us; weighted sum of T = 8: 3.3 us).
 #include <algorithm>
 
 #include "device_common.h"
@@ -37,7 +42,10 @@ __device__ __forceinline__ void wave_rank(int key, int bits, int lane, int& rank
   count = __popcll(same);
 }
 
-// Choices per expert and chunk of `chunk` slots: cnt [chunks][E]
+// Choices per expert and chunk of `chunk` slots: cnt [chunks][E].  Two launches
+// (this and k_sort_place) take 13 us for 262144 choices of 128 experts, 7 for
+// 16396; both are chains of latencies, not bandwidth.  Counting all choices
+// again in every workgroup instead of this launch takes 14.5 us for 16396.
 __global__ void __launch_bounds__(SORT_NT)
 k_sort_count(const int32_t* __restrict__ idx, int slots, int E, int chunk, int32_t* __restrict__ cnt) {
   __shared__ int h[SORT_MAX_E];
@@ -76,7 +84,8 @@ __device__ __forceinline__ int waves_before(const int (*wcount)[SORT_MAX_E], int
 }
 
 // Up to 1024 choices (one per thread) and experts: one workgroup, each choice
-// read once.  Launched with at least E threads.
+// read once.  Launched with at least E threads.  2.8 us for 8 choices of 256
+// experts, a launch and four barriers.
 __global__ void __launch_bounds__(SORT_NT)
 k_sort_small(const int32_t* __restrict__ idx, int slots, int K, int E, int align, int32_t* __restrict__ offsets,
              int32_t* __restrict__ counts, int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row) {

@@ -15,7 +15,7 @@
  * launched, the status codes and element types of moe.h, results bit-identical
  * from run to run.  The current device must be the one the buffers and the
  * stream belong to.  Calls share no state: two calls may overlap when neither
- * writes what the other one uses.
+ * writes what the other one uses.  An output overlaps no input of its call.
  *
  * E4M3 blocks.  Codes are OCP FP8 E4M3 bytes (largest value 448, no infinity).
  * A block of 128 values has one fp32 scale
@@ -150,8 +150,12 @@ int moe_fp8_quant_cols(const moe_plan_desc* desc, const moe_plan* plan, int dtyp
 /*
  * Product of E4M3 operands with a scale per block of 128 along the reduction:
  *     c[r,j] = sum over blocks B of  sa[r,B] * sb[e,B,j/128] * sum_{i in B} a[r,i] b[e,j,i]
- * for the rows r of expert e's segment; the inner sums and the sum over blocks
- * run in fp32.
+ * for the rows r of expert e's segment.  Precision: with an fp32 result every
+ * product is exact and all sums run in fp32.  With a bf16 result the 8-bit matrix
+ * cores may form the inner sums; they add eight neighbouring products at a time
+ * and cut those off 13 bits below the largest one's leading power of two (about
+ * 1.4e-5 of the result, its rounding to bf16 being 1.7e-3); all further sums run
+ * in fp32.
  *   a  [a_rows, K] codes, sa [a_rows, ceil(K/128)]
  *   b  [E, N, K] codes (the reduction contiguous), sb [E, ceil(K/128), ceil(N/128)]
  *      (or out-major, MOE_MM_SB_OUT_MAJOR)
@@ -186,7 +190,8 @@ int moe_fp8_mm(const moe_mm_desc* desc, const void* a, const float* sa, const vo
  *     dw[e,i,j] = sum_B sa[B,i] * sb[B,j] * sum_{r in B} a[B,i,r] b[B,j,r]
  *   a [cap/128, M, 128], sa [cap/128, M] and b [cap/128, N, 128], sb [cap/128, N]
  *   from moe_fp8_quant_cols with this plan; dw [E,M,N] (dtype `out`), zeros for
- *   an expert without rows.  M and N multiples of 16 and at most 2^20.
+ *   an expert without rows.  M and N multiples of 16 and at most 2^20.  Precision
+ *   as in moe_fp8_mm.
  */
 int moe_fp8_wgrad(const moe_plan_desc* desc, const moe_plan* plan, int M, int N, int out, const void* a,
                   const float* sa, const void* b, const float* sb, void* dw, void* stream);

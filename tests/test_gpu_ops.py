@@ -749,6 +749,96 @@ def test_layer_captured():
             assert torch.equal(a, b)
 
 
+def test_two_layers_at_once():
+    """Two layers on two streams, several rounds without waiting, give what each gives alone."""
+    cases = [layer_case(T=600, seed=41), layer_case(T=350, seed=42, drop=0.3)]
+    layers = [Experts(c[0].shape[0], 3, 8, 512, 256, c[2], c[3]) for c in cases]
+    refs = []
+    for L, (x, do, _, _, idx, w) in zip(layers, cases):
+        L.forward(x, idx, w)
+        L.backward(x, w, do)
+        refs.append([t.clone() for t in L.results()])
+        for t in L.results():
+            t.fill_(POISON)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for L, (x, do, _, _, idx, w), st in zip(layers, cases, streams):
+            with torch.cuda.stream(st):
+                L.forward(x, idx, w)
+                L.backward(x, w, do)
+    torch.cuda.synchronize()
+    for L, ref in zip(layers, refs):
+        for a, b in zip(L.results(), ref):
+            assert torch.equal(a, b)
+
+
+def test_rows_past_32_bits():
+    """Row buffers of several GiB: bytes and elements behind 2^31 (and 2^32) are reached like the first ones."""
+    T, K, E, d = 180000, 8, 8, 2048
+    g = gen(77)
+    idx = choices(g, T, K, E)
+    p = sorted_plan(idx, E, 128)
+    x = randn(g, T, d)
+    slots = p.slot_row.long()
+    rows = torch.cat([torch.randint(0, T * K, (150,), generator=g, device="cuda"),
+                      torch.topk(slots.view(-1), 150).indices])           # slots, the farthest rows among them
+    t, r = rows // K, slots.view(-1)[rows]
+    assert int(r.max()) * d > 2 ** 31
+    xp = torch.empty(p.cap, d, dtype=torch.bfloat16, device="cuda")
+    ops.moe_permute(p, x, xp)
+    assert torch.equal(xp[r], x[t])
+    q, s = torch.empty(p.cap, d, dtype=torch.uint8, device="cuda"), torch.empty(p.cap, d // 128, device="cuda")
+    ops.moe_permute_fp8(p, x, q, s)
+    rq, rs = R.quant_rows_ref(x[t])
+    assert torch.equal(R.decode(q[r]), R.decode(rq)) and torch.equal(s[r], rs)
+    q2, s2 = torch.empty_like(q), torch.empty_like(s)
+    ops.moe_fp8_quant_rows(xp, q2, s2, plan=p)
+    assert torch.equal(q2[r], q[r]) and torch.equal(s2[r], s[r])
+    del q2, s2
+
+    N = 1040
+    b, sb = codes(g, E, N, d), torch.rand(E, d // 128, ops.blocks(N), generator=g, device="cuda") + 0.1
+    c = torch.full((p.cap, N), POISON, dtype=torch.bfloat16, device="cuda")
+    ops.moe_fp8_mm(p, q, s, b, sb, c)
+    e = idx.view(-1)[rows].long()
+    for i in range(E):
+        m = e == i
+        av, wv = R.values(q[r[m]], s[r[m]]), weights_ref(b[i], sb[i])
+        ref = av @ wv
+        R.within(c[r[m]], ref, R.mm_bound(av.abs(), wv.abs(), d, ref, torch.bfloat16), f"expert {i}")
+
+    w = torch.rand(T, K, generator=g, device="cuda")
+    o = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    ops.moe_unpermute(p, xp, w, o)
+    ref = (w[t].double().sum(1))[:, None] * x[t].double()
+    R.within(o[t], ref, (K + 1) * 2.0 ** -23 * ref.abs() + 2.0 ** -8 * ref.abs() * 1.01, "o")
+    dw = torch.empty(T, K, device="cuda")
+    dyp = torch.empty_like(xp)
+    ops.moe_unpermute_bwd(p, x, xp, w, dyp, dw)
+    dots = x[t].double().square().sum(1)
+    R.within(dw[t, 0], dots, (d + 9) * 2.0 ** -24 * dots * 1.001, "dw")
+    assert torch.equal(dyp[r], (w.view(-1)[rows, None] * x[t].float()).bfloat16())
+    del dyp
+
+    # the last expert's weight gradient, a few of its values
+    (cq, cs), (yq, ys) = ops.column_buffers(p, d), ops.column_buffers(p, 16)
+    assert cq.numel() > 2 ** 31
+    dy = randn(g, p.cap, 16)
+    ops.moe_fp8_quant_cols(p, x, cq, cs, gather=True)
+    ops.moe_fp8_quant_cols(p, dy, yq, ys)
+    gw = torch.empty(E, d, 16, device="cuda")
+    ops.moe_fp8_wgrad(p, cq, cs, yq, ys, gw)
+    b0, n = int(p.offsets[E - 1]) // 128, int(p.counts[E - 1])
+    nb = -(-n // 128)
+    cols = torch.tensor([0, 700, d - 1], device="cuda")
+    xv = R.decode(cq[b0:b0 + nb][:, cols]) * cs[b0:b0 + nb][:, cols].double()[..., None]
+    yv = R.decode(yq[b0:b0 + nb]) * ys[b0:b0 + nb].double()[..., None]
+    xv, yv = xv.transpose(0, 1).reshape(3, -1), yv.transpose(0, 1).reshape(16, -1)
+    ref, mag = xv @ yv.t(), xv.abs() @ yv.abs().t()
+    R.within(gw[E - 1][cols], ref, R.mm_steps(128 * nb, 3, torch.float32) * mag + 2.0 ** -24 * ref.abs() * 1.001, "dw")
+
+
 def test_profile_names_the_launches():
     p = ops.Plan(64, 2, 8)
     prof = B.Profiler(8)
