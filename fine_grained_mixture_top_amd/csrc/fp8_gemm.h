@@ -22,7 +22,7 @@
 //    a, gathered or not, and rows of b) or a column's block of 128 rows
 //    (moe_fp8_wgrad).  A stage goes straight into LDS, 16 bytes per lane.  Two
 //    stage buffers: a stage's fragments are all in registers before its last
-//    two row pieces are multiplied, so the one barrier of a stage stands there, the
+//    two row pieces are multiplied, so the barrier of a stage stands there, the
 //    stage after next starts loading into the same buffer, and the next
 //    stage's fragments are read beside those pieces' matrix instructions.
 //  * The N-side operand is the MFMA's first: lane l then holds, for the row
@@ -334,22 +334,34 @@ k_fp8_gemm(Args g) {
       }
     }
   };
-  // The loads of a stage come in PARTS: every wave's load instructions in one
-  // burst would keep the matrix cores waiting for their issue.  part 0 starts
-  // the cursor's stage in buffer `par`, the last one moves the cursor on.  On
-  // entry lq is the cursor's tile (lk == 0: not set up yet) or, for lk > 0, the
-  // next one.
+  // A stage's loads.  begin starts the cursor's stage in buffer `par`: on entry lq
+  // is the cursor's tile (lk == 0: not set up yet) or, for lk > 0, the next one.
+  // The loads then come in PARTS, since every wave's load instructions in one
+  // burst would keep the matrix cores waiting for their issue; the last part
+  // moves the cursor on.
+  //   EARLY: the columns' codes of a stage are all in registers when it starts, so
+  // after a second barrier there, begin loads the stage after next's into their
+  // place, and only the rows' codes wait for the stage's end.  It pays for the
+  // weight gradient (65536 rows, E = 64, 2048 x 1024, with both quantizers 360 -> 335
+  // us), not for the row product (262144 rows 1.22 -> 1.21 ms, dense 8192^3 590 ->
+  // 600 us).
+  constexpr bool EARLY = WG;  // (never with gathered rows: begin's tokens would have to be waited for too)
   constexpr int PARTS = FN;
   int lnk = 0;
-  auto load_part = [&](int part, int par) {
-    if (lt < 0) return;
-    if (part == 0 && lk == 0) {
+  auto load_cols = [&](int i, int par, uint32_t k0, bool tail) {
+    const __amdgpu_buffer_rsrc_t rb = rsrc(uniform_ptr(pb), (uint32_t)uniform((int)nb));
+    load16_lds(rb, smem + par * C::STAGE + BM * 128 + (C::IB * w + i) * 1024,
+               !tail || chb(i) < (uint32_t)g.K - k0 ? ob[i] : OOB, k0);
+  };
+  auto begin = [&](int par) -> bool {
+    if (lt < 0) return false;
+    if (lk == 0) {
       // the next tile with stages (a weight gradient may have none)
       while (WG && lq.nk == 0) {
         lt += G;
         if (lt >= total) {
           lt = -1;
-          return;
+          return false;
         }
         lq = tile_at(lt, lq.e);
       }
@@ -361,30 +373,40 @@ k_fp8_gemm(Args g) {
         fetch_tokens(lq);
       }
     }
+    if constexpr (EARLY) {
+#pragma unroll
+      for (int i = 0; i < C::IB; ++i) load_cols(i, par, 0u, false);
+    }
+    return true;
+  };
+  auto load_part = [&](int part, int par) {
+    if (lt < 0) return;
     char* st = smem + par * C::STAGE;
     // (a descriptor shared by the parts would travel through vector registers)
-    const char *ua = uniform_ptr(pa), *ub = uniform_ptr(pb);
-    const __amdgpu_buffer_rsrc_t ra = rsrc(ua, (uint32_t)uniform((int)na)), rb = rsrc(ub, (uint32_t)uniform((int)nb));
+    const __amdgpu_buffer_rsrc_t ra = rsrc(uniform_ptr(pa), (uint32_t)uniform((int)na));
     const uint32_t k0 = WG ? 0u : (uint32_t)lk * 128u;
     // a shorter last block: its missing codes are zeros on both sides
     const bool tail = !WG && k0 + 128u > (uint32_t)g.K;
-    const uint32_t end = (uint32_t)g.K - k0;
+    constexpr int L = C::IA + (EARLY ? 0 : C::IB);
 #pragma unroll
     for (int i = 0; i < C::IA; ++i)
-      if (part == i * PARTS / (C::IA + C::IB))
-        load16_lds(ra, st + (C::IA * w + i) * 1024, !tail || cha < end ? oa[i] : OOB, k0);
+      if (part == i * PARTS / L)
+        load16_lds(ra, st + (C::IA * w + i) * 1024, !tail || cha < (uint32_t)g.K - k0 ? oa[i] : OOB, k0);
+    if constexpr (!EARLY) {
 #pragma unroll
-    for (int i = 0; i < C::IB; ++i)
-      if (part == (C::IA + i) * PARTS / (C::IA + C::IB))
-        load16_lds(rb, st + BM * 128 + (C::IB * w + i) * 1024, !tail || chb(i) < end ? ob[i] : OOB, k0);
+      for (int i = 0; i < C::IB; ++i)
+        if (part == (C::IA + i) * PARTS / L) load_cols(i, par, k0, tail);
+    }
     if (part != PARTS - 1) return;
+    auto rsa = [&] { return rsrc(uniform_ptr(psa), (uint32_t)uniform((int)nsa)); };
+    auto rsb = [&] { return rsrc(uniform_ptr(psb), (uint32_t)uniform((int)nsb)); };
     if constexpr (WG) {
-      if (w < BM / 64) load4_lds(rsrc(uniform_ptr(psa), (uint32_t)uniform((int)nsa)), st + C::SA_OFF + w * 256, os, 0);
-      else if (w < BM / 64 + BN / 64) load4_lds(rsrc(uniform_ptr(psb), (uint32_t)uniform((int)nsb)), st + C::SB_OFF + (w - BM / 64) * 256, os, 0);
+      if (w < BM / 64) load4_lds(rsa(), st + C::SA_OFF + w * 256, os, 0);
+      else if (w < BM / 64 + BN / 64) load4_lds(rsb(), st + C::SB_OFF + (w - BM / 64) * 256, os, 0);
       pa += na; pb += nb; psa += nsa; psb += nsb;  // the next block's
     } else {
-      if (w < BM / 64) load4_lds(rsrc(uniform_ptr(psa), (uint32_t)uniform((int)nsa)), st + C::SA_OFF + w * 256, os, (uint32_t)lk * 4u);
-      else if (w == BM / 64) load4_lds(rsrc(uniform_ptr(psb), (uint32_t)uniform((int)nsb)), st + C::SB_OFF, os, (uint32_t)(lk * g.sb_k) * 4u);
+      if (w < BM / 64) load4_lds(rsa(), st + C::SA_OFF + w * 256, os, (uint32_t)lk * 4u);
+      else if (w == BM / 64) load4_lds(rsb(), st + C::SB_OFF, os, (uint32_t)(lk * g.sb_k) * 4u);
     }
     if (++lk == lnk) {
       lk = 0;
@@ -394,6 +416,7 @@ k_fp8_gemm(Args g) {
     lk = uniform(lk);
   };
   auto load_stage = [&](int par) {
+    begin(par);
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) load_part(part, par);
   };
@@ -479,10 +502,15 @@ k_fp8_gemm(Args g) {
       const float sbk = WG ? 1.f : sbn;
       i32x8_v mx;
       float sx = 0.f;
+      bool sent = false;  // begin's loads are under way
 #pragma unroll
       for (int j = 0; j < FM - 2; ++j) {
         const Frag<EX> mf(mr);
         const float sj = sm;
+        if (EARLY && j == 1) {
+          lds_sync();  // every wave has read its columns of this stage
+          sent = begin(par);
+        }
         read_row(j + 1, mr, sm);
         if (j == FM - 3) read_row(FM - 1, mx, sx);
 #pragma unroll
@@ -498,14 +526,22 @@ k_fp8_gemm(Args g) {
       }
       const Frag<EX> m0(mr), m1(mx);
       const float s0 = sm * sbk, s1 = sx * sbk;
-      // this stage is read; the next one is there once everybody's loads are
-      if (stores) wait_vm<STORES>();
-      else wait_vm<0>();
+      // This stage is read; the next one is there once everybody's loads are: all
+      // but begin's and the stores, which are newer.
+      if (sent) {
+        if (stores) wait_vm<STORES + C::IB>();
+        else wait_vm<C::IB>();
+      } else if (stores) {
+        wait_vm<STORES>();
+      } else {
+        wait_vm<0>();
+      }
       stores = false;
       lds_sync();
       other_buffer();
       read_row(0, mr, sm);
       if constexpr (!WG) sbn = *reinterpret_cast<const float*>(smem + sbl);
+      if constexpr (!EARLY) begin(par);
       f32x4_v last;
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
