@@ -1,6 +1,6 @@
 """Build the HIP shared library (libmoe_gfx950.so) in-tree with hipcc.
 
-Each .hip file under csrc/ compiles to an object in ``_build/`` (in parallel),
+Each .hip file under csrc/ and csrc/ops/ compiles to an object in ``_build/`` (in parallel),
 then they link into ``fine_grained_mixture_top_amd/libmoe_gfx950.so``.
 Usage: ``python -m fine_grained_mixture_top_amd.build`` (or ``build()``).
 
@@ -52,7 +52,9 @@ LIB_SAN = os.path.join(PKG, "libmoe_gfx950_san.so")
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
+    """The layer's sources in csrc/ and those of the single operators in csrc/ops/."""
+    return sorted(os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "ops")) for f in os.listdir(d)
+                  if f.endswith(".hip"))
 
 
 def _compile(src: str, sanitize: bool = False) -> str:

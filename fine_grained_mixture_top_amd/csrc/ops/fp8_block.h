@@ -2,7 +2,7 @@
 // by every kernel that writes them.
 #pragma once
 
-#include "device_common.h"
+#include "../device_common.h"
 
 namespace moe {
 

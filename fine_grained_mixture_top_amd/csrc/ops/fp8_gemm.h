@@ -45,7 +45,7 @@
 
 #include <type_traits>
 
-#include "device_common.h"
+#include "../device_common.h"
 #include "ops_launch.h"
 
 namespace moe {

@@ -4,7 +4,7 @@
 
 #include <algorithm>
 
-#include "../../include/moe_ops.h"
+#include "../../../include/moe_ops.h"
 #include "ops_launch.h"
 
 namespace {

@@ -6,7 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "../../include/moe_ops.h"
+#include "../../../include/moe_ops.h"
 
 namespace moe {
 

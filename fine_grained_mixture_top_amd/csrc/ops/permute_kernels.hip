@@ -16,7 +16,7 @@
 // d = 7168: 2.7 us; weighted sum of T = 8: 3.3 us).
 #include <algorithm>
 
-#include "device_common.h"
+#include "../device_common.h"
 #include "fp8_block.h"
 #include "ops_launch.h"
 
