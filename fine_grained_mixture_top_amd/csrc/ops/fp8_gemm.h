@@ -252,7 +252,12 @@ k_fp8_gemm(Args g) {
     Tile q;
     const int mg = (int)((unsigned)t / (unsigned)NT);
     q.n0 = (t - mg * NT) * BN;
-    while (uniform(tprefix[e + 1]) <= mg) ++e;
+    // 64 experts at a time (one by one, at LDS latency each, a first tile behind
+    // 255 experts took 22 us)
+    for (int n = 64; n == 64; e += n) {
+      const int i = e + 1 + lane;
+      n = __popcll(__ballot(i <= g.E && tprefix[min(i, g.E)] <= mg));
+    }
     q.e = e;
     q.m0 = (mg - uniform(tprefix[e])) * BM;
     q.row0 = uniform(seg0[e]) + (WG ? 0 : q.m0);

@@ -64,27 +64,58 @@ hipError_t launch_thin(int out, const f8::Args& a, int64_t used, hipStream_t st)
 
 }  // namespace
 
-// Which kernel, by the rows per expert (avg; the host knows no segment's own).
-// Times in us at E = 64, K = N = 2048 and at E = 128, K = 1536, N = 512:
-//   avg                          4          8          12         16         24         32
-//   bf16, 16 rows, 64 columns    45 / -     47 / 20.5  50 / -     63 / 28    82 / -     - / 41
-//         32 rows, 64 columns    48 / -     50 / 23.8  51 / -     54 / 25    60 / -     - / 34
-//         64 x 128 tiles                                                                - / 28
-//         128 x 128 tiles        52 / -     50 / 29.6  53 / -     53 / 30    54 / -     - / 31
-//   fp32, 16 rows, 64 columns    45 / -     48 / 20.7  52 / -     65 / 28    85 / -     - / 42
-//         32 rows, 64 columns    50 / -     50 / 23.8  53 / -     56 / 25    63 / -     - / 34
-//   avg                          64         128        256        512
-//   bf16, 64 x 128 tiles         71 / -     112 / -    - / 67     295 / -
-//         128 x 128 tiles        64 / -     100 / -    - / 61     225 / -
-//         256 x 256 tiles        69 / -     81 / -     - / 62     193 / -
-//   fp32, 32 rows, 64 columns    (avg 48: 106, avg 64: 127)
-//         64 x 128 tiles         90 / -     145 / -    - / 96     396 / -
-//         128 x 256 tiles        85 / -     152 / -    - / 93     331 / -
-// Below one row per expert 32 columns give twice the workgroups (E = 256,
-// K = 2048, N = 512, 128 rows: 22.9 against 24.3; 8 rows: 6.5 against 9.4).
-// Large tiles need enough of them: 3003 rows, E = 24, K = 720, N = 1040 take
-// 21 (fp32) and 16.4 (bf16) with 64 x 128 tiles, 25 with 128 x 256, 17.5 with
-// 128 x 128.
+// Which kernel for a row product.  The host knows the rows and the experts, not
+// each expert's rows.
+//
+// Thin tiles or 64 x 128 ones: thin tiles have the CUs busy where there are few
+// of the others, and lose with more rows per expert (their codes go through the
+// bf16 matrix cores, and every 16 or 32 rows read the weights again) and with
+// more tiles than the card holds at once.  us, thin / 64 x 128, at E x K x N:
+//   rows per expert              2            8            16           24           32
+//   bf16, 16 x 4096 x 1024       15.0 / 26.5  16.5 / 26.8  18.8 / 27.2  19.9 / 27.6  31.9 / 28.0
+//         60 x 2048 x 1408       28.4 / 37.3  33.5 / 38.1  41.2 / 38.5  44.0 / 38.8
+//         64 x 2048 x 2048       38.1 / 41.5  45.3 / 44.2  56.6 / 43.4  62.0 / 44.4
+//         256 x 1024 x 2048      94.6 / 85.1  124 / 105    161 / 108    178 / 114
+//   fp32, 16 x 4096 x 1024       15.0 / 33.6  16.5 / 33.7  18.9 / 34.1  19.7 / 34.3  31.7 / 34.8
+//         60 x 2048 x 1408       28.4 / 46.6  33.9 / 46.6  41.3 / 47.1  43.9 / 47.9  56.0 / 49.1
+//         256 x 1024 x 2048      94.8 / 95.6  123 / 113    160 / 117    178 / 125
+// Thin tiles of 16 rows and 32, 16 and 64, 32 rows and 64 columns:
+//   rows per expert              1                    4                    12
+//   16 x 4096 x 1024             10.7 / 14.7 / 15.8   16.7 / 16.7 / 18.0   22.3 / 25.1 / 18.4
+//   24 x 720 x 1040              5.9 / 6.1 / 6.6      6.9 / 7.6 / 8.3      7.6 / 7.7 / 8.6
+//   128 x 1536 x 512             14.7 / 17.0 / 20.1   21.7 / 20.7 / 24.6
+//   256 x 2048 x 512             33.3 / 30.7 / 34.2   50.8 / 45.8 / 51.2
+// Returns 0 for none.
+int thin_tiles(const f8::Args& a, int64_t used, bool wide, int64_t cus) {
+  // (their grids, one workgroup per tile, stay below 2^32 threads)
+  if (row_tiles(a, used, 16) * div_up(a.N, 32) >= (1 << 24)) return 0;
+  const int64_t E = a.E, touched = std::min(E, used);
+  const int64_t t = touched * div_up(a.N, 128), t64 = touched * div_up(a.N, 64);
+  const int64_t most = t < cus ? (wide ? 40 : 24) : t < 4 * cus ? (wide ? 12 : 8) : t < 8 * cus ? (wide ? 8 : 3) : (wide ? 2 : 0);
+  if (used > most * E) return 0;
+  if ((t64 < 2 * cus && used <= 8 * E) || (t64 < 8 * cus && used <= E)) return 1;
+  return used <= 10 * E ? 2 : 3;
+}
+
+// The tile that ends first: rounds of tiles over the CUs, times what a stage
+// takes with its CU to itself (one) or beside another workgroup's (two).  us per
+// stage, from 16 x 4096 x 1024 to 128 x 1536 x 512 with 16 to 256 rows per expert:
+//          bf16    64 x 128    128 x 128    256 x 256    fp32    64 x 128    128 x 256
+//   one            0.7         0.9          1.9                  0.9         1.75
+//   two            1.1         1.45         -                    1.4         -
+// Half of an expert's last tile is taken to be empty.  Over ten shapes and 1/2 to
+// 256 rows per expert the choice is 1.5% behind the best one, in the mean; at
+// 32 x 2048 x 1536 with 64 rows 64 x 128, 128 x 128 and 256 x 256 take 35, 28 and
+// 33 us, at 128 x 1536 x 512 with 128 rows 39, 39.5 and 31, at 64 x 2048 x 2048
+// with 512 rows 295, 225 and 193.
+double tiles_time(const f8::Args& a, int64_t used, int64_t cus, int BM, int BN, double one, double two) {
+  const double touched = (double)std::min<int64_t>(a.E, used);
+  const double n = std::max(touched, (double)used / BM + 0.5 * touched) * (double)div_up(a.N, BN);
+  if (two == 0.0) return std::ceil(n / (double)cus) * one;
+  const double rounds = std::floor(n / (2.0 * (double)cus)), rest = n - rounds * 2.0 * (double)cus;
+  return rounds * two + (rest == 0.0 ? 0.0 : rest <= (double)cus ? one : two);
+}
+
 hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) {
   f8::Args a{};
   a.a = m.a; a.sa = m.sa; a.b = m.b; a.sb = m.sb; a.c = m.c;
@@ -96,26 +127,25 @@ hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) 
   const int nbn = (m.N + 127) / 128;
   a.sb_k = m.sb_out_major ? 1 : nbn;
   a.sb_n = m.sb_out_major ? a.kb : 1;
-  const int64_t used = m.rows_used, E = m.E;
+  const int64_t used = m.rows_used;
   const bool wide = m.out == MOE_F32;
-  // (their grids, one workgroup per tile, stay below 2^32 threads)
-  const bool thin = row_tiles(a, used, 16) * div_up(a.N, 32) < (1 << 24);
-  if (thin && used < E) return launch_thin<1, 2, 1>(m.out, a, used, st);
-  if (thin && used <= 12 * E) return launch_thin<1, 4, 1>(m.out, a, used, st);
-  if (thin && used <= (wide ? 40 : 18) * E) return launch_thin<2, 4, 1>(m.out, a, used, st);
-  // tiles of a size, about
-  auto full = [&](int BM, int BN) { return (used / BM + 1) * div_up(m.N, BN); };
+  const int64_t cus = cu_count(device());
+  switch (thin_tiles(a, used, wide, cus)) {
+    case 1: return launch_thin<1, 2, 1>(m.out, a, used, st);
+    case 2: return launch_thin<1, 4, 1>(m.out, a, used, st);
+    case 3: return launch_thin<2, 4, 1>(m.out, a, used, st);
+  }
   auto bound = [&](int BM, int BN) { return row_tiles(a, used, BM) * div_up(m.N, BN); };
-  const int cus = cu_count(device());
+  auto time = [&](int BM, int BN, double one, double two) { return tiles_time(a, used, cus, BM, BN, one, two); };
   if (wide) {
-    if (m.N > 128 && full(128, 256) >= cus) return launch_tiles<128, 256, 2, 4, false, float>(a, bound(128, 256), st);
+    if (time(128, 256, 1.75, 0.0) < time(64, 128, 0.9, 1.4))
+      return launch_tiles<128, 256, 2, 4, false, float>(a, bound(128, 256), st);
     return launch_tiles<64, 128, 1, 4, false, float>(a, bound(64, 128), st);
   }
-  if (used >= 96 * E && m.N > 128 && full(256, 256) >= cus)
-    return launch_tiles<256, 256, 2, 4, false, bf16_t>(a, bound(256, 256), st);
-  if (used < 48 * E || full(128, 128) < cus)
-    return launch_tiles<64, 128, 1, 4, false, bf16_t>(a, bound(64, 128), st);
-  return launch_tiles<128, 128, 2, 2, false, bf16_t>(a, bound(128, 128), st);
+  const double t64 = time(64, 128, 0.7, 1.1), t128 = time(128, 128, 0.9, 1.45), t256 = time(256, 256, 1.9, 0.0);
+  if (t256 < std::min(t64, t128)) return launch_tiles<256, 256, 2, 4, false, bf16_t>(a, bound(256, 256), st);
+  if (t128 < t64) return launch_tiles<128, 128, 2, 2, false, bf16_t>(a, bound(128, 128), st);
+  return launch_tiles<64, 128, 1, 4, false, bf16_t>(a, bound(64, 128), st);
 }
 
 // Weight gradients.  192 x 256 tiles (256 x 256 do not fit the registers: two

@@ -360,6 +360,14 @@ PRODUCTS = [  # T, K choices, E, reduction, columns, align, dropped, type, gathe
     (6007, 2, 40, 384, 1296, 1, 0.2, "bf16", True), (6007, 2, 40, 112, 1296, 1, 0.2, "bf16", True),
     (400, 2, 20, 1040, 2064, 1, 0.0, "bf16", True), (300, 2, 20, 1040, 400, 1, 0.0, "f32", True),
     (150, 1, 10, 528, 272, 1, 0.0, "bf16", False),
+    # many experts with few rows: a workgroup's next tile is many experts further on
+    (128, 4, 256, 400, 144, 1, 0.1, "bf16", True), (128, 4, 256, 272, 144, 1, 0.0, "f32", False),
+    (3200, 2, 160, 400, 656, 1, 0.2, "bf16", True), (3200, 2, 160, 128, 656, 1, 0.2, "bf16", False),
+    (1920, 2, 160, 400, 656, 1, 0.2, "f32", True), (1920, 2, 160, 128, 656, 128, 0.2, "f32", True),
+    (2000, 8, 1000, 144, 272, 1, 0.5, "bf16", True),
+    # the widest tiles, two to a workgroup: one block of the reduction, a ragged one, a short one
+    (7777, 2, 4, 128, 1808, 1, 0.1, "bf16", True), (7777, 2, 4, 272, 1808, 1, 0.1, "bf16", True),
+    (7777, 2, 3, 16, 2000, 128, 0.0, "bf16", False),
 ]
 
 
