@@ -98,22 +98,30 @@ int thin_tiles(const f8::Args& a, int64_t used, bool wide, int64_t cus) {
 }
 
 // The tile that ends first: rounds of tiles over the CUs, times what a stage
-// takes with its CU to itself (one) or beside another workgroup's (two).  us per
-// stage, from 16 x 4096 x 1024 to 128 x 1536 x 512 with 16 to 256 rows per expert:
+// takes with its CU to itself (one) or beside another workgroup's (two), times the
+// stages of the reduction and those that a tile's start and end are worth (ends).
+// Fitted (us) to ten shapes from 16 x 4096 x 1024 to 256 x 512 x 128 with 16 to
+// 256 rows per expert:
 //          bf16    64 x 128    128 x 128    256 x 256    fp32    64 x 128    128 x 256
-//   one            0.7         0.9          1.9                  0.9         1.75
+//   one            0.8         1.1          1.9                  0.7         1.6
 //   two            1.1         1.45         -                    1.4         -
-// Half of an expert's last tile is taken to be empty.  Over ten shapes and 1/2 to
-// 256 rows per expert the choice is 1.5% behind the best one, in the mean; at
-// 32 x 2048 x 1536 with 64 rows 64 x 128, 128 x 128 and 256 x 256 take 35, 28 and
-// 33 us, at 128 x 1536 x 512 with 128 rows 39, 39.5 and 31, at 64 x 2048 x 2048
-// with 512 rows 295, 225 and 193.
-double tiles_time(const f8::Args& a, int64_t used, int64_t cus, int BM, int BN, double one, double two) {
+//   ends           0           1            1                    0           2
+// Half of an expert's last tile is taken to be empty (a lone expert's rows are
+// known).  The choice is 0.7% (bf16) and 0.4% (fp32) behind the best one, in the
+// mean.  At 32 x 2048 x 1536 with 64 rows per expert 64 x 128, 128 x 128 and
+// 256 x 256 take 35, 28 and 33 us, at 128 x 1536 x 512 with 128 rows 39, 39.5 and
+// 31, at 64 x 2048 x 2048 with 512 rows 295, 225 and 193, at 1 x 2048 x 2048 with
+// 2048 rows 20.5, 26 and 35; in fp32 64 x 128 and 128 x 256 take 19.7 and 22.7 us
+// at 24 x 720 x 1040 with 125 rows, 209 and 196 at 64 x 2048 x 2048 with 256.
+double tiles_time(const f8::Args& a, int64_t used, int64_t cus, int BM, int BN, double one, double two, int ends) {
   const double touched = (double)std::min<int64_t>(a.E, used);
-  const double n = std::max(touched, (double)used / BM + 0.5 * touched) * (double)div_up(a.N, BN);
-  if (two == 0.0) return std::ceil(n / (double)cus) * one;
+  const double row_tiles =
+      a.E == 1 ? (double)div_up(used, BM) : std::max(touched, (double)used / BM + 0.5 * touched);
+  const double n = row_tiles * (double)div_up(a.N, BN);
+  const double stages = a.kb + ends;
+  if (two == 0.0) return std::ceil(n / (double)cus) * one * stages;
   const double rounds = std::floor(n / (2.0 * (double)cus)), rest = n - rounds * 2.0 * (double)cus;
-  return rounds * two + (rest == 0.0 ? 0.0 : rest <= (double)cus ? one : two);
+  return (rounds * two + (rest == 0.0 ? 0.0 : rest <= (double)cus ? one : two)) * stages;
 }
 
 hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) {
@@ -136,13 +144,15 @@ hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) 
     case 3: return launch_thin<2, 4, 1>(m.out, a, used, st);
   }
   auto bound = [&](int BM, int BN) { return row_tiles(a, used, BM) * div_up(m.N, BN); };
-  auto time = [&](int BM, int BN, double one, double two) { return tiles_time(a, used, cus, BM, BN, one, two); };
+  auto time = [&](int BM, int BN, double one, double two, int ends) {
+    return tiles_time(a, used, cus, BM, BN, one, two, ends);
+  };
   if (wide) {
-    if (time(128, 256, 1.75, 0.0) < time(64, 128, 0.9, 1.4))
+    if (time(128, 256, 1.6, 0.0, 2) < time(64, 128, 0.7, 1.4, 0))
       return launch_tiles<128, 256, 2, 4, false, float>(a, bound(128, 256), st);
     return launch_tiles<64, 128, 1, 4, false, float>(a, bound(64, 128), st);
   }
-  const double t64 = time(64, 128, 0.7, 1.1), t128 = time(128, 128, 0.9, 1.45), t256 = time(256, 256, 1.9, 0.0);
+  const double t64 = time(64, 128, 0.8, 1.1, 0), t128 = time(128, 128, 1.1, 1.45, 1), t256 = time(256, 256, 1.9, 0.0, 1);
   if (t256 < std::min(t64, t128)) return launch_tiles<256, 256, 2, 4, false, bf16_t>(a, bound(256, 256), st);
   if (t128 < t64) return launch_tiles<128, 128, 2, 2, false, bf16_t>(a, bound(128, 128), st);
   return launch_tiles<64, 128, 1, 4, false, bf16_t>(a, bound(64, 128), st);
@@ -150,9 +160,12 @@ hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) 
 
 // Weight gradients.  192 x 256 tiles (256 x 256 do not fit the registers: two
 // scales per value) read less than 128 x 128 ones, where they waste little at
-// the edges and there is one for every CU: 65536 rows, E = 64, 2048 x 1024
-// 251 against 272 us, 262144 rows, E = 128, 1536 x 512 307 against 332; 3000
-// rows, E = 16, 1040 x 720 19.4 against 16.2.
+// the edges and there is one for every CU; 64 x 128 ones keep more CUs busy.  us,
+// 192 x 256 / 128 x 128 / 64 x 128, at rows, E, M x N:
+//   65536, 64, 2048 x 1024     205 / 233 / 294     3000, 16, 1040 x 720     18.2 / 15.0 / 17.1
+//   262144, 128, 1536 x 512    265 / 299 / 376     8192, 8, 1024 x 1024     23.0 / 20.0 / 22.2
+//   65536, 32, 1408 x 2048     243 / 276 / 351     4096, 32, 768 x 768      19.5 / 19.6 / 19.2
+//   2048, 64, 2048 x 1024      69 / 86 / 91        65536, 8, 512 x 512      99 / 67 / 51
 hipError_t launch_fp8_wgrad(const PlanArgs& p, int M, int N, int out, const uint8_t* qa, const float* sa,
                             const uint8_t* qb, const float* sb, void* dw, hipStream_t st) {
   f8::Args a{};
@@ -163,8 +176,10 @@ hipError_t launch_fp8_wgrad(const PlanArgs& p, int M, int N, int out, const uint
   auto tiles = [&](int BM, int BN) { return a.E * div_up(M, BM) * div_up(N, BN); };
   if (out == MOE_F32) return launch_tiles<128, 64, 2, 2, true, float>(a, tiles(128, 64), st);
   const int64_t covered = div_up(M, 192) * 192 * div_up(N, 256) * 256;
-  if (100 * covered <= 105 * (int64_t)M * N && tiles(192, 256) >= cu_count(device()))
+  const int64_t cus = cu_count(device());
+  if (100 * covered <= 110 * (int64_t)M * N && tiles(192, 256) >= cus)
     return launch_tiles<192, 256, 2, 4, true, bf16_t>(a, tiles(192, 256), st);
+  if (2 * tiles(128, 128) <= cus) return launch_tiles<64, 128, 1, 4, true, bf16_t>(a, tiles(64, 128), st);
   return launch_tiles<128, 128, 2, 2, true, bf16_t>(a, tiles(128, 128), st);
 }
 

@@ -367,7 +367,9 @@ PRODUCTS = [  # T, K choices, E, reduction, columns, align, dropped, type, gathe
     (2000, 8, 1000, 144, 272, 1, 0.5, "bf16", True),
     # the widest tiles, two to a workgroup: one block of the reduction, a ragged one, a short one
     (7777, 2, 4, 128, 1808, 1, 0.1, "bf16", True), (7777, 2, 4, 272, 1808, 1, 0.1, "bf16", True),
-    (7777, 2, 3, 16, 2000, 128, 0.0, "bf16", False),
+    (7777, 2, 3, 16, 2000, 128, 0.0, "bf16", False), (4300, 2, 3, 400, 2320, 1, 0.1, "f32", True),
+    (4300, 2, 3, 400, 2320, 128, 0.0, "f32", False), (7680, 2, 60, 400, 640, 1, 0.1, "bf16", True),
+    (7680, 2, 60, 656, 640, 128, 0.0, "bf16", False),
 ]
 
 
