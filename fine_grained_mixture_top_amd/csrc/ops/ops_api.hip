@@ -233,6 +233,7 @@ int moe_fp8_mm(const moe_mm_desc* desc, const void* a, const float* sa, const vo
   const int64_t line = std::max<int64_t>(desc->K, 4 * ((desc->K + 127) / 128));
   if (gather && (int64_t)desc->a_rows * line >= INT32_MAX) return MOE_ESHAPE;
   if (desc->rows == 0) return MOE_OK;
+  if (desc->a_rows == 0) return MOE_EINVAL;  // rows of no token
   if (plan && (!plan->offsets || !plan->counts || (gather && !plan->row_token))) return MOE_EINVAL;
   if (!a || !sa || !b || !sb || !c) return MOE_EINVAL;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(c, 16) || !aligned(sa, 4) || !aligned(sb, 4)) return MOE_EINVAL;

@@ -128,6 +128,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _call(fn, device, stream, *args):
     """fn(*args, stream) with `device` current; raises on a non-zero status."""
+    if device.type != "cuda":
+        raise ValueError(f"{fn}: the call is on {device}, a GPU is needed")
     index = device.index
     if index is not None and index != torch.cuda.current_device():
         with torch.cuda.device(device):

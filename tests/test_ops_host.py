@@ -162,7 +162,8 @@ def mm(a_rows=8, rows=8, rows_used=0, E=2, K=128, N=128, out=B.MOE_BF16, flags=0
     (dict(rows=-1, a_rows=-1), B.MOE_EINVAL), (dict(rows_used=-1), B.MOE_EINVAL), (dict(rows_used=9), B.MOE_EINVAL), (dict(E=0), B.MOE_EINVAL), (dict(out=3), B.MOE_EDTYPE),
     (dict(K=0), B.MOE_EINVAL), (dict(K=72), B.MOE_ESHAPE), (dict(N=24), B.MOE_ESHAPE),
     (dict(K=(1 << 20) + 16), B.MOE_ESHAPE), (dict(E=1025), B.MOE_ESHAPE), (dict(K=1 << 16, N=1 << 15), B.MOE_ESHAPE),
-    (dict(a_rows=9), B.MOE_EINVAL), (dict(a_rows=1 << 24, K=128, flags=ops.MOE_MM_GATHER), B.MOE_ESHAPE),
+    (dict(a_rows=9), B.MOE_EINVAL), (dict(a_rows=0, flags=ops.MOE_MM_GATHER), B.MOE_EINVAL),
+    (dict(a_rows=1 << 24, K=128, flags=ops.MOE_MM_GATHER), B.MOE_ESHAPE),
 ])
 def test_mm_refused(kw, code):
     assert ops.lib().moe_fp8_mm(ref(mm(**kw)), P, P, P, P, ref(plan()), P, None) == code
@@ -210,6 +211,8 @@ def test_binding_refuses_tensors():
         ops.moe_sort(p, idx[:3])
     with pytest.raises(ValueError, match="contiguous"):
         ops.moe_sort(p, torch.zeros(2, 4, dtype=torch.int32).t())
+    with pytest.raises(ValueError, match="GPU"):
+        ops.moe_sort(p, idx)  # a plan on the host
     with pytest.raises(ValueError, match="GPU"):
         ops.moe_permute(p, torch.zeros(4, 32), torch.zeros(p.cap, 32))
     with pytest.raises(ValueError, match="float16|float32"):
