@@ -32,15 +32,22 @@
 //
 // What it reaches (one MI355X; a library product with one scale for everything:
 // 2910 TFLOP/s at 8192^3): 262144 gathered rows, E = 64, K = N = 2048, bf16 result
-// 1.21 ms, 1810 TFLOP/s; dense 8192^3 587 us, 1870.  Without its loads, stores
-// and sums the same loop runs at 2800 to 3100 (the card lowers its clock to
-// 1.7..2.0 GHz here); of 1.24 ms the loads account for 0.25, the stores for
-// 0.23, the sums for 0.12.  Tried and slower: loads spread over the whole stage
-// (1.40 ms), 128 x 128 tiles (1.57), 256 x 128 (1.69), a tile's stores beside the next
-// tile's first stage (1.26), stores of whole lines after exchanging halves
-// between lanes (1.23), stores past the caches (no change), staggered starts
-// (no change).  Touching the lines of the stage after next into L2: 1.20 here,
-// but 2 to 7% slower on dense products.
+// 1.17..1.21 ms, 1820..1880 TFLOP/s; dense 8192^3 585 us, 1880, 32768 x 2048 x 2048
+// 135 us, 2030.  What bounds it: of a 256 x 256 stage's 4400 cycles a SIMD's matrix
+// instructions take 2048, its two waves' other vector instructions 1540 (the sums
+// 1024 of them), the CU's LDS reads 930 (no bank conflicts); the waves wait for data
+// or the barrier 29% of the time, and the card lowers its clock to 1.7..2.0 GHz.
+// (Larger pieces of a wave, one wave per SIMD, do not fit the registers: the vector
+// units reach the fp32 sums only in the first half of them.)  Without its loads,
+// stores and sums the same loop runs at 2800 to 3100 TFLOP/s; of 1.24 ms the loads
+// accounted for 0.25, the stores for 0.23, the sums for 0.12.
+// Tried and slower: loads spread over the whole stage (1.40 ms), 128 x 128 tiles
+// (1.57), 256 x 128 (1.69), a tile's stores beside the next tile's first stage
+// (1.26), stores of whole lines after exchanging halves between lanes (1.23), stores
+// past the caches (no change), staggered starts (no change), three stage buffers
+// for the 64 x 128 tiles (no change: a lone workgroup's stage is bound by its
+// instructions, not by the loads' latency).  Touching the lines of the stage after
+// next into L2: 1.20 when this took 1.21, but 2 to 7% slower on dense products.
 #pragma once
 
 #include <type_traits>
@@ -606,7 +613,7 @@ k_fp8_gemm(Args g) {
 
 // Row product for segments of few rows (decode): the weights' bytes are all the
 // work, and every touched expert's are read once, straight into registers.  A
-// workgroup takes 16 RT rows of a segment and 32 columns; its four waves split
+// workgroup takes 16 RT rows of a segment and 16 FN columns; its four waves split
 // the reduction's blocks (wave w: blocks w, w + 4, ...), load UNR of theirs at a
 // time, and add up their sums in wave order.  The matrix work is small, so it
 // runs on the bf16 matrix cores whatever the result's type.  Bound by the
