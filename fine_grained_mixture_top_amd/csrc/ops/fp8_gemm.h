@@ -32,22 +32,24 @@
 //
 // What it reaches (one MI355X; a library product with one scale for everything:
 // 2910 TFLOP/s at 8192^3): 262144 gathered rows, E = 64, K = N = 2048, bf16 result
-// 1.17..1.21 ms, 1820..1880 TFLOP/s; dense 8192^3 585 us, 1880, 32768 x 2048 x 2048
-// 135 us, 2030.  What bounds it: of a 256 x 256 stage's 4400 cycles a SIMD's matrix
-// instructions take 2048, its two waves' other vector instructions 1540 (the sums
-// 1024 of them), the CU's LDS reads 930 (no bank conflicts); the waves wait for data
-// or the barrier 29% of the time, and the card lowers its clock to 1.7..2.0 GHz.
-// (Larger pieces of a wave, one wave per SIMD, do not fit the registers: the vector
-// units reach the fp32 sums only in the first half of them.)  Without its loads,
-// stores and sums the same loop runs at 2800 to 3100 TFLOP/s; of 1.24 ms the loads
-// accounted for 0.25, the stores for 0.23, the sums for 0.12.
+// 1.17 ms, 1880 TFLOP/s; dense 8192^3 551 us, 1990, 32768 x 2048 x 2048 128 us, 2140.
+// What bounds it: of a 256 x 256 stage's 4300 cycles a SIMD's matrix instructions
+// take 2048, its two waves' other vector instructions 1300 (the sums 1024 of them;
+// 24 fewer of the others were 4%), the CU's LDS reads 930 (no bank conflicts); the
+// waves wait for data or the barrier 29% of the time, and the card lowers its clock
+// to 1.7..2.0 GHz.  (Larger pieces of a wave, one wave per SIMD, do not fit the
+// registers: the vector units reach the fp32 sums only in the first half of them.)
+// Without its loads, stores and sums the same loop runs at 2800 to 3100 TFLOP/s; of
+// 1.24 ms the loads accounted for 0.25, the stores for 0.23, the sums for 0.12.
 // Tried and slower: loads spread over the whole stage (1.40 ms), 128 x 128 tiles
 // (1.57), 256 x 128 (1.69), a tile's stores beside the next tile's first stage
 // (1.26), stores of whole lines after exchanging halves between lanes (1.23), stores
-// past the caches (no change), staggered starts (no change), three stage buffers
-// for the 64 x 128 tiles (no change: a lone workgroup's stage is bound by its
-// instructions, not by the loads' latency).  Touching the lines of the stage after
-// next into L2: 1.20 when this took 1.21, but 2 to 7% slower on dense products.
+// past the caches (no change), staggered starts (no change), half of a stage's loads
+// beside the next one's first pieces (gathered rows 1.19 -> 1.17, dense products 1 to
+// 2% slower), three stage buffers for the 64 x 128 tiles (no change: a lone
+// workgroup's stage is bound by its instructions, not by the loads' latency).
+// Touching the lines of the stage after next into L2: 1.20 when this took 1.21, but 2
+// to 7% slower on dense products.
 #pragma once
 
 #include <type_traits>
@@ -58,8 +60,13 @@
 namespace moe {
 namespace f8 {
 
+typedef int i32x4_v __attribute__((ext_vector_type(4)));
 typedef int i32x8_v __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void_t;
+typedef const __attribute__((address_space(3))) char* lds_ptr_t;
+template <typename T> __device__ __forceinline__ T lds_ld(lds_ptr_t p) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) T*>(p);
+}
 
 constexpr int MAX_E = 1024;
 constexpr uint32_t OOB = 0x80000000u;  // past every record count
@@ -124,6 +131,9 @@ __device__ __forceinline__ f32x4_v dot(const Frag<true>& a, const Frag<true>& b)
   return d;
 }
 
+__device__ __forceinline__ i32x8_v join(const i32x4_v lo, const i32x4_v hi) {
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
 __device__ __forceinline__ i32x8_v join(const uint4 lo, const uint4 hi) {
   return i32x8_v{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
@@ -138,12 +148,6 @@ __device__ __forceinline__ int key_a(int r) { return r & 7; }
 template <bool WIDE> __device__ __forceinline__ int key_b(int r) { return WIDE ? r & 7 : (r & 3) | ((r >> 1) & 4); }
 template <bool WIDE> __device__ __forceinline__ int column(int i, int p) {
   return WIDE ? 16 * i + p : 32 * (i >> 1) + 8 * (p >> 2) + 4 * (i & 1) + (p & 3);
-}
-
-// this lane's codes of line r: chunks l / 16 and l / 16 + 4
-__device__ __forceinline__ i32x8_v line_codes(const char* op, int r, int key, int lane) {
-  const int h = lane >> 4;
-  return join(lds_ld16(op + r * 128 + (h ^ key) * 16), lds_ld16(op + r * 128 + ((h + 4) ^ key) * 16));
 }
 
 struct Args {
@@ -360,10 +364,9 @@ k_fp8_gemm(Args g) {
   constexpr bool EARLY = WG;  // (never with gathered rows: begin's tokens would have to be waited for too)
   constexpr int PARTS = FN;
   int lnk = 0;
-  auto load_cols = [&](int i, int par, uint32_t k0, bool tail) {
+  auto load_cols = [&](int i, int par, uint32_t k0) {
     const __amdgpu_buffer_rsrc_t rb = rsrc(uniform_ptr(pb), (uint32_t)uniform((int)nb));
-    load16_lds(rb, smem + par * C::STAGE + BM * 128 + (C::IB * w + i) * 1024,
-               !tail || chb(i) < (uint32_t)g.K - k0 ? ob[i] : OOB, k0);
+    load16_lds(rb, smem + par * C::STAGE + BM * 128 + (C::IB * w + i) * 1024, ob[i], k0);
   };
   auto begin = [&](int par) -> bool {
     if (lt < 0) return false;
@@ -387,7 +390,7 @@ k_fp8_gemm(Args g) {
     }
     if constexpr (EARLY) {
 #pragma unroll
-      for (int i = 0; i < C::IB; ++i) load_cols(i, par, 0u, false);
+      for (int i = 0; i < C::IB; ++i) load_cols(i, par, 0u);
     }
     return true;
   };
@@ -397,17 +400,23 @@ k_fp8_gemm(Args g) {
     // (a descriptor shared by the parts would travel through vector registers)
     const __amdgpu_buffer_rsrc_t ra = rsrc(uniform_ptr(pa), (uint32_t)uniform((int)na));
     const uint32_t k0 = WG ? 0u : (uint32_t)lk * 128u;
-    // a shorter last block: its missing codes are zeros on both sides
-    const bool tail = !WG && k0 + 128u > (uint32_t)g.K;
+    // a shorter last block, the tile's last: its missing codes are zeros on both sides
+    if (!WG && part == 0 && k0 + 128u > (uint32_t)g.K) {
+      asm volatile("");  // a branch, not selects in every stage
+#pragma unroll
+      for (int i = 0; i < C::IA; ++i) oa[i] = cha < (uint32_t)g.K - k0 ? oa[i] : OOB;
+#pragma unroll
+      for (int i = 0; i < C::IB; ++i) ob[i] = chb(i) < (uint32_t)g.K - k0 ? ob[i] : OOB;
+    }
     constexpr int L = C::IA + (EARLY ? 0 : C::IB);
 #pragma unroll
     for (int i = 0; i < C::IA; ++i)
       if (part == i * PARTS / L)
-        load16_lds(ra, st + (C::IA * w + i) * 1024, !tail || cha < (uint32_t)g.K - k0 ? oa[i] : OOB, k0);
+        load16_lds(ra, st + (C::IA * w + i) * 1024, oa[i], k0);
     if constexpr (!EARLY) {
 #pragma unroll
       for (int i = 0; i < C::IB; ++i)
-        if (part == (C::IA + i) * PARTS / L) load_cols(i, par, k0, tail);
+        if (part == (C::IA + i) * PARTS / L) load_cols(i, par, k0);
     }
     if (part != PARTS - 1) return;
     auto rsa = [&] { return rsrc(uniform_ptr(psa), (uint32_t)uniform((int)nsa)); };
@@ -439,13 +448,15 @@ k_fp8_gemm(Args g) {
   // soon as its last two instructions are out. ----
   const int la = wm * C::TM + (lane & 15);                 // line of a's piece 0
   const int lb = wn * C::TN + column<EX>(0, lane & 15);    // of b's piece 0
-  // addresses of the two chunks of a line and of the scales, in stage buffer 0
+  // the two chunks of a line and the scales in stage buffer 0 (as LDS pointers: from
+  // offsets the base would be added in every stage)
   auto slot = [&](int c, int key) { return (c ^ key) * 16; };
   const int h = lane >> 4, ka = key_a(lane & 15), kbl = key_b<EX>(column<EX>(0, lane & 15));
-  int al = la * 128 + slot(h, ka), ah = la * 128 + slot(h + 4, ka);
-  int bl = (BM + lb) * 128 + slot(h, kbl), bh = (BM + lb) * 128 + slot(h + 4, kbl);
-  int sal = C::SA_OFF + la * 4;
-  int sbl = C::SB_OFF + (WG ? wn * C::TN + column<EX>(0, 4 * h) : (wn * C::TN) >> 7) * 4;
+  const lds_ptr_t stage = (lds_ptr_t)smem;
+  lds_ptr_t al = stage + la * 128 + slot(h, ka), ah = stage + la * 128 + slot(h + 4, ka);
+  lds_ptr_t bl = stage + (BM + lb) * 128 + slot(h, kbl), bh = stage + (BM + lb) * 128 + slot(h + 4, kbl);
+  lds_ptr_t sal = stage + C::SA_OFF + la * 4;
+  lds_ptr_t sbl = stage + C::SB_OFF + (WG ? wn * C::TN + column<EX>(0, 4 * h) : (wn * C::TN) >> 7) * 4;
   int step = C::STAGE;  // to the other buffer
   auto other_buffer = [&] {
     al += step; ah += step; bl += step; bh += step; sal += step; sbl += step;
@@ -453,11 +464,11 @@ k_fp8_gemm(Args g) {
   };
   i32x8_v nr[FN];   // codes of the next stage's columns
   auto read_cols = [&](int i) {
-    nr[i] = join(lds_ld16(smem + bl + column<EX>(i, 0) * 128), lds_ld16(smem + bh + column<EX>(i, 0) * 128));
+    nr[i] = join(lds_ld<i32x4_v>(bl + column<EX>(i, 0) * 128), lds_ld<i32x4_v>(bh + column<EX>(i, 0) * 128));
   };
   auto read_row = [&](int j, i32x8_v& m, float& sc) {
-    m = join(lds_ld16(smem + al + j * 2048), lds_ld16(smem + ah + j * 2048));
-    sc = *reinterpret_cast<const float*>(smem + sal + j * 64);
+    m = join(lds_ld<i32x4_v>(al + j * 2048), lds_ld<i32x4_v>(ah + j * 2048));
+    sc = lds_ld<float>(sal + j * 64);
   };
 
   const bool gathered = !WG && g.row_token != nullptr;
@@ -480,7 +491,7 @@ k_fp8_gemm(Args g) {
 #pragma unroll
   for (int i = 0; i < FN; ++i) read_cols(i);
   read_row(0, mr, sm);
-  if constexpr (!WG) sbn = *reinterpret_cast<const float*>(smem + sbl);
+  if constexpr (!WG) sbn = lds_ld<float>(sbl);
 
   // A whole tile's stores are issued unconditionally, so their number is known
   // and the wait for the next stage's loads, which are older, can leave them be.
@@ -537,7 +548,7 @@ k_fp8_gemm(Args g) {
           d[i] = dot(nf[i], mf);
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (WG) {
-            if (j == 0) sn[i] = lds_ld_f4(smem + sbl + column<EX>(i, 0) * 4);
+            if (j == 0) sn[i] = lds_ld<f32x4_v>(sbl + column<EX>(i, 0) * 4);
           }
         }
         sp = sj * sbk;
@@ -558,7 +569,7 @@ k_fp8_gemm(Args g) {
       lds_sync();
       other_buffer();
       read_row(0, mr, sm);
-      if constexpr (!WG) sbn = *reinterpret_cast<const float*>(smem + sbl);
+      if constexpr (!WG) sbn = lds_ld<float>(sbl);
       if constexpr (!EARLY) begin(par);
       f32x4_v last;
 #pragma unroll
