@@ -4,7 +4,7 @@
 // MI355X (device copy of 1 GiB: 5.2 TB/s), bf16:
 //   rows      131072 x 2048                  134 us  6.0 TB/s
 //   weights   64 x 2048 x 1024, both layouts 102 us  5.3 TB/s
-//   columns   131072 x 2048                  153 us  5.3 TB/s (gathered: 105 us)
+//   columns   131072 x 2048                  153 us  5.3 TB/s
 //   SwiGLU    262144 x 256                    62 us  5.4 TB/s
 //   its gradient  131072 x 1024              230 us  5.8 TB/s
 #include <algorithm>
@@ -282,7 +282,11 @@ k_quant_weights_128(const T* __restrict__ w, int K, int N, bool stream, uint8_t*
   }
 }
 
-// columns of the segments: one workgroup per block of 128 rows and 128 columns
+// columns of the segments: one workgroup per block of 128 rows and 128 columns.
+// Gathered rows go column block by column block, each on one XCD, whose L2 then
+// holds much of the column block of all tokens for its K readings (131072 tokens,
+// K = 2, C = 2048 323 -> 288 us; 32768, 8, 1536 196 -> 189; 16384, 4, 2048 79 -> 78, with
+// nothing in the caches before); the plan's own rows go as they lie.
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_quant_cols_128(const T* __restrict__ src, int C, int Tn, bool gather, PlanArgs p, bool stream,
@@ -293,24 +297,26 @@ k_quant_cols_128(const T* __restrict__ src, int C, int Tn, bool gather, PlanArgs
   __shared__ __attribute__((aligned(16))) uint8_t tile[128 * TP];
   const int tid = threadIdx.x;
   const int ct = (C + 127) / 128;
-  const int64_t blk = blockIdx.x / ct;
-  const int r0 = (int)(blk * 128), c0 = (int)(blockIdx.x % ct) * 128;
-  if (r0 >= p.offsets[p.E]) return;
+  const int nb = p.cap / 128;
+  const int v = gather ? xcd_virtual_id(blockIdx.x, gridDim.x) : (int)blockIdx.x;
+  const int64_t blk = gather ? v % nb : v / ct;
+  const int r0 = (int)(blk * 128), c0 = (gather ? v / nb : v % ct) * 128;
+  if (c0 >= C || r0 >= p.offsets[p.E]) return;
   const int rk = (tid >> 4) * 8, cn = (tid & 15) * 8;
   int tok[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) tok[i] = p.row_token[r0 + rk + i];
-  V v;
+  V t8;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if ((unsigned)tok[i] < (unsigned)Tn && c0 + cn < C)
-      v.load(i, src + (size_t)(gather ? tok[i] : r0 + rk + i) * C + c0 + cn);
+      t8.load(i, src + (size_t)(gather ? tok[i] : r0 + rk + i) * C + c0 + cn);
     else
-      v.zero(i);
+      t8.zero(i);
   }
   // the columns' magnitudes: over this thread's rows, the wave's, the block's
   typename V::Mag m;
-  v.column_mags(m);
+  t8.column_mags(m);
 #pragma unroll
   for (int j = 0; j < MW; ++j) {
     m[j] = V::larger(m[j], (uint32_t)__shfl_xor((int)m[j], 16, 64));
@@ -334,8 +340,8 @@ k_quant_cols_128(const T* __restrict__ src, int C, int Tn, bool gather, PlanArgs
   uint32_t c[8][2], t[8][2];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    c[i][0] = e4m3x4(v.value(i, 0) * inv[0], v.value(i, 1) * inv[1], v.value(i, 2) * inv[2], v.value(i, 3) * inv[3]);
-    c[i][1] = e4m3x4(v.value(i, 4) * inv[4], v.value(i, 5) * inv[5], v.value(i, 6) * inv[6], v.value(i, 7) * inv[7]);
+    c[i][0] = e4m3x4(t8.value(i, 0) * inv[0], t8.value(i, 1) * inv[1], t8.value(i, 2) * inv[2], t8.value(i, 3) * inv[3]);
+    c[i][1] = e4m3x4(t8.value(i, 4) * inv[4], t8.value(i, 5) * inv[5], t8.value(i, 6) * inv[6], t8.value(i, 7) * inv[7]);
   }
   transpose8(c, t);
 #pragma unroll
@@ -410,8 +416,9 @@ hipError_t launch_quant_weights_128(int dtype, int E, int K, int N, const void* 
 
 hipError_t launch_quant_cols_128(const PlanArgs& p, int dtype, int C, bool gather, const void* src, uint8_t* q,
                                  float* s, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)(p.cap / 128) * ((C + 127) / 128)));
+  dim3 grid((unsigned)((int64_t)(p.cap / 128) * ((C + 127) / 128)));
   if (grid.x == 0) return hipSuccess;
+  if (gather) grid.x = (grid.x + 7) / 8 * 8;  // whole turns over the XCDs
   const bool stream = streams((int64_t)p.cap * C * (bytes_of(dtype) + 1));
   if (dtype == MOE_BF16)
     hipLaunchKernelGGL(k_quant_cols_128<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)src, C, p.T, gather,
