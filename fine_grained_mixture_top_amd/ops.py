@@ -112,18 +112,20 @@ _VALUES = (torch.float32, torch.bfloat16)
 _F32 = (torch.float32,)
 
 
-def _matrix(name, t, dtypes=_VALUES, dims=2):
-    """A GPU tensor of `dims` dimensions to take sizes from."""
-    if isinstance(t, torch.Tensor) and t.dim() == dims and t.dtype in dtypes and t.is_cuda:
-        return t
-    if not isinstance(t, torch.Tensor) or t.dim() != dims or t.dtype not in dtypes:
-        raise ValueError(f"{name}: a {dims}-dimensional tensor of {', '.join(str(d) for d in dtypes)} is needed")
-    raise ValueError(f"{name}: on {t.device}, a GPU tensor is needed")
+def _shape(name, t, dims=2):
+    """The sizes of a tensor of `dims` dimensions (_need checks the rest)."""
+    if isinstance(t, torch.Tensor):
+        s = t.shape
+        if len(s) == dims:
+            return s
+    raise ValueError(f"{name}: a {dims}-dimensional tensor is needed")
 
 
-# the current stream's handle without building a Stream object (2 us a call),
-# where this torch has it
+# the current stream's handle without building a Stream object (2 us a call), and
+# the current device without the check that the GPU is in use (a tensor is on it
+# by then), where this torch has them
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(fn, device, stream, *args):
@@ -131,7 +133,7 @@ def _call(fn, device, stream, *args):
     if device.type != "cuda":
         raise ValueError(f"{fn}: the call is on {device}, a GPU is needed")
     index = device.index
-    if index is not None and index != torch.cuda.current_device():
+    if index is not None and index != _current_device():
         with torch.cuda.device(device):
             return _call(fn, device, stream, *args)
     if stream is None:
@@ -199,7 +201,7 @@ def moe_sort(plan: Plan, expert_idx, stream=None):
 
 def moe_permute(plan: Plan, x, xp, stream=None):
     """xp[slot_row[t, k]] = x[t]."""
-    d = _matrix("x", x).shape[1]
+    d = _shape("x", x)[1]
     px = _need("x", x, _VALUES, (plan.T, d), plan.device)
     pxp = _need("xp", xp, (x.dtype,), (plan.cap, d), plan.device)
     _call("moe_permute", plan.device, stream, plan._d, plan._p, _DTYPE[x.dtype], d, px, pxp)
@@ -207,7 +209,7 @@ def moe_permute(plan: Plan, x, xp, stream=None):
 
 def moe_permute_fp8(plan: Plan, x, q, s, stream=None):
     """The rows of moe_permute as codes q [cap, d] and scales s [cap, ceil(d/128)]."""
-    d = _matrix("x", x).shape[1]
+    d = _shape("x", x)[1]
     px = _need("x", x, _VALUES, (plan.T, d), plan.device)
     pq = _need("q", q, _CODES, (plan.cap, d), plan.device)
     ps = _need("s", s, _F32, (plan.cap, blocks(d)), plan.device)
@@ -216,7 +218,7 @@ def moe_permute_fp8(plan: Plan, x, q, s, stream=None):
 
 def moe_permute_bwd(plan: Plan, dxp, dx, stream=None):
     """dx[t] = sum over k of dxp[slot_row[t, k]]."""
-    d = _matrix("dxp", dxp).shape[1]
+    d = _shape("dxp", dxp)[1]
     pg = _need("dxp", dxp, _VALUES, (plan.cap, d), plan.device)
     px = _need("dx", dx, (dxp.dtype,), (plan.T, d), plan.device)
     _call("moe_permute_bwd", plan.device, stream, plan._d, plan._p, _DTYPE[dxp.dtype], d, pg, px)
@@ -224,7 +226,7 @@ def moe_permute_bwd(plan: Plan, dxp, dx, stream=None):
 
 def moe_unpermute(plan: Plan, y, w, o, stream=None):
     """o[t] = sum over k of w[t, k] y[slot_row[t, k]] (w fp32)."""
-    d = _matrix("y", y).shape[1]
+    d = _shape("y", y)[1]
     py = _need("y", y, _VALUES, (plan.cap, d), plan.device)
     pw = _need("w", w, _F32, (plan.T, plan.K), plan.device)
     po = _need("o", o, (y.dtype,), (plan.T, d), plan.device)
@@ -234,7 +236,7 @@ def moe_unpermute(plan: Plan, y, w, o, stream=None):
 def moe_unpermute_bwd(plan: Plan, d_o, y, w, dy, dw, stream=None):
     """dy[slot_row[t, k]] = w[t, k] d_o[t]; dw[t, k] = <d_o[t], y[slot_row[t, k]]> (0 for a dropped choice).
     dw None: y is not read (may be None); dy None: w is not read."""
-    d = _matrix("d_o", d_o).shape[1]
+    d = _shape("d_o", d_o)[1]
     dt = (d_o.dtype,)
     pdo = _need("d_o", d_o, _VALUES, (plan.T, d), plan.device)
     py = None if y is None else _need("y", y, dt, (plan.cap, d), plan.device)
@@ -248,7 +250,7 @@ def moe_unpermute_bwd(plan: Plan, d_o, y, w, dy, dw, stream=None):
 
 def moe_fp8_quant_rows(src, q, s, plan: Plan = None, stream=None):
     """src [R, C] -> codes q [R, C] and scales s [R, ceil(C/128)]; with a plan (R = plan.cap) its rows only."""
-    R, C = _matrix("src", src).shape
+    R, C = _shape("src", src)
     _plan_rows("src", plan, R, src.device)
     p = _need("src", src, _VALUES, (R, C), src.device)
     pq = _need("q", q, _CODES, (R, C), src.device)
@@ -259,7 +261,7 @@ def moe_fp8_quant_rows(src, q, s, plan: Plan = None, stream=None):
 
 def moe_fp8_quant_weights(w, q, qt, s, stream=None):
     """w [E, K, N] -> codes q [E, K, N] and qt [E, N, K] (either may be None), scales s per 128 x 128 block."""
-    E, K, N = _matrix("w", w, dims=3).shape
+    E, K, N = _shape("w", w, 3)
     if q is None and qt is None:
         raise ValueError("one of q and qt is needed")
     p = _need("w", w, _VALUES, (E, K, N), w.device)
@@ -279,7 +281,7 @@ def column_buffers(plan: Plan, C: int):
 def moe_fp8_quant_cols(plan: Plan, src, q, s, gather: bool = False, stream=None):
     """Blocks of 128 rows per column and segment: src [cap, C], or with gather [T, C] read through row_token;
     q [cap//128, C, 128], s [cap//128, C].  The plan's align is a multiple of 128."""
-    C = _matrix("src", src).shape[1]
+    C = _shape("src", src)[1]
     p = _need("src", src, _VALUES, (plan.T if gather else plan.cap, C), plan.device)
     n = plan.cap // BLOCK
     pq = _need("q", q, _CODES, (n, C, BLOCK), plan.device)
@@ -293,8 +295,8 @@ def moe_fp8_mm(plan, a, sa, b, sb, c, gather: bool = False, sb_out_major: bool =
     a [cap, K] codes (gather: [T, K], row r reads a's row row_token[r]), sa [., ceil(K/128)]; b [E, N, K]
     codes; sb [E, ceil(K/128), ceil(N/128)], or with sb_out_major [E, ceil(N/128), ceil(K/128)]; c [cap, N]
     fp32 or bf16.  plan None: dense, a [R, K], b [N, K] or [1, N, K], c [R, N]."""
-    rows_a, K = _matrix("a", a, _CODES).shape
-    rows, N = _matrix("c", c).shape
+    rows_a, K = _shape("a", a)
+    rows, N = _shape("c", c)
     dev = a.device
     if plan is None:
         if gather:
@@ -320,8 +322,8 @@ def moe_fp8_mm(plan, a, sa, b, sb, c, gather: bool = False, sb_out_major: bool =
 def moe_fp8_wgrad(plan: Plan, a, sa, b, sb, dw, stream=None):
     """dw[e] = sum over expert e's rows of (a sa)^T (b sb): a [cap//128, M, 128], sa [cap//128, M], b and sb
     likewise with N columns, from moe_fp8_quant_cols; dw [E, M, N] fp32 or bf16."""
-    M = _matrix("a", a, _CODES, dims=3).shape[1]
-    N = _matrix("b", b, _CODES, dims=3).shape[1]
+    M = _shape("a", a, 3)[1]
+    N = _shape("b", b, 3)[1]
     n = plan.cap // BLOCK
     pa = _need("a", a, _CODES, (n, M, BLOCK), plan.device)
     psa = _need("sa", sa, _F32, (n, M), plan.device)
@@ -334,7 +336,7 @@ def moe_fp8_wgrad(plan: Plan, a, sa, b, sb, dw, stream=None):
 def moe_swiglu_fp8(h, q, s, a=None, plan: Plan = None, stream=None):
     """A = silu(G) U of h [R, 2n] = [G | U] -> codes q [R, n], scales s [R, ceil(n/128)]; a [R, n] (h's type)
     when given.  With a plan (R = plan.cap) its rows only."""
-    R, n2 = _matrix("h", h).shape
+    R, n2 = _shape("h", h)
     n = n2 // 2
     _plan_rows("h", plan, R, h.device)
     ph = _need("h", h, _VALUES, (R, 2 * n), h.device)
@@ -347,7 +349,7 @@ def moe_swiglu_fp8(h, q, s, a=None, plan: Plan = None, stream=None):
 
 def moe_swiglu_bwd(da, h, dh, plan: Plan = None, stream=None):
     """dh [R, 2n] = (da U s (1 + G (1 - s)), da silu(G)), s = sigmoid(G), from da [R, n] and h [R, 2n]."""
-    R, n2 = _matrix("h", h).shape
+    R, n2 = _shape("h", h)
     n = n2 // 2
     _plan_rows("h", plan, R, h.device)
     ph = _need("h", h, _VALUES, (R, 2 * n), h.device)
