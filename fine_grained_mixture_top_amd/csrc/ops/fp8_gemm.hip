@@ -15,9 +15,12 @@ int device() {
 }
 
 int cu_count(int dev) {
-  int cus = 0;
+  static std::atomic<int> known[64];  // asked for once per device
+  int cus = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (cus > 0) return cus;
   if (dev < 0 || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
     return 256;
+  if (dev < 64) known[dev].store(cus, std::memory_order_relaxed);
   return cus;
 }
 

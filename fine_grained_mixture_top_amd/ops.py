@@ -289,6 +289,20 @@ def moe_fp8_quant_cols(plan: Plan, src, q, s, gather: bool = False, stream=None)
     _call("moe_fp8_quant_cols", plan.device, stream, plan._d, plan._p, _DTYPE[src.dtype], C, int(gather), p, pq, ps)
 
 
+_mm_descs = {}  # (sizes, type, flags) -> descriptor without a profile: building one takes 1.5 us
+
+
+def _mm_desc(profile, *key):
+    if profile:
+        return MoeMmDesc(*key, 0, profile)
+    d = _mm_descs.get(key)
+    if d is None:
+        if len(_mm_descs) >= 1024:
+            _mm_descs.clear()
+        d = _mm_descs[key] = MoeMmDesc(*key, 0, None)
+    return d
+
+
 def moe_fp8_mm(plan, a, sa, b, sb, c, gather: bool = False, sb_out_major: bool = False, stream=None):
     """c[r] = (a sa)[r] (b sb)[e]^T for the rows r of expert e's segment.
 
@@ -301,21 +315,24 @@ def moe_fp8_mm(plan, a, sa, b, sb, c, gather: bool = False, sb_out_major: bool =
     if plan is None:
         if gather:
             raise ValueError("gather needs a plan")
-        E, want = 1, rows
-        b = b.unsqueeze(0) if isinstance(b, torch.Tensor) and b.dim() == 2 else b
-        sb = sb.unsqueeze(0) if isinstance(sb, torch.Tensor) and sb.dim() == 2 else sb
+        E, want, profile = 1, rows, None
     else:
-        E, want = plan.E, plan.T if gather else plan.cap
+        E, want, profile = plan.E, plan.T if gather else plan.cap, plan.desc.profile
         _plan_rows("c", plan, rows, dev)
     kb, nb = blocks(K), blocks(N)
+    shape_b, shape_sb = (N, K), (nb, kb) if sb_out_major else (kb, nb)
+    if plan is not None or (isinstance(b, torch.Tensor) and b.dim() == 3):
+        shape_b = (E, *shape_b)
+    if plan is not None or (isinstance(sb, torch.Tensor) and sb.dim() == 3):
+        shape_sb = (E, *shape_sb)
     pa = _need("a", a, _CODES, (want, K), dev)
     psa = _need("sa", sa, _F32, (want, kb), dev)
-    pb = _need("b", b, _CODES, (E, N, K), dev)
-    psb = _need("sb", sb, _F32, (E, nb, kb) if sb_out_major else (E, kb, nb), dev)
+    pb = _need("b", b, _CODES, shape_b, dev)
+    psb = _need("sb", sb, _F32, shape_sb, dev)
     pc = _need("c", c, _VALUES, (rows, N), dev)
     flags = (MOE_MM_GATHER if gather else 0) | (MOE_MM_SB_OUT_MAJOR if sb_out_major else 0)
     used = 0 if plan is None else plan.T * plan.K
-    d = MoeMmDesc(rows_a, rows, used, E, K, N, _DTYPE[c.dtype], flags, 0, _profile(plan))
+    d = _mm_desc(profile, rows_a, rows, used, E, K, N, _DTYPE[c.dtype], flags)
     _call("moe_fp8_mm", dev, stream, ctypes.byref(d), pa, psa, pb, psb, None if plan is None else plan._p, pc)
 
 
