@@ -13,7 +13,7 @@
 // K = 8, d = 2048, bf16: permute 106 us (5.7 TB/s), to 8 bits 54 us (6.3),
 // weighted sum 115 us (5.3), its two gradients 212 us (5.4).  Few tokens are
 // bound by launch and latency: a token's row is split over waves then (T = 1,
-// d = 7168: 2.7 us; weighted sum of T = 8: 3.3 us).
+// d = 7168: 2.5 us; weighted sum of T = 8: 2.85 us).
 #include <algorithm>
 
 #include "../device_common.h"
@@ -284,19 +284,26 @@ k_unpermute(const uint4* __restrict__ y, const float* __restrict__ wt, const int
   const int t = (int)(w / splits);
   if (t >= Tn) return;
   const int32_t* rows = slot_row + (size_t)t * K;
-  for (int c = (int)(w % splits) * 64 + lane; c < pieces; c += splits * 64) {
+  // (every lane stays to the end, since its choices are read by the others)
+  for (int c0 = (int)(w % splits) * 64; c0 < pieces; c0 += splits * 64) {
+    const int c = min(c0 + lane, pieces - 1);
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     for (int k0 = 0; k0 < K; k0 += ROWS_UNR) {
+      // (lane j reads choice j: from uniform addresses the choices come one by one,
+      // 8 tokens of 8 choices 3.1 us instead of 2.85)
+      const int kj = min(k0 + (lane & (ROWS_UNR - 1)), K - 1);
+      const int row = rows[kj];
+      const float weight = wt ? wt[(size_t)t * K + kj] : 1.f;
       uint4 raw[ROWS_UNR];
       float g[ROWS_UNR];
       bool ok[ROWS_UNR];
 #pragma unroll
       for (int j = 0; j < ROWS_UNR; ++j) {
-        const int r = k0 + j < K ? rows[k0 + j] : -1;
+        const int r = k0 + j < K ? __builtin_amdgcn_readlane(row, j) : -1;
         ok[j] = (unsigned)r < (unsigned)cap;
-        g[j] = wt ? wt[(size_t)t * K + min(k0 + j, K - 1)] : 1.f;
+        g[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), j));
         raw[j] = ok[j] ? load_stream(y + (size_t)r * pieces + c) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
@@ -308,34 +315,38 @@ k_unpermute(const uint4* __restrict__ y, const float* __restrict__ wt, const int
         for (int i = 0; i < V; ++i) acc[i] = fmaf(g[j], v[i], acc[i]);
       }
     }
-    o[(size_t)t * pieces + c] = pack16<T>(acc);
+    if (c0 + lane < pieces) o[(size_t)t * pieces + c] = pack16<T>(acc);
   }
 }
 
 // dy[r] = w[t,k] d_o[t] and dw[t,k] = <d_o[t], y[r]>, r = slot_row[t,k]: one
-// workgroup per token; the dot products end in a fixed tree over lanes and waves
-template <typename T>
-__global__ void __launch_bounds__(256)
+// workgroup of NT threads per token; the dot products end in a fixed order over
+// lanes and waves
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT)
 k_unpermute_bwd(const uint4* __restrict__ d_o, const uint4* __restrict__ y, const float* __restrict__ wt,
                 const int32_t* __restrict__ slot_row, int K, int cap, int pieces, bool stream,
                 uint4* __restrict__ dy, float* __restrict__ dw) {
   constexpr int V = VEC<T>;
   constexpr int KG = ROWS_UNR;
-  __shared__ float part[4][KG];
+  __shared__ float part[NT / 64][KG];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int t = blockIdx.x;
   const int32_t* rows = slot_row + (size_t)t * K;
   for (int k0 = 0; k0 < K; k0 += KG) {
+    const int kj = min(k0 + (lane & (KG - 1)), K - 1);  // (lane j reads choice j, as above)
+    const int row = rows[kj];
+    const float weight = dy ? wt[(size_t)t * K + kj] : 0.f;
     int r[KG];
     float g[KG], dot[KG];
 #pragma unroll
     for (int j = 0; j < KG; ++j) {
-      r[j] = k0 + j < K ? rows[k0 + j] : -1;
+      r[j] = k0 + j < K ? __builtin_amdgcn_readlane(row, j) : -1;
       if ((unsigned)r[j] >= (unsigned)cap) r[j] = -1;
-      g[j] = dy && r[j] >= 0 ? wt[(size_t)t * K + k0 + j] : 0.f;
+      g[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), j));
       dot[j] = 0.f;
     }
-    for (int c = tid; c < pieces; c += 256) {
+    for (int c = tid; c < pieces; c += NT) {
       float a[V];
       unpack16<T>(d_o[(size_t)t * pieces + c], a);
       if (dw) {
@@ -370,12 +381,21 @@ k_unpermute_bwd(const uint4* __restrict__ d_o, const uint4* __restrict__ y, cons
         if (lane == 0) part[wave][j] = s;
       }
       __syncthreads();
-      if (tid < KG && k0 + tid < K)
-        dw[(size_t)t * K + k0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+      if (tid < KG && k0 + tid < K) {
+        float s = 0.f;
+#pragma unroll
+        for (int x = 0; x < NT / 64; x += 4)
+          s += (part[x][tid] + part[x + 1][tid]) + (part[x + 2][tid] + part[x + 3][tid]);
+        dw[(size_t)t * K + k0 + tid] = s;
+      }
       __syncthreads();
     }
   }
 }
+
+// Tokens for which long rows get 1024 threads each instead of 256, 256 / 1024 in us:
+// 8 tokens of K = 8, d = 7168 9.7 / 6.8; 256 of d = 4096 10.1 / 8.7; 512 15.8 / 18.6.
+constexpr int BWD_FEW = 256;
 
 // Waves per token: rows of one token are split until there are about eight
 // waves per SIMD's share of the card, and no finer than one pass of 64 lanes.
@@ -453,13 +473,15 @@ hipError_t launch_unpermute(const PlanArgs& p, int dtype, int d, const void* y, 
 hipError_t launch_unpermute_bwd(const PlanArgs& p, int dtype, int d, const void* d_o, const void* y, const float* w,
                                 void* dy, float* dw, hipStream_t st) {
   const int pieces = (int)((int64_t)d * (dtype == MOE_BF16 ? 2 : 4) / 16);
-  if (dtype == MOE_BF16)
-    hipLaunchKernelGGL(k_unpermute_bwd<bf16_t>, dim3(p.T), dim3(256), 0, st, (const uint4*)d_o, (const uint4*)y, w,
-                       p.slot_row, p.K, p.cap, pieces, streamed(p, (int64_t)pieces * 16), (uint4*)dy, dw);
-  else
-    hipLaunchKernelGGL(k_unpermute_bwd<float>, dim3(p.T), dim3(256), 0, st, (const uint4*)d_o, (const uint4*)y, w,
-                       p.slot_row, p.K, p.cap, pieces, streamed(p, (int64_t)pieces * 16), (uint4*)dy, dw);
-  return hipGetLastError();
+  const bool stream = streamed(p, (int64_t)pieces * 16);
+  auto launch = [&](auto* k, int threads) {
+    hipLaunchKernelGGL(k, dim3(p.T), dim3(threads), 0, st, (const uint4*)d_o, (const uint4*)y, w, p.slot_row, p.K,
+                       p.cap, pieces, stream, (uint4*)dy, dw);
+    return hipGetLastError();
+  };
+  if (p.T <= BWD_FEW && pieces > 256)
+    return dtype == MOE_BF16 ? launch(k_unpermute_bwd<bf16_t, 1024>, 1024) : launch(k_unpermute_bwd<float, 1024>, 1024);
+  return dtype == MOE_BF16 ? launch(k_unpermute_bwd<bf16_t, 256>, 256) : launch(k_unpermute_bwd<float, 256>, 256);
 }
 
 }  // namespace moe

@@ -92,7 +92,8 @@ def test_sort_same_plan_again():
 MOVES = [  # T, K, E, d, align, share dropped, type
     (1, 8, 256, 7168, 1, 0.0, "bf16"), (1, 1, 1, 16, 1, 0.0, "f32"), (33, 3, 7, 48, 16, 0.4, "bf16"),
     (257, 8, 64, 2048, 128, 0.1, "bf16"), (100, 9, 5, 1040, 1, 0.2, "f32"), (4100, 2, 16, 528, 1, 0.0, "bf16"),
-    (19, 40, 8, 272, 3, 0.3, "f32"),
+    (19, 40, 8, 272, 3, 0.3, "f32"), (256, 11, 9, 2576, 1, 0.2, "bf16"), (300, 3, 12, 4112, 16, 0.1, "bf16"),
+    (7, 17, 30, 5008, 1, 0.2, "f32"),
 ]
 
 
