@@ -32,7 +32,7 @@
 //
 // What it reaches (one MI355X; a library product with one scale for everything:
 // 2910 TFLOP/s at 8192^3): 262144 gathered rows, E = 64, K = N = 2048, bf16 result
-// 1.17 ms, 1880 TFLOP/s; dense 8192^3 551 us, 1990, 32768 x 2048 x 2048 128 us, 2140.
+// 1.16 ms, 1900 TFLOP/s; dense 8192^3 551 us, 1990, 32768 x 2048 x 2048 128 us, 2140.
 // What bounds it: of a 256 x 256 stage's 4300 cycles a SIMD's matrix instructions
 // take 2048, its two waves' other vector instructions 1300 (the sums 1024 of them;
 // 24 fewer of the others were 4%), the CU's LDS reads 930 (no bank conflicts); the
@@ -44,10 +44,9 @@
 // Tried and slower: loads spread over the whole stage (1.40 ms), 128 x 128 tiles
 // (1.57), 256 x 128 (1.69), a tile's stores beside the next tile's first stage
 // (1.26), stores of whole lines after exchanging halves between lanes (1.23), stores
-// past the caches (no change), staggered starts (no change), half of a stage's loads
-// beside the next one's first pieces (gathered rows 1.19 -> 1.17, dense products 1 to
-// 2% slower), three stage buffers for the 64 x 128 tiles (no change: a lone
-// workgroup's stage is bound by its instructions, not by the loads' latency).
+// past the caches (no change), staggered starts (no change), three stage buffers
+// for the 64 x 128 tiles (no change: a lone workgroup's stage is bound by its
+// instructions, not by the loads' latency).
 // Touching the lines of the stage after next into L2: 1.20 when this took 1.21, but 2
 // to 7% slower on dense products.
 #pragma once
@@ -196,7 +195,8 @@ struct Tile {
   int e, m0, n0, nk, row0, rows;
 };
 
-template <int BM, int BN, int WM, int WN, bool WG, typename O>
+// LATE: that many of a stage's parts of loads go beside the next stage's first pieces.
+template <int BM, int BN, int WM, int WN, bool WG, typename O, int LATE = 0>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 k_fp8_gemm(Args g) {
   using C = Cfg<BM, BN, WM, WN, WG>;
@@ -362,7 +362,8 @@ k_fp8_gemm(Args g) {
   // us), not for the row product (262144 rows 1.22 -> 1.21 ms, dense 8192^3 590 ->
   // 600 us).
   constexpr bool EARLY = WG;  // (never with gathered rows: begin's tokens would have to be waited for too)
-  constexpr int PARTS = FN;
+  constexpr int PARTS = FN + LATE;
+  static_assert(LATE == 0 || (!EARLY && LATE <= FM - 2), "the parts have pieces to go beside");
   int lnk = 0;
   auto load_cols = [&](int i, int par, uint32_t k0) {
     const __amdgpu_buffer_rsrc_t rb = rsrc(uniform_ptr(pb), (uint32_t)uniform((int)nb));
@@ -503,6 +504,7 @@ k_fp8_gemm(Args g) {
     if (w >= 4) __builtin_amdgcn_s_setprio(1);
   }
   bool stores = false;
+  bool late = false;  // the last begun stage's LATE parts are still to come
   int par = 0;
   Tile q = tile_at(t0, 0);
   for (int t = t0; t < total; t += G) {
@@ -540,6 +542,7 @@ k_fp8_gemm(Args g) {
           lds_sync();  // every wave has read its columns of this stage
           sent = begin(par);
         }
+        if (j < LATE && late) load_part(FN + j, par ^ 1);
         read_row(j + 1, mr, sm);
         if (j == FM - 3) read_row(FM - 1, mx, sx);
 #pragma unroll
@@ -570,7 +573,7 @@ k_fp8_gemm(Args g) {
       other_buffer();
       read_row(0, mr, sm);
       if constexpr (!WG) sbn = lds_ld<float>(sbl);
-      if constexpr (!EARLY) begin(par);
+      if constexpr (!EARLY) late = begin(par);
       f32x4_v last;
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
@@ -587,6 +590,11 @@ k_fp8_gemm(Args g) {
       add(last, s0, FN - 1, FM - 2);
       sp = s1;
       par ^= 1;
+    }
+    if (LATE > 0 && late) {  // before the stores, which the next wait leaves be
+#pragma unroll
+      for (int n = 0; n < LATE; ++n) load_part(FN + n, par ^ 1);
+      late = false;
     }
 #pragma unroll
     for (int i = 0; i < FN; ++i) add(d[i], sp, i, FM - 1);
