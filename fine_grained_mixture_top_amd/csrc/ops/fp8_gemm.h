@@ -753,9 +753,13 @@ k_fp8_thin(Args g) {
   };
   load_b(w);  // (on the way while the tokens arrive)
   __builtin_amdgcn_sched_barrier(0);
+  bool ghosts = false;
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    real[r] = (uint64_t)row[r] < (uint64_t)g.a_rows;  // a token that does not exist counts as zeros
+    // a token that does not exist counts as zeros: in place of its codes, which are
+    // then row 0's and may be NaN, and of their scales
+    real[r] = (uint64_t)row[r] < (uint64_t)g.a_rows;
+    ghosts |= __any(!real[r]);
     if (!real[r]) row[r] = 0;
     pa[r] = g.a + row[r] * g.K + 16 * h;
     psa[r] = g.sa + row[r] * g.kb;
@@ -776,16 +780,17 @@ k_fp8_thin(Args g) {
     const bool whole = (k0 + 4 * (UNR - 1) + 1) * 128 <= g.K;
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
-      if (!whole) {
+      if (!whole || ghosts) {
         const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if ((k0 + 4 * u) * 128 + 64 * c + 16 * h >= g.K) {
+          const bool past = (k0 + 4 * u) * 128 + 64 * c + 16 * h >= g.K;
 #pragma unroll
-            for (int i = 0; i < FN; ++i) rb[u][i][c] = z;
+          for (int i = 0; i < FN; ++i)
+            if (past) rb[u][i][c] = z;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) ra[u][r][c] = z;
-          }
+          for (int r = 0; r < RT; ++r)
+            if (past || !real[r]) ra[u][r][c] = z;
         }
         if (k0 + 4 * u >= g.kb) sb[u] = 0.f;  // (a scale that is not finite would spoil the zeros)
 #pragma unroll

@@ -448,6 +448,39 @@ def test_product_of_a_broken_plan_stays_in_its_buffers():
     assert (c[p.cap:] == POISON).all() and (c[3:5] == 0).all()
 
 
+# One size for every kernel of the product (256 CUs): T, K choices, E, reduction, columns, type, gathered; the
+# reduction ends in a short block, rows and columns inside a tile.
+KERNELS = {
+    "16 rows x 32": (12, 2, 4, 400, 272, "bf16", True), "16 rows x 64": (18, 2, 4, 400, 272, "f32", True),
+    "32 rows x 64": (40, 2, 4, 400, 272, "bf16", False), "64 x 128": (300, 2, 4, 400, 272, "bf16", True),
+    "128 x 128": (1500, 2, 2, 400, 2064, "bf16", True), "256 x 256": (2100, 2, 3, 400, 2064, "bf16", False),
+    "256 x 256 gathered": (2600, 2, 3, 400, 2320, "bf16", True), "64 x 128 fp32": (300, 2, 4, 400, 272, "f32", False),
+    "128 x 256 fp32": (1500, 2, 2, 400, 2064, "f32", True),
+}
+NAN_CODE = 0x7f
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_rows_of_tokens_that_do_not_exist_are_zeros(kernel):
+    """Whatever a's first row holds, and the other rows are what they are without such tokens."""
+    T, K, E, Kd, N, dtype, _ = KERNELS[kernel]
+    g = gen(13)
+    p = sorted_plan(choices(g, T, K, E), E)
+    a, sa, b, sb = mm_case(g, T, E, Kd, N)
+    a[0] = NAN_CODE
+    sa[0] = float("nan")
+    clean = torch.full((p.cap, N), POISON, dtype=R.DT[dtype], device="cuda")
+    ops.moe_fp8_mm(p, a, sa, b, sb, clean, gather=True)
+    assert torch.isnan(clean[p.row_token == 0]).all()
+    gone = torch.zeros(p.cap, dtype=torch.bool, device="cuda")
+    gone[[1, p.cap // 2, p.cap - 2]] = True
+    p.row_token[gone] = torch.tensor([10 ** 6, -5, T], dtype=torch.int32, device="cuda")
+    c = torch.full_like(clean, POISON)
+    ops.moe_fp8_mm(p, a, sa, b, sb, c, gather=True)
+    assert (c[gone] == 0).all()
+    assert torch.equal(c[~gone].nan_to_num(nan=POISON), clean[~gone].nan_to_num(nan=POISON))
+
+
 WGRADS = [  # T, K, E, M, N, align, dropped, type, gathered
     (1, 1, 4, 16, 16, 128, 0.0, "f32", True), (5, 2, 3, 144, 272, 128, 0.0, "bf16", True),
     (300, 3, 9, 272, 144, 128, 0.2, "f32", False), (300, 2, 5, 256, 512, 256, 0.0, "bf16", True),
