@@ -96,9 +96,22 @@ __device__ __forceinline__ f32x4_v mfma128(i32x8_v a, i32x8_v b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
 }
 
+// One of a block's two scales, s = power(s) rest(s), the power of two kept within
+// 2^-100..2^100.  The sums' factor, the product of both scales, need not be a normal number
+// where they and the result are (rows of 1e-30 beside weights of 1e-9).  Codes that turn
+// into bf16 take the one scale's power with them, which costs nothing there; a block's sums
+// of them stay between 2^-118 and 2^125, and the rest times the other scale is below the
+// normal numbers only where the result is, and finite for products below 2^228.  (In the
+// 8-bit matrix instruction a power of two costs 15 to 25% of the call.)
+__device__ __forceinline__ int exponent(float s) {
+  return min(max((int)(__float_as_uint(s) >> 23) & 255, 127 - 100), 127 + 100);
+}
+__device__ __forceinline__ float power(float s) { return __uint_as_float((uint32_t)exponent(s) << 23); }
+__device__ __forceinline__ float rest(float s) { return __builtin_amdgcn_ldexpf(s, 127 - exponent(s)); }
+
 // A lane's 32 of the 128 codes of a line, as read, and as the matrix cores take
-// them.  Both operands place equal k in equal lanes and bytes, so any split of
-// the 128 does.
+// them (as bf16: times a power of two).  Both operands place equal k in equal lanes
+// and bytes, so any split of the 128 does.
 template <bool EXACT> struct Frag;
 template <> struct Frag<false> {
   i32x8_v v;
@@ -108,11 +121,11 @@ template <> struct Frag<false> {
 template <> struct Frag<true> {
   bf16x8_v v[4];
   __device__ __forceinline__ Frag() {}
-  __device__ __forceinline__ explicit Frag(const i32x8_v r) {
+  __device__ __forceinline__ explicit Frag(const i32x8_v r, float power = 1.f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const bf16x2_v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[i], 1.f, false);
-      const bf16x2_v b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[i], 1.f, true);
+      const bf16x2_v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[i], power, false);
+      const bf16x2_v b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[i], power, true);
       v[i >> 1][4 * (i & 1)] = a[0];
       v[i >> 1][4 * (i & 1) + 1] = a[1];
       v[i >> 1][4 * (i & 1) + 2] = b[0];
@@ -529,15 +542,24 @@ k_fp8_gemm(Args g) {
     for (int k = 0; k < q.nk; ++k) {
       Frag<EX> nf[FN];
 #pragma unroll
-      for (int i = 0; i < FN; ++i) nf[i] = Frag<EX>(nr[i]);
-      const float sbk = WG ? 1.f : sbn;
+      for (int i = 0; i < FN; ++i) {
+        if constexpr (EX && !WG) nf[i] = Frag<EX>(nr[i], power(sbn));
+        else nf[i] = Frag<EX>(nr[i]);
+      }
+      const float sbk = WG ? 1.f : EX ? rest(sbn) : sbn;
+      // a row piece as the matrix cores take it, and its sums' factor (weight gradient: of two)
+      auto row_frag = [&](const i32x8_v& r, float sc) {
+        if constexpr (EX && WG) return Frag<EX>(r, power(sc));
+        else return Frag<EX>(r);
+      };
+      auto row_scale = [&](float sc) { return !WG ? sc * sbk : EX ? rest(sc) : sc; };
       i32x8_v mx;
       float sx = 0.f;
       bool sent = false;  // begin's loads are under way
 #pragma unroll
       for (int j = 0; j < FM - 2; ++j) {
-        const Frag<EX> mf(mr);
-        const float sj = sm;
+        const Frag<EX> mf = row_frag(mr, sm);
+        const float sj = row_scale(sm);
         if (EARLY && j == 1) {
           lds_sync();  // every wave has read its columns of this stage
           sent = begin(par);
@@ -554,10 +576,10 @@ k_fp8_gemm(Args g) {
             if (j == 0) sn[i] = lds_ld<f32x4_v>(sbl + column<EX>(i, 0) * 4);
           }
         }
-        sp = sj * sbk;
+        sp = sj;
       }
-      const Frag<EX> m0(mr), m1(mx);
-      const float s0 = sm * sbk, s1 = sx * sbk;
+      const Frag<EX> m0 = row_frag(mr, sm), m1 = row_frag(mx, sx);
+      const float s0 = row_scale(sm), s1 = row_scale(sx);
       // This stage is read; the next one is there once everybody's loads are: all
       // but begin's and the stores, which are newer.
       if (sent) {
@@ -802,11 +824,11 @@ k_fp8_thin(Args g) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         mf[r] = Frag<true>(join(ra[u][r][0], ra[u][r][1]));
-        sc[r] = real[r] ? sa[u][r] * sb[u] : 0.f;
+        sc[r] = real[r] ? sa[u][r] * rest(sb[u]) : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
-        const Frag<true> nf(join(rb[u][i][0], rb[u][i][1]));
+        const Frag<true> nf(join(rb[u][i][0], rb[u][i][1]), power(sb[u]));
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           const f32x4_v d = dot(nf, mf[r]);

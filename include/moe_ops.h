@@ -156,6 +156,10 @@ int moe_fp8_quant_cols(const moe_plan_desc* desc, const moe_plan* plan, int dtyp
  * and cut those off 13 bits below the largest one's leading power of two (about
  * 1.4e-5 of the result, its rounding to bf16 being 1.7e-3); all further sums run
  * in fp32.
+ * Scales: an fp32 result takes any two, zero and subnormal ones too, whose product is
+ * below 2^228.  A bf16 result may be formed with their product sa * sb rounded to fp32
+ * first: where that is below 2^-126 a block's share is off by up to 2^-125 more, and
+ * where it passes the largest number the result is not finite.
  *   a  [a_rows, K] codes, sa [a_rows, ceil(K/128)]
  *   b  [E, N, K] codes (the reduction contiguous), sb [E, ceil(K/128), ceil(N/128)]
  *      (or out-major, MOE_MM_SB_OUT_MAJOR)
@@ -191,7 +195,7 @@ int moe_fp8_mm(const moe_mm_desc* desc, const void* a, const float* sa, const vo
  *   a [cap/128, M, 128], sa [cap/128, M] and b [cap/128, N, 128], sb [cap/128, N]
  *   from moe_fp8_quant_cols with this plan; dw [E,M,N] (dtype `out`), zeros for
  *   an expert without rows.  M and N multiples of 16 and at most 2^20.  Precision
- *   as in moe_fp8_mm.
+ *   and scales as in moe_fp8_mm.
  */
 int moe_fp8_wgrad(const moe_plan_desc* desc, const moe_plan* plan, int M, int N, int out, const void* a,
                   const float* sa, const void* b, const float* sb, void* dw, void* stream);

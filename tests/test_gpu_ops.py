@@ -517,6 +517,89 @@ def test_wgrad(T, K, E, M, N, align, drop, dtype, gather):
         R.within(dw[e], ref, bound, f"expert {e}")
 
 
+# One size for every tile of the weight gradient: T, K, E, M, N, type
+WTILES = {"192 x 256": (900, 2, 40, 752, 512, "bf16"), "128 x 128": (900, 2, 40, 528, 400, "bf16"),
+          "64 x 128": (900, 2, 9, 272, 144, "bf16"), "128 x 64 fp32": (900, 2, 9, 272, 144, "f32")}
+
+
+# Scales whose products leave fp32's normal range, beside results that do not.  a's scales go by row (column of
+# x), b's by column block (column of dy); tiny codes or zeros where both scales are large, so that results stay finite.
+EA, EB = (-60, 80, -120, 0, 100, 118), (-100, 50, 118, 0)
+
+
+def hard_scales(g, shape, exps, dim):
+    e = torch.tensor(exps, device="cuda").repeat(shape[dim])[:shape[dim]]
+    m = 1 + torch.rand(shape, generator=g, device="cuda")
+    return m * torch.exp2(e.float()).view([-1 if i == dim else 1 for i in range(len(shape))]), e
+
+
+def check_hard(c, ref, mag, steps, blocks, dt, apart, sa, sb):
+    """Sums' and result's rounding as for any scales; below the smallest normal number a result is a multiple of
+    2^-149 (fp32; each block's sum may round to one) or 2^-133 (bf16).  Where the kernel does not keep the scales
+    apart, their product (sa [rows, blocks] by sb [blocks, columns]) is off by up to 2^-150 below the normal numbers,
+    times at most 128 * 448 * 448 < 2^24.7: 2^-125 a block; and past the largest number nothing is asked.  Nor is it
+    of results past the largest number."""
+    ok = mag < 3e38
+    small = blocks * 2.0 ** -149 + (2.0 ** -133 if dt == torch.bfloat16 else 0.0)
+    if not apart:
+        for i in range(blocks):
+            ok &= torch.isfinite(sa[:, i, None] * sb[None, i])
+        small += blocks * 2.0 ** -125
+    bound = steps * mag + R.HALF[dt] * ref.abs() * (1 + 2.0 ** -7) + small
+    zero = torch.zeros((), dtype=torch.float64, device="cuda")
+    R.within(torch.where(ok, c.double(), zero), torch.where(ok, ref, zero), bound)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_product_of_scales_past_the_normal_range(kernel):
+    T, K, E, Kd, N, dtype, gather = KERNELS[kernel]
+    apart = dtype == "f32" or "rows x" in kernel
+    g, dt = gen(17), R.DT[dtype]
+    p = sorted_plan(choices(g, T, K, E), E)
+    a, _, b, _ = mm_case(g, T if gather else p.cap, E, Kd, N)
+    sa, ea = hard_scales(g, (len(a), ops.blocks(Kd)), EA, 0)
+    sb, eb = hard_scales(g, (E, ops.blocks(Kd), ops.blocks(N)), EB, 2)
+    a[ea >= 80] = a[ea >= 80] & 0x81  # 2^-9, 0 and their negatives
+    a[ea == 100] = 0
+    tiny = torch.repeat_interleave(eb, 128)[:N] == 50
+    b[:, tiny] = b[:, tiny] & 0x81
+    c = torch.full((p.cap, N), POISON, dtype=dt, device="cuda")
+    ops.moe_fp8_mm(p, a, sa, b, sb, c, gather=gather)
+    for e in range(E):
+        r0 = int(p.offsets[e])
+        rows = torch.arange(r0, r0 + int(p.counts[e]), device="cuda")
+        take = p.row_token[rows].long() if gather else rows
+        av, wv = R.values(a[take], sa[take]), weights_ref(b[e], sb[e])
+        # (per block: the scales' product, its product with the block's, its power of two and the sum)
+        check_hard(c[rows], av @ wv, av.abs() @ wv.abs(), R.mm_steps(Kd, 4, dt), ops.blocks(Kd), dt, apart,
+                   sa[take], torch.repeat_interleave(sb[e], 128, 1)[:, :N])
+
+
+@pytest.mark.parametrize("tile", WTILES)
+def test_wgrad_of_scales_past_the_normal_range(tile):
+    T, K, E, M, N, dtype = WTILES[tile]
+    g, dt = gen(18), R.DT[dtype]
+    p = sorted_plan(choices(g, T, K, E), E, 128)
+    nb = p.cap // 128
+    a, b = codes(g, nb, M, 128), codes(g, nb, N, 128)
+    sa, ea = hard_scales(g, (nb, M), EA, 1)
+    sb, eb = hard_scales(g, (nb, N), EB, 1)
+    a[:, ea >= 80] = a[:, ea >= 80] & 0x81
+    a[:, ea == 100] = 0
+    b[:, eb == 50] = b[:, eb == 50] & 0x81
+    dw = torch.full((E, M, N), POISON, dtype=dt, device="cuda")
+    ops.moe_fp8_wgrad(p, a, sa, b, sb, dw)
+    off, counts = p.offsets.tolist(), p.counts.tolist()
+    for e in range(E):
+        b0, n = off[e] // 128, -(-counts[e] // 128)
+        ref, mag = torch.zeros(M, N, dtype=torch.float64, device="cuda"), torch.zeros(M, N, dtype=torch.float64, device="cuda")
+        for i in range(b0, b0 + n):
+            xv, yv = R.decode(a[i]) * sa[i].double()[:, None], R.decode(b[i]) * sb[i].double()[:, None]
+            ref += xv @ yv.t()
+            mag += xv.abs() @ yv.abs().t()
+        check_hard(dw[e], ref, mag, R.mm_steps(128 * n, 4, dt), n, dt, dtype == "f32", sa[b0:b0 + n].t(), sb[b0:b0 + n])
+
+
 # ---------------------------------------------------------------- SwiGLU
 
 def swiglu64(h, n):
