@@ -457,6 +457,11 @@ KERNELS = {
     "256 x 256 gathered": (2600, 2, 3, 400, 2320, "bf16", True), "64 x 128 fp32": (300, 2, 4, 400, 272, "f32", False),
     "128 x 256 fp32": (1500, 2, 2, 400, 2064, "f32", True),
 }
+DENSE = {  # rows, reduction, columns, type
+    "16 rows x 32": (5, 400, 272, "f32"), "16 rows x 64": (9, 400, 272, "bf16"), "32 rows x 64": (20, 400, 272, "bf16"),
+    "64 x 128": (300, 400, 272, "bf16"), "128 x 128": (1900, 400, 4064, "bf16"), "256 x 256": (4000, 400, 4064, "bf16"),
+    "64 x 128 fp32": (300, 400, 272, "f32"), "128 x 256 fp32": (4000, 400, 4064, "f32"),
+}
 NAN_CODE = 0x7f
 
 
@@ -479,6 +484,62 @@ def test_rows_of_tokens_that_do_not_exist_are_zeros(kernel):
     ops.moe_fp8_mm(p, a, sa, b, sb, c, gather=True)
     assert (c[gone] == 0).all()
     assert torch.equal(c[~gone].nan_to_num(nan=POISON), clean[~gone].nan_to_num(nan=POISON))
+
+
+def spoil(a, sa, b, sb, Kd):
+    """NaN and infinities in some rows of a, one column and one column block of b's first expert -> those rows."""
+    rows = [1, len(a) // 2, len(a) - 2, len(a) - 1]
+    sa[rows[0], 1] = float("nan")
+    a[rows[1], Kd - 1] = NAN_CODE
+    sa[rows[2], -1] = float("inf")
+    a[rows[3], 0] = 0x80 | NAN_CODE
+    b[0, 5, Kd - 1] = NAN_CODE
+    sb[0, -1, 1] = float("nan")
+    return rows
+
+
+def check_spoiled(c, clean, bad_rows, first):
+    """bad_rows are not finite; rows of the first expert (`first`) are NaN in columns 5 and 128..255; the rest as clean."""
+    assert not torch.isfinite(c[bad_rows]).any()
+    cols = torch.zeros(c.shape[1], dtype=torch.bool, device="cuda")
+    cols[5] = cols[128:256] = True
+    assert torch.isnan(c[first][:, cols]).all()
+    good = ~bad_rows[:, None] & ~(first[:, None] & cols)
+    assert torch.equal(c[good], clean[good])
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_product_contains_what_is_not_finite(kernel):
+    T, K, E, Kd, N, dtype, gather = KERNELS[kernel]
+    g = gen(14)
+    p = sorted_plan(choices(g, T, K, E), E)
+    a, sa, b, sb = mm_case(g, T if gather else p.cap, E, Kd, N)
+    clean = torch.empty(p.cap, N, dtype=R.DT[dtype], device="cuda")
+    ops.moe_fp8_mm(p, a, sa, b, sb, clean, gather=gather)
+    rows = spoil(a, sa, b, sb, Kd)
+    c = torch.empty_like(clean)
+    ops.moe_fp8_mm(p, a, sa, b, sb, c, gather=gather)
+    bad = torch.zeros(len(a), dtype=torch.bool, device="cuda")
+    bad[rows] = True
+    check_spoiled(c, clean, bad[p.row_token.long()] if gather else bad,
+                  torch.arange(p.cap, device="cuda") < p.counts[0])
+
+
+@pytest.mark.parametrize("kernel", DENSE)
+def test_dense_product_contains_what_is_not_finite(kernel):
+    rows, Kd, N, dtype = DENSE[kernel]
+    g = gen(15)
+    a, sa, b, sb = mm_case(g, rows, 1, Kd, N)
+    clean = torch.empty(rows, N, dtype=R.DT[dtype], device="cuda")
+    ops.moe_fp8_mm(None, a, sa, b, sb, clean)
+    av, wv = R.values(a, sa), weights_ref(b[0], sb[0])
+    ref = av @ wv
+    R.within(clean, ref, R.mm_bound(av.abs(), wv.abs(), Kd, ref, R.DT[dtype]))
+    bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    bad[spoil(a, sa, b, sb, Kd)] = True
+    c = torch.empty_like(clean)
+    ops.moe_fp8_mm(None, a, sa, b, sb, c)
+    check_spoiled(c, clean, bad, torch.ones(rows, dtype=torch.bool, device="cuda"))
 
 
 WGRADS = [  # T, K, E, M, N, align, dropped, type, gathered
@@ -520,6 +581,30 @@ def test_wgrad(T, K, E, M, N, align, drop, dtype, gather):
 # One size for every tile of the weight gradient: T, K, E, M, N, type
 WTILES = {"192 x 256": (900, 2, 40, 752, 512, "bf16"), "128 x 128": (900, 2, 40, 528, 400, "bf16"),
           "64 x 128": (900, 2, 9, 272, 144, "bf16"), "128 x 64 fp32": (900, 2, 9, 272, 144, "f32")}
+
+
+@pytest.mark.parametrize("tile", WTILES)
+def test_wgrad_contains_what_is_not_finite(tile):
+    """A value of x or dy that is not finite spoils its column's row or column of its own expert's gradient alone."""
+    T, K, E, M, N, dtype = WTILES[tile]
+    g = gen(16)
+    p = sorted_plan(choices(g, T, K, E), E, 128)
+    x, dy = randn(g, p.cap, M), randn(g, p.cap, N)
+    bufs = ops.column_buffers(p, M) + ops.column_buffers(p, N)
+
+    def wgrad():
+        dw = torch.full((E, M, N), POISON, dtype=R.DT[dtype], device="cuda")
+        ops.moe_fp8_quant_cols(p, x, *bufs[:2])
+        ops.moe_fp8_quant_cols(p, dy, *bufs[2:])
+        ops.moe_fp8_wgrad(p, *bufs, dw)
+        return dw
+    clean = wgrad()
+    off = p.offsets.tolist()
+    x[off[1], 7], x[off[E - 1], M - 1], dy[off[2] + 1, 33] = float("nan"), float("inf"), float("-inf")
+    bad = torch.zeros(E, M, N, dtype=torch.bool, device="cuda")
+    bad[1, 7] = bad[E - 1, M - 1] = bad[2, :, 33] = True
+    dw = wgrad()
+    assert torch.isnan(dw[bad]).all() and torch.equal(dw[~bad], clean[~bad])
 
 
 # Scales whose products leave fp32's normal range, beside results that do not.  a's scales go by row (column of
