@@ -56,8 +56,8 @@ k_quant_rows_128(const T* __restrict__ src, int64_t R, int C, RowFilter rows, bo
   }
 }
 
-// logistic sigmoid to about half a step more than correct rounding: the
-// exponential's argument in two parts, the reciprocal with a Newton step.
+// logistic sigmoid to 5 * 2^-24 of itself whatever g is (correct rounding: 1): the
+// exponential's argument in two parts, the reciprocal with a Newton step; 0 below 2^-126.
 // (device_common.h's sigmoidf_ is off by |g| steps, and a value near the border
 // of two codes then falls on the other side more often than it needs to.)
 __device__ __forceinline__ float sigmoid_(float g) {

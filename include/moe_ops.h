@@ -204,6 +204,8 @@ int moe_fp8_wgrad(const moe_plan_desc* desc, const moe_plan* plan, int M, int N,
  * SwiGLU between the two products.  h [R,2n]: columns 0..n-1 (G) feed SiLU,
  * n..2n-1 (U) are the up half, as in moe.h; n a multiple of 16.  With a plan
  * (R = moe_plan_rows) only the plan's rows are read and written.
+ * The sigmoid is off by at most 5 * 2^-24 of itself; below 2^-126 (gates under -87.3)
+ * it may count as 0.
  *   moe_swiglu_fp8   A = silu(G) U in fp32 -> codes q [R,n], scales
  *                    s [R, ceil(n/128)], and when `a` is non-NULL A itself
  *                    [R,n] in h's type

@@ -756,6 +756,89 @@ def test_swiglu_bwd_against_differences():
         assert abs((v[0] - v[1]) / (2 * step) - float(dh[i, j])) <= 1e-6 + 1e-5 * abs(float(dh[i, j]))
 
 
+# The sigmoid's relative error: the hardware exponential's last place (2^-23, its argument in two parts is exact to
+# 2^-40) and the sum that joins the parts (2^-24), the denominator's rounding and the reciprocal's after its Newton
+# step (2^-24 each): 5 * 2^-24, whatever g is, where it is a normal number; below 2^-126 it may be 0.
+SIGMOID = 5 * 2.0 ** -24
+
+
+def wide_gates(gn, Rn, n, dt):
+    h = randn(gn, Rn, 2 * n, dtype=torch.float32)
+    h[:, :n] = (torch.rand(Rn, n, generator=gn, device="cuda") - 0.5) * 174.0  # -87..87
+    return h.to(dt)
+
+
+def type_step(dt):
+    """What the result's type adds: nothing to fp32 sums; to bf16 half a step of the value, and below 2^-126, where a
+    result is a multiple of 2^-133, half of that."""
+    return (R.HALF[dt] * 1.01, 2.0 ** -134) if dt == torch.bfloat16 else (0.0, 0.0)
+
+
+@pytest.mark.parametrize("Rn,n,dtype", [(64, 256, "f32"), (33, 400, "bf16")])
+def test_swiglu_error_does_not_grow_with_the_gate(Rn, n, dtype):
+    gn, dt = gen(19), R.DT[dtype]
+    h = wide_gates(gn, Rn, n, dt)
+    q, s = torch.empty(Rn, n, dtype=torch.uint8, device="cuda"), torch.empty(Rn, ops.blocks(n), device="cuda")
+    a = torch.empty(Rn, n, dtype=dt, device="cuda")
+    ops.moe_swiglu_fp8(h, q, s, a)
+    g, u, sg = swiglu64(h, n)
+    ref = g * sg * u
+    err = (SIGMOID + 2 * 2.0 ** -24) * 1.001 * ref.abs() + 2.0 ** -140  # two products
+    half, tiny = type_step(dt)
+    R.within(a, ref, err + half * ref.abs() + tiny, "a")
+    # a block's scale is off as its largest value is, and rounds once
+    amax = torch.stack([ref[:, c:c + 128].abs().amax(1) for c in range(0, n, 128)], 1)
+    R.within(s, (amax / 448).clamp(min=R.TINY), (SIGMOID + 3 * 2.0 ** -24) * 1.001 * amax / 448 + 2.0 ** -140, "s")
+    wide = torch.repeat_interleave(s.double(), 128, 1)[:, :n]
+    R.within(R.decode(q) * wide, ref, ref.abs() * 2.0 ** -4 * 1.001 + wide * 2.0 ** -10 + err, "q")
+
+
+@pytest.mark.parametrize("Rn,n,dtype", [(64, 256, "f32"), (33, 400, "bf16")])
+def test_swiglu_bwd_error_does_not_grow_with_the_gate(Rn, n, dtype):
+    gn, dt = gen(20), R.DT[dtype]
+    h, da = wide_gates(gn, Rn, n, dt), randn(gn, Rn, n, dtype=dt)
+    dh = torch.empty_like(h)
+    ops.moe_swiglu_bwd(da, h, dh)
+    g, u, s = swiglu64(h, n)
+    d, step = da.double(), 2.0 ** -24
+    half, tiny = type_step(dt)
+    du = d * g * s
+    R.within(dh[:, n:], du, (SIGMOID + 2 * step) * 1.001 * du.abs() + half * du.abs() + tiny + 2.0 ** -140, "du")
+    # t = 1 - s is off by s SIGMOID and a rounding, m = g t by g times that and a rounding, q = 1 + m by a rounding
+    # more; d u s q: the sigmoid's error and three products
+    t, q = 1 - s, 1 + g * (1 - s)
+    eq = g.abs() * (s * SIGMOID + 2 * step * t) + step * q.abs()
+    dg = d * u * s * q
+    bound = (d * u * s).abs() * (q.abs() * (SIGMOID + 3 * step) + eq) * 1.001 + half * dg.abs() + tiny + 2.0 ** -140
+    R.within(dh[:, :n], dg, bound, "dg")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_swiglu_of_the_farthest_gates(dtype):
+    """Gates down to the type's lowest value give zeros, up to its largest the gate itself, with finite gradients."""
+    dt, n = R.DT[dtype], 16
+    big = torch.finfo(dt).max
+    gates = torch.tensor([-big, -1e30, -1e4, -200.0, -105.0, -90.0, -88.0, -87.5, 0.0, -0.0, 88.0, 90.0, 200.0, 1e4, 1e30, big],
+                         device="cuda")
+    h = torch.ones(1, 2 * n, device="cuda")
+    h[0, :n] = gates
+    h = h.to(dt)
+    q, s = torch.empty(1, n, dtype=torch.uint8, device="cuda"), torch.empty(1, 1, device="cuda")
+    a, dh, da = torch.empty(1, n, dtype=dt, device="cuda"), torch.empty_like(h), torch.ones(1, n, dtype=dt, device="cuda")
+    ops.moe_swiglu_fp8(h, q, s, a)
+    ops.moe_swiglu_bwd(da, h, dh)
+    g = h[:, :n].double()
+    ref = g * torch.sigmoid(g)
+    # a sigmoid below 2^-126 may be 0: at most 105 * 2^-126 of these sums (farther gates: less than 2^-149 of them)
+    tol = ref.abs() * 1e-6 + R.HALF[dt] * ref.abs() * (dt == torch.bfloat16) + 105 * 2.0 ** -126
+    R.within(a, ref, tol, "a")
+    R.within(dh[:, n:], ref, tol, "du")
+    sg = torch.sigmoid(g)
+    dg = sg * (1 + g * (1 - sg))
+    R.within(dh[:, :n], dg, dg.abs() * 1e-5 + R.HALF[dt] * dg.abs() * (dt == torch.bfloat16) + 105 * 2.0 ** -126, "dg")
+    assert float(s) == float(torch.tensor(big, dtype=torch.float32) / torch.tensor(448.0))
+
+
 def test_swiglu_of_a_plan():
     """Only the plan's rows are read and written."""
     T, K, E, n = 200, 3, 7, 144
