@@ -13,10 +13,11 @@
 // time, cut off 13 bits below the largest one's leading power of two (measured:
 // beside 256 * 256 a product of 2^3 counts, one of 2^2 does not, and eight
 // codes further on everything counts down to 2^-7); those sums then add up in
-// fp32.  On normally distributed values that is an error of 1.35e-5 of the
-// result (fp32 products: 3e-7).  Under a bf16 result, rounded by 1.7e-3, it does not
-// show.  An fp32 result is for callers who need more, so there the codes turn
-// into bf16, exactly, and run on the bf16 matrix cores, at half their rate or less.
+// fp32.  Seven products may lose less than 2^-13 of the largest each: less than
+// 7 * 2^-13 of sum |a b|, and on normally distributed values 1.35e-5 of the result in
+// the mean square (fp32 products: 3e-7), where a bf16 result's rounding is 1.7e-3.  An fp32
+// result is for callers who need more, so there the codes turn into bf16, exactly,
+// and run on the bf16 matrix cores, at half their rate or less.
 //
 //  * Both operands are lines of 128 codes: a row's block (moe_fp8_mm: rows of
 //    a, gathered or not, and rows of b) or a column's block of 128 rows
