@@ -112,11 +112,16 @@ _VALUES = (torch.float32, torch.bfloat16)
 _F32 = (torch.float32,)
 
 
+_INT32 = 2 ** 31 - 1  # ctypes cuts a larger size off without a word
+
+
 def _shape(name, t, dims=2):
-    """The sizes of a tensor of `dims` dimensions (_need checks the rest)."""
+    """The sizes of a tensor of `dims` dimensions, a row's within 32 bits (_need checks the rest)."""
     if isinstance(t, torch.Tensor):
         s = t.shape
         if len(s) == dims:
+            if s[1] > _INT32 or s[-1] > _INT32:
+                raise ValueError(f"{name}: shape {tuple(s)}, sizes past 32 bits")
             return s
     raise ValueError(f"{name}: a {dims}-dimensional tensor is needed")
 
@@ -159,6 +164,8 @@ class Plan:
         device = torch.device(device)
         if device.type == "cuda" and device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
+        if max(T, K, E, align) > _INT32 or min(T, K, E, align) < -_INT32:
+            raise B.MoEError("moe_plan_rows", B.MOE_ESHAPE)
         self.T, self.K, self.E, self.align, self.device = T, K, E, align, device
         self.desc = MoePlanDesc(T, K, E, align, 0, 0, None)
         self.cap = int(lib().moe_plan_rows(ctypes.byref(self.desc)))
@@ -311,6 +318,8 @@ def moe_fp8_mm(plan, a, sa, b, sb, c, gather: bool = False, sb_out_major: bool =
     fp32 or bf16.  plan None: dense, a [R, K], b [N, K] or [1, N, K], c [R, N]."""
     rows_a, K = _shape("a", a)
     rows, N = _shape("c", c)
+    if rows_a > _INT32 or rows > _INT32:
+        raise ValueError(f"a and c: {rows_a} and {rows} rows, sizes past 32 bits")
     dev = a.device
     if plan is None:
         if gather:

@@ -224,6 +224,32 @@ def test_binding_refuses_tensors():
     assert ops.Plan(0, 2, 8, device="cpu").cap == 0
 
 
+def test_sizes_past_32_bits_refused():
+    """Sizes that the C interface holds in 32 bits are refused, never cut off (tensors without memory)."""
+    n = 2 ** 32 + 16  # 16 in 32 bits
+
+    def t(*shape, dtype=torch.bfloat16):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+    for kw in (dict(T=2 ** 32 + 8), dict(K=2 ** 32 + 1), dict(E=2 ** 32 + 4), dict(align=2 ** 32 + 1), dict(T=8 - 2 ** 32)):
+        with pytest.raises(B.MoEError):
+            ops.Plan(**{**dict(T=8, K=1, E=4, align=1, device="meta"), **kw})
+    p = ops.Plan(1, 1, 1, align=128, device="meta")
+    q, s = t(1, n, dtype=torch.uint8), t(1, ops.blocks(n), dtype=torch.float32)
+    for call in (lambda: ops.moe_permute(p, t(1, n), t(p.cap, n)), lambda: ops.moe_permute_bwd(p, t(p.cap, n), t(1, n)),
+                 lambda: ops.moe_permute_fp8(p, t(1, n), q, s), lambda: ops.moe_unpermute(p, t(p.cap, n), s, t(1, n)),
+                 lambda: ops.moe_unpermute_bwd(p, t(1, n), None, s, None, None),
+                 lambda: ops.moe_fp8_quant_rows(t(1, n), q, s), lambda: ops.moe_fp8_quant_cols(p, t(p.cap, n), q, s),
+                 lambda: ops.moe_fp8_quant_weights(t(1, n, 16), q, None, s),
+                 lambda: ops.moe_fp8_quant_weights(t(1, 16, n), q, None, s),
+                 lambda: ops.moe_swiglu_fp8(t(1, 2 * n), q, s), lambda: ops.moe_swiglu_bwd(t(1, n), t(1, 2 * n), t(1, 2 * n)),
+                 lambda: ops.moe_fp8_mm(None, q, s, q, s, t(1, 16)), lambda: ops.moe_fp8_mm(None, q, s, q, s, t(1, n)),
+                 lambda: ops.moe_fp8_mm(None, t(n, 16, dtype=torch.uint8), t(n, 1, dtype=torch.float32),
+                                        t(16, 16, dtype=torch.uint8), t(1, 1, dtype=torch.float32), t(n, 16)),
+                 lambda: ops.moe_fp8_wgrad(p, t(1, n, 128), s, t(1, 16, 128), s, t(1, n, 16))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+
+
 def test_reference_encoder():
     """The tests' own E4M3 encoder: every code's value encodes to itself, midpoints go to the even code."""
     v = R.e4m3_values()
