@@ -404,8 +404,8 @@ int row_splits(int T, int passes) {
   return std::max(1, std::min(want, passes));
 }
 
-// T rows read and T*K written of so many bytes
-bool streamed(const PlanArgs& p, int64_t row_bytes) { return streams((int64_t)p.T * (p.K + 1) * row_bytes); }
+// T rows of so many bytes on one side and T*K on the other
+bool streamed(const PlanArgs& p, int64_t one, int64_t many) { return streams((int64_t)p.T * (one + p.K * many)); }
 
 unsigned wave_blocks(int T, int splits) { return (unsigned)(((int64_t)T * splits + 3) / 4); }
 
@@ -439,7 +439,7 @@ hipError_t launch_permute(const PlanArgs& p, int dtype, int d, const void* x, vo
   const int pieces = (int)((int64_t)d * (dtype == MOE_BF16 ? 2 : 4) / 16);
   const int splits = row_splits(p.T, (pieces + 63) / 64);
   hipLaunchKernelGGL(k_permute, dim3(wave_blocks(p.T, splits)), dim3(256), 0, st, (const uint4*)x, p.slot_row, p.T,
-                     p.K, p.cap, pieces, splits, streamed(p, (int64_t)pieces * 16), (uint4*)xp);
+                     p.K, p.cap, pieces, splits, streamed(p, (int64_t)pieces * 16, (int64_t)pieces * 16), (uint4*)xp);
   return hipGetLastError();
 }
 
@@ -447,12 +447,13 @@ hipError_t launch_permute_fp8(const PlanArgs& p, int dtype, int d, const void* x
                               hipStream_t st) {
   const int splits = row_splits(p.T, (d + 1023) / 1024);
   const dim3 grid(wave_blocks(p.T, splits));
+  const bool stream = streamed(p, (int64_t)d * (dtype == MOE_BF16 ? 2 : 4), d);
   if (dtype == MOE_BF16)
     hipLaunchKernelGGL(k_permute_fp8<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)x, p.slot_row, p.T, p.K, p.cap,
-                       d, splits, streamed(p, d), q, s);
+                       d, splits, stream, q, s);
   else
     hipLaunchKernelGGL(k_permute_fp8<float>, grid, dim3(256), 0, st, (const float*)x, p.slot_row, p.T, p.K, p.cap, d,
-                       splits, streamed(p, d), q, s);
+                       splits, stream, q, s);
   return hipGetLastError();
 }
 
@@ -473,7 +474,7 @@ hipError_t launch_unpermute(const PlanArgs& p, int dtype, int d, const void* y, 
 hipError_t launch_unpermute_bwd(const PlanArgs& p, int dtype, int d, const void* d_o, const void* y, const float* w,
                                 void* dy, float* dw, hipStream_t st) {
   const int pieces = (int)((int64_t)d * (dtype == MOE_BF16 ? 2 : 4) / 16);
-  const bool stream = streamed(p, (int64_t)pieces * 16);
+  const bool stream = streamed(p, (int64_t)pieces * 16, (int64_t)pieces * 16 * ((dy ? 1 : 0) + (dw ? 1 : 0)));
   auto launch = [&](auto* k, int threads) {
     hipLaunchKernelGGL(k, dim3(p.T), dim3(threads), 0, st, (const uint4*)d_o, (const uint4*)y, w, p.slot_row, p.K,
                        p.cap, pieces, stream, (uint4*)dy, dw);
