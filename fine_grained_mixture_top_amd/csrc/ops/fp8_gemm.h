@@ -656,13 +656,13 @@ k_fp8_gemm(Args g) {
 // Row product for segments of few rows (decode): the weights' bytes are all the
 // work, and every touched expert's are read once, straight into registers.  A
 // workgroup takes 16 RT rows of a segment and 16 FN columns; its four waves split
-// the reduction's blocks (wave w: blocks w, w + 4, ...), load UNR of theirs at a
-// time, and add up their sums in wave order.  The matrix work is small, so it
-// runs on the bf16 matrix cores whatever the result's type.  Bound by the
-// weights' bytes: 8 rows of K = 7168, N = 4096 38.9 us (6.0 TB/s), 512 rows over 64
-// experts of K = N = 2048 43.7 us (6.1 TB/s), 128 rows over 101 of 256 experts of
-// K = 2048, N = 512 23 us (4.7 TB/s: about 4 us are launch and look-up).
-template <int RT, int FN, int UNR, typename O>
+// the reduction's blocks (wave w: blocks w, w + 4, ...) and add up their sums in wave
+// order.  The matrix work is small, so it runs on the bf16 matrix cores whatever the
+// result's type.  Bound by the weights' bytes: 8 rows of 8 experts of K = 7168, N = 4096
+// 38.9 us (6.0 TB/s), 512 rows over 64 experts of K = N = 2048 43.7 us (6.1 TB/s), 128 rows
+// over 101 of 256 experts of K = 2048, N = 512 23 us (4.7 TB/s: about 4 us are launch
+// and look-up).
+template <int RT, int FN, typename O>
 __global__ void __launch_bounds__(256)
 k_fp8_thin(Args g) {
   constexpr int BN = 16 * FN, BM = 16 * RT;
@@ -745,34 +745,28 @@ k_fp8_thin(Args g) {
   for (int i = 0; i < FN; ++i) pb[i] = g.b + ((int64_t)e * g.N + min(n0 + 16 * i + p, g.N - 1)) * g.K + 16 * h;
   const float* psb = g.sb + (int64_t)e * g.kb * ((g.N + 127) >> 7) + (int64_t)(n0 >> 7) * g.sb_n;
 
-  // Loads of the blocks k0, k0 + 4, ..: none under a condition; past the
-  // reduction they read its first codes, and both sides' become zeros later.
-  uint4 ra[UNR][RT][2], rb[UNR][FN][2];
-  float sa[UNR][RT], sb[UNR];
+  // Block k's loads: none under a condition; past the reduction they read its
+  // first codes, and both sides' become zeros later.
+  uint4 ra[RT][2], rb[FN][2];
+  float sa[RT], sb;
   auto from = [&](int k, int c) {  // this lane's chunk: 16 h further on
     const int at = k * 128 + 64 * c;
     return at + 16 * h < g.K ? at : -16 * h;
   };
-  auto load_b = [&](int k0) {
+  auto load_b = [&](int k) {
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int i = 0; i < FN; ++i) rb[u][i][c] = *reinterpret_cast<const uint4*>(pb[i] + from(k0 + 4 * u, c));
-      sb[u] = psb[(int64_t)min(k0 + 4 * u, g.kb - 1) * g.sb_k];
-    }
+      for (int i = 0; i < FN; ++i) rb[i][c] = *reinterpret_cast<const uint4*>(pb[i] + from(k, c));
+    sb = psb[(int64_t)min(k, g.kb - 1) * g.sb_k];
   };
-  auto load_a = [&](int k0) {
+  auto load_a = [&](int k) {
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int r = 0; r < RT; ++r) ra[r][c] = *reinterpret_cast<const uint4*>(pa[r] + from(k, c));
 #pragma unroll
-        for (int r = 0; r < RT; ++r) ra[u][r][c] = *reinterpret_cast<const uint4*>(pa[r] + from(k0 + 4 * u, c));
-#pragma unroll
-      for (int r = 0; r < RT; ++r) sa[u][r] = psa[r][min(k0 + 4 * u, g.kb - 1)];
-    }
+    for (int r = 0; r < RT; ++r) sa[r] = psa[r][min(k, g.kb - 1)];
   };
   load_b(w);  // (on the way while the tokens arrive)
   __builtin_amdgcn_sched_barrier(0);
@@ -794,48 +788,40 @@ k_fp8_thin(Args g) {
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int i = 0; i < FN; ++i) acc[r][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = w; k0 < g.kb; k0 += 4 * UNR) {
-    if (k0 > w) {
-      load_b(k0);
-      load_a(k0);
+  for (int k = w; k < g.kb; k += 4) {
+    if (k > w) {
+      load_b(k);
+      load_a(k);
     }
     __builtin_amdgcn_sched_barrier(0);
-    const bool whole = (k0 + 4 * (UNR - 1) + 1) * 128 <= g.K;
+    if ((k + 1) * 128 > g.K || ghosts) {
+      const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-      if (!whole || ghosts) {
-        const uint4 z = make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < 2; ++c) {
+        const bool past = k * 128 + 64 * c + 16 * h >= g.K;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const bool past = (k0 + 4 * u) * 128 + 64 * c + 16 * h >= g.K;
-#pragma unroll
-          for (int i = 0; i < FN; ++i)
-            if (past) rb[u][i][c] = z;
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            if (past || !real[r]) ra[u][r][c] = z;
-        }
-        if (k0 + 4 * u >= g.kb) sb[u] = 0.f;  // (a scale that is not finite would spoil the zeros)
+        for (int i = 0; i < FN; ++i)
+          if (past) rb[i][c] = z;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-          if (k0 + 4 * u >= g.kb) sa[u][r] = 0.f;
+          if (past || !real[r]) ra[r][c] = z;
       }
-      Frag<true> mf[RT];
-      float sc[RT];
+    }
+    Frag<true> mf[RT];
+    float sc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      mf[r] = Frag<true>(join(ra[r][0], ra[r][1]));
+      sc[r] = real[r] ? sa[r] * rest(sb) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      const Frag<true> nf(join(rb[i][0], rb[i][1]), power(sb));
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        mf[r] = Frag<true>(join(ra[u][r][0], ra[u][r][1]));
-        sc[r] = real[r] ? sa[u][r] * rest(sb[u]) : 0.f;
-      }
+        const f32x4_v d = dot(nf, mf[r]);
 #pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        const Frag<true> nf(join(rb[u][i][0], rb[u][i][1]), power(sb[u]));
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const f32x4_v d = dot(nf, mf[r]);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) acc[r][i][x] = fmaf(d[x], sc[r], acc[r][i][x]);
-        }
+        for (int x = 0; x < 4; ++x) acc[r][i][x] = fmaf(d[x], sc[r], acc[r][i][x]);
       }
     }
   }

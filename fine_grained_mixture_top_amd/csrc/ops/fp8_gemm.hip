@@ -55,13 +55,13 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Row tiles at most: every segment with rows may end inside one.
 int64_t row_tiles(const f8::Args& a, int64_t used, int BM) { return div_up(used, BM) + std::min<int64_t>(a.E, used); }
 
-template <int RT, int FN, int UNR>
+template <int RT, int FN>
 hipError_t launch_thin(int out, const f8::Args& a, int64_t used, hipStream_t st) {
   const int64_t tiles = row_tiles(a, used, 16 * RT) * div_up(a.N, 16 * FN);
   if (out == MOE_BF16)
-    hipLaunchKernelGGL((f8::k_fp8_thin<RT, FN, UNR, bf16_t>), dim3((unsigned)tiles), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((f8::k_fp8_thin<RT, FN, bf16_t>), dim3((unsigned)tiles), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((f8::k_fp8_thin<RT, FN, UNR, float>), dim3((unsigned)tiles), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((f8::k_fp8_thin<RT, FN, float>), dim3((unsigned)tiles), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -142,9 +142,9 @@ hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) 
   const bool wide = m.out == MOE_F32;
   const int64_t cus = cu_count(device());
   switch (thin_tiles(a, used, wide, cus)) {
-    case 1: return launch_thin<1, 2, 1>(m.out, a, used, st);
-    case 2: return launch_thin<1, 4, 1>(m.out, a, used, st);
-    case 3: return launch_thin<2, 4, 1>(m.out, a, used, st);
+    case 1: return launch_thin<1, 2>(m.out, a, used, st);
+    case 2: return launch_thin<1, 4>(m.out, a, used, st);
+    case 3: return launch_thin<2, 4>(m.out, a, used, st);
   }
   auto bound = [&](int BM, int BN) { return row_tiles(a, used, BM) * div_up(m.N, BN); };
   auto time = [&](int BM, int BN, double one, double two, int ends) {
@@ -176,6 +176,10 @@ hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) 
 //   262144, 128, 1536 x 512    265 / 299 / 376     8192, 8, 1024 x 1024     23.0 / 20.0 / 22.2
 //   65536, 32, 1408 x 2048     243 / 276 / 351     4096, 32, 768 x 768      19.5 / 19.6 / 19.2
 //   2048, 64, 2048 x 1024      69 / 86 / 91        65536, 8, 512 x 512      99 / 67 / 51
+// fp32 results take 128 x 64 tiles whatever the sizes (their codes turn into bf16, so
+// the instructions bound them, not the reads that larger tiles would save), us:
+//   65536, 64, 2048 x 1024     500                 3000, 16, 1040 x 720     24.2
+//   262144, 128, 1536 x 512    665                 65536, 8, 512 x 512      73
 hipError_t launch_fp8_wgrad(const PlanArgs& p, int M, int N, int out, const uint8_t* qa, const float* sa,
                             const uint8_t* qb, const float* sb, void* dw, hipStream_t st) {
   f8::Args a{};

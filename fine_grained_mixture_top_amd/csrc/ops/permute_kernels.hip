@@ -397,8 +397,8 @@ k_unpermute_bwd(const uint4* __restrict__ d_o, const uint4* __restrict__ y, cons
 // 8 tokens of K = 8, d = 7168 9.7 / 6.8; 256 of d = 4096 10.1 / 8.7; 512 15.8 / 18.6.
 constexpr int BWD_FEW = 256;
 
-// Waves per token: rows of one token are split until there are about eight
-// waves per SIMD's share of the card, and no finer than one pass of 64 lanes.
+// Waves per token: rows of one token are split until there are 4096 waves, four
+// for each SIMD of the card, and no finer than one pass of 64 lanes.
 int row_splits(int T, int passes) {
   const int want = (4096 + T - 1) / std::max(T, 1);
   return std::max(1, std::min(want, passes));
