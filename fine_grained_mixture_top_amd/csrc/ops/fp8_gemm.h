@@ -33,11 +33,11 @@
 //
 // What it reaches (one MI355X; a library product with one scale for everything:
 // 2910 TFLOP/s at 8192^3): 262144 gathered rows, E = 64, K = N = 2048, bf16 result
-// 1.16 ms, 1900 TFLOP/s; dense 8192^3 551 us, 1990, 32768 x 2048 x 2048 128 us, 2140.
-// What bounds it: of a 256 x 256 stage's 4300 cycles a SIMD's matrix instructions
-// take 2048, its two waves' other vector instructions 1300 (the sums 1024 of them;
+// 1.16 to 1.19 ms, 1850 to 1900 TFLOP/s; dense 8192^3 551 us, 1990, 32768 x 2048 x 2048 128 us, 2140.
+// What bounds it: of a 256 x 256 stage's 4100 cycles a SIMD's matrix instructions
+// take 2048, its two waves' other vector instructions 1400 (the sums 1024 of them;
 // 24 fewer of the others were 4%), the CU's LDS reads 930 (no bank conflicts); the
-// waves wait for data or the barrier 29% of the time, and the card lowers its clock
+// waves wait for data or the barrier 34% of the time, and the card lowers its clock
 // to 1.7..2.0 GHz.  (Larger pieces of a wave, one wave per SIMD, do not fit the
 // registers: the vector units reach the fp32 sums only in the first half of them.)
 // Without its loads, stores and sums the same loop runs at 2800 to 3100 TFLOP/s; of
