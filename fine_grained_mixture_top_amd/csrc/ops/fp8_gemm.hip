@@ -176,8 +176,8 @@ hipError_t launch_fp8_mm(const PlanArgs& p, const Fp8MmArgs& m, hipStream_t st) 
 //   262144, 128, 1536 x 512    265 / 299 / 376     8192, 8, 1024 x 1024     23.0 / 20.0 / 22.2
 //   65536, 32, 1408 x 2048     243 / 276 / 351     4096, 32, 768 x 768      19.5 / 19.6 / 19.2
 //   2048, 64, 2048 x 1024      69 / 86 / 91        65536, 8, 512 x 512      99 / 67 / 51
-// fp32 results take 128 x 64 tiles whatever the sizes, which lose little anywhere; no
-// choice by size is made.  us, 128 x 64 / 128 x 128:
+// fp32 results take 128 x 64 tiles whatever the sizes; no choice is made.  us, 128 x 64 /
+// 128 x 128:
 //   65536, 64, 2048 x 1024     500 / 450           3000, 16, 1040 x 720     24.7 / 22.7
 //   262144, 128, 1536 x 512    660 / 545           65536, 8, 512 x 512      76 / 103
 hipError_t launch_fp8_wgrad(const PlanArgs& p, int M, int N, int out, const uint8_t* qa, const float* sa,
