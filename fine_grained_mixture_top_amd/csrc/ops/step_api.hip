@@ -1,0 +1,99 @@
+// C ABI of the operators in include/moe_step_ops.h: argument validation and
+// launches.  Everything here runs on the host.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../../include/moe_step_ops.h"
+#include "step_launch.h"
+
+namespace {
+
+using namespace moe;
+
+constexpr int64_t MAX_T = (1 << 24) - 1;
+constexpr int64_t MAX_SLOTS = 1 << 30;
+constexpr int MAX_K = 1024, MAX_E = 1024;
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+int check_dtype(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 ? MOE_OK : MOE_EDTYPE; }
+
+size_t elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+
+// a workspace of `need` bytes
+int check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return MOE_OK;
+  if (!ws || !aligned(ws, 256)) return MOE_EINVAL;
+  return ws_bytes < need ? MOE_EWORKSPACE : MOE_OK;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Event pair around an operator's launches when the caller asked for timing.
+template <typename F>
+int timed(moe_profile* p, void* stream, int kernel, F launch) {
+  hipStream_t st = (hipStream_t)stream;
+  int slot = -1;
+  if (p && p->count < p->capacity && p->start && p->stop) {
+    slot = p->count++;
+    if (p->kernel) p->kernel[slot] = kernel;
+    (void)hipEventRecord((hipEvent_t)p->start[slot], st);
+  }
+  const hipError_t e = launch(st);
+  if (slot >= 0) (void)hipEventRecord((hipEvent_t)p->stop[slot], st);
+  return e == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+int check_balance(const moe_balance_desc* d) {
+  if (!d || d->flags || d->reserved) return MOE_EINVAL;
+  if (d->T < 0 || d->K < 1 || d->E < 1) return MOE_EINVAL;
+  const int s = check_dtype(d->dtype);
+  if (s != MOE_OK) return s;
+  if (d->T > MAX_T || d->K > MAX_K || d->E > MAX_E || (int64_t)d->T * d->K > MAX_SLOTS) return MOE_ESHAPE;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_balance_workspace_bytes(const moe_balance_desc* desc) {
+  return check_balance(desc) == MOE_OK ? up256(balance_ws_bytes(desc->T, desc->E)) : 0;
+}
+
+int moe_balance(const moe_balance_desc* desc, const void* logits, const int32_t* expert_idx, const uint8_t* valid,
+                int32_t* counts, int32_t* tokens, float* load, float* lse, float* loss, void* ws, size_t ws_bytes,
+                void* stream) {
+  int s = check_balance(desc);
+  if (s != MOE_OK) return s;
+  if (!counts || !tokens || !load || !loss) return MOE_EINVAL;
+  if (!aligned(counts, 4) || !aligned(tokens, 4) || !aligned(load, 4) || !aligned(loss, 4)) return MOE_EINVAL;
+  if (desc->T > 0 && (!logits || !expert_idx || !lse)) return MOE_EINVAL;
+  if (!aligned(logits, elem_bytes(desc->dtype)) || !aligned(expert_idx, 4) || !aligned(lse, 4)) return MOE_EINVAL;
+  s = check_ws(ws, ws_bytes, moe_balance_workspace_bytes(desc));
+  if (s != MOE_OK) return s;
+  const BalanceArgs a{desc->T, desc->E, desc->K, desc->dtype, logits, expert_idx, valid, counts, tokens, load, lse,
+                      loss, ws};
+  return timed(desc->profile, stream, MOE_STEP_K_BALANCE, [&](hipStream_t st) { return launch_balance(a, st); });
+}
+
+int moe_balance_bwd(const moe_balance_desc* desc, const void* logits, const int32_t* counts, const int32_t* tokens,
+                    const float* lse, const float* d_loss, const int32_t* expert_idx, const float* gate,
+                    const float* d_gate, void* dz, void* stream) {
+  const int s = check_balance(desc);
+  if (s != MOE_OK) return s;
+  if ((expert_idx || gate || d_gate) && !(expert_idx && gate && d_gate)) return MOE_EINVAL;
+  if (desc->T == 0) return MOE_OK;
+  if (!logits || !counts || !tokens || !lse || !d_loss || !dz) return MOE_EINVAL;
+  const size_t e = elem_bytes(desc->dtype);
+  if (!aligned(logits, e) || !aligned(dz, e) || !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(lse, 4) ||
+      !aligned(d_loss, 4) || !aligned(expert_idx, 4) || !aligned(gate, 4) || !aligned(d_gate, 4))
+    return MOE_EINVAL;
+  const BalanceBwdArgs a{desc->T, desc->E, desc->K, desc->dtype, logits, counts, tokens, lse, d_loss,
+                         expert_idx, gate, d_gate, dz};
+  return timed(desc->profile, stream, MOE_STEP_K_BALANCE_BWD,
+               [&](hipStream_t st) { return launch_balance_bwd(a, st); });
+}
+
+}  // extern "C"

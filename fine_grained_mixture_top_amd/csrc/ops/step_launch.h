@@ -1,0 +1,43 @@
+// Launchers of the operators declared in include/moe_step_ops.h.  They only
+// enqueue work on `st`; the ABI layer has validated every size.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../../include/moe_step_ops.h"
+
+namespace moe {
+
+// ---- balance_kernels.hip ----
+struct BalanceArgs {
+  int T, E, K, dtype;
+  const void* z;
+  const int32_t* idx;
+  const uint8_t* valid;  // or null
+  int32_t* counts;
+  int32_t* tokens;
+  float* load;
+  float* lse;
+  float* loss;
+  void* ws;
+};
+size_t balance_ws_bytes(int T, int E);
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t st);
+
+struct BalanceBwdArgs {
+  int T, E, K, dtype;
+  const void* z;
+  const int32_t* counts;
+  const int32_t* tokens;
+  const float* lse;
+  const float* d_loss;
+  const int32_t* idx;    // null: the losses' gradient alone
+  const float* gate;
+  const float* d_gate;
+  void* dz;
+};
+hipError_t launch_balance_bwd(const BalanceBwdArgs& a, hipStream_t st);
+
+}  // namespace moe

@@ -1,6 +1,8 @@
 """Single operators around the experts' products (include/moe_ops.h): tokens
 sorted by expert and back, E4M3 products with a scale per block of 128, SwiGLU
-quantized for the next product.
+quantized for the next product; and around the layer's training step
+(include/moe_step_ops.h): the router's balance and z losses with the gradient of
+its logits.
 
 Argument marshalling only, as in ``binding``: torch tensors in caller-owned
 device memory, ``MoEError`` on a non-zero status.  Tensors whose type, shape,
@@ -29,6 +31,8 @@ from . import binding as B
  MOE_OPS_K_SWIGLU_FP8, MOE_OPS_K_SWIGLU_BWD) = range(29, 41)
 KERNEL_NAMES = B.KERNEL_NAMES + ["sort", "permute", "permute_fp8", "unpermute", "unpermute_bwd", "quant_rows",
                                  "quant_weights", "quant_cols", "fp8_mm", "fp8_wgrad", "swiglu_fp8", "swiglu_bwd_rows"]
+(MOE_STEP_K_BALANCE, MOE_STEP_K_BALANCE_BWD) = range(41, 43)
+STEP_KERNEL_NAMES = KERNEL_NAMES + ["balance", "balance_bwd"]
 MOE_MM_GATHER = 1
 MOE_MM_SB_OUT_MAJOR = 2
 
@@ -51,6 +55,11 @@ class MoeMmDesc(ctypes.Structure):
     _fields_ = [("a_rows", ctypes.c_int32), ("rows", ctypes.c_int32), ("rows_used", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("out", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32), ("profile", ctypes.POINTER(B.MoeProfile))]
+
+
+class MoeBalanceDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("profile", ctypes.POINTER(B.MoeProfile))]
 
 
 _lib = None
@@ -81,6 +90,12 @@ def lib() -> ctypes.CDLL:
             "moe_swiglu_fp8": ([pd, pp, i32, i64, i32, vp, vp, vp, vp, prof, vp], i32),
             "moe_swiglu_bwd": ([pd, pp, i32, i64, i32, vp, vp, vp, prof, vp], i32),
         }
+        pb = ctypes.POINTER(MoeBalanceDesc)
+        sig.update({
+            "moe_balance_workspace_bytes": ([pb], sz),
+            "moe_balance": ([pb, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+            "moe_balance_bwd": ([pb, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
+        })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
@@ -152,6 +167,14 @@ def _call(fn, device, stream, *args):
         raise B.MoEError(fn, status)
 
 
+def _device(device):
+    """The device with its number."""
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
 class Plan:
     """Which rows belong to which expert: the sizes of a call sequence, the
     plan's device buffers (written by ``moe_sort``) and its workspace.
@@ -161,9 +184,7 @@ class Plan:
     gradients).  A plan belongs to one sequence of calls at a time."""
 
     def __init__(self, T: int, K: int, E: int, align: int = 1, device="cuda"):
-        device = torch.device(device)
-        if device.type == "cuda" and device.index is None:
-            device = torch.device("cuda", torch.cuda.current_device())
+        device = _device(device)
         if max(T, K, E, align) > _INT32 or min(T, K, E, align) < -_INT32:
             raise B.MoEError("moe_plan_rows", B.MOE_ESHAPE)
         self.T, self.K, self.E, self.align, self.device = T, K, E, align, device
@@ -383,3 +404,72 @@ def moe_swiglu_bwd(da, h, dh, plan: Plan = None, stream=None):
     pd = _need("dh", dh, (h.dtype,), (R, 2 * n), h.device)
     d, c = _plan_or_none(plan)
     _call("moe_swiglu_bwd", h.device, stream, d, c, _DTYPE[h.dtype], R, n, pa, ph, pd, _profile(plan))
+
+
+class Balance:
+    """A router's losses: the sizes of a call sequence, its results and workspace.
+
+    Written by ``moe_balance``: counts [E], tokens [1] (int32), load [E], lse [T] and loss [2] (fp32), loss[0]
+    the balance loss and loss[1] the z loss; counts, tokens and lse are what ``moe_balance_bwd`` reads.
+    A handle belongs to one sequence of calls at a time."""
+
+    def __init__(self, T: int, K: int, E: int, device="cuda"):
+        device = _device(device)
+        if max(T, K, E) > _INT32 or min(T, K, E) < -_INT32:
+            raise B.MoEError("moe_balance_workspace_bytes", B.MOE_ESHAPE)
+        self.T, self.K, self.E, self.device = T, K, E, device
+        self._descs = {dt: MoeBalanceDesc(T, E, K, code, 0, 0, None) for dt, code in _DTYPE.items()}
+        self._refs = {dt: ctypes.byref(d) for dt, d in self._descs.items()}
+        if min(T, K - 1, E - 1) < 0:
+            raise B.MoEError("moe_balance_workspace_bytes", B.MOE_EINVAL)
+        if T >= 1 << 24 or K > 1024 or E > 1024 or T * K > 1 << 30:
+            raise B.MoEError("moe_balance_workspace_bytes", B.MOE_ESHAPE)
+        self.counts = torch.zeros(E, dtype=torch.int32, device=device)
+        self.tokens = torch.zeros(1, dtype=torch.int32, device=device)
+        self.load, self.lse, self.loss = (torch.zeros(n, dtype=torch.float32, device=device) for n in (E, T, 2))
+        need = max(int(lib().moe_balance_workspace_bytes(r)) for r in self._refs.values())
+        self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        self._out = tuple(t.data_ptr() for t in (self.counts, self.tokens, self.load, self.lse, self.loss, self.ws))
+        self._ws_bytes = self.ws.numel()
+
+    def attach(self, profiler: B.Profiler):
+        """Records launch timing of the calls that take this handle."""
+        for d in self._descs.values():
+            profiler.attach(d)
+
+    def detach(self):
+        for d in self._descs.values():
+            d.profile = None
+
+
+_FLAGS = (torch.bool, torch.uint8)
+
+
+def moe_balance(bal: Balance, logits, expert_idx, valid=None, stream=None):
+    """The losses of logits [T, E] (fp32 or bf16) and the choices expert_idx [T, K] (int32; ids outside 0..E-1 are
+    no choices) into the handle.  valid [T] (bool or uint8): the tokens that count, None all; a token whose
+    logits are all -inf does not count either."""
+    pz = _need("logits", logits, _VALUES, (bal.T, bal.E), bal.device)
+    pi = _need("expert_idx", expert_idx, (torch.int32,), (bal.T, bal.K), bal.device)
+    pv = None if valid is None else _need("valid", valid, _FLAGS, (bal.T,), bal.device)
+    _call("moe_balance", bal.device, stream, bal._refs[logits.dtype], pz, pi, pv, *bal._out, bal._ws_bytes)
+
+
+def moe_balance_bwd(bal: Balance, logits, d_loss, dz, expert_idx=None, gate=None, d_gate=None, stream=None):
+    """dz [T, E] (the logits' type): the gradient of d_loss[0] loss[0] + d_loss[1] loss[1] (d_loss [2], fp32, on the
+    device), and with expert_idx, gate and d_gate [T, K] that of gates which are a softmax over the token's chosen
+    logits.  The handle holds moe_balance's results for the same logits."""
+    dt = logits.dtype if isinstance(logits, torch.Tensor) else None
+    pz = _need("logits", logits, _VALUES, (bal.T, bal.E), bal.device)
+    pd = _need("d_loss", d_loss, _F32, (2,), bal.device)
+    po = _need("dz", dz, (dt,), (bal.T, bal.E), bal.device)
+    given = [t is not None for t in (expert_idx, gate, d_gate)]
+    if any(given) and not all(given):
+        raise ValueError("expert_idx, gate and d_gate: all three or none")
+    pi = pg = pdg = None
+    if all(given):
+        pi = _need("expert_idx", expert_idx, (torch.int32,), (bal.T, bal.K), bal.device)
+        pg = _need("gate", gate, _F32, (bal.T, bal.K), bal.device)
+        pdg = _need("d_gate", d_gate, _F32, (bal.T, bal.K), bal.device)
+    counts, tokens, _, lse, _, _ = bal._out
+    _call("moe_balance_bwd", bal.device, stream, bal._refs[dt], pz, counts, tokens, lse, pd, pi, pg, pdg, po)

@@ -1,0 +1,85 @@
+/*
+ * moe_step_ops.h -- operators for what surrounds a layer's products in a
+ * training step, and for the weights that the step leaves:
+ *
+ *   moe_balance, moe_balance_bwd: the router's balance loss and z loss with
+ *     the experts' counts, and the gradient of the router's logits;
+ *   moe_orthogonalize: an update (a weight gradient or its momentum)
+ *     orthogonalised by Newton-Schulz products, for a stack of matrices;
+ *   moe_mxfp4_quant_weights, moe_mxfp4_mm: weights in OCP MXFP4 (4 bits, a
+ *     scale per 32) and products of bf16 rows with them, grouped or dense.
+ *
+ * The conventions of moe.h and moe_ops.h hold: device pointers owned by the
+ * caller, no allocation, no host synchronisation, stream-ordered calls that can
+ * be captured into a graph, arguments checked on the host before anything is
+ * launched, results bit-identical from run to run.  The current device must be
+ * the one the buffers and the stream belong to.  Calls share no state: two calls
+ * may overlap when neither writes what the other one uses (a workspace is
+ * written by its call).  An output overlaps no input of its call.
+ */
+#ifndef MOE_STEP_OPS_H
+#define MOE_STEP_OPS_H
+
+#include "moe_ops.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* kernel ids reported in moe_profile.kernel, after those of moe_ops.h */
+#define MOE_STEP_K_BALANCE       41
+#define MOE_STEP_K_BALANCE_BWD   42
+
+/*
+ * Balance loss and z loss of a router.  logits z [T,E] (dtype MOE_F32 or
+ * MOE_BF16), expert_idx [T,K] int32 the experts chosen, valid [T] bytes or NULL
+ * (all valid).  A token counts when it is valid and one of its logits is above
+ * -inf (masked experts have logits of -inf, and any value in a token that does
+ * not count is without effect).  With n counting tokens, p_t = softmax(z_t):
+ *     counts[e]  choices of expert e by counting tokens (an id outside 0..E-1
+ *                is no choice; an expert chosen twice by a token counts twice)
+ *     tokens[0]  n
+ *     load[e]    (1/n) sum_t p_te
+ *     lse[t]     log sum_e exp z_te, -inf for a token that does not count
+ *     loss[0]    E / (n K) sum_e counts[e] load[e]     (1 when balanced)
+ *     loss[1]    (1/n) sum_t lse_t^2
+ * All zeros (lse -inf) for n = 0.  Sums run in fp32 or wider.
+ *   0 <= T < 2^24, 1 <= K <= 1024, 1 <= E <= 1024, T * K <= 2^30.
+ */
+typedef struct moe_balance_desc {
+    int32_t  T, E, K;
+    int32_t  dtype;         /* of the logits and their gradient */
+    uint32_t flags;         /* must be 0 */
+    uint32_t reserved;      /* must be 0 */
+    moe_profile* profile;   /* NULL, or launch timing (see moe.h) */
+} moe_balance_desc;
+
+/* Workspace of moe_balance in bytes; 0 for an invalid descriptor.  Host only. */
+size_t moe_balance_workspace_bytes(const moe_balance_desc* desc);
+
+int moe_balance(const moe_balance_desc* desc, const void* logits, const int32_t* expert_idx, const uint8_t* valid,
+                int32_t* counts, int32_t* tokens, float* load, float* lse, float* loss, void* ws, size_t ws_bytes,
+                void* stream);
+
+/*
+ * Gradient of the logits.  counts, tokens, lse: of moe_balance on the same
+ * logits; d_loss [2] fp32 on the device, the gradients of the two losses (their
+ * weights in the total loss):
+ *     dz[t,e] = p_te ( d_loss[0] E / (n^2 K) (counts[e] - sum_j counts[j] p_tj)
+ *                      + d_loss[1] 2/n lse_t )             (0 for a token that does not count)
+ * and, when gate and d_gate [T,K] fp32 are given, the gradient of gates that
+ * are a softmax over the token's chosen logits (moe_route's):
+ *     dz[t, expert_idx[t,k]] += gate[t,k] (d_gate[t,k] - sum_j gate[t,j] d_gate[t,j])
+ * for the choices inside 0..E-1, of every token (what a dropped choice holds is
+ * without effect).  expert_idx, gate and d_gate: all three or none.  dz [T,E] in
+ * the logits' type, rounded once.
+ */
+int moe_balance_bwd(const moe_balance_desc* desc, const void* logits, const int32_t* counts, const int32_t* tokens,
+                    const float* lse, const float* d_loss, const int32_t* expert_idx, const float* gate,
+                    const float* d_gate, void* dz, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_STEP_OPS_H */

@@ -1,0 +1,102 @@
+"""The operators of include/moe_step_ops.h in float64, written from their
+formulas (nothing shared with the kernels), and the error bounds their results
+are held to.
+
+Rounding to a type is off by at most half a step: bf16 2^-8, fp32 2^-24 of the
+value.  A sum of fp32 terms is off by at most its chain of additions times 2^-24
+of the sum of magnitudes."""
+import torch
+
+NEG = float("-inf")
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+def within(got, ref, bound, what=""):
+    """Equal infinities and NaNs, everything else inside its bound."""
+    got, ref = got.double(), ref.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), (what, "NaN")
+    inf = torch.isinf(ref)
+    assert torch.equal(got[inf], ref[inf]), (what, "inf")
+    fine = torch.isfinite(ref)
+    assert bool(torch.isfinite(got[fine]).all()), (what, "not finite")
+    off = (got - ref).abs()[fine]
+    bound = bound.expand_as(ref)[fine] if isinstance(bound, torch.Tensor) else torch.full_like(off, bound)
+    bad = ~(off <= bound)
+    assert not bad.any(), (what, int(bad.sum()), float(off[bad].max()), float((off / bound.clamp(min=1e-300))[bad].max()))
+
+
+# ---------------------------------------------------------------- balance
+
+def balance_ref(z, idx, valid=None):
+    """Everything moe_balance gives, in float64, and p with zeros for tokens that do not count."""
+    T, E = z.shape
+    K = idx.shape[1]
+    z = z.double()
+    counting = (z > NEG).any(1) | torch.isnan(z).any(1)
+    if valid is not None:
+        counting = counting & valid.bool()
+    p, lse = torch.zeros_like(z), torch.full((T,), NEG, dtype=torch.float64, device=z.device)
+    if counting.any():
+        p[counting] = torch.softmax(z[counting], 1)
+        lse[counting] = torch.logsumexp(z[counting], 1)
+    n = int(counting.sum())
+    counts = torch.zeros(E, dtype=torch.int64, device=z.device)
+    for k in range(K):
+        e = idx[:, k].long()
+        e = e[counting & (e >= 0) & (e < E)]
+        counts += torch.bincount(e, minlength=E)
+    per = 1.0 / n if n else 0.0
+    load = p.sum(0) * per
+    loss = torch.stack([(counts.double() * load).sum() * per * E / K, (lse[counting] ** 2).sum() * per])
+    return dict(counts=counts, n=n, load=load, lse=lse, loss=loss, p=p, counting=counting)
+
+
+def spread(z):
+    """The largest distance of a finite logit from its row's maximum."""
+    z = z.double()
+    m = z.amax(1, keepdim=True)
+    d = torch.where(torch.isfinite(z) & torch.isfinite(m), m - z, torch.zeros_like(z))
+    return float(d.max()) if d.numel() else 0.0
+
+
+def balance_steps(z):
+    """Relative error of a mean probability in steps of 2^-23.  An exponential of x = z - max: x and x log2(e)
+    round and log2(e) itself is rounded, |x| 2^-24 each, and the instruction 2^-23; the row's sum and its
+    reciprocal: at most 16 additions in a lane, 6 between lanes, 2 more.  Then a lane's sum over its rows
+    (at most T / 2048 + 64, or for the one-workgroup form T L / 512 <= 64 as T E <= 2^14), 6 between lanes, 8
+    waves, 512 / 16 lines and 16 of their sums, the multiplication by 1 / n."""
+    return 2 * spread(z) + 24 + z.shape[0] / 2048 + 64 + 6 + 8 + 32 + 16 + 4
+
+
+def lse_bound(lse):
+    """max + ln(2) log2(sum): the sum's relative error is at most sum_i p_i (2 |x_i| + 24) 2^-23, and sum p |x| is at
+    most the entropy, ln 1024 < 7; the logarithm's instruction, its constant and the addition: 2^-22 of 7 + |lse|."""
+    return torch.where(torch.isfinite(lse), (lse.abs() + 7) * 2.0 ** -22 + 38 * 2.0 ** -23, torch.zeros_like(lse))
+
+
+def balance_bwd_ref(z, idx, ref, d_loss, gate=None, d_gate=None):
+    """(dz, its bound without the result's rounding) in float64."""
+    T, E = z.shape
+    K = idx.shape[1]
+    n = max(ref["n"], 1)
+    gb, gz = float(d_loss[0]), float(d_loss[1])
+    p, f = ref["p"], ref["counts"].double() * (gb * E / (n * n * K))
+    lse = torch.where(ref["counting"], ref["lse"], torch.zeros_like(ref["lse"]))
+    inner = (p * f).sum(1, keepdim=True)
+    dz = p * (f - inner + (2.0 * gz / n) * lse[:, None])
+    mag = p * (f.abs() + (p * f.abs()).sum(1, keepdim=True) + abs(2.0 * gz / n) * lse.abs()[:, None])
+    # p: its exponent's three roundings and lse's error; the sums: E terms at most 16 in a lane and 6 lanes; products
+    # (above 32 lse is not used for p)
+    finite = lse.abs().max().clamp(max=32.0) if T else 0.0
+    bound = mag * ((3 * spread(z) + 4 * float(finite) + 14 + 38 + 24 + 16) * 2.0 ** -23)
+    if gate is not None:
+        there = (idx >= 0) & (idx < E)
+        g = torch.where(there, gate.double(), 0.0)
+        d = torch.where(there, d_gate.double(), 0.0)
+        v = g * (d - (g * d).sum(1, keepdim=True))
+        m = g.abs() * (d.abs() + (g * d).abs().sum(1, keepdim=True))
+        at = torch.where(there, idx, torch.zeros_like(idx)).long()
+        dz = dz.scatter_add(1, at, v)
+        # the inner sum: K terms; the products; then up to K values join an element
+        bound = bound.scatter_add(1, at, m * ((2 * K + 8) * 2.0 ** -23)) + dz.abs() * K * 2.0 ** -24
+    return dz, bound

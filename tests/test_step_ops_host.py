@@ -1,0 +1,106 @@
+"""Host-side checks of the C ABI and binding of include/moe_step_ops.h (no GPU):
+exports, constants, sizes, refusals before anything is launched."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+from fine_grained_mixture_top_amd import binding as B
+from fine_grained_mixture_top_amd import ops
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "moe_step_ops.h")
+P = 4096  # an aligned address that no refused call touches
+
+
+def ref(x):
+    return ctypes.byref(x)
+
+
+def test_header_functions_and_constants():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    lib = ops.lib()
+    names = set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", text))
+    assert names
+    for n in names:
+        assert hasattr(lib, n) and getattr(lib, n).argtypes is not None, n
+    consts = dict(re.findall(r"#define\s+(MOE_[A-Z0-9_]+)\s+(\d+)u?", text))
+    ids = [int(v) for k, v in consts.items() if k.startswith("MOE_STEP_K_")]
+    assert sorted(ids) == list(range(len(ops.KERNEL_NAMES), len(ops.STEP_KERNEL_NAMES)))
+    for k, v in consts.items():
+        assert getattr(ops, k) == int(v), k
+
+
+def bdesc(T=8, E=4, K=2, dtype=B.MOE_F32, flags=0, reserved=0):
+    return ops.MoeBalanceDesc(T, E, K, dtype, flags, reserved, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), B.MOE_EINVAL), (dict(K=0), B.MOE_EINVAL), (dict(E=0), B.MOE_EINVAL), (dict(dtype=2), B.MOE_EDTYPE),
+    (dict(flags=1), B.MOE_EINVAL), (dict(reserved=1), B.MOE_EINVAL), (dict(T=1 << 24), B.MOE_ESHAPE),
+    (dict(K=1025), B.MOE_ESHAPE), (dict(E=1025), B.MOE_ESHAPE), (dict(T=(1 << 24) - 1, K=65), B.MOE_ESHAPE),
+])
+def test_balance_descriptors_refused(kw, code):
+    lib, d = ops.lib(), bdesc(**kw)
+    assert lib.moe_balance_workspace_bytes(ref(d)) == 0
+    assert lib.moe_balance(ref(d), P, P, None, P, P, P, P, P, P, 1 << 30, None) == code
+    assert lib.moe_balance_bwd(ref(d), P, P, P, P, P, None, None, None, P, None) == code
+
+
+def test_balance_refusals():
+    lib, d = ops.lib(), bdesc(T=3000, E=64)
+    need = lib.moe_balance_workspace_bytes(ref(d))
+    assert need > 0 and need % 256 == 0
+    good = [P, P, None, P, P, P, P, P, P, need]
+    for i in (0, 1, 3, 4, 5, 6, 7, 8):
+        bad = list(good)
+        bad[i] = None
+        assert lib.moe_balance(ref(d), *bad, None) == B.MOE_EINVAL, i
+        if i != 2:
+            bad[i] = P + 1
+            assert lib.moe_balance(ref(d), *bad, None) == B.MOE_EINVAL, i
+    assert lib.moe_balance(ref(d), *good[:-1], need - 1, None) == B.MOE_EWORKSPACE
+    assert lib.moe_balance(None, *good, None) == B.MOE_EINVAL
+    good = [P, P, P, P, P, None, None, None, P]
+    for i in (0, 1, 2, 3, 4, 8):
+        bad = list(good)
+        bad[i] = None
+        assert lib.moe_balance_bwd(ref(d), *bad, None) == B.MOE_EINVAL, i
+        bad[i] = P + 2 if i else P + 1
+        assert lib.moe_balance_bwd(ref(d), *bad, None) == B.MOE_EINVAL, i
+    for gates in ((P, None, None), (None, P, P), (P, P, None), (P, None, P)):
+        assert lib.moe_balance_bwd(ref(d), *good[:5], *gates, P, None) == B.MOE_EINVAL
+    # no tokens: nothing to do
+    assert lib.moe_balance_bwd(ref(bdesc(T=0)), *[None] * 9, None) == B.MOE_OK
+
+
+def test_balance_binding_refuses():
+    for kw, code in ((dict(T=-1, K=1, E=1), B.MOE_EINVAL), (dict(T=1, K=0, E=1), B.MOE_EINVAL),
+                     (dict(T=1 << 24, K=1, E=1), B.MOE_ESHAPE), (dict(T=1, K=1, E=1025), B.MOE_ESHAPE),
+                     (dict(T=1 << 40, K=1, E=1), B.MOE_ESHAPE)):
+        with pytest.raises(B.MoEError) as e:
+            ops.Balance(**kw, device="cpu")
+        assert e.value.status == code
+    b = ops.Balance(6, 2, 4, device="cpu")
+    z, idx, dz = torch.zeros(6, 4), torch.zeros(6, 2, dtype=torch.int32), torch.zeros(6, 4)
+    d = torch.ones(2)
+    with pytest.raises(ValueError, match="a GPU is needed"):
+        ops.moe_balance(b, z, idx)
+    with pytest.raises(ValueError, match="logits"):
+        ops.moe_balance(b, z.half(), idx)
+    with pytest.raises(ValueError, match="logits"):
+        ops.moe_balance(b, torch.zeros(4, 6).t(), idx)
+    with pytest.raises(ValueError, match="expert_idx"):
+        ops.moe_balance(b, z, idx.long())
+    with pytest.raises(ValueError, match="valid"):
+        ops.moe_balance(b, z, idx, valid=torch.ones(6))
+    with pytest.raises(ValueError, match="dz"):
+        ops.moe_balance_bwd(b, z, d, dz.bfloat16())
+    with pytest.raises(ValueError, match="d_loss"):
+        ops.moe_balance_bwd(b, z, torch.ones(3), dz)
+    with pytest.raises(ValueError, match="all three or none"):
+        ops.moe_balance_bwd(b, z, d, dz, idx, torch.ones(6, 2))
+    with pytest.raises(ValueError, match="a tensor is needed"):
+        ops.moe_balance_bwd(b, None, d, dz)
