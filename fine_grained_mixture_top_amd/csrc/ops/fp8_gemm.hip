@@ -1,39 +1,12 @@
 // Launches of the E4M3 products (fp8_gemm.h).
 #include <algorithm>
-#include <atomic>
 
 #include "fp8_gemm.h"
+#include "launch_util.h"
 
 namespace moe {
 
 namespace {
-
-// the current device, or -1
-int device() {
-  int dev = -1;
-  return hipGetDevice(&dev) == hipSuccess ? dev : -1;
-}
-
-int cu_count(int dev) {
-  static std::atomic<int> known[64];  // asked for once per device
-  int cus = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-  if (cus > 0) return cus;
-  if (dev < 0 || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    return 256;
-  if (dev < 64) known[dev].store(cus, std::memory_order_relaxed);
-  return cus;
-}
-
-// Dynamic LDS beyond the default, allowed once per kernel (its `done`) and device.
-template <typename K>
-hipError_t allow_lds(K* kernel, int bytes, int dev, std::atomic<uint64_t>& done) {
-  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-  if (bit && (done.load(std::memory_order_relaxed) & bit)) return hipSuccess;
-  const hipError_t e =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
 
 template <int BM, int BN, int WM, int WN, bool WG, typename O, int LATE = 0>
 hipError_t launch_tiles(const f8::Args& a, int64_t tiles, hipStream_t st) {
@@ -49,8 +22,6 @@ hipError_t launch_tiles(const f8::Args& a, int64_t tiles, hipStream_t st) {
   hipLaunchKernelGGL(k, dim3(grid), dim3(C::NTH), C::SMEM, st, a);
   return hipGetLastError();
 }
-
-int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Row tiles at most: every segment with rows may end inside one.
 int64_t row_tiles(const f8::Args& a, int64_t used, int BM) { return div_up(used, BM) + std::min<int64_t>(a.E, used); }

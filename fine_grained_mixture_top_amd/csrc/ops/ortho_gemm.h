@@ -1,0 +1,274 @@
+// Products of the matrices that orthogonalise an update (include/moe_step_ops.h:
+// moe_orthogonalize).
+//
+// Numbers.  The matrices of the iteration are fp32 numbers times a power of two,
+// held as the sum of two fp16 numbers (22 bits: the second holds what the first's
+// rounding left), and a product of two of them is three fp16 products summed in
+// fp32, hi hi + hi lo + lo hi; the fourth is below 2^-22 of the product.  The fp16
+// matrix cores do that at a third of 2.5 PFLOP/s where the fp32 ones reach 0.16.
+// bf16 input needs one fp16 number per value (its 8 bits fit, scaled by a power of
+// two), so products with it take one or two.
+//
+// Layout.  Both operands of C = A B^T are rows with the reduction contiguous,
+// padded with zeros to a multiple of 64: one part, the fp16 numbers themselves; two
+// parts, lines of 128 bytes with 32 numbers' hi and then their lo.
+#pragma once
+
+#include "lds_stage.h"
+
+namespace moe {
+namespace ortho {
+
+typedef _Float16 f16x8_v __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4_v __attribute__((ext_vector_type(4)));
+
+// x as hi + lo
+__device__ __forceinline__ void split(float x, _Float16& hi, _Float16& lo) {
+  hi = (_Float16)x;
+  lo = (_Float16)(x - (float)hi);
+}
+
+// bytes of a row of n numbers in `parts` parts
+__host__ __device__ inline int64_t pitch(int64_t n, int parts) { return (n + 63) / 64 * 128 * parts; }
+// byte of number i of a row of two parts (its lo is 64 bytes further on)
+__device__ __forceinline__ int64_t at2(int i) { return (int64_t)(i >> 5) * 128 + (i & 31) * 2; }
+
+// One product per matrix of the batch.  c = alpha * acc, and where d is given
+// + beta * d + diag * I; alpha times alpha_e[matrix] (power_e: its square) when given.
+struct Job {
+  const char* a;
+  const char* b;
+  char* c;
+  const char* d;
+  float alpha, beta, diag;
+};
+
+struct Args {
+  Job job[2];
+  int jobs, batch;
+  const float* alpha_e;
+  bool square;              // alpha_e squared
+  int ra, rb;               // rows of a and b (of c, and its columns)
+  int stages;
+  int64_t sa, sb, sc;       // bytes from one matrix to the next
+  int pa, pb, pc;           // bytes of a row (pc: of c, in two parts)
+  // results of the last product
+  void* o;
+  int64_t so;               // elements from one matrix to the next
+  // products between groups of steps: c in two parts, and its transpose
+  char* ct;
+  int64_t sct;
+  int pct;
+};
+
+enum Epi { SYM, SPLIT, OUT };
+
+template <int BM, int BN, int WM, int WN, int PA, int PB>
+struct Cfg {
+  static constexpr int W = WM * WN, NTH = 64 * W;
+  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  // one part on both sides: 64 numbers of the reduction per stage, else 32
+  static constexpr bool WIDE = PA == 1 && PB == 1;
+  static constexpr int LA = WIDE || PA == 2 ? 128 : 64, LB = WIDE || PB == 2 ? 128 : 64;  // bytes of a line per stage
+  static constexpr int IA = BM * LA / 1024 / W, IB = BN * LB / 1024 / W;                  // 1 KB loads per wave
+  static constexpr int STAGE = BM * LA + BN * LB;
+  static constexpr int SMEM = 2 * STAGE;
+  static_assert(BM * LA % (1024 * W) == 0 && BN * LB % (1024 * W) == 0, "loads per wave");
+};
+
+// The 16-byte chunk c of line r of a stage lies in slot c ^ key(r), so that eight
+// lanes that read a chunk of eight neighbouring lines hit eight different ones.
+template <int LINE> __device__ __forceinline__ int key(int r) { return LINE == 128 ? r & 7 : (r >> 1) & 3; }
+
+template <int BM, int BN, int WM, int WN, int PA, int PB, Epi EPI, typename O>
+__global__ void __launch_bounds__(64 * WM * WN, 2)
+k_ortho_gemm(Args g) {
+  using C = Cfg<BM, BN, WM, WN, PA, PB>;
+  constexpr int FM = C::FM, FN = C::FN;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w / WN, wn = w % WN;
+
+  // ---- the tile: matrix by matrix, a matrix's tiles on one XCD ----
+  const int MT = (g.ra + BM - 1) / BM, NT = (g.rb + BN - 1) / BN;
+  const int per = EPI == SYM ? MT * (MT + 1) / 2 : MT * NT;
+  int id = xcd_virtual_id(blockIdx.x, gridDim.x);
+  if (id >= per * g.jobs * g.batch) return;
+  const int e = id / (per * g.jobs);
+  id -= e * per * g.jobs;
+  const int jb = id / per;
+  id -= jb * per;
+  const Job& job = g.job[jb];
+  int ti, tj;
+  if constexpr (EPI == SYM) {  // the lower triangle, row by row
+    ti = (int)((sqrtf(8.f * (float)id + 1.f) - 1.f) * 0.5f);
+    while (ti * (ti + 1) / 2 > id) --ti;
+    while ((ti + 1) * (ti + 2) / 2 <= id) ++ti;
+    tj = id - ti * (ti + 1) / 2;
+  } else {
+    ti = id / NT;
+    tj = id - ti * NT;
+  }
+  const int m0 = ti * BM, n0 = tj * BN;
+
+  // ---- loads ----
+  const __amdgpu_buffer_rsrc_t ra = rsrc(job.a + e * g.sa, (uint32_t)(g.ra * (int64_t)g.pa));
+  const __amdgpu_buffer_rsrc_t rb = rsrc(job.b + e * g.sb, (uint32_t)(g.rb * (int64_t)g.pb));
+  auto offset = [&](auto line, int i, int first, int rows, int pitch) -> uint32_t {
+    constexpr int LINE = decltype(line)::value, SLOTS = LINE / 16;
+    const int r = i * (1024 / LINE) + lane / SLOTS;  // line of the stage
+    const int c = (lane & (SLOTS - 1)) ^ key<LINE>(r);
+    return first + r < rows ? (uint32_t)(first + r) * (uint32_t)pitch + c * 16u : OOB;
+  };
+  uint32_t oa[C::IA], ob[C::IB];
+#pragma unroll
+  for (int i = 0; i < C::IA; ++i) oa[i] = offset(std::integral_constant<int, C::LA>(), C::IA * w + i, m0, g.ra, g.pa);
+#pragma unroll
+  for (int i = 0; i < C::IB; ++i) ob[i] = offset(std::integral_constant<int, C::LB>(), C::IB * w + i, n0, g.rb, g.pb);
+  auto load = [&](int s, int buf) {
+    char* st = smem + buf * C::STAGE;
+#pragma unroll
+    for (int i = 0; i < C::IA; ++i) load16_lds(ra, st + (C::IA * w + i) * 1024, oa[i], (uint32_t)(s * C::LA));
+#pragma unroll
+    for (int i = 0; i < C::IB; ++i) load16_lds(rb, st + BM * C::LA + (C::IB * w + i) * 1024, ob[i], (uint32_t)(s * C::LB));
+  };
+
+  // ---- products ----
+  f32x4_v acc[FM][FN];
+#pragma unroll
+  for (int j = 0; j < FM; ++j)
+#pragma unroll
+    for (int i = 0; i < FN; ++i) acc[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  const int p = lane & 15, h = lane >> 4;
+  constexpr int NA = C::LA / 64, NB = C::LB / 64;  // fragments of a line
+  const lds_ptr_t la = (lds_ptr_t)smem + (wm * C::TM + p) * C::LA;
+  const lds_ptr_t lb = (lds_ptr_t)smem + BM * C::LA + (wn * C::TN + p) * C::LB;
+  int slot_a[NA], slot_b[NB];
+#pragma unroll
+  for (int x = 0; x < NA; ++x) slot_a[x] = ((h + 4 * x) ^ key<C::LA>(p)) * 16;
+#pragma unroll
+  for (int x = 0; x < NB; ++x) slot_b[x] = ((h + 4 * x) ^ key<C::LB>(p)) * 16;
+
+  load(0, 0);
+  for (int s = 0; s < g.stages; ++s) {
+    const int buf = s & 1;
+    wait_vm<0>();
+    lds_sync();  // the stage is there, and everybody is done with the other buffer
+    if (s + 1 < g.stages) load(s + 1, buf ^ 1);
+    const int at = buf * C::STAGE;
+    f16x8_v fb[FN][NB], fa[2][NA];
+#pragma unroll
+    for (int x = 0; x < NA; ++x) fa[0][x] = lds_ld<f16x8_v>(la + at + slot_a[x]);
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int x = 0; x < NB; ++x) fb[i][x] = lds_ld<f16x8_v>(lb + at + 16 * i * C::LB + slot_b[x]);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      if (j + 1 < FM)
+#pragma unroll
+        for (int x = 0; x < NA; ++x) fa[(j + 1) & 1][x] = lds_ld<f16x8_v>(la + at + 16 * (j + 1) * C::LA + slot_a[x]);
+      auto mul = [&](int xa, int xb) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[i][xb], fa[j & 1][xa], acc[j][i], 0, 0, 0);
+      };
+      mul(0, 0);
+      if constexpr (C::WIDE) {
+        mul(1, 1);  // the next 32 of the reduction
+      } else {
+        if constexpr (PB == 2) mul(0, 1);
+        if constexpr (PA == 2) mul(1, 0);
+      }
+    }
+  }
+
+  // ---- results: a lane holds, of row p of a piece, the columns 4 h .. 4 h + 3 ----
+  float alpha = job.alpha;
+  if (g.alpha_e) alpha *= g.square ? g.alpha_e[e] * g.alpha_e[e] : g.alpha_e[e];
+  const int r0 = m0 + wm * C::TM + p, c0 = n0 + wn * C::TN + 4 * h;
+  if constexpr (EPI == OUT) {
+    O* const out = reinterpret_cast<O*>(g.o) + e * g.so;
+    const bool vec = g.rb % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(O) - 1)) == 0;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int r = r0 + 16 * j;
+      if (r >= g.ra) continue;
+      O* row = out + (int64_t)r * g.rb;
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        const int c = c0 + 16 * i;
+        const f32x4_v v = acc[j][i] * alpha;
+        if (vec && c < g.rb) {
+          if constexpr (sizeof(O) == 2)
+            *reinterpret_cast<uint2*>(row + c) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
+          else
+            *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (c + x < g.rb) row[c + x] = Elem<O>::from_f(v[x]);
+        }
+      }
+    }
+  } else {
+    // c [ra][columns up to the padding] and, but for a diagonal tile, its transpose: a
+    // symmetric product's other half, or the next group's other layout
+    const int cols = (g.rb + 63) & ~63, rows = (g.ra + 63) & ~63;
+    char* const out = job.c + e * g.sc;
+    char* const outt = EPI == SYM ? out : g.ct + e * g.sct;
+    const int pt = EPI == SYM ? g.pc : g.pct;
+    const char* const d = job.d ? job.d + e * g.sc : nullptr;
+    const bool mirror = EPI != SYM || ti != tj;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int r = r0 + 16 * j;
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        const int c = c0 + 16 * i;
+        if (c >= cols || r >= rows) continue;
+        f32x4_v v = acc[j][i] * alpha;
+        if (EPI == SYM && d) {
+          f32x4_v u = {0.f, 0.f, 0.f, 0.f};
+          if (r < g.ra) {
+            const char* at = d + (int64_t)r * g.pc + at2(c);
+            const f16x4_v dh = *reinterpret_cast<const f16x4_v*>(at), dl = *reinterpret_cast<const f16x4_v*>(at + 64);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) u[x] = (float)dh[x] + (float)dl[x];
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            v[x] = fmaf(job.beta, u[x], v[x]);
+            if (r == c + x && r < g.ra) v[x] += job.diag;
+          }
+        }
+        f16x4_v hi, lo;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          _Float16 vh, vl;
+          split(v[x], vh, vl);
+          hi[x] = vh;
+          lo[x] = vl;
+        }
+        if (r < g.ra) {
+          char* at = out + (int64_t)r * g.pc + at2(c);
+          *reinterpret_cast<f16x4_v*>(at) = hi;
+          *reinterpret_cast<f16x4_v*>(at + 64) = lo;
+        }
+        if (mirror) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (c + x >= g.rb) continue;
+            char* at = outt + (int64_t)(c + x) * pt + at2(r);
+            *reinterpret_cast<_Float16*>(at) = hi[x];
+            *reinterpret_cast<_Float16*>(at + 64) = lo[x];
+          }
+        }
+      }
+    }
+  }
+}
+
+}  // namespace ortho
+}  // namespace moe

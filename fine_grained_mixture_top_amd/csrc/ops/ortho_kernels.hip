@@ -1,0 +1,452 @@
+// An update orthogonalised by Newton-Schulz products (include/moe_step_ops.h:
+// moe_orthogonalize).
+//
+// X is the update, m x k with m <= k (transposed where it is tall), over its
+// Frobenius norm; a step is X <- (a I + b A + c A^2) X with A = X X^T.  A, its
+// polynomials P = a I + b A + c A^2 and their products commute and are symmetric, so
+// steps can run on them alone:
+//     A_1 = P A P,   Q = P_n ... P_1,   X_n = Q X_0
+// which needs one product with the m x k matrix for a group of steps, and half the
+// tiles of every product but that one.
+//   Rounding.  A singular value s enters A as s^2 beside the largest one's 1, and
+// every step multiplies a small one's share by a^2: what A's fp32 sums lost grows
+// with it, to (product of a)^2 2^-24 of a small direction's P.  Measured on m x k =
+// 64 x 64 to 512 x 512, gaussian, 1/i and low-rank spectra, five steps with a = 3.4445:
+// error of the result 1.3e-6 to 3.2e-6 with one step a group (products in fp32
+// throughout: 1.1e-6 to 3.4e-6), 1.4e-6 to 1.1e-5 with two and three, 1.4e-6 to 3.7e-4
+// with five.  So fp32 results take one step a group, and bf16 results, whose
+// rounding is 1.7e-3, as many as keep the product of the |a| at 512 or below.
+#include <algorithm>
+#include <cmath>
+
+#include "launch_util.h"
+#include "ortho_gemm.h"
+#include "step_launch.h"
+
+namespace moe {
+
+namespace {
+
+using namespace ortho;
+
+constexpr int NORM_PARTS = 64;    // partial sums of a matrix at most
+constexpr int X_EXP = 13;         // X's norm in fp16 parts lies in [2^13, 2^14)
+
+// ---- sum of squares, in 64 bits: no scaling is needed for any finite input ----
+template <typename T, int V>
+__global__ void __launch_bounds__(256)
+k_ortho_norm(const T* g, int64_t elems, int parts, double* sums) {
+  const int e = blockIdx.y;
+  const T* p = g + (int64_t)e * elems;
+  double s = 0.0;
+  const int64_t vecs = elems / V, step = (int64_t)parts * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += step) {
+    T v[V];
+    if constexpr (V > 1) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+      __builtin_memcpy(v, &u, 16);
+    } else {
+      v[0] = p[i];
+    }
+#pragma unroll
+    for (int x = 0; x < V; ++x) {
+      const double d = (double)Elem<T>::to_f(v[x]);
+      s = fma(d, d, s);
+    }
+  }
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  __shared__ double ws[4];
+  if ((threadIdx.x & 63) == 0) ws[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) sums[(int64_t)e * NORM_PARTS + blockIdx.x] = (ws[0] + ws[1]) + (ws[2] + ws[3]);
+}
+
+// The update as fp16 parts in both layouts, times a power of two that brings its norm
+// to 2^13 .. 2^14, and the factors that go with the groups of steps.  A matrix whose
+// norm is far below eps starts far below 1 and grows with the steps; so that its parts
+// keep their bits, the X between two groups carries a power of two of its own, from a
+// bound of its norm that is followed through the steps:
+//     back[i]    X of group i over its stored numbers (but for the exponent that all have)
+//     on[i]      what the stored numbers of group i + 1 are of Q times those of group i
+constexpr int MAX_STEPS = 64;
+struct Convert {
+  const void* g;
+  int M, N;
+  const double* sums;
+  int parts;      // partial sums of a matrix
+  double eps;
+  char* same;     // rows of g
+  char* trans;    // columns of g
+  int64_t ssame, strans;
+  float* back;    // [groups][gridDim.z]
+  float* on;
+  int groups;
+  uint8_t steps[MAX_STEPS];  // of each group
+  float coef[3 * MAX_STEPS];
+};
+
+// (one thread)
+__device__ void factors(const Convert& a, int e, int nb, double norm, int ex) {
+  const bool fine = norm < __builtin_inf();
+  const double first = norm == 0.0 ? 0.0 : scalbn(1.0 / (norm + a.eps), -ex);
+  const float nan = __builtin_nanf("");
+  a.back[e] = fine ? (float)first : nan;
+  float most = norm == 0.0 ? 0.f : (float)(norm / (norm + a.eps));  // of |X|
+  const float* c = a.coef;
+  int t = 0;
+  for (int i = 0; i + 1 < a.groups; ++i) {
+    for (int s = 0; s < a.steps[i]; ++s, c += 3) {
+      float m = 0.f;
+      for (int x = 1; x <= 16; ++x) {
+        const float v = most * (float)x * 0.0625f, l = v * v;
+        m = fmaxf(m, fabsf(v * fmaf(l, fmaf(l, c[2], c[1]), c[0])));
+      }
+      most = m;
+    }
+    const int next = most > 0.f && most < __builtin_inff() ? max(-60, min(120, -ilogbf(most))) : 0;
+    const double f = i == 0 ? first : scalbn(1.0, -t);
+    a.on[i * nb + e] = fine ? (float)scalbn(f, next) : nan;
+    a.back[(i + 1) * nb + e] = fine ? (float)scalbn(1.0, -next) : nan;
+    t = next;
+  }
+}
+
+template <typename T, int P>
+__global__ void __launch_bounds__(256)
+k_ortho_convert(Convert a) {
+  __shared__ float tile[64][65];
+  const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tid = threadIdx.x;
+  double s = 0.0;
+  for (int i = 0; i < a.parts; ++i) s += a.sums[(int64_t)e * NORM_PARTS + i];
+  const double norm = sqrt(s);
+  const int ex = norm > 0.0 && norm < __builtin_inf() ? X_EXP - ilogb(norm) : 0;
+  // (no rows, no gradient: a matrix of zeros stays one)
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) factors(a, e, gridDim.z, norm, ex);
+  const T* g = (const T*)a.g + (int64_t)e * a.M * a.N;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int r = i * 4 + (tid >> 6), c = tid & 63;
+    tile[r][c] = r0 + r < a.M && c0 + c < a.N
+                     ? ldexpf(Elem<T>::to_f(g[(int64_t)(r0 + r) * a.N + c0 + c]), ex) : 0.f;
+  }
+  __syncthreads();
+  const int line = tid >> 3, x0 = (tid & 7) * 8;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = half * 32 + line;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      if (side == 0 ? r0 + r >= a.M : c0 + r >= a.N) continue;
+      f16x8_v hi, lo;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        _Float16 vh, vl;
+        split(side == 0 ? tile[r][x0 + x] : tile[x0 + x][r], vh, vl);
+        hi[x] = vh;
+        lo[x] = vl;
+      }
+      const int row = side == 0 ? r0 + r : c0 + r, col = (side == 0 ? c0 : r0) + x0;
+      char* to = side == 0 ? a.same + e * a.ssame + row * pitch(a.N, P) : a.trans + e * a.strans + row * pitch(a.M, P);
+      if constexpr (P == 1) {
+        *reinterpret_cast<f16x8_v*>(to + col * 2) = hi;
+      } else {
+        *reinterpret_cast<f16x8_v*>(to + at2(col)) = hi;
+        *reinterpret_cast<f16x8_v*>(to + at2(col) + 64) = lo;
+      }
+    }
+  }
+}
+
+// ---- launches ----
+template <int BM, int BN, int WM, int WN, int PA, int PB, Epi EPI, typename O>
+hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
+  using C = Cfg<BM, BN, WM, WN, PA, PB>;
+  auto* k = k_ortho_gemm<BM, BN, WM, WN, PA, PB, EPI, O>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = allow_lds(k, C::SMEM, device(), done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(C::NTH), C::SMEM, st, a);
+  return hipGetLastError();
+}
+
+template <int PA, int PB, Epi EPI, typename O = float>
+hipError_t gemm(const Args& a, hipStream_t st) {
+  auto tiles = [&](int B) {
+    const int64_t mt = div_up(a.ra, B), nt = div_up(a.rb, B);
+    return a.batch * a.jobs * (EPI == SYM ? mt * (mt + 1) / 2 : mt * nt);
+  };
+  const int64_t t256 = tiles(256);
+  if (t256 >= 512) return launch_gemm<256, 256, 2, 4, PA, PB, EPI, O>(a, t256, st);
+  return launch_gemm<128, 128, 2, 2, PA, PB, EPI, O>(a, tiles(128), st);
+}
+
+// What the singular values and with them the matrices of a step can be: samples of
+// the spectrum followed through the steps.
+struct Spectrum {
+  static constexpr int N = 97;
+  double s[N], l[N], q[N];
+  Spectrum() {
+    for (int i = 0; i < N; ++i) s[i] = (double)i / (N - 1);  // norms of X_0 are at most 1
+  }
+  void begin() {
+    for (int i = 0; i < N; ++i) {
+      l[i] = s[i] * s[i];
+      q[i] = 1.0;
+    }
+  }
+  // largest |P|, |P A|, |P A P|, |Q| of a step
+  void step(const float* c, double* p, double* t, double* a, double* qm) {
+    *p = *t = *a = *qm = 0.0;
+    for (int i = 0; i < N; ++i) {
+      const double v = c[0] + l[i] * (c[1] + l[i] * c[2]);
+      *p = std::max(*p, std::fabs(v));
+      *t = std::max(*t, std::fabs(v * l[i]));
+      l[i] *= v * v;
+      q[i] *= v;
+      *a = std::max(*a, std::fabs(l[i]));
+      *qm = std::max(*qm, std::fabs(q[i]));
+    }
+  }
+  void end() {
+    for (int i = 0; i < N; ++i) s[i] = std::fabs(s[i] * q[i]);
+  }
+};
+
+// The exponent that brings numbers up to `most` below 2^13, four times below what
+// fp16 holds (the samples' gaps, and rounding).
+int exponent_for(double most) {
+  if (!(most > 0.0) || !std::isfinite(most)) return 0;
+  return std::max(-30, std::min(30, 13 - std::ilogb(most) - 1));
+}
+
+struct Sizes {
+  int m, k, parts, nb;           // parts of the update; matrices at a time
+  int64_t sx, sxt, sm;           // bytes of X, its transpose (two parts), an m x m matrix
+  int groups;
+  int64_t x0, xt0, x1, xt1, mat, f, sums, total;
+};
+
+// How many steps from step s on form a group.
+int group_steps(const OrthoArgs& a, int s) {
+  if (a.dtype == MOE_F32) return 1;
+  double growth = 1.0;
+  int n = 0;
+  while (s + n < a.steps) {
+    growth *= std::max(1.0, std::fabs((double)a.coef[3 * (s + n)]));
+    if (n > 0 && growth > 512.0) break;
+    ++n;
+  }
+  return n;
+}
+
+Sizes sizes(const OrthoArgs& a) {
+  Sizes z{};
+  z.m = std::min(a.M, a.N);
+  z.k = std::max(a.M, a.N);
+  z.parts = a.dtype == MOE_F32 ? 2 : 1;
+  // Matrices at a time: enough for nine rounds of 256 x 256 tiles over 256 CUs
+  const int64_t mt = div_up(z.m, 256), tiles = mt * (mt + 1) / 2;
+  const int64_t most = std::min<int64_t>(a.E, div_up(2304, tiles));
+  z.nb = (int)div_up(a.E, div_up(a.E, most));
+  for (int s = 0; s < a.steps; s += group_steps(a, s)) ++z.groups;
+  z.sx = z.m * pitch(z.k, 2);
+  z.sxt = z.k * pitch(z.m, 2);
+  z.sm = z.m * pitch(z.m, 2);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  z.x0 = take(z.nb * z.sx * z.parts / 2);
+  z.xt0 = take(z.nb * z.sxt * z.parts / 2);
+  if (z.groups > 1) {
+    // X in two parts for the groups after the first, which one-part input leaves no place for
+    z.x1 = take(z.nb * z.sx * (z.parts == 1 ? 2 : 1));
+    z.xt1 = take(z.nb * z.sxt * (z.parts == 1 ? 2 : 1));
+  }
+  z.mat = take(5 * z.nb * z.sm);
+  z.f = take(4 * z.nb * 2 * z.groups);
+  z.sums = take(8 * (int64_t)z.nb * NORM_PARTS);
+  z.total = at;
+  return z;
+}
+
+template <typename T>
+hipError_t prepare(const OrthoArgs& a, const Sizes& z, int e0, int nb, hipStream_t st) {
+  char* ws = (char*)a.ws;
+  const int64_t elems = (int64_t)a.M * a.N;
+  const T* g = (const T*)a.g + e0 * elems;
+  double* sums = (double*)(ws + z.sums);
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = elems % V == 0 && ((uintptr_t)a.g & 15) == 0;
+  const int parts = (int)std::min<int64_t>(NORM_PARTS, div_up(elems, 256 * 16));
+  if (vec) hipLaunchKernelGGL((k_ortho_norm<T, V>), dim3(parts, nb), dim3(256), 0, st, g, elems, parts, sums);
+  else hipLaunchKernelGGL((k_ortho_norm<T, 1>), dim3(parts, nb), dim3(256), 0, st, g, elems, parts, sums);
+  const bool tall = a.M > a.N;
+  constexpr int P = sizeof(T) == 4 ? 2 : 1;
+  Convert c{};
+  c.g = g; c.M = a.M; c.N = a.N; c.sums = sums; c.parts = parts; c.eps = a.eps;
+  char *x = ws + z.x0, *xt = ws + z.xt0;
+  const int64_t sx = z.sx * P / 2, sxt = z.sxt * P / 2;
+  c.same = tall ? xt : x;
+  c.trans = tall ? x : xt;
+  c.ssame = tall ? sxt : sx;
+  c.strans = tall ? sx : sxt;
+  c.back = (float*)(ws + z.f);
+  c.on = c.back + z.groups * nb;
+  c.groups = z.groups;
+  for (int s = 0, i = 0; s < a.steps; s += c.steps[i], ++i) c.steps[i] = (uint8_t)group_steps(a, s);
+  std::copy(a.coef, a.coef + 3 * a.steps, c.coef);
+  hipLaunchKernelGGL((k_ortho_convert<T, P>), dim3((a.N + 63) / 64, (a.M + 63) / 64, nb), dim3(256), 0, st, c);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t ortho_ws_bytes(const OrthoArgs& a) { return (size_t)sizes(a).total; }
+
+hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
+  const Sizes z = sizes(a);
+  const bool tall = a.M > a.N;
+  char* ws = (char*)a.ws;
+  for (int e0 = 0; e0 < a.E; e0 += z.nb) {
+    const int nb = std::min(z.nb, a.E - e0);
+    hipError_t err = a.dtype == MOE_F32 ? prepare<float>(a, z, e0, nb, st) : prepare<bf16_t>(a, z, e0, nb, st);
+    if (err != hipSuccess) return err;
+    Spectrum spec;
+    char *x = ws + z.x0, *xt = ws + z.xt0;
+    int parts = z.parts, x_exp = 0;
+    const float *back = (const float*)(ws + z.f), *on = back + z.groups * nb;
+    char* mats[5];
+    for (int i = 0; i < 5; ++i) mats[i] = ws + z.mat + i * nb * z.sm;
+    auto two = [](int n) { return (float)std::ldexp(1.0, n); };
+
+    bool second = false;  // which of the later groups' buffers is free
+    for (int s = 0; s < a.steps;) {
+      const int n = group_steps(a, s);
+      spec.begin();
+      // mats in use: A, P, Q, T (any: a scratch)
+      char *A = mats[0], *T = mats[1], *P = mats[2], *Q = nullptr, *spare[2] = {mats[3], mats[4]};
+      double lmax = 0.0;
+      for (int i = 0; i < Spectrum::N; ++i) lmax = std::max(lmax, spec.l[i]);
+      int ea = exponent_for(lmax), eq = 0;
+
+      Args g{};
+      g.batch = nb;
+      g.jobs = 1;
+      g.ra = g.rb = z.m;
+      g.pc = (int)pitch(z.m, 2);
+      g.sc = z.sm;
+      // A = X X^T
+      g.job[0] = Job{x, x, A, nullptr, two(ea - 2 * x_exp), 0.f, 0.f};
+      g.alpha_e = back;
+      g.square = true;
+      g.sa = g.sb = z.sx * parts / 2;
+      g.pa = g.pb = (int)pitch(z.k, parts);
+      g.stages = (int)((z.k + 63) / 64) * (parts == 1 ? 1 : 2);
+      err = parts == 1 ? gemm<1, 1, SYM>(g, st) : gemm<2, 2, SYM>(g, st);
+      if (err != hipSuccess) return err;
+      g.alpha_e = nullptr;
+      g.sa = g.sb = z.sm;
+      g.pa = g.pb = g.pc;
+      g.stages = (int)((z.m + 63) / 64) * 2;
+      for (int i = 0; i < n; ++i) {
+        const float* c = a.coef + 3 * (s + i);
+        double pm, tm, am, qm;
+        spec.step(c, &pm, &tm, &am, &qm);
+        const int ep = exponent_for(pm), et = exponent_for(tm), en = exponent_for(am), eqn = exponent_for(qm);
+        const bool last = i + 1 == n;
+        // P = a I + b A + c A^2
+        g.jobs = 1;
+        g.job[0] = Job{A, A, P, A, c[2] * two(ep - 2 * ea), c[1] * two(ep - ea), c[0] * two(ep)};
+        err = gemm<2, 2, SYM>(g, st);
+        if (err != hipSuccess) return err;
+        // T = P A and the next Q = P Q
+        g.jobs = 0;
+        char* qn = nullptr;
+        if (!last) g.job[g.jobs++] = Job{P, A, T, nullptr, two(et - ep - ea), 0.f, 0.f};
+        if (Q) {
+          qn = spare[0];
+          g.job[g.jobs++] = Job{P, Q, qn, nullptr, two(eqn - ep - eq), 0.f, 0.f};
+        }
+        if (g.jobs > 0) {
+          err = gemm<2, 2, SYM>(g, st);
+          if (err != hipSuccess) return err;
+        }
+        if (!last) {  // the next A = T P
+          g.jobs = 1;
+          g.job[0] = Job{T, P, A, nullptr, two(en - et - ep), 0.f, 0.f};
+          err = gemm<2, 2, SYM>(g, st);
+          if (err != hipSuccess) return err;
+          ea = en;
+        }
+        if (Q) {
+          spare[0] = Q;  // free again
+          Q = qn;
+          eq = eqn;
+        } else {
+          Q = P;
+          eq = ep;
+          P = spare[1];
+        }
+      }
+      s += n;
+      spec.end();
+      // X = Q X, as rows of X or, for a tall update's result, of its transpose
+      const bool final = s == a.steps;
+      const bool swap = final && tall;
+      Args r{};
+      r.batch = nb;
+      r.jobs = 1;
+      r.stages = (int)((z.m + 63) / 64) * 2;
+      r.alpha_e = final ? back : on;
+      r.square = false;
+      const int nx_exp = X_EXP - 1;  // (a norm below 2, with its own power of two)
+      const float alpha = final ? a.scale * two(-eq - x_exp) : two(nx_exp - eq - x_exp);
+      const int px = (int)pitch(z.m, parts);
+      const int64_t sxt = z.sxt * parts / 2;
+      if (swap) {
+        r.job[0] = Job{xt, Q, nullptr, nullptr, alpha, 0.f, 0.f};
+        r.ra = z.k; r.rb = z.m; r.sa = sxt; r.sb = z.sm; r.pa = px; r.pb = g.pc;
+      } else {
+        r.job[0] = Job{Q, xt, nullptr, nullptr, alpha, 0.f, 0.f};
+        r.ra = z.m; r.rb = z.k; r.sa = z.sm; r.sb = sxt; r.pa = g.pc; r.pb = px;
+      }
+      if (final) {
+        r.so = (int64_t)a.M * a.N;
+        if (a.dtype == MOE_F32) {
+          r.o = (float*)a.o + e0 * r.so;
+          err = gemm<2, 2, OUT, float>(r, st);
+        } else {
+          r.o = (bf16_t*)a.o + e0 * r.so;
+          err = parts == 2 ? gemm<2, 2, OUT, bf16_t>(r, st)
+                           : swap ? gemm<1, 2, OUT, bf16_t>(r, st) : gemm<2, 1, OUT, bf16_t>(r, st);
+        }
+        if (err != hipSuccess) return err;
+      } else {
+        const int64_t half = z.parts == 1 && second ? 1 : 0;
+        char* nx = z.parts == 1 || !second ? ws + z.x1 + half * nb * z.sx : ws + z.x0;
+        char* nxt = z.parts == 1 || !second ? ws + z.xt1 + half * nb * z.sxt : ws + z.xt0;
+        second = !second;
+        r.job[0].c = nx;
+        r.sc = z.sx;
+        r.pc = (int)pitch(z.k, 2);
+        r.ct = nxt;
+        r.sct = z.sxt;
+        r.pct = (int)pitch(z.m, 2);
+        err = parts == 2 ? gemm<2, 2, SPLIT>(r, st) : gemm<2, 1, SPLIT>(r, st);
+        if (err != hipSuccess) return err;
+        x = nx;
+        xt = nxt;
+        parts = 2;
+        x_exp = nx_exp;
+        back += nb;
+        on += nb;
+      }
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe

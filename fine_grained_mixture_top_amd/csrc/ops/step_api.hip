@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "../../../include/moe_step_ops.h"
 #include "step_launch.h"
@@ -54,6 +55,26 @@ int check_balance(const moe_balance_desc* d) {
   return MOE_OK;
 }
 
+constexpr int MAX_STEPS = 64, MAX_SIDE = 16384;
+constexpr int64_t MAX_MATRIX = (int64_t)1 << 29;  // a two-part matrix's byte offsets stay below 2^31
+
+int check_ortho(const moe_ortho_desc* d) {
+  if (!d || d->flags || d->reserved) return MOE_EINVAL;
+  if (d->E < 1 || d->M < 1 || d->N < 1 || d->steps < 1 || !d->coef) return MOE_EINVAL;
+  const int s = check_dtype(d->dtype);
+  if (s != MOE_OK) return s;
+  if (d->E > MAX_E || d->steps > MAX_STEPS || std::min(d->M, d->N) > MAX_SIDE) return MOE_ESHAPE;
+  if (((int64_t)d->M + 63) / 64 * 64 * (((int64_t)d->N + 63) / 64 * 64) >= MAX_MATRIX) return MOE_ESHAPE;
+  if (!std::isfinite(d->eps) || d->eps < 0.f || !std::isfinite(d->scale)) return MOE_EINVAL;
+  for (int i = 0; i < 3 * d->steps; ++i)
+    if (!std::isfinite(d->coef[i])) return MOE_EINVAL;
+  return MOE_OK;
+}
+
+OrthoArgs ortho_args(const moe_ortho_desc* d, const void* g, void* o, void* ws) {
+  return OrthoArgs{d->E, d->M, d->N, d->dtype, d->steps, d->coef, d->eps, d->scale, g, o, ws};
+}
+
 }  // namespace
 
 extern "C" {
@@ -94,6 +115,22 @@ int moe_balance_bwd(const moe_balance_desc* desc, const void* logits, const int3
                          expert_idx, gate, d_gate, dz};
   return timed(desc->profile, stream, MOE_STEP_K_BALANCE_BWD,
                [&](hipStream_t st) { return launch_balance_bwd(a, st); });
+}
+
+size_t moe_orthogonalize_workspace_bytes(const moe_ortho_desc* desc) {
+  return check_ortho(desc) == MOE_OK ? up256(ortho_ws_bytes(ortho_args(desc, nullptr, nullptr, nullptr))) : 0;
+}
+
+int moe_orthogonalize(const moe_ortho_desc* desc, const void* g, void* o, void* ws, size_t ws_bytes, void* stream) {
+  int s = check_ortho(desc);
+  if (s != MOE_OK) return s;
+  const size_t e = elem_bytes(desc->dtype);
+  if (!g || !o || !aligned(g, e) || !aligned(o, e)) return MOE_EINVAL;
+  const OrthoArgs a = ortho_args(desc, g, o, ws);
+  s = check_ws(ws, ws_bytes, up256(ortho_ws_bytes(a)));
+  if (s != MOE_OK) return s;
+  return timed(desc->profile, stream, MOE_STEP_K_ORTHOGONALIZE,
+               [&](hipStream_t st) { return launch_orthogonalize(a, st); });
 }
 
 }  // extern "C"

@@ -40,4 +40,16 @@ struct BalanceBwdArgs {
 };
 hipError_t launch_balance_bwd(const BalanceBwdArgs& a, hipStream_t st);
 
+// ---- ortho_kernels.hip ----
+struct OrthoArgs {
+  int E, M, N, dtype, steps;
+  const float* coef;     // host, [steps][3]
+  float eps, scale;
+  const void* g;
+  void* o;
+  void* ws;
+};
+size_t ortho_ws_bytes(const OrthoArgs& a);
+hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st);
+
 }  // namespace moe

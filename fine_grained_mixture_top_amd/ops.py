@@ -2,7 +2,7 @@
 sorted by expert and back, E4M3 products with a scale per block of 128, SwiGLU
 quantized for the next product; and around the layer's training step
 (include/moe_step_ops.h): the router's balance and z losses with the gradient of
-its logits.
+its logits, updates orthogonalised by Newton-Schulz products.
 
 Argument marshalling only, as in ``binding``: torch tensors in caller-owned
 device memory, ``MoEError`` on a non-zero status.  Tensors whose type, shape,
@@ -21,6 +21,7 @@ Codes are ``torch.float8_e4m3fn`` or ``torch.uint8`` tensors.  Calls run on
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -31,8 +32,8 @@ from . import binding as B
  MOE_OPS_K_SWIGLU_FP8, MOE_OPS_K_SWIGLU_BWD) = range(29, 41)
 KERNEL_NAMES = B.KERNEL_NAMES + ["sort", "permute", "permute_fp8", "unpermute", "unpermute_bwd", "quant_rows",
                                  "quant_weights", "quant_cols", "fp8_mm", "fp8_wgrad", "swiglu_fp8", "swiglu_bwd_rows"]
-(MOE_STEP_K_BALANCE, MOE_STEP_K_BALANCE_BWD) = range(41, 43)
-STEP_KERNEL_NAMES = KERNEL_NAMES + ["balance", "balance_bwd"]
+(MOE_STEP_K_BALANCE, MOE_STEP_K_BALANCE_BWD, MOE_STEP_K_ORTHOGONALIZE) = range(41, 44)
+STEP_KERNEL_NAMES = KERNEL_NAMES + ["balance", "balance_bwd", "orthogonalize"]
 MOE_MM_GATHER = 1
 MOE_MM_SB_OUT_MAJOR = 2
 
@@ -60,6 +61,13 @@ class MoeMmDesc(ctypes.Structure):
 class MoeBalanceDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("profile", ctypes.POINTER(B.MoeProfile))]
+
+
+class MoeOrthoDesc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("M", ctypes.c_int32), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("coef", ctypes.POINTER(ctypes.c_float)),
+                ("profile", ctypes.POINTER(B.MoeProfile))]
 
 
 _lib = None
@@ -90,11 +98,13 @@ def lib() -> ctypes.CDLL:
             "moe_swiglu_fp8": ([pd, pp, i32, i64, i32, vp, vp, vp, vp, prof, vp], i32),
             "moe_swiglu_bwd": ([pd, pp, i32, i64, i32, vp, vp, vp, prof, vp], i32),
         }
-        pb = ctypes.POINTER(MoeBalanceDesc)
+        pb, po = ctypes.POINTER(MoeBalanceDesc), ctypes.POINTER(MoeOrthoDesc)
         sig.update({
             "moe_balance_workspace_bytes": ([pb], sz),
             "moe_balance": ([pb, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
             "moe_balance_bwd": ([pb, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
+            "moe_orthogonalize_workspace_bytes": ([po], sz),
+            "moe_orthogonalize": ([po, vp, vp, vp, sz, vp], i32),
         })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -473,3 +483,52 @@ def moe_balance_bwd(bal: Balance, logits, d_loss, dz, expert_idx=None, gate=None
         pdg = _need("d_gate", d_gate, _F32, (bal.T, bal.K), bal.device)
     counts, tokens, _, lse, _, _ = bal._out
     _call("moe_balance_bwd", bal.device, stream, bal._refs[dt], pz, counts, tokens, lse, pd, pi, pg, pdg, po)
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)  # singular values to about 0.7 .. 1.2 in five steps
+
+
+class Ortho:
+    """The sizes, coefficients and workspace of ``moe_orthogonalize`` for stacks [E, M, N] of a type.
+
+    coef: three numbers for every step, or a triple for each.  A handle belongs to one sequence of calls at
+    a time."""
+
+    def __init__(self, E: int, M: int, N: int, dtype=torch.bfloat16, steps: int = 5, coef=NEWTON_SCHULZ,
+                 eps: float = 1e-7, scale: float = 1.0, device="cuda"):
+        if dtype not in _VALUES:
+            raise ValueError(f"dtype {dtype} is not one of {', '.join(str(d) for d in _VALUES)}")
+        device = _device(device)
+        if max(E, M, N, steps) > _INT32 or min(E, M, N, steps) < 1:
+            raise B.MoEError("moe_orthogonalize", B.MOE_ESHAPE if min(E, M, N, steps) >= 1 else B.MOE_EINVAL)
+        if steps > 64:
+            raise B.MoEError("moe_orthogonalize", B.MOE_ESHAPE)
+        rows = list(coef)
+        if len(rows) == 3 and not hasattr(rows[0], "__len__"):
+            rows = [rows] * steps
+        if len(rows) != steps or any(len(r) != 3 for r in rows):
+            raise ValueError(f"coef: three numbers, or three for each of {steps} steps")
+        self.E, self.M, self.N, self.dtype, self.device = E, M, N, dtype, device
+        self.coef = (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
+        self.desc = MoeOrthoDesc(E, M, N, _DTYPE[dtype], steps, eps, scale, 0, 0, self.coef, None)
+        need = int(lib().moe_orthogonalize_workspace_bytes(ctypes.byref(self.desc)))
+        if need == 0:
+            finite = all(math.isfinite(v) for v in (*self.coef, self.desc.eps, self.desc.scale))
+            raise B.MoEError("moe_orthogonalize", B.MOE_ESHAPE if finite and eps >= 0 else B.MOE_EINVAL)
+        self.ws = torch.empty(need, dtype=torch.uint8, device=device)
+        self._d, self._shape = ctypes.byref(self.desc), (E, M, N)
+
+    def attach(self, profiler: B.Profiler):
+        """Records launch timing of the calls that take this handle."""
+        profiler.attach(self.desc)
+
+    def detach(self):
+        self.desc.profile = None
+
+
+def moe_orthogonalize(ortho: Ortho, g, o, stream=None):
+    """o = scale X for each matrix of g [E, M, N], X the result of the handle's Newton-Schulz steps from
+    g / (its Frobenius norm + eps)."""
+    pg = _need("g", g, (ortho.dtype,), ortho._shape, ortho.device)
+    po = _need("o", o, (ortho.dtype,), ortho._shape, ortho.device)
+    _call("moe_orthogonalize", ortho.device, stream, ortho._d, pg, po, ortho.ws.data_ptr(), ortho.ws.numel())

@@ -100,3 +100,45 @@ def balance_bwd_ref(z, idx, ref, d_loss, gate=None, d_gate=None):
         # the inner sum: K terms; the products; then up to K values join an element
         bound = bound.scatter_add(1, at, m * ((2 * K + 8) * 2.0 ** -23)) + dz.abs() * K * 2.0 ** -24
     return dz, bound
+
+
+# ---------------------------------------------------------------- orthogonalised updates
+
+QUINTIC = (3.4445, -4.7750, 2.0315)
+SMOOTH = (1.875, -1.25, 0.375)  # x (15 - 10 x^2 + 3 x^4) / 8: rises to 1 and stays there
+
+
+def ortho_ref(g, steps, coef, eps=1e-7, scale=1.0):
+    """One matrix in float64; coef [steps][3]."""
+    x = g.double()
+    x = x / (x.norm() + eps) if x.any() else x
+    for i in range(steps):
+        a, b, c = coef[i]
+        y = x @ x.t()
+        x = a * x + b * (y @ x) + c * (y @ (y @ x))
+    return scale * x
+
+
+def ortho_tolerance(dtype, steps, coef, smallest=0.0):
+    """Error of a result before its rounding, relative to its Frobenius norm.
+
+    A step's map of the singular values, f(s) = s p(s^2), carries an error of X on by at most its steepest
+    difference, which is below 4 for QUINTIC on 0 .. 1.25 (3.9 at 1.2, a = 3.44 at 0) and a = 1.875 for SMOOTH;
+    for SMOOTH, concave and at most 1, all steps together carry it on by at most 1 / `smallest`, X_0's smallest
+    singular value.  One step a group: a step is off by 2^-22 of X's norm, three products' parts and sums.
+      Several steps a group (bf16): what A's sums and parts lost, 2 * 2^-24 of its largest singular value, grows by
+    a^2 with every step that A itself goes through, the last P of the group sees it times |b| / a, and the ones before
+    it lose less by a^2 each."""
+    a, b, _ = coef[0]
+    steep = 4.0 if tuple(coef[0]) == QUINTIC else a
+    each = steep ** steps / (steep - 1)
+    if smallest:
+        each = min(each, steps / smallest)
+    tol = each * 2.0 ** -22
+    if dtype == torch.bfloat16:
+        group = 1
+        while group < steps and a ** (group + 1) <= 512:
+            group += 1
+        grown = 2 * abs(b) / a * a ** (2 * (group - 1)) * 2.0 ** -24 / (1 - a ** -2)
+        tol += grown * -(-steps // group)
+    return tol

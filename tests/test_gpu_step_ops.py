@@ -251,3 +251,168 @@ def test_balance_profile():
     rec = prof.records()
     prof.close()
     assert [ops.STEP_KERNEL_NAMES[k] for k, _ in rec] == ["balance", "balance_bwd"] and all(ms >= 0 for _, ms in rec)
+
+
+# ---------------------------------------------------------------- orthogonalised updates
+
+def update(g, M, N, kind="gauss"):
+    w = randn(g, M, N)
+    if kind == "low":  # a few large directions and small noise, as weight gradients have them
+        r = max(1, min(M, N) // 16)
+        w = 0.01 * w + randn(g, M, r) @ randn(g, r, N)
+    return w
+
+
+def check_ortho(o, ref, tol, what=""):
+    """The error's norm, and every row's: a result's rounding is at most half a step of each value; a row may
+    hold more than its share of the rest, not 8 times the largest row's."""
+    half = R.HALF[o.dtype]
+    off = o.double() - ref
+    assert bool(torch.isfinite(o).all()), what
+    n = float(ref.norm())
+    assert float(off.norm()) <= (tol + half) * n + 1e-300, (what, float(off.norm()) / n, tol)
+    rows = ref.norm(dim=1)
+    bad = off.norm(dim=1) > half * rows + 8 * tol * rows.max() + 1e-300
+    assert not bad.any(), (what, bad.nonzero().flatten()[:8].tolist())
+
+
+ORTHO = [  # E, M, N, dtype, steps, coefficients, spectrum
+    (1, 1, 1, "f32", 5, R.QUINTIC, "gauss"), (1, 1, 7, "bf16", 5, R.QUINTIC, "gauss"), (2, 3, 2, "f32", 5, R.QUINTIC, "gauss"),
+    (3, 1, 300, "bf16", 3, R.QUINTIC, "gauss"), (2, 300, 1, "f32", 2, R.QUINTIC, "gauss"),
+    (3, 63, 65, "bf16", 5, R.QUINTIC, "low"), (3, 65, 63, "f32", 5, R.QUINTIC, "low"), (2, 64, 64, "bf16", 1, R.QUINTIC, "gauss"),
+    (1, 1536, 128, "f32", 5, R.QUINTIC, "low"), (1, 1537, 127, "bf16", 5, R.QUINTIC, "low"), (2, 130, 257, "bf16", 5, R.QUINTIC, "gauss"),
+    (5, 40, 2000, "bf16", 4, R.QUINTIC, "gauss"), (2, 720, 1040, "f32", 5, R.QUINTIC, "low"), (2, 1040, 720, "bf16", 5, R.QUINTIC, "low"),
+    (2, 40, 200, "bf16", 12, R.SMOOTH, "gauss"), (2, 200, 40, "bf16", 12, R.SMOOTH, "gauss"),
+    (2, 40, 200, "bf16", 20, R.SMOOTH, "gauss"), (2, 200, 40, "bf16", 20, R.SMOOTH, "gauss"), (2, 41, 199, "f32", 12, R.SMOOTH, "gauss"),
+    (1, 256, 1024, "bf16", 10, R.SMOOTH, "gauss"), (70, 16, 48, "bf16", 5, R.QUINTIC, "low"), (40, 1030, 1033, "f32", 2, R.QUINTIC, "low"),
+    (36, 1033, 1027, "bf16", 3, R.QUINTIC, "low"),
+]
+
+
+@pytest.mark.parametrize("E,M,N,dtype,steps,coef,kind", ORTHO)
+def test_orthogonalize(E, M, N, dtype, steps, coef, kind):
+    g = gen(E + M + N)
+    w = torch.stack([update(g, M, N, kind) for _ in range(E)]).to(DT[dtype])
+    if E > 1:
+        w[1] = 0.0  # an expert without rows
+    h = ops.Ortho(E, M, N, dtype=DT[dtype], steps=steps, coef=coef, scale=0.2)
+    h.ws.fill_(255)
+    o = torch.full_like(w, 7.0)
+    ops.moe_orthogonalize(h, w, o)
+    for e in range(E) if E < 8 else (0, 1, 2, E // 2, E - 2, E - 1):
+        ref = R.ortho_ref(w[e], steps, [coef] * steps, scale=0.2)
+        if e == 1:
+            assert not o[e].any()
+            continue
+        smallest = 0.0
+        if coef == R.SMOOTH:
+            s = torch.linalg.svdvals(w[e].double().cpu())
+            smallest = float(s.min() / w[e].double().norm())
+        check_ortho(o[e], ref, R.ortho_tolerance(w.dtype, steps, [coef], smallest), e)
+    again = torch.empty_like(o)
+    ops.moe_orthogonalize(h, w, again)
+    assert torch.equal(o, again)
+
+
+def test_orthogonalize_more_matrices_than_at_a_time():
+    """160 matrices of 1100 x 1101 go through the workspace in two parts."""
+    g = gen(8)
+    E, M, N = 160, 1100, 1101
+    w = randn(g, E, M, N, dtype=torch.bfloat16)
+    h = ops.Ortho(E, M, N, steps=2)
+    assert h.ws.numel() < 5 * E * 1152 * 1152 * 4
+    o = torch.empty_like(w)
+    ops.moe_orthogonalize(h, w, o)
+    for e in (0, 79, 80, 81, 153, 154, 159):
+        check_ortho(o[e], R.ortho_ref(w[e], 2, [R.QUINTIC] * 2), R.ortho_tolerance(w.dtype, 2, [R.QUINTIC]), e)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_orthogonalize_any_size_of_values(dtype):
+    """Results do not depend on the update's scale, up to the ends of its type."""
+    g = gen(9)
+    w = update(g, 50, 70, "low").to(DT[dtype])
+    h = ops.Ortho(1, 50, 70, dtype=DT[dtype], eps=0.0)
+    o, one = torch.empty(1, 50, 70, dtype=DT[dtype], device="cuda"), torch.empty(1, 50, 70, dtype=DT[dtype], device="cuda")
+    ops.moe_orthogonalize(h, w[None].contiguous(), one)
+    for p in (-100, -60, 60, 124 - int(w.float().abs().max().log2().ceil())):
+        ops.moe_orthogonalize(h, (w.double() * 2.0 ** p).to(DT[dtype])[None].contiguous(), o)
+        assert torch.equal(o, one), p  # (powers of two)
+    tiny = ops.Ortho(1, 50, 70, dtype=DT[dtype], eps=1.0)
+    small = (w.double() * 2.0 ** -70).to(DT[dtype])
+    ops.moe_orthogonalize(tiny, small[None].contiguous(), o)  # far below eps: the steps' linear part
+    ref = small.double() * 3.4445 ** 5
+    assert float((o[0].double() - ref).norm() / ref.norm()) < R.HALF[DT[dtype]] + 1e-5
+
+
+def test_orthogonalize_spoiled_matrix_stays_alone():
+    g = gen(10)
+    w = randn(g, 4, 60, 90, dtype=torch.bfloat16)
+    h, o, clean = ops.Ortho(4, 60, 90), torch.empty_like(w), torch.empty_like(w)
+    ops.moe_orthogonalize(h, w, clean)
+    w[1, 5, 7], w[2, 0, 0] = float("nan"), float("-inf")
+    ops.moe_orthogonalize(h, w, o)
+    assert bool(torch.isnan(o[1]).all()) and bool(torch.isnan(o[2]).all())
+    assert torch.equal(o[0], clean[0]) and torch.equal(o[3], clean[3])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_orthogonalize_addresses(dtype):
+    """Matrices whose addresses are aligned to their element alone."""
+    g = gen(12)
+    for M, N in ((33, 65), (64, 96)):
+        w = randn(g, 2, M, N, dtype=DT[dtype])
+        h, o = ops.Ortho(2, M, N, dtype=DT[dtype]), torch.empty_like(w)
+        ops.moe_orthogonalize(h, w, o)
+        odd = offset(torch.zeros_like(w), 3)
+        ops.moe_orthogonalize(h, offset(w, 1), odd)
+        assert torch.equal(o, odd)
+
+
+def test_orthogonalize_leaves_what_lies_around():
+    g = gen(13)
+    buf = torch.full((2, 50, 66), 3.0, device="cuda")
+    flat = buf.view(-1)
+    o = flat[64:64 + 2 * 33 * 65].view(2, 33, 65)
+    w = randn(g, 2, 33, 65)
+    keep = w.clone()
+    ops.moe_orthogonalize(ops.Ortho(2, 33, 65, dtype=torch.float32), w, o)
+    assert torch.equal(w, keep)
+    assert bool((flat[:64] == 3).all()) and bool((flat[64 + 2 * 33 * 65:] == 3).all())
+
+
+def test_orthogonalize_two_captured_calls():
+    """Two handles in one graph, a tall and a wide update, replayed beside eager calls on another stream."""
+    g = gen(14)
+    a, b = randn(g, 3, 200, 70, dtype=torch.bfloat16), randn(g, 2, 70, 200)
+    ha, hb = ops.Ortho(3, 200, 70), ops.Ortho(2, 70, 200, dtype=torch.float32)
+    ea, eb = ops.Ortho(3, 200, 70), ops.Ortho(2, 70, 200, dtype=torch.float32)
+    oa, ob = torch.empty_like(a), torch.empty_like(b)
+
+    def work():
+        ops.moe_orthogonalize(ha, a, oa)
+        ops.moe_orthogonalize(hb, b, ob)
+
+    def eager(i):
+        a.copy_(randn(gen(70 + i), 3, 200, 70))
+        b.copy_(randn(gen(80 + i), 2, 70, 200))
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        wa, wb = torch.empty_like(a), torch.empty_like(b)
+        ops.moe_orthogonalize(ea, a, wa, stream=s)
+        ops.moe_orthogonalize(eb, b, wb, stream=s)
+        s.synchronize()
+        return wa, wb
+
+    replay(work, (oa, ob), eager)
+
+
+def test_orthogonalize_coefficients_per_step():
+    g = gen(15)
+    coef = [(3.0, -3.2, 1.2), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0)]
+    for dtype in (torch.float32, torch.bfloat16):
+        w = randn(g, 1, 48, 100, dtype=dtype)
+        o = torch.empty_like(w)
+        ops.moe_orthogonalize(ops.Ortho(1, 48, 100, dtype=dtype, steps=3, coef=coef), w, o)
+        # differences of any of these maps on 0 .. 1.25 are below 4
+        check_ortho(o[0], R.ortho_ref(w[0], 3, coef), R.ortho_tolerance(dtype, 3, [R.QUINTIC]))

@@ -104,3 +104,60 @@ def test_balance_binding_refuses():
         ops.moe_balance_bwd(b, z, d, dz, idx, torch.ones(6, 2))
     with pytest.raises(ValueError, match="a tensor is needed"):
         ops.moe_balance_bwd(b, None, d, dz)
+
+
+def odesc(E=2, M=64, N=96, dtype=B.MOE_BF16, steps=5, eps=1e-7, scale=1.0, flags=0, reserved=0, coef=(3.4445, -4.775, 2.0315)):
+    c = None if coef is None else (ctypes.c_float * (3 * max(steps, 1)))(*(list(coef) * max(steps, 1)))
+    d = ops.MoeOrthoDesc(E, M, N, dtype, steps, eps, scale, flags, reserved, c, None)
+    d.keep = c
+    return d
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(E=0), B.MOE_EINVAL), (dict(M=0), B.MOE_EINVAL), (dict(N=-1), B.MOE_EINVAL), (dict(steps=0), B.MOE_EINVAL),
+    (dict(coef=None), B.MOE_EINVAL), (dict(dtype=3), B.MOE_EDTYPE), (dict(flags=1), B.MOE_EINVAL), (dict(reserved=1), B.MOE_EINVAL),
+    (dict(E=1025), B.MOE_ESHAPE), (dict(steps=65), B.MOE_ESHAPE), (dict(M=16385, N=16385), B.MOE_ESHAPE),
+    (dict(M=1, N=1 << 23), B.MOE_ESHAPE), (dict(M=1 << 30, N=1 << 30), B.MOE_ESHAPE), (dict(eps=-1.0), B.MOE_EINVAL),
+    (dict(eps=float("nan")), B.MOE_EINVAL), (dict(scale=float("inf")), B.MOE_EINVAL), (dict(coef=(1.0, float("nan"), 0.0)), B.MOE_EINVAL),
+])
+def test_ortho_descriptors_refused(kw, code):
+    lib, d = ops.lib(), odesc(**kw)
+    assert lib.moe_orthogonalize_workspace_bytes(ref(d)) == 0
+    assert lib.moe_orthogonalize(ref(d), P, P, P, 1 << 40, None) == code
+
+
+def test_ortho_refusals():
+    lib, d = ops.lib(), odesc()
+    need = lib.moe_orthogonalize_workspace_bytes(ref(d))
+    assert need > 0 and need % 256 == 0
+    assert lib.moe_orthogonalize(None, P, P, P, need, None) == B.MOE_EINVAL
+    for bad in ((None, P, P), (P, None, P), (P, P, None), (P + 1, P, P), (P, P + 1, P), (P, P, P + 16)):
+        assert lib.moe_orthogonalize(ref(d), *bad, need, None) == B.MOE_EINVAL
+    assert lib.moe_orthogonalize(ref(d), P, P, P, need - 1, None) == B.MOE_EWORKSPACE
+    assert lib.moe_orthogonalize(ref(odesc(dtype=B.MOE_F32)), P + 2, P, P, 1 << 40, None) == B.MOE_EINVAL
+    # the workspace grows with the matrices at a time, not with all of them
+    big = [lib.moe_orthogonalize_workspace_bytes(ref(odesc(E=e, M=4096, N=4096))) for e in (17, 34, 1024)]
+    assert big[0] == big[1] and big[2] <= big[0]
+
+
+def test_ortho_binding_refuses():
+    for kw, code in ((dict(E=0, M=1, N=1), B.MOE_EINVAL), (dict(E=1, M=1, N=1, steps=65), B.MOE_ESHAPE),
+                     (dict(E=1, M=1 << 40, N=1), B.MOE_ESHAPE), (dict(E=1, M=20000, N=20000), B.MOE_ESHAPE),
+                     (dict(E=1, M=4, N=4, eps=-1.0), B.MOE_EINVAL), (dict(E=1, M=4, N=4, scale=float("nan")), B.MOE_EINVAL),
+                     (dict(E=1, M=4, N=4, coef=(1.0, 1e39, 0.0)), B.MOE_EINVAL)):
+        with pytest.raises(B.MoEError) as e:
+            ops.Ortho(**kw, device="cpu")
+        assert e.value.status == code
+    for kw in (dict(dtype=torch.float16), dict(coef=(1.0, 2.0)), dict(coef=[(1.0, 2.0, 3.0)] * 4), dict(coef=[(1.0, 2.0)] * 5)):
+        with pytest.raises(ValueError):
+            ops.Ortho(1, 4, 4, device="cpu", **kw)
+    h = ops.Ortho(2, 4, 6, device="cpu")
+    g = torch.zeros(2, 4, 6, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="a GPU is needed"):
+        ops.moe_orthogonalize(h, g, torch.zeros_like(g))
+    with pytest.raises(ValueError, match="g: dtype"):
+        ops.moe_orthogonalize(h, g.float(), g)
+    with pytest.raises(ValueError, match="g: shape"):
+        ops.moe_orthogonalize(h, g[0], g)
+    with pytest.raises(ValueError, match="o: not contiguous"):
+        ops.moe_orthogonalize(h, g, torch.zeros(2, 6, 4, dtype=torch.bfloat16).transpose(1, 2))
