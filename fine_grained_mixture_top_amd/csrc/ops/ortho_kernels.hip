@@ -68,7 +68,6 @@ k_ortho_norm(const T* g, int64_t elems, int parts, double* sums) {
 // bound of its norm that is followed through the steps:
 //     back[i]    X of group i over its stored numbers (but for the exponent that all have)
 //     on[i]      what the stored numbers of group i + 1 are of Q times those of group i
-constexpr int MAX_STEPS = 64;
 struct Convert {
   const void* g;
   int M, N;
@@ -79,34 +78,62 @@ struct Convert {
   char* trans;    // columns of g
   int64_t ssame, strans;
   float* back;    // [groups][gridDim.z]
+};
+
+// A matrix's norm, from its partial sums (a wave, a lane each)
+__device__ __forceinline__ double norm_of(const double* sums, int parts, int e) {
+  static_assert(NORM_PARTS == 64, "a lane each");
+  const int lane = threadIdx.x & 63;
+  double s = lane < parts ? sums[(int64_t)e * NORM_PARTS + lane] : 0.0;
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  return sqrt(s);
+}
+// the power of two of a matrix's stored numbers, and X_0 over them (a matrix of zeros,
+// as an expert without rows has it, stays one)
+__device__ __forceinline__ int power_of(double norm) {
+  return norm > 0.0 && norm < __builtin_inf() ? X_EXP - ilogb(norm) : 0;
+}
+__device__ __forceinline__ double first_of(double norm, double eps) {
+  if (!(norm < __builtin_inf())) return __builtin_nan("");
+  return norm == 0.0 ? 0.0 : scalbn(1.0 / (norm + eps), -power_of(norm));
+}
+
+// (a launch of its own, for more than one group: coefficients at an index that the
+// compiler does not know would have every thread copy the arguments)
+constexpr int MAX_STEPS = 64;
+struct Factors {
+  const double* sums;
+  int parts;
+  double eps;
+  float* back;
   float* on;
   int groups;
   uint8_t steps[MAX_STEPS];  // of each group
   float coef[3 * MAX_STEPS];
 };
-
-// (one thread)
-__device__ void factors(const Convert& a, int e, int nb, double norm, int ex) {
+__global__ void __launch_bounds__(64)
+k_ortho_factors(Factors a) {
+  const int e = blockIdx.x, nb = gridDim.x;
+  const double norm = norm_of(a.sums, a.parts, e), first = first_of(norm, a.eps);
   const bool fine = norm < __builtin_inf();
-  const double first = norm == 0.0 ? 0.0 : scalbn(1.0 / (norm + a.eps), -ex);
   const float nan = __builtin_nanf("");
-  a.back[e] = fine ? (float)first : nan;
+  const int lane = threadIdx.x;
   float most = norm == 0.0 ? 0.f : (float)(norm / (norm + a.eps));  // of |X|
   const float* c = a.coef;
   int t = 0;
   for (int i = 0; i + 1 < a.groups; ++i) {
     for (int s = 0; s < a.steps[i]; ++s, c += 3) {
-      float m = 0.f;
-      for (int x = 1; x <= 16; ++x) {
-        const float v = most * (float)x * 0.0625f, l = v * v;
-        m = fmaxf(m, fabsf(v * fmaf(l, fmaf(l, c[2], c[1]), c[0])));
-      }
+      const float v = most * (float)(lane + 1) * 0.015625f, l = v * v;
+      float m = fabsf(v * fmaf(l, fmaf(l, c[2], c[1]), c[0]));
+      for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
       most = m;
     }
     const int next = most > 0.f && most < __builtin_inff() ? max(-60, min(120, -ilogbf(most))) : 0;
     const double f = i == 0 ? first : scalbn(1.0, -t);
-    a.on[i * nb + e] = fine ? (float)scalbn(f, next) : nan;
-    a.back[(i + 1) * nb + e] = fine ? (float)scalbn(1.0, -next) : nan;
+    if (lane == 0) {
+      a.on[i * nb + e] = fine ? (float)scalbn(f, next) : nan;
+      a.back[(i + 1) * nb + e] = fine ? (float)scalbn(1.0, -next) : nan;
+    }
     t = next;
   }
 }
@@ -116,14 +143,11 @@ __global__ void __launch_bounds__(256)
 k_ortho_convert(Convert a) {
   __shared__ float tile[64][65];
   const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tid = threadIdx.x;
-  double s = 0.0;
-  for (int i = 0; i < a.parts; ++i) s += a.sums[(int64_t)e * NORM_PARTS + i];
-  const double norm = sqrt(s);
-  const int ex = norm > 0.0 && norm < __builtin_inf() ? X_EXP - ilogb(norm) : 0;
-  // (no rows, no gradient: a matrix of zeros stays one)
-  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) factors(a, e, gridDim.z, norm, ex);
+  const double norm = norm_of(a.sums, a.parts, e);
+  const int ex = power_of(norm);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.back[e] = (float)first_of(norm, a.eps);
   const T* g = (const T*)a.g + (int64_t)e * a.M * a.N;
-#pragma unroll 4
+#pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int r = i * 4 + (tid >> 6), c = tid & 63;
     tile[r][c] = r0 + r < a.M && c0 + c < a.N
@@ -158,10 +182,10 @@ k_ortho_convert(Convert a) {
 }
 
 // ---- launches ----
-template <int BM, int BN, int WM, int WN, int PA, int PB, Epi EPI, typename O>
+template <int BM, int BN, int WM, int WN, int PA, int PB, bool FINE, Epi EPI, typename O>
 hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
   using C = Cfg<BM, BN, WM, WN, PA, PB>;
-  auto* k = k_ortho_gemm<BM, BN, WM, WN, PA, PB, EPI, O>;
+  auto* k = k_ortho_gemm<BM, BN, WM, WN, PA, PB, FINE, EPI, O>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = allow_lds(k, C::SMEM, device(), done);
   if (e != hipSuccess) return e;
@@ -169,15 +193,24 @@ hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int PA, int PB, Epi EPI, typename O = float>
-hipError_t gemm(const Args& a, hipStream_t st) {
+template <int PA, int PB, bool FINE, Epi EPI, typename O>
+hipError_t gemm_by_size(const Args& a, hipStream_t st) {
   auto tiles = [&](int B) {
     const int64_t mt = div_up(a.ra, B), nt = div_up(a.rb, B);
     return a.batch * a.jobs * (EPI == SYM ? mt * (mt + 1) / 2 : mt * nt);
   };
   const int64_t t256 = tiles(256);
-  if (t256 >= 512) return launch_gemm<256, 256, 2, 4, PA, PB, EPI, O>(a, t256, st);
-  return launch_gemm<128, 128, 2, 2, PA, PB, EPI, O>(a, tiles(128), st);
+  if (t256 >= 512) return launch_gemm<256, 256, 2, 4, PA, PB, FINE, EPI, O>(a, t256, st);
+  return launch_gemm<128, 128, 2, 2, PA, PB, FINE, EPI, O>(a, tiles(128), st);
+}
+
+// (fp32 updates are two parts throughout, and FINE)
+template <int PA, int PB, Epi EPI, typename O = bf16_t>
+hipError_t gemm(const Args& a, bool fine, hipStream_t st) {
+  if constexpr (PA == 2 && PB == 2) {
+    if (fine) return gemm_by_size<PA, PB, true, EPI, float>(a, st);
+  }
+  return gemm_by_size<PA, PB, false, EPI, O>(a, st);
 }
 
 // What the singular values and with them the matrices of a step can be: samples of
@@ -294,10 +327,14 @@ hipError_t prepare(const OrthoArgs& a, const Sizes& z, int e0, int nb, hipStream
   c.ssame = tall ? sxt : sx;
   c.strans = tall ? sx : sxt;
   c.back = (float*)(ws + z.f);
-  c.on = c.back + z.groups * nb;
-  c.groups = z.groups;
-  for (int s = 0, i = 0; s < a.steps; s += c.steps[i], ++i) c.steps[i] = (uint8_t)group_steps(a, s);
-  std::copy(a.coef, a.coef + 3 * a.steps, c.coef);
+  if (z.groups > 1) {
+    Factors f{};
+    f.sums = sums; f.parts = parts; f.eps = a.eps;
+    f.back = c.back; f.on = c.back + z.groups * nb; f.groups = z.groups;
+    for (int s = 0, i = 0; s < a.steps; s += f.steps[i], ++i) f.steps[i] = (uint8_t)group_steps(a, s);
+    std::copy(a.coef, a.coef + 3 * a.steps, f.coef);
+    hipLaunchKernelGGL(k_ortho_factors, dim3(nb), dim3(64), 0, st, f);
+  }
   hipLaunchKernelGGL((k_ortho_convert<T, P>), dim3((a.N + 63) / 64, (a.M + 63) / 64, nb), dim3(256), 0, st, c);
   return hipGetLastError();
 }
@@ -308,7 +345,7 @@ size_t ortho_ws_bytes(const OrthoArgs& a) { return (size_t)sizes(a).total; }
 
 hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
   const Sizes z = sizes(a);
-  const bool tall = a.M > a.N;
+  const bool tall = a.M > a.N, fine = a.dtype == MOE_F32;
   char* ws = (char*)a.ws;
   for (int e0 = 0; e0 < a.E; e0 += z.nb) {
     const int nb = std::min(z.nb, a.E - e0);
@@ -345,7 +382,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
       g.sa = g.sb = z.sx * parts / 2;
       g.pa = g.pb = (int)pitch(z.k, parts);
       g.stages = (int)((z.k + 63) / 64) * (parts == 1 ? 1 : 2);
-      err = parts == 1 ? gemm<1, 1, SYM>(g, st) : gemm<2, 2, SYM>(g, st);
+      err = parts == 1 ? gemm<1, 1, SYM>(g, fine, st) : gemm<2, 2, SYM>(g, fine, st);
       if (err != hipSuccess) return err;
       g.alpha_e = nullptr;
       g.sa = g.sb = z.sm;
@@ -360,7 +397,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
         // P = a I + b A + c A^2
         g.jobs = 1;
         g.job[0] = Job{A, A, P, A, c[2] * two(ep - 2 * ea), c[1] * two(ep - ea), c[0] * two(ep)};
-        err = gemm<2, 2, SYM>(g, st);
+        err = gemm<2, 2, SYM>(g, fine, st);
         if (err != hipSuccess) return err;
         // T = P A and the next Q = P Q
         g.jobs = 0;
@@ -371,13 +408,13 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
           g.job[g.jobs++] = Job{P, Q, qn, nullptr, two(eqn - ep - eq), 0.f, 0.f};
         }
         if (g.jobs > 0) {
-          err = gemm<2, 2, SYM>(g, st);
+          err = gemm<2, 2, SYM>(g, fine, st);
           if (err != hipSuccess) return err;
         }
         if (!last) {  // the next A = T P
           g.jobs = 1;
           g.job[0] = Job{T, P, A, nullptr, two(en - et - ep), 0.f, 0.f};
-          err = gemm<2, 2, SYM>(g, st);
+          err = gemm<2, 2, SYM>(g, fine, st);
           if (err != hipSuccess) return err;
           ea = en;
         }
@@ -415,14 +452,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
       }
       if (final) {
         r.so = (int64_t)a.M * a.N;
-        if (a.dtype == MOE_F32) {
-          r.o = (float*)a.o + e0 * r.so;
-          err = gemm<2, 2, OUT, float>(r, st);
-        } else {
-          r.o = (bf16_t*)a.o + e0 * r.so;
-          err = parts == 2 ? gemm<2, 2, OUT, bf16_t>(r, st)
-                           : swap ? gemm<1, 2, OUT, bf16_t>(r, st) : gemm<2, 1, OUT, bf16_t>(r, st);
-        }
+        r.o = fine ? (void*)((float*)a.o + e0 * r.so) : (void*)((bf16_t*)a.o + e0 * r.so);
+        err = parts == 2 ? gemm<2, 2, OUT>(r, fine, st) : swap ? gemm<1, 2, OUT>(r, fine, st) : gemm<2, 1, OUT>(r, fine, st);
         if (err != hipSuccess) return err;
       } else {
         const int64_t half = z.parts == 1 && second ? 1 : 0;
@@ -435,7 +466,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
         r.ct = nxt;
         r.sct = z.sxt;
         r.pct = (int)pitch(z.m, 2);
-        err = parts == 2 ? gemm<2, 2, SPLIT>(r, st) : gemm<2, 1, SPLIT>(r, st);
+        err = parts == 2 ? gemm<2, 2, SPLIT>(r, fine, st) : gemm<2, 1, SPLIT>(r, fine, st);
         if (err != hipSuccess) return err;
         x = nx;
         xt = nxt;
