@@ -57,6 +57,7 @@
 #include "../device_common.h"
 #include "lds_stage.h"
 #include "ops_launch.h"
+#include "segments.h"
 
 namespace moe {
 namespace f8 {
@@ -151,10 +152,7 @@ struct Args {
   int sb_k, sb_n;            // strides of sb in (reduction block, column block)
 };
 
-// n rows from row o on, as far as they lie in the buffers (rows past them are never touched)
-__device__ __forceinline__ int rows_in(const Args& g, int o, int n) {
-  return o < 0 || o >= g.rows ? 0 : max(0, min(n, g.rows - o));
-}
+__device__ __forceinline__ int rows_in(const Args& g, int o, int n) { return rows_inside(g.rows, o, n); }
 
 // BM x BN tiles, WM x WN waves.  WG: weight gradient (tiles of dw over the
 // segment's blocks), else rows of c.
@@ -645,62 +643,8 @@ k_fp8_thin(Args g) {
   const int NT = (g.N + BN - 1) / BN;
   const int mg = (int)(blockIdx.x / (unsigned)NT), n0 = (int)(blockIdx.x % (unsigned)NT) * BN;
 
-  // The row tile's segment: lanes scan `per` experts each, four at a time
-  // (loads of four in flight; up to 256 experts they stay in registers).
-  const int per = (g.E + 63) >> 6;
-  int first[4], rws[4];
-  int mine = 0;
-  for (int x0 = 0; x0 < per; x0 += 4) {
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int e = lane * per + x0 + x;
-      const bool is = x0 + x < per && e < g.E;
-      first[x] = is && g.offsets ? g.offsets[e] : 0;
-      rws[x] = is ? (g.offsets ? g.counts[e] : g.rows) : 0;
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      rws[x] = rows_in(g, first[x], rws[x]);
-      mine += (rws[x] + BM - 1) / BM;
-    }
-  }
-  int incl = mine;
-  for (int s = 1; s < 64; s <<= 1) {
-    const int y = __shfl_up(incl, s, 64);
-    if (lane >= s) incl += y;
-  }
-  const uint64_t past = __ballot(incl > mg);
-  if (past == 0) return;  // no such tile
-  const int src = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
-  int left = mg - (__builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(mine, src));
-  int e = src * per, n = 0, row0 = 0;
-  if (per <= 4) {
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int nx = __builtin_amdgcn_readlane(rws[x], src), tiles = (nx + BM - 1) / BM;
-      if (left >= 0 && left < tiles) {
-        e = src * per + x;
-        n = nx;
-        row0 = __builtin_amdgcn_readlane(first[x], src) + left * BM;
-        n -= left * BM;
-        left = -1;
-      }
-      if (left >= 0) left -= tiles;
-    }
-  } else {
-    for (;; ++e) {
-      row0 = __builtin_amdgcn_readfirstlane(g.offsets[e]);
-      n = rows_in(g, row0, __builtin_amdgcn_readfirstlane(g.counts[e]));
-      const int tiles = (n + BM - 1) / BM;
-      if (left < tiles) break;
-      left -= tiles;
-    }
-    row0 += left * BM;
-    n -= left * BM;
-  }
-  e = __builtin_amdgcn_readfirstlane(e);
-  row0 = __builtin_amdgcn_readfirstlane(row0);
-  const int rows = min(__builtin_amdgcn_readfirstlane(n), BM);
+  int e, row0, rows;
+  if (!segment_tile<BM>(g.offsets, g.counts, g.E, g.rows, mg, lane, e, row0, rows)) return;  // no such tile
 
   const int p = lane & 15, h = lane >> 4;
   // rows and columns past the end repeat the last one (their results are dropped)

@@ -1,0 +1,310 @@
+// Products of bf16 rows with MXFP4 weights (include/moe_step_ops.h: moe_mxfp4_mm).
+//
+// A code (E2M1) times its block's scale (2^(code - 127)) is a bf16 number exactly, and
+// one instruction turns two codes into two of them, so the weights stay 4-bit up to
+// the registers and the products run on the bf16 matrix cores: every product exact, sums
+// in fp32.  Any split of the reduction over lanes does as long as both operands agree.
+#pragma once
+
+#include <type_traits>
+
+#include "lds_stage.h"
+#include "segments.h"
+#include "step_launch.h"
+
+namespace moe {
+namespace f4 {
+
+struct Args {
+  const bf16_t* a;
+  const uint8_t* q;
+  const uint8_t* s;
+  void* c;
+  const int32_t* offsets;    // null: one segment of `rows` rows
+  const int32_t* counts;
+  const int32_t* row_token;  // gathered rows of a, or null
+  int a_rows, rows, E, K, N;
+};
+
+// 8 codes (a word, the first in its lowest bits) as bf16 values, times 2^(scale - 127);
+// 255 is NaN
+__device__ __forceinline__ bf16x8_v values(uint32_t w, uint32_t scale) {
+  const float f = __uint_as_float(scale << 23);
+  const bf16x2_v v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 0);
+  const bf16x2_v v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 1);
+  const bf16x2_v v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 2);
+  const bf16x2_v v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 3);
+  return bf16x8_v{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+}
+
+// ---------------------------------------------------------------------------
+// Few rows per expert (decode): the weights' bytes are the work, every touched
+// expert's are read once, straight into registers.  A workgroup takes 16 RT rows of a
+// segment and 16 FN columns; its four waves split the reduction (chunks of 256: wave w
+// takes w, w + 4, ...) and add up their sums in wave order.  A lane's 16 bytes of
+// codes are one block of 32 and have one scale.
+// ---------------------------------------------------------------------------
+template <int RT, int FN, typename O>
+__global__ void __launch_bounds__(256)
+k_mxfp4_thin(Args g) {
+  constexpr int BN = 16 * FN, BM = 16 * RT;
+  __shared__ float part[3][RT][FN][64][4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int NT = (g.N + BN - 1) / BN;
+  const int mg = (int)(blockIdx.x / (unsigned)NT), n0 = (int)(blockIdx.x % (unsigned)NT) * BN;
+  int e, row0, rows;
+  if (!segment_tile<BM>(g.offsets, g.counts, g.E, g.rows, mg, lane, e, row0, rows)) return;  // no such tile
+
+  const int p = lane & 15, h = lane >> 4;
+  const int kb = g.K / 32, chunks = (kb + 7) / 8;
+  // rows and columns past the end repeat the last one (their results are dropped)
+  int64_t row[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    row[r] = row0 + min(16 * r + p, rows - 1);
+    if (g.row_token) row[r] = g.row_token[row[r]];
+  }
+  const uint8_t *pq[FN], *ps[FN];
+#pragma unroll
+  for (int i = 0; i < FN; ++i) {
+    const int64_t n = (int64_t)e * g.N + min(n0 + 16 * i + p, g.N - 1);
+    pq[i] = g.q + n * (g.K / 2);
+    ps[i] = g.s + n * kb;
+  }
+  // Chunk k's loads: none under a condition; past the reduction they read the first
+  // block again, and the rows' values become zeros.
+  uint4 rq[2][FN], ra[2][RT][4];
+  uint32_t rs[2][FN];
+  auto block = [&](int k, int c) { return 8 * k + 4 * c + h; };
+  auto load_q = [&](int k) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int b = block(k, c) < kb ? block(k, c) : 0;
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        rq[c][i] = *reinterpret_cast<const uint4*>(pq[i] + 16 * (int64_t)b);
+        rs[c][i] = ps[i][b];
+      }
+    }
+  };
+  load_q(w < chunks ? w : 0);  // (on the way while the tokens arrive)
+  __builtin_amdgcn_sched_barrier(0);
+  const bf16_t* pa[RT];
+  bool real[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    // a token that does not exist counts as zeros
+    real[r] = (uint64_t)row[r] < (uint64_t)g.a_rows;
+    pa[r] = g.a + (real[r] ? row[r] : 0) * g.K;
+  }
+  auto load_a = [&](int k) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const bool there = block(k, c) < kb;
+      const int b = there ? block(k, c) : 0;
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint4 v = reinterpret_cast<const uint4*>(pa[r] + 32 * (int64_t)b)[x];
+          ra[c][r][x] = there && real[r] ? v : make_uint4(0, 0, 0, 0);
+        }
+    }
+  };
+
+  f32x4_v acc[RT][FN];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int i = 0; i < FN; ++i) acc[r][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  for (int k = w; k < chunks; k += 4) {
+    if (k > w) load_q(k);
+    load_a(k);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const bool there = block(k, c) < kb;
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        const uint32_t sc = there ? rs[c][i] : 127u;  // (zeros times a NaN would not be zeros)
+        const uint32_t words[4] = {rq[c][i].x, rq[c][i].y, rq[c][i].z, rq[c][i].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const bf16x8_v b = values(words[x], sc);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, __builtin_bit_cast(bf16x8_v, ra[c][r][x]), acc[r][i], 0, 0, 0);
+        }
+      }
+    }
+  }
+  if (w > 0)
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < FN; ++i) *reinterpret_cast<f32x4_v*>(part[w - 1][r][i][lane]) = acc[r][i];
+  __syncthreads();
+  if (w > 0) return;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int m = 16 * r + p;
+    if (m >= rows) continue;
+    O* out = reinterpret_cast<O*>(g.c) + ((int64_t)row0 + m) * g.N;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      f32x4_v v = acc[r][i];
+#pragma unroll
+      for (int x = 0; x < 3; ++x) v += *reinterpret_cast<const f32x4_v*>(part[x][r][i][lane]);
+      const int c = n0 + 16 * i + 4 * h;
+      if (c >= g.N) continue;
+      if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(out + c) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
+      else *reinterpret_cast<float4*>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows per expert: tiles of BM x BN, WM x WN waves.  A stage is 64 of the
+// reduction: 128 bytes of every row and 32 of every column's codes go straight into
+// LDS, three stages in turn, the columns' scales into registers one stage ahead.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WM, int WN>
+struct Cfg {
+  static constexpr int W = WM * WN, NTH = 64 * W;
+  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  static constexpr int IA = BM / 8 / W, IB = BN / 32 / W;  // 1 KB loads per wave and stage
+  static constexpr int STAGE = BM * 128 + BN * 32;
+  static constexpr int BUFS = 3, SMEM = BUFS * STAGE;
+  static_assert(BM % (8 * W) == 0 && BN % (32 * W) == 0, "loads per wave");
+};
+
+template <int BM, int BN, int WM, int WN, typename O>
+__global__ void __launch_bounds__(64 * WM * WN, 2)
+k_mxfp4_tile(Args g) {
+  using C = Cfg<BM, BN, WM, WN>;
+  constexpr int FM = C::FM, FN = C::FN;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w / WN, wn = w % WN;
+  const int NT = (g.N + BN - 1) / BN;
+  const int id = xcd_virtual_id(blockIdx.x, gridDim.x);
+  const int mg = id / NT, n0 = (id - mg * NT) * BN;
+  int e, row0, rows;
+  if (!segment_tile<BM>(g.offsets, g.counts, g.E, g.rows, mg, lane, e, row0, rows)) return;  // no such tile
+
+  // ---- loads ----
+  const int kb = g.K / 32, stages = (kb + 1) / 2;
+  const bool gather = g.row_token != nullptr;
+  const int sub = lane >> 3, ca = ((lane & 7) ^ sub) * 8;  // line of a 1 KB load, first of its 8 values
+  uint32_t oa[C::IA], oq[C::IB], os[FN];
+#pragma unroll
+  for (int i = 0; i < C::IA; ++i) {
+    const int r = (C::IA * w + i) * 8 + sub;
+    uint32_t line = OOB;
+    if (r < rows) {
+      const uint32_t t = gather ? (uint32_t)g.row_token[row0 + r] : (uint32_t)r;
+      if (!gather || t < (uint32_t)g.a_rows) line = t * (uint32_t)g.K * 2u + ca * 2u;
+    }
+    oa[i] = line;
+  }
+#pragma unroll
+  for (int i = 0; i < C::IB; ++i) {
+    const int n = n0 + (C::IB * w + i) * 32 + (lane >> 1);
+    oq[i] = n < g.N ? (uint32_t)n * (uint32_t)(g.K / 2) + (lane & 1) * 16u : OOB;
+  }
+  const int p = lane & 15, h = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < FN; ++i) {
+    const int n = n0 + wn * C::TN + 16 * i + p;
+    os[i] = n < g.N ? (uint32_t)n * (uint32_t)kb + (h >> 1) : OOB;
+  }
+  const bf16_t* a0 = gather ? g.a : g.a + (int64_t)row0 * g.K;
+  const __amdgpu_buffer_rsrc_t ra = rsrc(a0, (uint32_t)(gather ? g.a_rows : rows) * (uint32_t)g.K * 2u);
+  const __amdgpu_buffer_rsrc_t rq = rsrc(g.q + (int64_t)e * g.N * (g.K / 2), (uint32_t)g.N * (uint32_t)(g.K / 2));
+  const __amdgpu_buffer_rsrc_t rs = rsrc(g.s + (int64_t)e * g.N * kb, (uint32_t)g.N * (uint32_t)kb);
+  auto load = [&](int s, int buf) {
+    char* st = smem + buf * C::STAGE;
+    // (a last stage of 32: the missing values are zeros, whatever codes lie there)
+    const bool half = 2 * s + 1 >= kb;
+#pragma unroll
+    for (int i = 0; i < C::IA; ++i)
+      load16_lds(ra, st + (C::IA * w + i) * 1024, half && ca >= 32 ? OOB : oa[i], (uint32_t)s * 128u);
+#pragma unroll
+    for (int i = 0; i < C::IB; ++i)
+      load16_lds(rq, st + BM * 128 + (C::IB * w + i) * 1024, half && (lane & 1) ? OOB : oq[i], (uint32_t)s * 32u);
+  };
+  uint32_t sc[FN];
+  auto load_scales = [&](int s) {
+    const bool there = 2 * s + (h >> 1) < kb;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+      sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, there ? os[i] : OOB, (uint32_t)s * 2u, 0);
+  };
+
+  // ---- products ----
+  f32x4_v acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  // a lane's 16 of a stage's 64: 16 h .. 16 h + 15
+  const lds_ptr_t la = (lds_ptr_t)smem + (wm * C::TM + p) * 128;
+  const lds_ptr_t lq = (lds_ptr_t)smem + BM * 128 + (wn * C::TN + p) * 32 + 8 * h;
+  const int slot0 = ((2 * h) ^ (p & 7)) * 16, slot1 = ((2 * h + 1) ^ (p & 7)) * 16;
+
+  load_scales(0);
+  load(0, 0);
+  if (stages > 1) load(1, 1);
+  int buf = 0;
+  for (int s = 0; s < stages; ++s) {
+    // this stage and its scales are there once all but the next stage's loads are
+    if (s + 1 < stages) wait_vm<C::IA + C::IB>();
+    else wait_vm<0>();
+    lds_sync();
+    uint32_t cur[FN];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) cur[i] = sc[i];
+    if (s + 1 < stages) load_scales(s + 1);
+    if (s + 2 < stages) load(s + 2, buf == 0 ? 2 : buf - 1);
+    const int at = buf * C::STAGE;
+    bf16x8_v fa[FM][2];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      fa[j][0] = lds_ld<bf16x8_v>(la + at + j * 2048 + slot0);
+      fa[j][1] = lds_ld<bf16x8_v>(la + at + j * 2048 + slot1);
+    }
+    typedef uint32_t u32x2_q __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      const u32x2_q c = lds_ld<u32x2_q>(lq + at + i * 512);
+      const bf16x8_v b0 = values(c[0], cur[i]), b1 = values(c[1], cur[i]);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0, fa[j][0], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1, fa[j][1], acc[i][j], 0, 0, 0);
+    }
+    buf = buf == 2 ? 0 : buf + 1;
+  }
+
+  // results: a lane holds, of row p of a piece, the columns 4 h .. 4 h + 3
+  const int c0 = n0 + wn * C::TN + 4 * h;
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int r = wm * C::TM + 16 * j + p;
+    if (r >= rows) continue;
+    O* out = reinterpret_cast<O*>(g.c) + ((int64_t)row0 + r) * g.N;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      const int c = c0 + 16 * i;
+      if (c >= g.N) continue;
+      const f32x4_v v = acc[i][j];
+      if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(out + c) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
+      else *reinterpret_cast<float4*>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
+}  // namespace f4
+}  // namespace moe

@@ -55,6 +55,13 @@ int check_balance(const moe_balance_desc* d) {
   return MOE_OK;
 }
 
+constexpr int MAX_DIM = 1 << 20;
+
+int check_mxfp4(int E, int K, int N) {
+  if (E < 1 || K < 1 || N < 1) return MOE_EINVAL;
+  return E <= MAX_E && K % 32 == 0 && N % 16 == 0 && K <= MAX_DIM && N <= MAX_DIM ? MOE_OK : MOE_ESHAPE;
+}
+
 constexpr int MAX_STEPS = 64, MAX_SIDE = 16384;
 constexpr int64_t MAX_MATRIX = (int64_t)1 << 29;  // a two-part matrix's byte offsets stay below 2^31
 
@@ -131,6 +138,45 @@ int moe_orthogonalize(const moe_ortho_desc* desc, const void* g, void* o, void* 
   if (s != MOE_OK) return s;
   return timed(desc->profile, stream, MOE_STEP_K_ORTHOGONALIZE,
                [&](hipStream_t st) { return launch_orthogonalize(a, st); });
+}
+
+int moe_mxfp4_quant_weights(int dtype, int E, int K, int N, const void* w, void* q, void* s, moe_profile* profile,
+                            void* stream) {
+  int e = check_dtype(dtype);
+  if (e == MOE_OK) e = check_mxfp4(E, K, N);
+  if (e != MOE_OK) return e;
+  if ((int64_t)K * N > ((int64_t)1 << 37) / E) return MOE_ESHAPE;
+  if (!w || !q || !s || !aligned(w, 16) || !aligned(q, 16)) return MOE_EINVAL;
+  return timed(profile, stream, MOE_STEP_K_MXFP4_WEIGHTS, [&](hipStream_t st) {
+    return launch_mxfp4_weights(dtype, E, K, N, w, (uint8_t*)q, (uint8_t*)s, st);
+  });
+}
+
+int moe_mxfp4_mm(const moe_mm_desc* desc, const void* a, const void* q, const void* s, const moe_plan* plan, void* c,
+                 void* stream) {
+  if (!desc || desc->reserved || (desc->flags & ~MOE_MM_GATHER)) return MOE_EINVAL;
+  const bool gather = (desc->flags & MOE_MM_GATHER) != 0;
+  if (desc->a_rows < 0 || desc->rows < 0 || desc->rows_used < 0 || desc->rows_used > desc->rows) return MOE_EINVAL;
+  int e = check_dtype(desc->out);
+  if (e == MOE_OK) e = check_mxfp4(desc->E, desc->K, desc->N);
+  if (e != MOE_OK) return e;
+  if (!plan && (desc->E != 1 || gather)) return MOE_EINVAL;
+  if (!gather && desc->a_rows != desc->rows) return MOE_EINVAL;
+  if ((int64_t)desc->N * desc->K >= INT32_MAX) return MOE_ESHAPE;
+  if (gather && (int64_t)desc->a_rows * desc->K >= ((int64_t)1 << 30)) return MOE_ESHAPE;
+  if (desc->rows == 0) return MOE_OK;
+  if (desc->a_rows == 0) return MOE_EINVAL;  // rows of no token
+  if (plan && (!plan->offsets || !plan->counts || (gather && !plan->row_token))) return MOE_EINVAL;
+  if (!a || !q || !s || !c || !aligned(a, 16) || !aligned(q, 16) || !aligned(c, 16)) return MOE_EINVAL;
+  PlanArgs p{};
+  if (plan) {
+    p.offsets = plan->offsets;
+    p.counts = plan->counts;
+    p.row_token = plan->row_token;
+  }
+  const Mxfp4Args g{(const bf16_t*)a, (const uint8_t*)q, (const uint8_t*)s, c, desc->a_rows, desc->rows,
+                    desc->rows_used > 0 ? desc->rows_used : desc->rows, desc->E, desc->K, desc->N, desc->out, gather};
+  return timed(desc->profile, stream, MOE_STEP_K_MXFP4_MM, [&](hipStream_t st) { return launch_mxfp4_mm(p, g, st); });
 }
 
 }  // extern "C"

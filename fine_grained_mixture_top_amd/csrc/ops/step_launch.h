@@ -7,6 +7,8 @@
 #include <stdint.h>
 
 #include "../../../include/moe_step_ops.h"
+#include "../device_common.h"
+#include "ops_launch.h"
 
 namespace moe {
 
@@ -51,5 +53,18 @@ struct OrthoArgs {
 };
 size_t ortho_ws_bytes(const OrthoArgs& a);
 hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st);
+
+// ---- mxfp4_kernels.hip ----
+struct Mxfp4Args {
+  const bf16_t* a;
+  const uint8_t* q;
+  const uint8_t* s;
+  void* c;
+  int a_rows, rows, rows_used, E, K, N;
+  int out;
+  bool gather;
+};
+hipError_t launch_mxfp4_weights(int dtype, int E, int K, int N, const void* w, uint8_t* q, uint8_t* s, hipStream_t st);
+hipError_t launch_mxfp4_mm(const PlanArgs& p, const Mxfp4Args& m, hipStream_t st);
 
 }  // namespace moe

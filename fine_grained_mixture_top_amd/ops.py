@@ -2,7 +2,8 @@
 sorted by expert and back, E4M3 products with a scale per block of 128, SwiGLU
 quantized for the next product; and around the layer's training step
 (include/moe_step_ops.h): the router's balance and z losses with the gradient of
-its logits, updates orthogonalised by Newton-Schulz products.
+its logits, updates orthogonalised by Newton-Schulz products, weights in MXFP4 and
+products with them.
 
 Argument marshalling only, as in ``binding``: torch tensors in caller-owned
 device memory, ``MoEError`` on a non-zero status.  Tensors whose type, shape,
@@ -32,8 +33,9 @@ from . import binding as B
  MOE_OPS_K_SWIGLU_FP8, MOE_OPS_K_SWIGLU_BWD) = range(29, 41)
 KERNEL_NAMES = B.KERNEL_NAMES + ["sort", "permute", "permute_fp8", "unpermute", "unpermute_bwd", "quant_rows",
                                  "quant_weights", "quant_cols", "fp8_mm", "fp8_wgrad", "swiglu_fp8", "swiglu_bwd_rows"]
-(MOE_STEP_K_BALANCE, MOE_STEP_K_BALANCE_BWD, MOE_STEP_K_ORTHOGONALIZE) = range(41, 44)
-STEP_KERNEL_NAMES = KERNEL_NAMES + ["balance", "balance_bwd", "orthogonalize"]
+(MOE_STEP_K_BALANCE, MOE_STEP_K_BALANCE_BWD, MOE_STEP_K_ORTHOGONALIZE, MOE_STEP_K_MXFP4_WEIGHTS,
+ MOE_STEP_K_MXFP4_MM) = range(41, 46)
+STEP_KERNEL_NAMES = KERNEL_NAMES + ["balance", "balance_bwd", "orthogonalize", "mxfp4_weights", "mxfp4_mm"]
 MOE_MM_GATHER = 1
 MOE_MM_SB_OUT_MAJOR = 2
 
@@ -105,6 +107,8 @@ def lib() -> ctypes.CDLL:
             "moe_balance_bwd": ([pb, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
             "moe_orthogonalize_workspace_bytes": ([po], sz),
             "moe_orthogonalize": ([po, vp, vp, vp, sz, vp], i32),
+            "moe_mxfp4_quant_weights": ([i32, i32, i32, i32, vp, vp, vp, prof, vp], i32),
+            "moe_mxfp4_mm": ([pm, vp, vp, vp, pp, vp, vp], i32),
         })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -532,3 +536,53 @@ def moe_orthogonalize(ortho: Ortho, g, o, stream=None):
     pg = _need("g", g, (ortho.dtype,), ortho._shape, ortho.device)
     po = _need("o", o, (ortho.dtype,), ortho._shape, ortho.device)
     _call("moe_orthogonalize", ortho.device, stream, ortho._d, pg, po, ortho.ws.data_ptr(), ortho.ws.numel())
+
+
+_BYTES = (torch.uint8,)
+_BF16 = (torch.bfloat16,)
+
+
+def moe_mxfp4_quant_weights(w, q, s, stream=None):
+    """w [E, K, N] (fp32 or bf16) -> MXFP4 codes q [E, N, K/2] and scale codes s [E, N, K/32] (uint8), blocks of 32
+    along K.  K a multiple of 32, N of 16."""
+    E, K, N = _shape("w", w, 3)
+    if K % 32:
+        raise ValueError(f"w: {K} rows, a multiple of 32 is needed")
+    p = _need("w", w, _VALUES, (E, K, N), w.device)
+    pq = _need("q", q, _BYTES, (E, N, K // 2), w.device)
+    ps = _need("s", s, _BYTES, (E, N, K // 32), w.device)
+    _call("moe_mxfp4_quant_weights", w.device, stream, _DTYPE[w.dtype], E, K, N, p, pq, ps, None)
+
+
+def moe_mxfp4_mm(plan, a, q, s, c, gather: bool = False, stream=None):
+    """c[r] = a[r] w[e]^T for the rows r of expert e's segment, w the values of MXFP4 weights.
+
+    a [cap, K] bf16 (gather: [T, K], row r reads a's row row_token[r]); q [E, N, K/2] and s [E, N, K/32] from
+    ``moe_mxfp4_quant_weights``; c [cap, N] fp32 or bf16.  plan None: dense, a [R, K], q [N, K/2] or [1, N, K/2],
+    c [R, N]."""
+    rows_a, K = _shape("a", a)
+    rows, N = _shape("c", c)
+    if rows_a > _INT32 or rows > _INT32:
+        raise ValueError(f"a and c: {rows_a} and {rows} rows, sizes past 32 bits")
+    if K % 32:
+        raise ValueError(f"a: {K} columns, a multiple of 32 is needed")
+    dev = a.device
+    if plan is None:
+        if gather:
+            raise ValueError("gather needs a plan")
+        E, want, profile = 1, rows, None
+    else:
+        E, want, profile = plan.E, plan.T if gather else plan.cap, plan.desc.profile
+        _plan_rows("c", plan, rows, dev)
+    shape_q, shape_s = (N, K // 2), (N, K // 32)
+    if plan is not None or (isinstance(q, torch.Tensor) and q.dim() == 3):
+        shape_q = (E, *shape_q)
+    if plan is not None or (isinstance(s, torch.Tensor) and s.dim() == 3):
+        shape_s = (E, *shape_s)
+    pa = _need("a", a, _BF16, (want, K), dev)
+    pq = _need("q", q, _BYTES, shape_q, dev)
+    ps = _need("s", s, _BYTES, shape_s, dev)
+    pc = _need("c", c, _VALUES, (rows, N), dev)
+    used = 0 if plan is None else plan.T * plan.K
+    d = _mm_desc(profile, rows_a, rows, used, E, K, N, _DTYPE[c.dtype], MOE_MM_GATHER if gather else 0)
+    _call("moe_mxfp4_mm", dev, stream, ctypes.byref(d), pa, pq, ps, None if plan is None else plan._p, pc)

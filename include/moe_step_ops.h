@@ -30,6 +30,8 @@ extern "C" {
 #define MOE_STEP_K_BALANCE       41
 #define MOE_STEP_K_BALANCE_BWD   42
 #define MOE_STEP_K_ORTHOGONALIZE 43
+#define MOE_STEP_K_MXFP4_WEIGHTS 44
+#define MOE_STEP_K_MXFP4_MM      45
 
 /*
  * Balance loss and z loss of a router.  logits z [T,E] (dtype MOE_F32 or
@@ -115,6 +117,37 @@ typedef struct moe_ortho_desc {
 
 size_t moe_orthogonalize_workspace_bytes(const moe_ortho_desc* desc);
 int moe_orthogonalize(const moe_ortho_desc* desc, const void* g, void* o, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Weights in OCP MXFP4.  32 values along the reduction share an E8M0 scale code,
+ * 2^(code - 127) (255: NaN, and every product with the block is NaN); a value is an
+ * E2M1 code times it: 0, 0.5, 1, 1.5, 2, 3, 4, 6 for codes 0..7, their negatives for
+ * 8..15.  A byte holds two codes, the lower index in its lower half.
+ *   moe_mxfp4_quant_weights  w [E,K,N] (dtype MOE_F32 or MOE_BF16, 16-byte aligned)
+ *       -> q [E,N,K/2] bytes, s [E,N,K/32] bytes: the reduction contiguous.  Scale
+ *       exponent floor(log2(largest magnitude)) - 2, at least -127; values to nearest, ties
+ *       to the even code, at most 6; a block with a NaN or an infinity gets code 255.
+ *       K a multiple of 32, N of 16, each at most 2^20, 1 <= E <= 1024.
+ */
+int moe_mxfp4_quant_weights(int dtype, int E, int K, int N, const void* w, void* q, void* s, moe_profile* profile,
+                            void* stream);
+
+/*
+ * Product of bf16 rows with MXFP4 weights:  c[r,j] = sum_i a[r,i] w[e,j,i] for the rows r of expert
+ * e's segment, w the values of q and s.  desc (moe_mm_desc) and plan as in moe_fp8_mm:
+ * a [a_rows, K] bf16; rows = the plan's capacity, a_rows = rows or with MOE_MM_GATHER T
+ * (row r reads a's row row_token[r]; a token outside 0..a_rows-1 counts as zeros); plan
+ * NULL: dense, E = 1.  c [rows, N] in desc->out, rounded once; rows of no segment are left as they were.
+ *   Precision: every product is exact and sums run in fp32 (a value past the largest bf16
+ * number, which scale codes 253 and 254 allow, counts as an infinity).  Calls of few rows
+ * per expert add up in another order, so a row's result may depend, within fp32's rounding,
+ * on the sizes of the call.  The same call gives the same bits.
+ *   Limits: K a multiple of 32, N of 16, each at most 2^20, E <= 1024, N * K below 2^31, with
+ * MOE_MM_GATHER a_rows * K below 2^30 (MOE_ESHAPE; larger ones go through moe_permute).
+ * a, q and c 16-byte aligned.
+ */
+int moe_mxfp4_mm(const moe_mm_desc* desc, const void* a, const void* q, const void* s, const moe_plan* plan, void* c,
+                 void* stream);
 
 #ifdef __cplusplus
 }

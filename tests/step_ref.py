@@ -142,3 +142,48 @@ def ortho_tolerance(dtype, steps, coef, smallest=0.0):
         grown = 2 * abs(b) / a * a ** (2 * (group - 1)) * 2.0 ** -24 / (1 - a ** -2)
         tol += grown * -(-steps // group)
     return tol
+
+
+# ---------------------------------------------------------------- MXFP4 weights
+
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def power(e):
+    """2^e in float64 from its bits (a GPU's pow may be off by a step)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def mxfp4_values(q, s):
+    """float64 values [..., K] of codes [..., K/2] and scale codes [..., K/32]."""
+    t = torch.tensor(E2M1 + tuple(-v for v in E2M1), dtype=torch.float64, device=q.device)
+    v = torch.stack([t[(q & 15).long()], t[(q >> 4).long()]], -1).flatten(-2)
+    f = power(s.long() - 127)
+    f = torch.where(s == 255, torch.full_like(f, float("nan")), f)
+    return v * torch.repeat_interleave(f, 32, -1)
+
+
+def mxfp4_codes(w):
+    """q [E, N, K/2], s [E, N, K/32] of w [E, K, N], by the definition in float64."""
+    E, K, N = w.shape
+    v = w.double().transpose(1, 2).reshape(E, N, K // 32, 32)
+    m = v.abs().amax(-1)
+    finite = torch.isfinite(v).all(-1)
+    e = torch.frexp(torch.where(finite, m, torch.ones_like(m)))[1] - 1 - 2
+    e = torch.where(m > 0, e, torch.full_like(e, -127)).clamp(min=-127)
+    a = v.abs() * power(-e)[..., None]
+    mags = torch.tensor(E2M1, dtype=torch.float64, device=w.device)
+    near = (a[..., None] - mags).abs()
+    best = near.amin(-1, keepdim=True)
+    # of two equally near values the one with the even code; from 6 on: 6
+    even = torch.arange(8, device=w.device) % 2 == 0
+    c = torch.where(near == best, torch.where(even, 0, 1), 2).argmin(-1)
+    c = torch.where(finite[..., None], c + 8 * torch.signbit(v).long(), torch.zeros_like(c)).view(E, N, K)
+    s = torch.where(finite, e + 127, torch.full_like(e, 255))
+    return (c[..., ::2] + 16 * c[..., 1::2]).to(torch.uint8), s.to(torch.uint8)
+
+
+def mxfp4_mm_bound(a, w, K, ref, out):
+    """Every one of the K exact products, and 16 sums of the waves', may round once in fp32 (one step each, 2^-23, so
+    that an adder which cuts off is covered), and the result once in its type."""
+    return (K + 16) * 2.0 ** -23 * (a.abs() @ w.abs().t()) + HALF[out] * ref.abs() * (1 + 2.0 ** -7) + 1e-37

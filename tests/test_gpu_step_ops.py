@@ -416,3 +416,191 @@ def test_orthogonalize_coefficients_per_step():
         ops.moe_orthogonalize(ops.Ortho(1, 48, 100, dtype=dtype, steps=3, coef=coef), w, o)
         # differences of any of these maps on 0 .. 1.25 are below 4
         check_ortho(o[0], R.ortho_ref(w[0], 3, coef), R.ortho_tolerance(dtype, 3, [R.QUINTIC]))
+
+
+# ---------------------------------------------------------------- MXFP4 weights
+
+def weights(g, E, K, N, dtype=torch.float32, std=0.02):
+    return randn(g, E, K, N, dtype=dtype, std=std)
+
+
+def quantized(w):
+    E, K, N = w.shape
+    q = torch.full((E, N, K // 2), 0xaa, dtype=torch.uint8, device="cuda")
+    s = torch.full((E, N, K // 32), 0xaa, dtype=torch.uint8, device="cuda")
+    ops.moe_mxfp4_quant_weights(w, q, s)
+    return q, s
+
+
+@pytest.mark.parametrize("E,K,N,dtype", [(1, 32, 16, "f32"), (3, 96, 48, "bf16"), (2, 128, 64, "f32"), (1, 160, 80, "bf16"),
+                                         (5, 736, 1040, "f32"), (2, 2048, 512, "bf16"), (1, 64, 4112, "bf16")])
+def test_mxfp4_weights(E, K, N, dtype):
+    g = gen(K + N)
+    w = weights(g, E, K, N)
+    w.view(-1)[::7] *= 2.0 ** 12
+    w[0, :32, 0] = 0.0
+    # borders between two codes, in a block whose largest value, 6, sets the scale to 1
+    ties = torch.tensor([6.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5.0, 7.5, -7.5,
+                         0.0, -0.0] + [0.1] * 13, device="cuda")
+    w[0, :32, 1] = ties
+    w[0, :32, 2] = ties * 2.0 ** -128  # subnormal numbers
+    w[0, :32, 3] = ties * 2.0 ** 125
+    w[0, :32, 4] = 1e-45
+    w = w.to(DT[dtype])
+    q, s = quantized(w)
+    rq, rs = R.mxfp4_codes(w)
+    assert torch.equal(s, rs)
+    assert torch.equal(q, rq)
+
+
+def test_mxfp4_weights_not_finite():
+    g = gen(21)
+    w = weights(g, 2, 96, 32)
+    w[0, 40, 3], w[1, 95, 31] = float("inf"), float("nan")
+    q, s = quantized(w)
+    rq, rs = R.mxfp4_codes(w)
+    assert torch.equal(s, rs) and torch.equal(q, rq) and int((s == 255).sum()) == 2
+
+
+def segments(T, K, E, drop, seed, align=1, lo=0):
+    g = gen(seed)
+    idx = torch.randint(lo, E, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    idx[torch.rand(T, K, generator=g, device="cuda") < drop] = -1
+    plan = ops.Plan(T, K, E, align=align)
+    ops.moe_sort(plan, idx)
+    return plan
+
+
+def check_mm(plan, a, q, s, c, gather, poison):
+    """Every segment's rows, and the rows of none as they were."""
+    offsets, counts, token = plan.offsets.tolist(), plan.counts.tolist(), plan.row_token.long()
+    mine = torch.zeros(plan.cap, dtype=torch.bool, device="cuda")
+    for e in range(plan.E):
+        if not counts[e]:
+            continue
+        at = slice(offsets[e], offsets[e] + counts[e])
+        mine[at] = True
+        x = (a[token[at]] if gather else a[at]).double()
+        w = R.mxfp4_values(q[e], s[e])
+        ref, got = x @ w.t(), c[at].double()
+        # where the magnitudes add up past fp32's largest number, below 2^128, a partial sum may pass it, and
+        # opposite ones make it a NaN: the definition's value is no fp32 number there
+        past = (x.abs() @ w.abs().t() >= 2.0 ** 128) & torch.isfinite(ref)
+        ref, got = ref.masked_fill(past, 0.0), got.masked_fill(past, 0.0)
+        R.within(got, ref, R.mxfp4_mm_bound(x, w, a.shape[1], ref, c.dtype).masked_fill(past, 0.0), e)
+    assert bool((c[~mine] == poison).all())
+
+
+MM = [  # T, K, E, align, drop, reduction, columns, result, gathered
+    (1, 1, 1, 1, 0.0, 32, 16, "bf16", False), (1, 8, 16, 1, 0.0, 7168, 64, "bf16", True), (3, 2, 5, 16, 0.3, 96, 48, "f32", True),
+    (40, 4, 300, 1, 0.1, 288, 80, "bf16", True), (37, 3, 8, 1, 0.15, 736, 1040, "f32", False), (64, 8, 128, 1, 0.0, 256, 512, "bf16", True),
+    (200, 2, 3, 1, 0.0, 1024, 272, "bf16", False), (200, 2, 3, 1, 0.2, 32, 16, "f32", True), (301, 5, 7, 128, 0.1, 160, 528, "bf16", True),
+    (1000, 2, 4, 1, 0.0, 224, 256, "f32", True), (129, 1, 1, 1, 0.0, 64, 272, "bf16", False), (4000, 3, 24, 1, 0.05, 512, 320, "bf16", True),
+    (2500, 4, 1000, 1, 0.0, 128, 32, "bf16", True), (6000, 1, 2, 256, 0.0, 2048, 768, "f32", False), (50, 6, 1024, 1, 0.5, 64, 48, "f32", False),
+    (700, 8, 64, 1, 0.0, 1056, 144, "bf16", True), (900, 8, 600, 1, 0.0, 96, 304, "bf16", True),
+]
+
+
+@pytest.mark.parametrize("T,K,E,align,drop,d,N,out,gather", MM)
+def test_mxfp4_mm(T, K, E, align, drop, d, N, out, gather):
+    plan = segments(T, K, E, drop, T + E, align)
+    g = gen(d + N)
+    q, s = quantized(weights(g, E, d, N, dtype=torch.bfloat16))
+    a = randn(g, T if gather else plan.cap, d, dtype=torch.bfloat16)
+    if not gather:  # rows of no segment are never read
+        mine = torch.zeros(plan.cap, dtype=torch.bool, device="cuda")
+        for o, n in zip(plan.offsets.tolist(), plan.counts.tolist()):
+            mine[o:o + n] = True
+        a[~mine] = float("nan")
+    c = torch.full((plan.cap, N), -7.25, dtype=DT[out], device="cuda")
+    ops.moe_mxfp4_mm(plan, a, q, s, c, gather=gather)
+    check_mm(plan, a, q, s, c, gather, -7.25)
+    again = torch.full_like(c, -7.25)
+    ops.moe_mxfp4_mm(plan, a, q, s, again, gather=gather)
+    assert torch.equal(c, again)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 33, 100, 300])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_mxfp4_mm_dense(rows, out):
+    g = gen(rows)
+    q, s = quantized(weights(g, 1, 416, 208))
+    a = randn(g, rows, 416, dtype=torch.bfloat16)
+    c = torch.empty(rows, 208, dtype=DT[out], device="cuda")
+    ops.moe_mxfp4_mm(None, a, q[0], s[0], c)
+    w, x = R.mxfp4_values(q[0], s[0]), a.double()
+    R.within(c, x @ w.t(), R.mxfp4_mm_bound(x, w, 416, x @ w.t(), c.dtype))
+    ops.moe_mxfp4_mm(None, torch.empty(0, 416, dtype=torch.bfloat16, device="cuda"), q, s, c[:0])
+
+
+@pytest.mark.parametrize("T", [4, 600])
+def test_mxfp4_mm_keeps_what_is_not_finite_in_its_place(T):
+    """NaN and infinity in a row stay in that row, a block without a number in its column and expert; scale
+    codes from one end to the other; tokens that do not exist count as zeros."""
+    E, d, N = 3, 160, 64
+    plan = segments(T, 2, E, 0.0, 5)
+    g = gen(T)
+    q, s = quantized(weights(g, E, d, N))
+    s[0, 5, 4], s[1, 6, 0], s[2, 7, 1], s[1, 8] = 255, 0, 252, 1
+    a = randn(g, T, d, dtype=torch.bfloat16)
+    a[1, 3] = float("nan")
+    a[2, 159] = float("inf")
+    q[:, :, 79] = 0x11  # (no zero meets the infinity)
+    c = torch.full((plan.cap, N), -7.25, device="cuda")
+    ops.moe_mxfp4_mm(plan, a, q, s, c, gather=True)
+    check_mm(plan, a, q, s, c, True, -7.25)
+    ghosts = plan.row_token.clone()
+    lost = torch.arange(plan.cap, device="cuda") % 3 == 0
+    plan.row_token[lost] = T + 7
+    plan.row_token[0] = -1
+    c2 = torch.full_like(c, -7.25)
+    ops.moe_mxfp4_mm(plan, a, q, s, c2, gather=True)
+    keep = ~lost
+    assert torch.equal(c2[keep].nan_to_num(7, 8, 9), c[keep].nan_to_num(7, 8, 9))
+    e0 = slice(int(plan.offsets[0]), int(plan.offsets[0] + plan.counts[0]))
+    z = c2[lost]
+    assert bool(((z == 0) | torch.isnan(z)).all())  # zeros, NaN in the spoiled block's column
+    assert bool((torch.isnan(c2[e0][lost[e0]]).nonzero()[:, 1] == 5).all())
+    plan.row_token.copy_(ghosts)
+
+
+def test_mxfp4_mm_captured_and_on_another_stream():
+    """Decode through two products, captured: sort, product, product back; and a few hundred rows."""
+    g = gen(31)
+    for T in (3, 500):
+        E, K, d, n = 6, 2, 192, 96
+        w1, w2 = quantized(weights(g, E, d, n)), quantized(weights(g, E, n, d))
+        x, idx = randn(g, T, d, dtype=torch.bfloat16), torch.zeros(T, K, dtype=torch.int32, device="cuda")
+        pa, pb = ops.Plan(T, K, E), ops.Plan(T, K, E)
+        h, y = torch.zeros(pa.cap, n, dtype=torch.bfloat16, device="cuda"), torch.zeros(pa.cap, d, device="cuda")
+
+        def work(p=pa, h=h, y=y, stream=None):
+            ops.moe_sort(p, idx, stream=stream)
+            ops.moe_mxfp4_mm(p, x, *w1, h, gather=True, stream=stream)
+            ops.moe_mxfp4_mm(p, h, *w2, y, stream=stream)
+
+        def eager(i):
+            x.copy_(randn(gen(90 + i), T, d))
+            idx.copy_(torch.randint(0, E, (T, K), generator=gen(95 + i), device="cuda"))
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            h2, y2 = torch.zeros_like(h), torch.zeros_like(y)
+            work(pb, h2, y2, s)
+            s.synchronize()
+            return h2, y2
+
+        replay(work, (h, y), eager)
+
+
+def test_mxfp4_profile():
+    q, s = quantized(torch.ones(1, 32, 16, device="cuda"))
+    plan = ops.Plan(2, 1, 1)
+    ops.moe_sort(plan, torch.zeros(2, 1, dtype=torch.int32, device="cuda"))
+    prof = B.Profiler(2)
+    plan.attach(prof)
+    ops.moe_mxfp4_mm(plan, torch.ones(2, 32, dtype=torch.bfloat16, device="cuda"), q, s, torch.empty(2, 16, device="cuda"))
+    torch.cuda.synchronize()
+    plan.detach()
+    rec = prof.records()
+    prof.close()
+    assert [ops.STEP_KERNEL_NAMES[k] for k, _ in rec] == ["mxfp4_mm"]

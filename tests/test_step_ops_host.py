@@ -161,3 +161,65 @@ def test_ortho_binding_refuses():
         ops.moe_orthogonalize(h, g[0], g)
     with pytest.raises(ValueError, match="o: not contiguous"):
         ops.moe_orthogonalize(h, g, torch.zeros(2, 6, 4, dtype=torch.bfloat16).transpose(1, 2))
+
+
+def mdesc(a_rows=8, rows=8, used=0, E=2, K=64, N=48, out=B.MOE_BF16, flags=0, reserved=0):
+    return ops.MoeMmDesc(a_rows, rows, used, E, K, N, out, flags, reserved, None)
+
+
+PLAN = ops.MoePlan(P, P, P, P)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(a_rows=-1), B.MOE_EINVAL), (dict(rows=-1), B.MOE_EINVAL), (dict(used=9), B.MOE_EINVAL), (dict(E=0), B.MOE_EINVAL),
+    (dict(K=0), B.MOE_EINVAL), (dict(N=0), B.MOE_EINVAL), (dict(K=48), B.MOE_ESHAPE), (dict(N=24), B.MOE_ESHAPE), (dict(E=1025), B.MOE_ESHAPE),
+    (dict(K=(1 << 20) + 32), B.MOE_ESHAPE), (dict(K=1 << 16, N=1 << 15), B.MOE_ESHAPE), (dict(out=5), B.MOE_EDTYPE), (dict(flags=2), B.MOE_EINVAL),
+    (dict(reserved=1), B.MOE_EINVAL), (dict(a_rows=9), B.MOE_EINVAL), (dict(a_rows=1 << 24, flags=1), B.MOE_ESHAPE),
+    (dict(a_rows=0, flags=1), B.MOE_EINVAL),
+])
+def test_mxfp4_mm_descriptors_refused(kw, code):
+    assert ops.lib().moe_mxfp4_mm(ref(mdesc(**kw)), P, P, P, ref(PLAN), P, None) == code
+
+
+def test_mxfp4_refusals():
+    lib, bf = ops.lib(), B.MOE_BF16
+    mm = lambda d, *a: lib.moe_mxfp4_mm(ref(d), *a, None)  # noqa: E731
+    assert lib.moe_mxfp4_mm(None, P, P, P, ref(PLAN), P, None) == B.MOE_EINVAL
+    for bad in ((None, P, P, ref(PLAN), P), (P, None, P, ref(PLAN), P), (P, P, None, ref(PLAN), P), (P, P, P, ref(PLAN), None),
+                (P + 8, P, P, ref(PLAN), P), (P, P + 8, P, ref(PLAN), P), (P, P, P, ref(PLAN), P + 8), (P, P, P, None, P)):
+        assert mm(mdesc(), *bad) == B.MOE_EINVAL
+    assert mm(mdesc(flags=1), P, P, P, ref(ops.MoePlan(P, P, 0, P)), P) == B.MOE_EINVAL
+    assert mm(mdesc(), P, P, P, ref(ops.MoePlan(0, P, P, P)), P) == B.MOE_EINVAL
+    assert mm(mdesc(E=1, flags=1), P, P, P, None, P) == B.MOE_EINVAL
+    assert mm(mdesc(a_rows=0, rows=0), None, None, None, ref(PLAN), None) == B.MOE_OK
+    w = lambda *a: lib.moe_mxfp4_quant_weights(*a, None, None)  # noqa: E731
+    assert w(4, 1, 32, 16, P, P, P) == B.MOE_EDTYPE
+    for E, K, N, code in ((0, 32, 16, B.MOE_EINVAL), (1, 0, 16, B.MOE_EINVAL), (1, 16, 16, B.MOE_ESHAPE), (1, 32, 8, B.MOE_ESHAPE),
+                          (1025, 32, 16, B.MOE_ESHAPE), (1024, 1 << 20, 1 << 20, B.MOE_ESHAPE)):
+        assert w(bf, E, K, N, P, P, P) == code
+    for bad in ((None, P, P), (P, None, P), (P, P, None), (P + 8, P, P), (P, P + 8, P)):
+        assert w(bf, 1, 32, 16, *bad) == B.MOE_EINVAL
+
+
+def test_mxfp4_binding_refuses():
+    z = lambda *n, dtype=torch.uint8: torch.zeros(*n, dtype=dtype)  # noqa: E731
+    bf = torch.bfloat16
+    a, q, s, c = z(4, 64, dtype=bf), z(1, 16, 32), z(1, 16, 2), z(4, 16, dtype=bf)
+    with pytest.raises(ValueError, match="a GPU is needed"):
+        ops.moe_mxfp4_mm(None, a, q, s, c)
+    with pytest.raises(ValueError, match="a: dtype"):
+        ops.moe_mxfp4_mm(None, a.float(), q, s, c)
+    with pytest.raises(ValueError, match="multiple of 32"):
+        ops.moe_mxfp4_mm(None, z(4, 48, dtype=bf), q, s, c)
+    with pytest.raises(ValueError, match="q: shape"):
+        ops.moe_mxfp4_mm(None, a, q[..., :31].contiguous(), s, c)
+    with pytest.raises(ValueError, match="s: dtype"):
+        ops.moe_mxfp4_mm(None, a, q, s.float(), c)
+    with pytest.raises(ValueError, match="gather needs a plan"):
+        ops.moe_mxfp4_mm(None, a, q, s, c, gather=True)
+    with pytest.raises(ValueError, match="c: not contiguous"):
+        ops.moe_mxfp4_mm(None, a, q, s, z(16, 4, dtype=bf).t())
+    with pytest.raises(ValueError, match="multiple of 32"):
+        ops.moe_mxfp4_quant_weights(z(1, 48, 16, dtype=bf), z(1, 16, 24), z(1, 16, 1))
+    with pytest.raises(ValueError, match="q: shape"):
+        ops.moe_mxfp4_quant_weights(z(1, 64, 16, dtype=bf), z(1, 64, 16), s)
