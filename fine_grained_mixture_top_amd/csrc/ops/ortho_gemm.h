@@ -19,11 +19,17 @@
 namespace moe {
 namespace ortho {
 
+constexpr int NORM_PARTS = 64;    // partial sums of a matrix's norm at most
+constexpr int X_EXP = 13;         // X's norm in fp16 parts lies in [2^13, 2^14)
+constexpr int MAX_STEPS = 64;
+
 typedef _Float16 f16x8_v __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4_v __attribute__((ext_vector_type(4)));
 
-// x as hi + lo
+// x as hi + lo.  (x has to be the one rounded fp32 number for both: the compiler would
+// round a product straight to fp16 for the hi that is stored and take the lo from another)
 __device__ __forceinline__ void split(float x, _Float16& hi, _Float16& lo) {
+  asm("" : "+v"(x));
   hi = (_Float16)x;
   lo = (_Float16)(x - (float)hi);
 }

@@ -21,6 +21,7 @@
 
 #include "launch_util.h"
 #include "ortho_gemm.h"
+#include "ortho_small.h"
 #include "step_launch.h"
 
 namespace moe {
@@ -28,9 +29,6 @@ namespace moe {
 namespace {
 
 using namespace ortho;
-
-constexpr int NORM_PARTS = 64;    // partial sums of a matrix at most
-constexpr int X_EXP = 13;         // X's norm in fp16 parts lies in [2^13, 2^14)
 
 // ---- sum of squares, in 64 bits: no scaling is needed for any finite input ----
 template <typename T, int V>
@@ -62,12 +60,7 @@ k_ortho_norm(const T* g, int64_t elems, int parts, double* sums) {
 }
 
 // The update as fp16 parts in both layouts, times a power of two that brings its norm
-// to 2^13 .. 2^14, and the factors that go with the groups of steps.  A matrix whose
-// norm is far below eps starts far below 1 and grows with the steps; so that its parts
-// keep their bits, the X between two groups carries a power of two of its own, from a
-// bound of its norm that is followed through the steps:
-//     back[i]    X of group i over its stored numbers (but for the exponent that all have)
-//     on[i]      what the stored numbers of group i + 1 are of Q times those of group i
+// to 2^13 .. 2^14.
 struct Convert {
   const void* g;
   int M, N;
@@ -80,62 +73,11 @@ struct Convert {
   float* back;    // [groups][gridDim.z]
 };
 
-// A matrix's norm, from its partial sums (a wave, a lane each)
-__device__ __forceinline__ double norm_of(const double* sums, int parts, int e) {
-  static_assert(NORM_PARTS == 64, "a lane each");
-  const int lane = threadIdx.x & 63;
-  double s = lane < parts ? sums[(int64_t)e * NORM_PARTS + lane] : 0.0;
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
-  return sqrt(s);
-}
-// the power of two of a matrix's stored numbers, and X_0 over them (a matrix of zeros,
-// as an expert without rows has it, stays one)
-__device__ __forceinline__ int power_of(double norm) {
-  return norm > 0.0 && norm < __builtin_inf() ? X_EXP - ilogb(norm) : 0;
-}
-__device__ __forceinline__ double first_of(double norm, double eps) {
-  if (!(norm < __builtin_inf())) return __builtin_nan("");
-  return norm == 0.0 ? 0.0 : scalbn(1.0 / (norm + eps), -power_of(norm));
-}
-
-// (a launch of its own, for more than one group: coefficients at an index that the
-// compiler does not know would have every thread copy the arguments)
-constexpr int MAX_STEPS = 64;
-struct Factors {
-  const double* sums;
-  int parts;
-  double eps;
-  float* back;
-  float* on;
-  int groups;
-  uint8_t steps[MAX_STEPS];  // of each group
-  float coef[3 * MAX_STEPS];
-};
+// (a launch of its own, for more than one group)
 __global__ void __launch_bounds__(64)
-k_ortho_factors(Factors a) {
-  const int e = blockIdx.x, nb = gridDim.x;
-  const double norm = norm_of(a.sums, a.parts, e), first = first_of(norm, a.eps);
-  const bool fine = norm < __builtin_inf();
-  const float nan = __builtin_nanf("");
-  const int lane = threadIdx.x;
-  float most = norm == 0.0 ? 0.f : (float)(norm / (norm + a.eps));  // of |X|
-  const float* c = a.coef;
-  int t = 0;
-  for (int i = 0; i + 1 < a.groups; ++i) {
-    for (int s = 0; s < a.steps[i]; ++s, c += 3) {
-      const float v = most * (float)(lane + 1) * 0.015625f, l = v * v;
-      float m = fabsf(v * fmaf(l, fmaf(l, c[2], c[1]), c[0]));
-      for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-      most = m;
-    }
-    const int next = most > 0.f && most < __builtin_inff() ? max(-60, min(120, -ilogbf(most))) : 0;
-    const double f = i == 0 ? first : scalbn(1.0, -t);
-    if (lane == 0) {
-      a.on[i * nb + e] = fine ? (float)scalbn(f, next) : nan;
-      a.back[(i + 1) * nb + e] = fine ? (float)scalbn(1.0, -next) : nan;
-    }
-    t = next;
-  }
+k_ortho_factors(Factors) {
+  const auto* a = arguments<Factors>();
+  factors(*a, norm_of(a->sums, a->parts, blockIdx.x), blockIdx.x, gridDim.x);
 }
 
 template <typename T, int P>
@@ -305,17 +247,33 @@ Sizes sizes(const OrthoArgs& a) {
   return z;
 }
 
+Factors factors_of(const OrthoArgs& a, int groups, int nb, const double* sums, int parts, float* back) {
+  Factors f{};
+  f.sums = sums; f.parts = parts; f.eps = a.eps;
+  f.back = back; f.on = back + groups * nb; f.groups = groups;
+  for (int s = 0, i = 0; s < a.steps; s += f.steps[i], ++i) f.steps[i] = (uint8_t)group_steps(a, s);
+  std::copy(a.coef, a.coef + 3 * a.steps, f.coef);
+  return f;
+}
+
+// the sums of squares of nb updates; returns their number of parts
+template <typename T>
+int launch_norm(const T* g, int64_t elems, int nb, double* sums, hipStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = elems % V == 0 && ((uintptr_t)g & 15) == 0;
+  const int parts = (int)std::min<int64_t>(NORM_PARTS, div_up(elems, 256 * 16));
+  if (vec) hipLaunchKernelGGL((k_ortho_norm<T, V>), dim3(parts, nb), dim3(256), 0, st, g, elems, parts, sums);
+  else hipLaunchKernelGGL((k_ortho_norm<T, 1>), dim3(parts, nb), dim3(256), 0, st, g, elems, parts, sums);
+  return parts;
+}
+
 template <typename T>
 hipError_t prepare(const OrthoArgs& a, const Sizes& z, int e0, int nb, hipStream_t st) {
   char* ws = (char*)a.ws;
   const int64_t elems = (int64_t)a.M * a.N;
   const T* g = (const T*)a.g + e0 * elems;
   double* sums = (double*)(ws + z.sums);
-  constexpr int V = 16 / sizeof(T);
-  const bool vec = elems % V == 0 && ((uintptr_t)a.g & 15) == 0;
-  const int parts = (int)std::min<int64_t>(NORM_PARTS, div_up(elems, 256 * 16));
-  if (vec) hipLaunchKernelGGL((k_ortho_norm<T, V>), dim3(parts, nb), dim3(256), 0, st, g, elems, parts, sums);
-  else hipLaunchKernelGGL((k_ortho_norm<T, 1>), dim3(parts, nb), dim3(256), 0, st, g, elems, parts, sums);
+  const int parts = launch_norm(g, elems, nb, sums, st);
   const bool tall = a.M > a.N;
   constexpr int P = sizeof(T) == 4 ? 2 : 1;
   Convert c{};
@@ -328,22 +286,170 @@ hipError_t prepare(const OrthoArgs& a, const Sizes& z, int e0, int nb, hipStream
   c.strans = tall ? sx : sxt;
   c.back = (float*)(ws + z.f);
   if (z.groups > 1) {
-    Factors f{};
-    f.sums = sums; f.parts = parts; f.eps = a.eps;
-    f.back = c.back; f.on = c.back + z.groups * nb; f.groups = z.groups;
-    for (int s = 0, i = 0; s < a.steps; s += f.steps[i], ++i) f.steps[i] = (uint8_t)group_steps(a, s);
-    std::copy(a.coef, a.coef + 3 * a.steps, f.coef);
+    const Factors f = factors_of(a, z.groups, nb, sums, parts, c.back);
     hipLaunchKernelGGL(k_ortho_factors, dim3(nb), dim3(64), 0, st, f);
   }
   hipLaunchKernelGGL((k_ortho_convert<T, P>), dim3((a.N + 63) / 64, (a.M + 63) / 64, nb), dim3(256), 0, st, c);
   return hipGetLastError();
 }
 
+// ---- the smaller side at most 128 (ortho_small.h) ----
+bool is_small(const OrthoArgs& a) {
+  return std::min(a.M, a.N) <= 128 && (a.dtype == MOE_F32 || group_steps(a, 0) == a.steps);
+}
+
+struct SmallSizes {
+  int mp, chunks, nb, slices, per, groups;
+  int64_t part, x, q, f, sums, total;
+};
+SmallSizes small_sizes(const OrthoArgs& a) {
+  SmallSizes z{};
+  const bool two = a.dtype == MOE_F32;
+  z.mp = std::min(a.M, a.N) <= 64 ? 64 : 128;
+  z.chunks = (int)div_up(std::max(a.M, a.N), CHUNK);
+  z.groups = two ? a.steps : 1;
+  const int64_t square = (int64_t)z.mp * z.mp * 4, wide = (int64_t)z.mp * CHUNK * 4 * z.chunks;
+  // matrices at a time: X of fp32 updates within 1 GB (or one of them)
+  z.nb = two ? (int)std::max<int64_t>(1, std::min<int64_t>(a.E, ((int64_t)1 << 30) / wide)) : a.E;
+  z.nb = (int)div_up(a.E, div_up(a.E, z.nb));
+  // slices: two workgroups for every CU, and few enough for one workgroup to add up
+  z.slices = (int)std::min<int64_t>(std::min(z.chunks, 16), div_up(512, z.nb));
+  z.per = (int)div_up(z.chunks, z.slices);
+  z.slices = (int)div_up(z.chunks, z.per);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  z.part = take(square * z.slices * z.nb * (two ? 2 : 1));
+  if (two) z.x = take(wide * z.nb);
+  else z.q = take(square * z.nb);
+  z.f = take(4 * (int64_t)z.nb * 2 * z.groups);
+  z.sums = take(8 * (int64_t)z.nb * NORM_PARTS);
+  z.total = at;
+  return z;
+}
+
+template <typename K, typename A>
+hipError_t small_launch(K* k, dim3 grid, int lds, const A& args, std::atomic<uint64_t>& done, hipStream_t st) {
+  const hipError_t e = allow_lds(k, lds, device(), done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k, grid, dim3(SMALL_THREADS), lds, st, args);
+  return hipGetLastError();
+}
+
+template <typename T, int MP, bool TALL>
+hipError_t small_gram(const GramArgs& g, int nb, hipStream_t st) {
+  constexpr int P = sizeof(T) == 4 ? 2 : 1;
+  static std::atomic<uint64_t> done{0};
+  return small_launch(k_small_gram<T, P, MP, TALL>, dim3(g.a.slices, nb), MP * CHUNK * 2 * P, g, done, st);
+}
+template <int MP, bool TALL, bool FIRST, bool LAST>
+hipError_t small_step(const StepArgs& s, int nb, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  return small_launch(k_small_step<MP, TALL, FIRST, LAST>, dim3(s.a.slices, nb), SmallCfg<MP>::WIDE + SmallCfg<MP>::SQUARE, s,
+                      done, st);
+}
+
+template <int MP, bool TALL>
+hipError_t launch_small_as(const OrthoArgs& a, hipStream_t st) {
+  const SmallSizes z = small_sizes(a);
+  char* ws = (char*)a.ws;
+  const bool two = a.dtype == MOE_F32;
+  auto pow2 = [](int n) { return (float)std::ldexp(1.0, n); };
+  for (int e0 = 0; e0 < a.E; e0 += z.nb) {
+    const int nb = std::min(z.nb, a.E - e0);
+    GramArgs g{};
+    Small& s = g.a;
+    const int64_t elems = (int64_t)a.M * a.N;
+    s.g = two ? (const void*)((const float*)a.g + e0 * elems) : (const void*)((const bf16_t*)a.g + e0 * elems);
+    s.o = two ? (void*)((float*)a.o + e0 * elems) : (void*)((bf16_t*)a.o + e0 * elems);
+    s.M = a.M; s.N = a.N; s.m = std::min(a.M, a.N); s.k = std::max(a.M, a.N);
+    s.chunks = z.chunks; s.per = z.per; s.slices = z.slices;
+    s.vec = a.N % (two ? 4 : 8) == 0 && (((uintptr_t)a.g | (uintptr_t)a.o) & 15) == 0;
+    s.eps = a.eps;
+    double* sums = (double*)(ws + z.sums);
+    s.sums = sums;
+    s.parts = two ? launch_norm((const float*)s.g, elems, nb, sums, st) : launch_norm((const bf16_t*)s.g, elems, nb, sums, st);
+    const int64_t part = (int64_t)MP * MP * z.slices * nb;
+    s.part = (float*)(ws + z.part);
+    s.part_next = s.part + part;
+    s.x = ws + z.x;
+    s.q = ws + z.q;
+    s.back = (float*)(ws + z.f);
+    s.on = s.back + z.groups * nb;
+    g.f = factors_of(a, z.groups, nb, sums, s.parts, s.back);
+    hipError_t err = two ? small_gram<float, MP, TALL>(g, nb, st) : small_gram<bf16_t, MP, TALL>(g, nb, st);
+    if (err != hipSuccess) return err;
+    Spectrum spec;
+    spec.begin();
+    int ea = exponent_for(1.0);
+    if (!two) {
+      StepsArgs q{};
+      q.a = s;
+      q.steps = a.steps;
+      q.gram = pow2(ea);
+      int eq = 0;
+      for (int i = 0; i < a.steps; ++i) {
+        const float* c = a.coef + 3 * i;
+        double pm, tm, am, qm;
+        spec.step(c, &pm, &tm, &am, &qm);
+        const int ep = exponent_for(pm), et = exponent_for(tm), en = exponent_for(am), eqn = i == 0 ? ep : exponent_for(qm);
+        q.s[i] = Recurrence{c[0] * pow2(ep), c[1] * pow2(ep - ea), c[2] * pow2(ep - 2 * ea), pow2(et - ep - ea),
+                            pow2(en - et - ep), pow2(eqn - ep - eq)};
+        ea = en;
+        eq = eqn;
+      }
+      static std::atomic<uint64_t> done{0}, done_apply{0};
+      err = small_launch(k_small_steps<MP>, dim3(nb), 2 * SmallCfg<MP>::SQUARE, q, done, st);
+      if (err != hipSuccess) return err;
+      ApplyArgs p{s, a.scale * pow2(-eq)};
+      // (a Q is read by every workgroup: chunks enough for two of them on a CU)
+      p.a.per = (int)std::max<int64_t>(1, (int64_t)z.chunks * nb / 1024);
+      err = small_launch(k_small_apply<MP, TALL>, dim3((unsigned)div_up(z.chunks, p.a.per), nb),
+                         MP * CHUNK * 2 + SmallCfg<MP>::SQUARE, p, done_apply, st);
+      if (err != hipSuccess) return err;
+      continue;
+    }
+    int x_exp = 0;
+    for (int i = 0; i < a.steps; ++i) {
+      const float* c = a.coef + 3 * i;
+      double pm, tm, am, qm, lmax = 0.0;
+      spec.begin();
+      for (int n = 0; n < Spectrum::N; ++n) lmax = std::max(lmax, spec.l[n]);
+      ea = exponent_for(lmax);
+      spec.step(c, &pm, &tm, &am, &qm);
+      spec.end();
+      const int ep = exponent_for(pm);
+      const bool last = i + 1 == a.steps;
+      const int nx = X_EXP - 1;
+      StepArgs q{s, pow2(ea - 2 * x_exp), c[0] * pow2(ep), c[1] * pow2(ep - ea), c[2] * pow2(ep - 2 * ea),
+                 last ? a.scale * pow2(-ep - x_exp) : pow2(nx - ep - x_exp)};
+      err = i == 0 ? (last ? small_step<MP, TALL, true, true>(q, nb, st) : small_step<MP, TALL, true, false>(q, nb, st))
+                   : (last ? small_step<MP, TALL, false, true>(q, nb, st) : small_step<MP, TALL, false, false>(q, nb, st));
+      if (err != hipSuccess) return err;
+      x_exp = nx;
+      std::swap(s.part, s.part_next);
+      s.back += nb;
+      s.on += nb;
+    }
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_small(const OrthoArgs& a, hipStream_t st) {
+  const bool tall = a.M > a.N;
+  if (std::min(a.M, a.N) <= 64) return tall ? launch_small_as<64, true>(a, st) : launch_small_as<64, false>(a, st);
+  return tall ? launch_small_as<128, true>(a, st) : launch_small_as<128, false>(a, st);
+}
+
 }  // namespace
 
-size_t ortho_ws_bytes(const OrthoArgs& a) { return (size_t)sizes(a).total; }
+size_t ortho_ws_bytes(const OrthoArgs& a) { return (size_t)(is_small(a) ? small_sizes(a).total : sizes(a).total); }
 
 hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
+  if (is_small(a)) return launch_small(a, st);
   const Sizes z = sizes(a);
   const bool tall = a.M > a.N, fine = a.dtype == MOE_F32;
   char* ws = (char*)a.ws;

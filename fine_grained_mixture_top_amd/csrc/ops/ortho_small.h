@@ -1,0 +1,587 @@
+// Orthogonalised updates whose smaller side m is at most 128: the m x m matrices of a
+// step fit a CU's LDS, so a workgroup goes through whole steps without a launch
+// between two products (ortho_kernels.hip has the formulas, ortho_gemm.h the numbers).
+//
+// The larger side is cut into chunks of 128.  A matrix in LDS is MP or 128 rows
+// of K numbers (MP = 64 or 128, padded with zeros): two parts, K / 32 planes of lines of 128
+// bytes (32 numbers' hi, then their lo); one part, K / 64 planes of 64 numbers.
+// Eight waves, two along the rows of a product and four along its columns.
+#pragma once
+
+#include <type_traits>
+
+#include "ortho_gemm.h"
+
+namespace moe {
+namespace ortho {
+
+constexpr int CHUNK = 128;
+constexpr int SMALL_THREADS = 512;
+
+// line address of row r, plane c of a matrix of ROWS rows, and the slot of 16 bytes in it
+template <int ROWS> __device__ __forceinline__ int line_at(int c, int r) { return (c * ROWS + r) * 128; }
+
+// 4 numbers from column k on (a multiple of 4) of row r
+template <int ROWS>
+__device__ __forceinline__ void put4(char* m, int r, int k, const f32x4_v v) {
+  f16x4_v hi, lo;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    _Float16 vh, vl;
+    split(v[x], vh, vl);
+    hi[x] = vh;
+    lo[x] = vl;
+  }
+  char* line = m + line_at<ROWS>(k >> 5, r);
+  const int c = (k & 31) >> 3, half = (k & 4) * 2;
+  *reinterpret_cast<f16x4_v*>(line + ((c ^ (r & 7)) * 16) + half) = hi;
+  *reinterpret_cast<f16x4_v*>(line + (((c + 4) ^ (r & 7)) * 16) + half) = lo;
+}
+// one number
+template <int ROWS>
+__device__ __forceinline__ void put1(char* m, int r, int k, float v) {
+  _Float16 hi, lo;
+  split(v, hi, lo);
+  char* line = m + line_at<ROWS>(k >> 5, r);
+  const int c = (k & 31) >> 3, at = (k & 7) * 2;
+  *reinterpret_cast<_Float16*>(line + ((c ^ (r & 7)) * 16) + at) = hi;
+  *reinterpret_cast<_Float16*>(line + (((c + 4) ^ (r & 7)) * 16) + at) = lo;
+}
+
+// acc = A B^T for the rows ra0 .. and rb0 .. of two matrices in LDS, over `planes` times 32
+// of the reduction.  ROWS_FIRST: a lane holds, of row p of A, four neighbouring rows of B;
+// else of row p of B four of A.
+template <int FM, int FN, int RA, int RB, int PA, int PB, bool FINE, bool ROWS_FIRST>
+__device__ __forceinline__ void product(f32x4_v (&acc)[FM][FN], const char* a, int ra0, const char* b, int rb0, int planes,
+                                        int lane) {
+  const int p = lane & 15, h = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < FM; ++j)
+#pragma unroll
+    for (int i = 0; i < FN; ++i) acc[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  auto mul = [](const f16x8_v x, const f16x8_v y, const f32x4_v c) {  // x rows of A, y rows of B
+    return ROWS_FIRST ? __builtin_amdgcn_mfma_f32_16x16x32_f16(y, x, c, 0, 0, 0)
+                      : __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
+  };
+  for (int c = 0; c < planes; ++c) {
+    f16x8_v fa[FM][PA], fb[FN][PB];
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int x = 0; x < PA; ++x) {
+        const int r = ra0 + 16 * j + p, slot = PA == 2 ? h + 4 * x : h + 4 * (c & 1);
+        fa[j][x] = *reinterpret_cast<const f16x8_v*>(a + line_at<RA>(PA == 2 ? c : c >> 1, r) + ((slot ^ (r & 7)) * 16));
+      }
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int x = 0; x < PB; ++x) {
+        const int r = rb0 + 16 * i + p, slot = PB == 2 ? h + 4 * x : h + 4 * (c & 1);
+        fb[i][x] = *reinterpret_cast<const f16x8_v*>(b + line_at<RB>(PB == 2 ? c : c >> 1, r) + ((slot ^ (r & 7)) * 16));
+      }
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        if constexpr (FINE) {
+          f32x4_v d = mul(fa[j][0], fb[i][1], f32x4_v{0.f, 0.f, 0.f, 0.f});
+          d = mul(fa[j][1], fb[i][0], d);
+          acc[j][i] = mul(fa[j][0], fb[i][0], acc[j][i]);
+          acc[j][i] += d;
+        } else {
+          acc[j][i] = mul(fa[j][0], fb[i][0], acc[j][i]);
+          if constexpr (PB == 2) acc[j][i] = mul(fa[j][0], fb[i][1], acc[j][i]);
+          if constexpr (PA == 2) acc[j][i] = mul(fa[j][1], fb[i][0], acc[j][i]);
+        }
+      }
+  }
+}
+
+// A chunk of the update, times 2^ex, as a matrix in LDS.  The update's part is gr x gc
+// numbers (row stride ld) of GR x GC, zeros past them; TURN: its columns become the rows.
+template <typename T, int P, int GR, int GC, bool TURN>
+__device__ __forceinline__ void load_update(char* m, const T* g, int64_t ld, int gr, int gc, int ex, bool vec, int tid) {
+  constexpr int V = 8, ROWS = TURN ? GC : GR;
+  constexpr int TASKS = GR * GC / V / SMALL_THREADS;
+  float v[TASKS][V];
+#pragma unroll
+  for (int t = 0; t < TASKS; ++t) {
+    const int id = t * SMALL_THREADS + tid, r = id / (GC / V), c = id % (GC / V) * V;
+    const T* p = g + r * ld + c;
+    if (r < gr && c + V <= gc && vec) {
+      T x[V];
+      const uint4* u = reinterpret_cast<const uint4*>(p);
+      uint4 w[sizeof(T) * V / 16];
+#pragma unroll
+      for (int y = 0; y < (int)(sizeof(T) * V / 16); ++y) w[y] = u[y];
+      __builtin_memcpy(x, w, sizeof(x));
+#pragma unroll
+      for (int y = 0; y < V; ++y) v[t][y] = Elem<T>::to_f(x[y]);
+    } else {
+#pragma unroll
+      for (int y = 0; y < V; ++y) v[t][y] = r < gr && c + y < gc ? Elem<T>::to_f(p[y]) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TASKS; ++t) {
+    const int id = t * SMALL_THREADS + tid, r = id / (GC / V), c = id % (GC / V) * V;
+    f16x8_v hi, lo;
+#pragma unroll
+    for (int y = 0; y < V; ++y) {
+      _Float16 vh, vl;
+      split(ldexpf(v[t][y], ex), vh, vl);
+      hi[y] = vh;
+      lo[y] = vl;
+    }
+    if constexpr (TURN) {
+      // number k = r of the rows c .. c + 7
+#pragma unroll
+      for (int y = 0; y < V; ++y) {
+        const int row = c + y, plane = P == 2 ? r >> 5 : r >> 6, slot = P == 2 ? (r & 31) >> 3 : (r & 63) >> 3;
+        char* line = m + line_at<ROWS>(plane, row) + (r & 7) * 2;
+        *reinterpret_cast<_Float16*>(line + ((slot ^ (row & 7)) * 16)) = hi[y];
+        if constexpr (P == 2) *reinterpret_cast<_Float16*>(line + (((slot + 4) ^ (row & 7)) * 16)) = lo[y];
+      }
+    } else {
+      const int plane = P == 2 ? c >> 5 : c >> 6, slot = P == 2 ? (c & 31) >> 3 : (c & 63) >> 3;
+      char* line = m + line_at<ROWS>(plane, r);
+      *reinterpret_cast<f16x8_v*>(line + ((slot ^ (r & 7)) * 16)) = hi;
+      if constexpr (P == 2) *reinterpret_cast<f16x8_v*>(line + (((slot + 4) ^ (r & 7)) * 16)) = lo;
+    }
+  }
+}
+
+// A call's sizes, for matrices e = blockIdx.y
+struct Small {
+  const void* g;         // the updates
+  void* o;
+  int M, N, m, k;        // m <= k, k = N or (tall) M
+  int chunks, per;       // chunks of k; chunks of a slice
+  int slices;            // of the sums
+  bool vec;              // rows of g and o lie at multiples of 16 bytes
+  const double* sums;    // partial sums of squares
+  int parts;
+  float eps;
+  float* part;           // [matrices][slices][MP * MP], sums of X X^T as the threads hold them
+  float* part_next;
+  char* x;               // fp32 updates: X between two steps, two parts [matrices][chunks * 128][MP]
+  char* q;               // bf16 updates: Q [matrices], as it lies in LDS
+  float* back;           // see Convert
+  float* on;
+};
+
+template <int MP> struct SmallCfg {
+  static constexpr int FM = MP / 32, FN = MP / 64;   // pieces of a wave, of an MP x MP matrix
+  static constexpr int XN = CHUNK / 64;              // of an MP x 128 one along its columns
+  static constexpr int SQUARE = MP * MP * 4;         // bytes, two parts
+  static constexpr int WIDE = MP * CHUNK * 4;
+};
+
+// a chunk of the update as X, m rows of 128, or as its transpose
+template <typename T, int P, int MP, bool TALL, bool TRANSPOSED>
+__device__ __forceinline__ void load_chunk(char* to, const Small& a, int e, int chunk, int ex, int tid) {
+  const int k0 = chunk * CHUNK, left = min(CHUNK, a.k - k0);
+  const T* g = (const T*)a.g + (int64_t)e * a.M * a.N;
+  if constexpr (TALL) load_update<T, P, CHUNK, MP, !TRANSPOSED>(to, g + (int64_t)k0 * a.N, a.N, left, a.m, ex, a.vec, tid);
+  else load_update<T, P, MP, CHUNK, TRANSPOSED>(to, g + k0, a.N, a.m, left, ex, a.vec, tid);
+}
+
+template <int MP>
+__device__ __forceinline__ void put_square(char* to, const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], float scale, int w,
+                                           int lane) {
+  using C = SmallCfg<MP>;
+  const int r0 = (w >> 2) * (MP / 2) + (lane & 15), c0 = (w & 3) * (MP / 4) + 4 * (lane >> 4);
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) put4<MP>(to, r0 + 16 * j, c0 + 16 * i, v[j][i] * scale);
+}
+// The lower half of a symmetric matrix, on both sides of the diagonal: products of
+// matrices that commute are symmetric up to their rounding, and what is not would
+// grow with the steps (63 x 65, five steps: error 3.7e-2 with both halves as computed).
+template <int MP>
+__device__ __forceinline__ void put_symmetric(char* to, const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], float scale,
+                                              int w, int lane) {
+  using C = SmallCfg<MP>;
+  const int p = lane & 15, h = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) {
+      const int R = (w >> 2) * (MP / 2) + 16 * j, K = (w & 3) * (MP / 4) + 16 * i;  // the piece's first row and column
+      if (R < K) continue;
+      const int r = R + p, k = K + 4 * h;
+      const f32x4_v u = v[j][i] * scale;
+      if (R > K) put4<MP>(to, r, k, u);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (R == K && k + x > r) continue;
+        if (R == K) put1<MP>(to, r, k + x, u[x]);
+        put1<MP>(to, k + x, r, u[x]);
+      }
+    }
+}
+
+// v = diag I + beta a + alpha v, for the rows and columns below m
+template <int MP>
+__device__ __forceinline__ void polynomial(f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN],
+                                           const f32x4_v (&a)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], float diag, float beta,
+                                           float alpha, int m, int w, int lane) {
+  using C = SmallCfg<MP>;
+  const int r0 = (w >> 2) * (MP / 2) + (lane & 15), c0 = (w & 3) * (MP / 4) + 4 * (lane >> 4);
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int r = r0 + 16 * j, c = c0 + 16 * i + x;
+        v[j][i][x] = fmaf(beta, a[j][i][x], alpha * v[j][i][x]) + (r == c && r < m ? diag : 0.f);
+      }
+}
+
+template <int MP>
+__device__ __forceinline__ void write_part(float* part, int slices, int e, int slice,
+                                           const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], int tid) {
+  using C = SmallCfg<MP>;
+  f32x4_v* p = reinterpret_cast<f32x4_v*>(part + ((int64_t)e * slices + slice) * (MP * MP)) + tid;
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) p[(j * C::FN + i) * SMALL_THREADS] = v[j][i];
+}
+// the slices' sum, in order
+template <int MP>
+__device__ __forceinline__ void read_parts(f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], const float* part, int slices,
+                                           int e, int tid) {
+  using C = SmallCfg<MP>;
+  const f32x4_v* p = reinterpret_cast<const f32x4_v*>(part + (int64_t)e * slices * (MP * MP)) + tid;
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) v[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < slices; ++s)
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i) v[j][i] += p[((int64_t)s * (MP * MP / 4)) + (j * C::FN + i) * SMALL_THREADS];
+}
+
+
+// A call's arguments where they lie: an index that the compiler does not know would
+// have it copy them to every thread's own memory.
+template <typename A>
+__device__ __forceinline__ const __attribute__((address_space(4))) A* arguments() {
+  return (const __attribute__((address_space(4))) A*)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
+// A matrix's norm, from its partial sums (a wave, a lane each)
+__device__ __forceinline__ double norm_of(const double* sums, int parts, int e) {
+  static_assert(NORM_PARTS == 64, "a lane each");
+  const int lane = threadIdx.x & 63;
+  double s = lane < parts ? sums[(int64_t)e * NORM_PARTS + lane] : 0.0;
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  return sqrt(s);
+}
+// the power of two of a matrix's stored numbers, and X_0 over them (a matrix of zeros,
+// as an expert without rows has it, stays one)
+__device__ __forceinline__ int power_of(double norm) {
+  return norm > 0.0 && norm < __builtin_inf() ? X_EXP - ilogb(norm) : 0;
+}
+__device__ __forceinline__ double first_of(double norm, double eps) {
+  if (!(norm < __builtin_inf())) return __builtin_nan("");
+  return norm == 0.0 ? 0.0 : scalbn(1.0 / (norm + eps), -power_of(norm));
+}
+
+// The factors that go with the groups of steps.  A matrix whose norm is far below eps
+// starts far below 1 and grows with the steps; so that its parts keep their bits, the X
+// between two groups carries a power of two of its own, from a bound of its norm that
+// is followed through the steps:
+//     back[i]    X of group i over its stored numbers (but for the exponent that all have)
+//     on[i]      what the stored numbers of group i + 1 are of Q times those of group i
+struct Factors {
+  const double* sums;
+  int parts;
+  float eps;
+  float* back;    // [groups][matrices]
+  float* on;
+  int groups;
+  uint8_t steps[MAX_STEPS];  // of each group
+  float coef[3 * MAX_STEPS];
+};
+// (one wave)
+__device__ __forceinline__ void factors(const __attribute__((address_space(4))) Factors& a, double norm, int e, int nb) {
+  const double first = first_of(norm, a.eps);
+  const bool fine = norm < __builtin_inf();
+  const float nan = __builtin_nanf("");
+  const int lane = threadIdx.x & 63;
+  if (lane == 0) a.back[e] = (float)first;
+  float most = norm == 0.0 ? 0.f : (float)(norm / (norm + (double)a.eps));  // of |X|
+  int t = 0, c = 0;
+  for (int i = 0; i + 1 < a.groups; ++i) {
+    for (int s = 0; s < a.steps[i]; ++s, c += 3) {
+      const float v = most * (float)(lane + 1) * 0.015625f, l = v * v;
+      float m = fabsf(v * fmaf(l, fmaf(l, a.coef[c + 2], a.coef[c + 1]), a.coef[c]));
+      for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+      most = m;
+    }
+    const int next = most > 0.f && most < __builtin_inff() ? max(-60, min(120, -ilogbf(most))) : 0;
+    const double f = i == 0 ? first : scalbn(1.0, -t);
+    if (lane == 0) {
+      a.on[i * nb + e] = fine ? (float)scalbn(f, next) : nan;
+      a.back[(i + 1) * nb + e] = fine ? (float)scalbn(1.0, -next) : nan;
+    }
+    t = next;
+  }
+}
+
+// ---- X X^T of the update, slice by slice, and the factors ----
+struct GramArgs {
+  Small a;
+  Factors f;
+};
+template <typename T, int P, int MP, bool TALL>
+__global__ void __launch_bounds__(SMALL_THREADS, 2)
+k_small_gram(GramArgs) {
+  using C = SmallCfg<MP>;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const auto* g = arguments<GramArgs>();
+  const Small a = *(const Small*)&g->a;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int e = blockIdx.y, slice = blockIdx.x;
+  const double norm = norm_of(a.sums, a.parts, e);
+  const int ex = power_of(norm);
+  f32x4_v tot[C::FM][C::FN], acc[C::FM][C::FN];
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) tot[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  const int last = min(a.chunks, (slice + 1) * a.per);
+  for (int c = slice * a.per; c < last; ++c) {
+    __syncthreads();
+    load_chunk<T, P, MP, TALL, false>(smem, a, e, c, ex, tid);
+    __syncthreads();
+    product<C::FM, C::FN, MP, MP, P, P, P == 2, true>(acc, smem, (w >> 2) * (MP / 2), smem, (w & 3) * (MP / 4), CHUNK / 32, lane);
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i) tot[j][i] += acc[j][i];
+  }
+  write_part<MP>(a.part, a.slices, e, slice, tot, tid);
+  if (slice == 0 && w == 0) factors(g->f, norm, e, gridDim.y);
+}
+
+// A call's X = Q X, times alpha, at its place in o
+template <typename O, int MP, bool TALL, bool ROWS_FIRST>
+__device__ __forceinline__ void write_out(const Small& a, int e, int chunk,
+                                          const f32x4_v (&y)[SmallCfg<MP>::FM][SmallCfg<MP>::XN], float alpha, int w, int lane) {
+  using C = SmallCfg<MP>;
+  static_assert(ROWS_FIRST != TALL, "four neighbours along o's rows");
+  const int p = lane & 15, h = lane >> 4, k0 = chunk * CHUNK, left = min(CHUNK, a.k - k0);
+  O* o = (O*)a.o + (int64_t)e * a.M * a.N + (TALL ? (int64_t)k0 * a.N : k0);
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::XN; ++i) {
+      const int mr = (w >> 2) * (MP / 2) + 16 * j, kr = (w & 3) * 32 + 16 * i;
+      const int r = TALL ? kr + p : mr + p, c = TALL ? mr + 4 * h : kr + 4 * h;
+      const int rows = TALL ? left : a.m, cols = TALL ? a.m : left;
+      if (r >= rows) continue;
+      O* to = o + (int64_t)r * a.N + c;
+      const f32x4_v v = y[j][i] * alpha;
+      if (a.vec && c + 4 <= cols) {
+        if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(to) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
+        else *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (c + x < cols) to[x] = Elem<O>::from_f(v[x]);
+      }
+    }
+}
+
+// ---- a step of fp32 updates: A from the slices' sums, P, and per chunk X = P X and the
+// next sums ----
+struct StepArgs {
+  Small a;
+  float gram;               // A over the sums (times back[0]^2)
+  float diag, beta, alpha;  // P = diag I + beta A + alpha A^2
+  float x;                  // X over P X (times on[0], or at the end back[0])
+};
+template <int MP, bool TALL, bool FIRST, bool LAST>
+__global__ void __launch_bounds__(SMALL_THREADS, 2)
+k_small_step(StepArgs s) {
+  using C = SmallCfg<MP>;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  char *const b0 = smem, *const b1 = smem + C::WIDE;  // (an MP x 128 matrix is the larger one)
+  const Small& a = s.a;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int e = blockIdx.y, slice = blockIdx.x;
+  const int wr = (w >> 2) * (MP / 2), wc = (w & 3) * (MP / 4);
+  f32x4_v A[C::FM][C::FN], P[C::FM][C::FN];
+  read_parts<MP>(A, a.part, a.slices, e, tid);
+  const float f = a.back[e], ga = s.gram * f * f;
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) A[j][i] *= ga;
+  put_square<MP>(b0, A, 1.f, w, lane);
+  __syncthreads();
+  product<C::FM, C::FN, MP, MP, 2, 2, true, true>(P, b0, wr, b0, wc, MP / 32, lane);
+  polynomial<MP>(P, A, s.diag, s.beta, s.alpha, a.m, w, lane);
+  put_square<MP>(b1, P, 1.f, w, lane);
+
+  int ex = 0;
+  if constexpr (FIRST) ex = power_of(norm_of(a.sums, a.parts, e));
+  const float ax = s.x * (LAST ? f : a.on[e]);
+  f32x4_v tot[C::FM][C::FN];
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) tot[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  const int end = min(a.chunks, (slice + 1) * a.per);
+  for (int c = slice * a.per; c < end; ++c) {
+    __syncthreads();  // everybody is done with b0
+    char* image = a.x + ((int64_t)e * a.chunks + c) * C::WIDE;
+    if constexpr (FIRST) {
+      load_chunk<float, 2, MP, TALL, true>(b0, a, e, c, ex, tid);
+    } else {
+      uint4 v[C::WIDE / 16 / SMALL_THREADS];
+#pragma unroll
+      for (int i = 0; i < C::WIDE / 16 / SMALL_THREADS; ++i)
+        v[i] = reinterpret_cast<const uint4*>(image)[i * SMALL_THREADS + tid];
+#pragma unroll
+      for (int i = 0; i < C::WIDE / 16 / SMALL_THREADS; ++i) reinterpret_cast<uint4*>(b0)[i * SMALL_THREADS + tid] = v[i];
+    }
+    __syncthreads();
+    f32x4_v y[C::FM][C::XN];
+    product<C::FM, C::XN, MP, CHUNK, 2, 2, true, LAST && !TALL>(y, b1, wr, b0, (w & 3) * 32, MP / 32, lane);
+    if constexpr (LAST) {
+      write_out<float, MP, TALL, !TALL>(a, e, c, y, ax, w, lane);
+    } else {
+      __syncthreads();
+      // X^T as it will be read next, and X over the old one; a lane holds, of row k = p,
+      // four neighbouring m
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+        for (int i = 0; i < C::XN; ++i) {
+          const int k = (w & 3) * 32 + 16 * i + (lane & 15), m = wr + 16 * j + 4 * (lane >> 4);
+          const f32x4_v v = y[j][i] * ax;
+          put4<CHUNK>(image, k, m, v);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) put1<MP>(b0, m + x, k, v[x]);
+        }
+      __syncthreads();
+      f32x4_v acc[C::FM][C::FN];
+      product<C::FM, C::FN, MP, MP, 2, 2, true, true>(acc, b0, wr, b0, wc, CHUNK / 32, lane);
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+        for (int i = 0; i < C::FN; ++i) tot[j][i] += acc[j][i];
+    }
+  }
+  if constexpr (!LAST) write_part<MP>(a.part_next, a.slices, e, slice, tot, tid);
+}
+
+// ---- bf16 updates: all steps on the m x m matrices, a workgroup per update ----
+struct Recurrence {
+  float diag, beta, alpha;  // P = diag I + beta A + alpha A^2
+  float t, next, q;         // of T = P A, A = T P, Q = P Q
+};
+struct StepsArgs {
+  Small a;
+  float gram;
+  int steps;
+  Recurrence s[MAX_STEPS];
+};
+template <int MP>
+__global__ void __launch_bounds__(SMALL_THREADS, 2)
+k_small_steps(StepsArgs) {
+  using C = SmallCfg<MP>;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  char *const b0 = smem, *const b1 = smem + C::SQUARE;
+  const auto* g = arguments<StepsArgs>();
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), e = blockIdx.x;
+  const int wr = (w >> 2) * (MP / 2), wc = (w & 3) * (MP / 4), m = g->a.m;
+  f32x4_v A[C::FM][C::FN], P[C::FM][C::FN], Q[C::FM][C::FN];
+  read_parts<MP>(A, g->a.part, g->a.slices, e, tid);
+  const float f = g->a.back[e], ga = g->gram * f * f;
+  auto scaled = [&](f32x4_v (&v)[C::FM][C::FN], float by) {
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i) v[j][i] *= by;
+  };
+  auto times = [&](f32x4_v (&v)[C::FM][C::FN], const char* x, const char* y) {
+    product<C::FM, C::FN, MP, MP, 2, 2, false, true>(v, x, wr, y, wc, MP / 32, lane);
+  };
+  scaled(A, ga);
+  const int steps = g->steps;
+  for (int i = 0; i < steps; ++i) {
+    const auto& s = g->s[i];
+    __syncthreads();  // the buffers are free
+    put_symmetric<MP>(b0, A, 1.f, w, lane);
+    __syncthreads();
+    times(P, b0, b0);
+    polynomial<MP>(P, A, s.diag, s.beta, s.alpha, m, w, lane);
+    put_symmetric<MP>(b1, P, 1.f, w, lane);
+    __syncthreads();
+    if (i + 1 < steps) {
+      times(A, b1, b0);  // T = P A
+      __syncthreads();
+      put_symmetric<MP>(b0, A, s.t, w, lane);
+      __syncthreads();
+      times(A, b0, b1);  // the next A = T P
+      scaled(A, s.next);
+    }
+    if (i == 0) {
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+        for (int x = 0; x < C::FN; ++x) Q[j][x] = P[j][x];
+    } else {
+      __syncthreads();
+      put_symmetric<MP>(b0, Q, 1.f, w, lane);
+      __syncthreads();
+      times(Q, b1, b0);
+      scaled(Q, s.q);
+    }
+  }
+  put_symmetric<MP>(g->a.q + (int64_t)e * C::SQUARE, Q, 1.f, w, lane);
+}
+
+// ---- o = Q X ----
+struct ApplyArgs {
+  Small a;
+  float x;
+};
+template <int MP, bool TALL>
+__global__ void __launch_bounds__(SMALL_THREADS, 2)
+k_small_apply(ApplyArgs s) {
+  using C = SmallCfg<MP>;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  char *const b0 = smem, *const b1 = smem + MP * CHUNK * 2;  // X^T in one part, Q
+  const Small& a = s.a;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int e = blockIdx.y;
+  const uint4* q = reinterpret_cast<const uint4*>(a.q + (int64_t)e * C::SQUARE);
+#pragma unroll
+  for (int i = 0; i < C::SQUARE / 16 / SMALL_THREADS; ++i)
+    reinterpret_cast<uint4*>(b1)[i * SMALL_THREADS + tid] = q[i * SMALL_THREADS + tid];
+  const int ex = power_of(norm_of(a.sums, a.parts, e));
+  const float ax = s.x * a.back[e];
+  const int end = min(a.chunks, ((int)blockIdx.x + 1) * a.per);
+  for (int c = blockIdx.x * a.per; c < end; ++c) {
+    __syncthreads();
+    load_chunk<bf16_t, 1, MP, TALL, true>(b0, a, e, c, ex, tid);
+    __syncthreads();
+    f32x4_v y[C::FM][C::XN];
+    product<C::FM, C::XN, MP, CHUNK, 2, 1, false, !TALL>(y, b1, (w >> 2) * (MP / 2), b0, (w & 3) * 32, MP / 32, lane);
+    write_out<bf16_t, MP, TALL, !TALL>(a, e, c, y, ax, w, lane);
+  }
+}
+
+}  // namespace ortho
+}  // namespace moe
