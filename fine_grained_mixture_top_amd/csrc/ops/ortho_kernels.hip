@@ -300,7 +300,7 @@ bool is_small(const OrthoArgs& a) {
 
 struct SmallSizes {
   int mp, chunks, nb, slices, per, groups;
-  int64_t part, x, q, f, sums, total;
+  int64_t part, gram, x, q, f, sums, total;
 };
 SmallSizes small_sizes(const OrthoArgs& a) {
   SmallSizes z{};
@@ -322,7 +322,8 @@ SmallSizes small_sizes(const OrthoArgs& a) {
     at += (bytes + 255) / 256 * 256;
     return here;
   };
-  z.part = take(square * z.slices * z.nb * (two ? 2 : 1));
+  z.part = take(square * z.slices * z.nb);
+  z.gram = take(square * z.nb);
   if (two) z.x = take(wide * z.nb);
   else z.q = take(square * z.nb);
   z.f = take(4 * (int64_t)z.nb * 2 * z.groups);
@@ -340,10 +341,15 @@ hipError_t small_launch(K* k, dim3 grid, int lds, const A& args, std::atomic<uin
 }
 
 template <typename T, int MP, bool TALL>
-hipError_t small_gram(const GramArgs& g, int nb, hipStream_t st) {
+hipError_t small_gram(const Small& s, int nb, hipStream_t st) {
   constexpr int P = sizeof(T) == 4 ? 2 : 1;
   static std::atomic<uint64_t> done{0};
-  return small_launch(k_small_gram<T, P, MP, TALL>, dim3(g.a.slices, nb), MP * CHUNK * 2 * P, g, done, st);
+  return small_launch(k_small_gram<T, P, MP, TALL>, dim3(s.slices, nb), MP * CHUNK * 2 * P, s, done, st);
+}
+template <int MP>
+hipError_t small_reduce(const ReduceArgs& r, int nb, hipStream_t st) {
+  hipLaunchKernelGGL(k_small_reduce<MP>, dim3(MP * MP / 4 / 256 + r.first, nb), dim3(256), 0, st, r);
+  return hipGetLastError();
 }
 template <int MP, bool TALL, bool FIRST, bool LAST>
 hipError_t small_step(const StepArgs& s, int nb, hipStream_t st) {
@@ -360,8 +366,7 @@ hipError_t launch_small_as(const OrthoArgs& a, hipStream_t st) {
   auto pow2 = [](int n) { return (float)std::ldexp(1.0, n); };
   for (int e0 = 0; e0 < a.E; e0 += z.nb) {
     const int nb = std::min(z.nb, a.E - e0);
-    GramArgs g{};
-    Small& s = g.a;
+    Small s{};
     const int64_t elems = (int64_t)a.M * a.N;
     s.g = two ? (const void*)((const float*)a.g + e0 * elems) : (const void*)((const bf16_t*)a.g + e0 * elems);
     s.o = two ? (void*)((float*)a.o + e0 * elems) : (void*)((bf16_t*)a.o + e0 * elems);
@@ -372,24 +377,25 @@ hipError_t launch_small_as(const OrthoArgs& a, hipStream_t st) {
     double* sums = (double*)(ws + z.sums);
     s.sums = sums;
     s.parts = two ? launch_norm((const float*)s.g, elems, nb, sums, st) : launch_norm((const bf16_t*)s.g, elems, nb, sums, st);
-    const int64_t part = (int64_t)MP * MP * z.slices * nb;
     s.part = (float*)(ws + z.part);
-    s.part_next = s.part + part;
+    s.gram = ws + z.gram;
     s.x = ws + z.x;
     s.q = ws + z.q;
     s.back = (float*)(ws + z.f);
     s.on = s.back + z.groups * nb;
-    g.f = factors_of(a, z.groups, nb, sums, s.parts, s.back);
-    hipError_t err = two ? small_gram<float, MP, TALL>(g, nb, st) : small_gram<bf16_t, MP, TALL>(g, nb, st);
+    hipError_t err = two ? small_gram<float, MP, TALL>(s, nb, st) : small_gram<bf16_t, MP, TALL>(s, nb, st);
     if (err != hipSuccess) return err;
     Spectrum spec;
     spec.begin();
     int ea = exponent_for(1.0);
+    ReduceArgs r{s, pow2(ea), 1, factors_of(a, z.groups, nb, sums, s.parts, s.back)};
+    err = small_reduce<MP>(r, nb, st);
+    if (err != hipSuccess) return err;
+    r.first = 0;
     if (!two) {
       StepsArgs q{};
       q.a = s;
       q.steps = a.steps;
-      q.gram = pow2(ea);
       int eq = 0;
       for (int i = 0; i < a.steps; ++i) {
         const float* c = a.coef + 3 * i;
@@ -415,24 +421,27 @@ hipError_t launch_small_as(const OrthoArgs& a, hipStream_t st) {
     int x_exp = 0;
     for (int i = 0; i < a.steps; ++i) {
       const float* c = a.coef + 3 * i;
-      double pm, tm, am, qm, lmax = 0.0;
-      spec.begin();
-      for (int n = 0; n < Spectrum::N; ++n) lmax = std::max(lmax, spec.l[n]);
-      ea = exponent_for(lmax);
+      double pm, tm, am, qm;
       spec.step(c, &pm, &tm, &am, &qm);
       spec.end();
       const int ep = exponent_for(pm);
       const bool last = i + 1 == a.steps;
       const int nx = X_EXP - 1;
-      StepArgs q{s, pow2(ea - 2 * x_exp), c[0] * pow2(ep), c[1] * pow2(ep - ea), c[2] * pow2(ep - 2 * ea),
+      StepArgs q{s, c[0] * pow2(ep), c[1] * pow2(ep - ea), c[2] * pow2(ep - 2 * ea),
                  last ? a.scale * pow2(-ep - x_exp) : pow2(nx - ep - x_exp)};
       err = i == 0 ? (last ? small_step<MP, TALL, true, true>(q, nb, st) : small_step<MP, TALL, true, false>(q, nb, st))
                    : (last ? small_step<MP, TALL, false, true>(q, nb, st) : small_step<MP, TALL, false, false>(q, nb, st));
       if (err != hipSuccess) return err;
+      if (last) break;
       x_exp = nx;
-      std::swap(s.part, s.part_next);
       s.back += nb;
       s.on += nb;
+      spec.begin();
+      ea = exponent_for(*std::max_element(spec.l, spec.l + Spectrum::N));
+      r.a = s;
+      r.gram = pow2(ea - 2 * x_exp);
+      err = small_reduce<MP>(r, nb, st);
+      if (err != hipSuccess) return err;
     }
   }
   return hipSuccess;

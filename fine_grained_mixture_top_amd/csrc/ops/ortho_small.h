@@ -23,6 +23,13 @@ template <int ROWS> __device__ __forceinline__ int line_at(int c, int r) { retur
 
 // 4 numbers from column k on (a multiple of 4) of row r
 template <int ROWS>
+__device__ __forceinline__ void put4(char* m, int r, int k, const f16x4_v hi, const f16x4_v lo) {
+  char* line = m + line_at<ROWS>(k >> 5, r);
+  const int c = (k & 31) >> 3, half = (k & 4) * 2;
+  *reinterpret_cast<f16x4_v*>(line + ((c ^ (r & 7)) * 16) + half) = hi;
+  *reinterpret_cast<f16x4_v*>(line + (((c + 4) ^ (r & 7)) * 16) + half) = lo;
+}
+template <int ROWS>
 __device__ __forceinline__ void put4(char* m, int r, int k, const f32x4_v v) {
   f16x4_v hi, lo;
 #pragma unroll
@@ -32,16 +39,22 @@ __device__ __forceinline__ void put4(char* m, int r, int k, const f32x4_v v) {
     hi[x] = vh;
     lo[x] = vl;
   }
-  char* line = m + line_at<ROWS>(k >> 5, r);
+  put4<ROWS>(m, r, k, hi, lo);
+}
+template <int ROWS>
+__device__ __forceinline__ f32x4_v get4(const char* m, int r, int k) {
+  const char* line = m + line_at<ROWS>(k >> 5, r);
   const int c = (k & 31) >> 3, half = (k & 4) * 2;
-  *reinterpret_cast<f16x4_v*>(line + ((c ^ (r & 7)) * 16) + half) = hi;
-  *reinterpret_cast<f16x4_v*>(line + (((c + 4) ^ (r & 7)) * 16) + half) = lo;
+  const f16x4_v hi = *reinterpret_cast<const f16x4_v*>(line + ((c ^ (r & 7)) * 16) + half);
+  const f16x4_v lo = *reinterpret_cast<const f16x4_v*>(line + (((c + 4) ^ (r & 7)) * 16) + half);
+  f32x4_v v;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) v[x] = (float)hi[x] + (float)lo[x];
+  return v;
 }
 // one number
 template <int ROWS>
-__device__ __forceinline__ void put1(char* m, int r, int k, float v) {
-  _Float16 hi, lo;
-  split(v, hi, lo);
+__device__ __forceinline__ void put1(char* m, int r, int k, _Float16 hi, _Float16 lo) {
   char* line = m + line_at<ROWS>(k >> 5, r);
   const int c = (k & 31) >> 3, at = (k & 7) * 2;
   *reinterpret_cast<_Float16*>(line + ((c ^ (r & 7)) * 16) + at) = hi;
@@ -163,7 +176,7 @@ struct Small {
   int parts;
   float eps;
   float* part;           // [matrices][slices][MP * MP], sums of X X^T as the threads hold them
-  float* part_next;
+  char* gram;            // [matrices] A, as it lies in LDS
   char* x;               // fp32 updates: X between two steps, two parts [matrices][chunks * 128][MP]
   char* q;               // bf16 updates: Q [matrices], as it lies in LDS
   float* back;           // see Convert
@@ -187,15 +200,31 @@ __device__ __forceinline__ void load_chunk(char* to, const Small& a, int e, int 
 }
 
 template <int MP>
-__device__ __forceinline__ void put_square(char* to, const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], float scale, int w,
-                                           int lane) {
+__device__ __forceinline__ void put_square(char* to, const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], int w, int lane) {
   using C = SmallCfg<MP>;
   const int r0 = (w >> 2) * (MP / 2) + (lane & 15), c0 = (w & 3) * (MP / 4) + 4 * (lane >> 4);
 #pragma unroll
   for (int j = 0; j < C::FM; ++j)
 #pragma unroll
-    for (int i = 0; i < C::FN; ++i) put4<MP>(to, r0 + 16 * j, c0 + 16 * i, v[j][i] * scale);
+    for (int i = 0; i < C::FN; ++i) put4<MP>(to, r0 + 16 * j, c0 + 16 * i, v[j][i]);
 }
+
+// Four neighbouring lanes hold four numbers each, a 4 x 4 block of 16-bit values by rows;
+// by columns afterwards.
+__device__ __forceinline__ f16x4_v turn4(const f16x4_v v, int lane) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  const u32x2_t d = __builtin_bit_cast(u32x2_t, v);
+  auto swap1 = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 15, 15, true); };  // lane ^ 1
+  auto swap2 = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 15, 15, true); };  // lane ^ 2
+  const uint32_t o0 = swap1(d[0]), o1 = swap1(d[1]);
+  const bool odd = lane & 1, high = lane & 2;
+  // columns 0 and 2 of two rows in even lanes, 1 and 3 in odd ones
+  const uint32_t e0 = odd ? (o0 >> 16) | (d[0] & 0xffff0000u) : (d[0] & 0xffffu) | (o0 << 16);
+  const uint32_t e1 = odd ? (o1 >> 16) | (d[1] & 0xffff0000u) : (d[1] & 0xffffu) | (o1 << 16);
+  const uint32_t got = swap2(high ? e0 : e1);
+  return __builtin_bit_cast(f16x4_v, high ? u32x2_t{got, e1} : u32x2_t{e0, got});
+}
+
 // The lower half of a symmetric matrix, on both sides of the diagonal: products of
 // matrices that commute are symmetric up to their rounding, and what is not would
 // grow with the steps (63 x 65, five steps: error 3.7e-2 with both halves as computed).
@@ -212,12 +241,21 @@ __device__ __forceinline__ void put_symmetric(char* to, const f32x4_v (&v)[Small
       if (R < K) continue;
       const int r = R + p, k = K + 4 * h;
       const f32x4_v u = v[j][i] * scale;
-      if (R > K) put4<MP>(to, r, k, u);
+      f16x4_v hi, lo;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        if (R == K && k + x > r) continue;
-        if (R == K) put1<MP>(to, r, k + x, u[x]);
-        put1<MP>(to, k + x, r, u[x]);
+        _Float16 vh, vl;
+        split(u[x], vh, vl);
+        hi[x] = vh;
+        lo[x] = vl;
+      }
+      put4<MP>(to, r, k, hi, lo);
+      if (R > K) {
+        put4<MP>(to, k + (p & 3), R + (p & ~3), turn4(hi, lane), turn4(lo, lane));
+      } else {  // over what the lines above put there (a wave's LDS writes stay in order)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (k + x < r) put1<MP>(to, k + x, r, hi[x], lo[x]);
       }
     }
 }
@@ -240,35 +278,24 @@ __device__ __forceinline__ void polynomial(f32x4_v (&v)[SmallCfg<MP>::FM][SmallC
       }
 }
 
+// A wave's piece j, i lies above the diagonal: its mirror stands for it.
+template <int MP>
+__device__ __forceinline__ bool above(int j, int i, int w) {
+  return (w >> 2) * (MP / 2) + 16 * j < (w & 3) * (MP / 4) + 16 * i;
+}
+
+// The lower half of a slice's sum, as the threads hold it
 template <int MP>
 __device__ __forceinline__ void write_part(float* part, int slices, int e, int slice,
-                                           const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], int tid) {
+                                           const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], int w, int tid) {
   using C = SmallCfg<MP>;
   f32x4_v* p = reinterpret_cast<f32x4_v*>(part + ((int64_t)e * slices + slice) * (MP * MP)) + tid;
 #pragma unroll
   for (int j = 0; j < C::FM; ++j)
 #pragma unroll
-    for (int i = 0; i < C::FN; ++i) p[(j * C::FN + i) * SMALL_THREADS] = v[j][i];
+    for (int i = 0; i < C::FN; ++i)
+      if (!above<MP>(j, i, w)) p[(j * C::FN + i) * SMALL_THREADS] = v[j][i];
 }
-// the slices' sum, in order
-template <int MP>
-__device__ __forceinline__ void read_parts(f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], const float* part, int slices,
-                                           int e, int tid) {
-  using C = SmallCfg<MP>;
-  const f32x4_v* p = reinterpret_cast<const f32x4_v*>(part + (int64_t)e * slices * (MP * MP)) + tid;
-#pragma unroll
-  for (int j = 0; j < C::FM; ++j)
-#pragma unroll
-    for (int i = 0; i < C::FN; ++i) v[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < slices; ++s)
-#pragma unroll
-    for (int j = 0; j < C::FM; ++j)
-#pragma unroll
-      for (int i = 0; i < C::FN; ++i) v[j][i] += p[((int64_t)s * (MP * MP / 4)) + (j * C::FN + i) * SMALL_THREADS];
-}
-
-
 // A call's arguments where they lie: an index that the compiler does not know would
 // have it copy them to every thread's own memory.
 template <typename A>
@@ -336,18 +363,12 @@ __device__ __forceinline__ void factors(const __attribute__((address_space(4))) 
   }
 }
 
-// ---- X X^T of the update, slice by slice, and the factors ----
-struct GramArgs {
-  Small a;
-  Factors f;
-};
+// ---- X X^T of the update, slice by slice ----
 template <typename T, int P, int MP, bool TALL>
 __global__ void __launch_bounds__(SMALL_THREADS, 2)
-k_small_gram(GramArgs) {
+k_small_gram(Small a) {
   using C = SmallCfg<MP>;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  const auto* g = arguments<GramArgs>();
-  const Small a = *(const Small*)&g->a;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int e = blockIdx.y, slice = blockIdx.x;
   const double norm = norm_of(a.sums, a.parts, e);
@@ -368,8 +389,76 @@ k_small_gram(GramArgs) {
 #pragma unroll
       for (int i = 0; i < C::FN; ++i) tot[j][i] += acc[j][i];
   }
-  write_part<MP>(a.part, a.slices, e, slice, tot, tid);
-  if (slice == 0 && w == 0) factors(g->f, norm, e, gridDim.y);
+  write_part<MP>(a.part, a.slices, e, slice, tot, w, tid);
+}
+
+// ---- A from the slices' sums: a thread per float4, the slices in order.  (By the
+// workgroups that use it, 12 slices took 6.5 us and their parts 3.2.)  The first time
+// the last workgroup of a matrix makes its factors. ----
+struct ReduceArgs {
+  Small a;
+  float gram;      // A over the sums (times back^2)
+  int first;
+  Factors f;
+};
+template <int MP>
+__global__ void __launch_bounds__(256)
+k_small_reduce(ReduceArgs) {
+  using C = SmallCfg<MP>;
+  const auto* g = arguments<ReduceArgs>();
+  const int e = blockIdx.y, nb = gridDim.y, tid = threadIdx.x;
+  constexpr int BLOCKS = MP * MP / 4 / 256;
+  if (blockIdx.x == BLOCKS) {
+    if (tid < 64) factors(g->f, norm_of(g->a.sums, g->a.parts, e), e, nb);
+    return;
+  }
+  const int id = blockIdx.x * 256 + tid, lane = id & 63, w = id / 64 % 8, piece = id / SMALL_THREADS;
+  const int j = piece / C::FN, i = piece % C::FN;
+  if (above<MP>(j, i, w)) return;
+  const int slices = g->a.slices;
+  const f32x4_v* p = reinterpret_cast<const f32x4_v*>(g->a.part + (int64_t)e * slices * (MP * MP)) + id;
+  f32x4_v v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 16
+  for (int s = 0; s < slices; ++s) v += p[(int64_t)s * (MP * MP / 4)];
+  const float f = g->first ? (float)first_of(norm_of(g->a.sums, g->a.parts, e), g->a.eps) : g->a.back[e];
+  v *= g->gram * f * f;
+  const int R = (w >> 2) * (MP / 2) + 16 * j, K = (w & 3) * (MP / 4) + 16 * i, r = R + (lane & 15), k = K + 4 * (lane >> 4);
+  char* to = g->a.gram + (int64_t)e * C::SQUARE;
+  f16x4_v hi, lo;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    _Float16 vh, vl;
+    split(v[x], vh, vl);
+    hi[x] = vh;
+    lo[x] = vl;
+  }
+  if (R > K) put4<MP>(to, r, k, hi, lo);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    if (R == K && k + x <= r) put1<MP>(to, r, k + x, hi[x], lo[x]);
+    if (k + x < r) put1<MP>(to, k + x, r, hi[x], lo[x]);
+  }
+}
+
+// a matrix as it lies in LDS, from memory
+template <int BYTES>
+__device__ __forceinline__ void copy_in(char* to, const char* from, int tid) {
+  constexpr int N = BYTES / 16 / SMALL_THREADS;
+  uint4 v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = reinterpret_cast<const uint4*>(from)[i * SMALL_THREADS + tid];
+#pragma unroll
+  for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(to)[i * SMALL_THREADS + tid] = v[i];
+}
+// ... and as the waves hold its pieces
+template <int MP>
+__device__ __forceinline__ void get_square(f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], const char* m, int w, int lane) {
+  using C = SmallCfg<MP>;
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i)
+      v[j][i] = get4<MP>(m, (w >> 2) * (MP / 2) + 16 * j + (lane & 15), (w & 3) * (MP / 4) + 16 * i + 4 * (lane >> 4));
 }
 
 // A call's X = Q X, times alpha, at its place in o
@@ -405,7 +494,6 @@ __device__ __forceinline__ void write_out(const Small& a, int e, int chunk,
 // next sums ----
 struct StepArgs {
   Small a;
-  float gram;               // A over the sums (times back[0]^2)
   float diag, beta, alpha;  // P = diag I + beta A + alpha A^2
   float x;                  // X over P X (times on[0], or at the end back[0])
 };
@@ -420,21 +508,16 @@ k_small_step(StepArgs s) {
   const int e = blockIdx.y, slice = blockIdx.x;
   const int wr = (w >> 2) * (MP / 2), wc = (w & 3) * (MP / 4);
   f32x4_v A[C::FM][C::FN], P[C::FM][C::FN];
-  read_parts<MP>(A, a.part, a.slices, e, tid);
-  const float f = a.back[e], ga = s.gram * f * f;
-#pragma unroll
-  for (int j = 0; j < C::FM; ++j)
-#pragma unroll
-    for (int i = 0; i < C::FN; ++i) A[j][i] *= ga;
-  put_square<MP>(b0, A, 1.f, w, lane);
+  copy_in<C::SQUARE>(b0, a.gram + (int64_t)e * C::SQUARE, tid);
   __syncthreads();
+  get_square<MP>(A, b0, w, lane);
   product<C::FM, C::FN, MP, MP, 2, 2, true, true>(P, b0, wr, b0, wc, MP / 32, lane);
   polynomial<MP>(P, A, s.diag, s.beta, s.alpha, a.m, w, lane);
-  put_square<MP>(b1, P, 1.f, w, lane);
+  put_square<MP>(b1, P, w, lane);
 
   int ex = 0;
   if constexpr (FIRST) ex = power_of(norm_of(a.sums, a.parts, e));
-  const float ax = s.x * (LAST ? f : a.on[e]);
+  const float ax = s.x * (LAST ? a.back[e] : a.on[e]);
   f32x4_v tot[C::FM][C::FN];
 #pragma unroll
   for (int j = 0; j < C::FM; ++j)
@@ -447,12 +530,7 @@ k_small_step(StepArgs s) {
     if constexpr (FIRST) {
       load_chunk<float, 2, MP, TALL, true>(b0, a, e, c, ex, tid);
     } else {
-      uint4 v[C::WIDE / 16 / SMALL_THREADS];
-#pragma unroll
-      for (int i = 0; i < C::WIDE / 16 / SMALL_THREADS; ++i)
-        v[i] = reinterpret_cast<const uint4*>(image)[i * SMALL_THREADS + tid];
-#pragma unroll
-      for (int i = 0; i < C::WIDE / 16 / SMALL_THREADS; ++i) reinterpret_cast<uint4*>(b0)[i * SMALL_THREADS + tid] = v[i];
+      copy_in<C::WIDE>(b0, image, tid);
     }
     __syncthreads();
     f32x4_v y[C::FM][C::XN];
@@ -469,9 +547,16 @@ k_small_step(StepArgs s) {
         for (int i = 0; i < C::XN; ++i) {
           const int k = (w & 3) * 32 + 16 * i + (lane & 15), m = wr + 16 * j + 4 * (lane >> 4);
           const f32x4_v v = y[j][i] * ax;
-          put4<CHUNK>(image, k, m, v);
+          f16x4_v hi, lo;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) put1<MP>(b0, m + x, k, v[x]);
+          for (int x = 0; x < 4; ++x) {
+            _Float16 vh, vl;
+            split(v[x], vh, vl);
+            hi[x] = vh;
+            lo[x] = vl;
+          }
+          put4<CHUNK>(image, k, m, hi, lo);
+          put4<MP>(b0, m + (lane & 3), k & ~3, turn4(hi, lane), turn4(lo, lane));
         }
       __syncthreads();
       f32x4_v acc[C::FM][C::FN];
@@ -482,7 +567,7 @@ k_small_step(StepArgs s) {
         for (int i = 0; i < C::FN; ++i) tot[j][i] += acc[j][i];
     }
   }
-  if constexpr (!LAST) write_part<MP>(a.part_next, a.slices, e, slice, tot, tid);
+  if constexpr (!LAST) write_part<MP>(a.part, a.slices, e, slice, tot, w, tid);
 }
 
 // ---- bf16 updates: all steps on the m x m matrices, a workgroup per update ----
@@ -492,7 +577,6 @@ struct Recurrence {
 };
 struct StepsArgs {
   Small a;
-  float gram;
   int steps;
   Recurrence s[MAX_STEPS];
 };
@@ -506,8 +590,6 @@ k_small_steps(StepsArgs) {
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), e = blockIdx.x;
   const int wr = (w >> 2) * (MP / 2), wc = (w & 3) * (MP / 4), m = g->a.m;
   f32x4_v A[C::FM][C::FN], P[C::FM][C::FN], Q[C::FM][C::FN];
-  read_parts<MP>(A, g->a.part, g->a.slices, e, tid);
-  const float f = g->a.back[e], ga = g->gram * f * f;
   auto scaled = [&](f32x4_v (&v)[C::FM][C::FN], float by) {
 #pragma unroll
     for (int j = 0; j < C::FM; ++j)
@@ -517,13 +599,17 @@ k_small_steps(StepsArgs) {
   auto times = [&](f32x4_v (&v)[C::FM][C::FN], const char* x, const char* y) {
     product<C::FM, C::FN, MP, MP, 2, 2, false, true>(v, x, wr, y, wc, MP / 32, lane);
   };
-  scaled(A, ga);
+  copy_in<C::SQUARE>(b0, g->a.gram + (int64_t)e * C::SQUARE, tid);
+  __syncthreads();
+  get_square<MP>(A, b0, w, lane);
   const int steps = g->steps;
   for (int i = 0; i < steps; ++i) {
     const auto& s = g->s[i];
-    __syncthreads();  // the buffers are free
-    put_symmetric<MP>(b0, A, 1.f, w, lane);
-    __syncthreads();
+    if (i > 0) {
+      __syncthreads();  // the buffers are free
+      put_symmetric<MP>(b0, A, 1.f, w, lane);
+      __syncthreads();
+    }
     times(P, b0, b0);
     polynomial<MP>(P, A, s.diag, s.beta, s.alpha, m, w, lane);
     put_symmetric<MP>(b1, P, 1.f, w, lane);
@@ -566,10 +652,7 @@ k_small_apply(ApplyArgs s) {
   const Small& a = s.a;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int e = blockIdx.y;
-  const uint4* q = reinterpret_cast<const uint4*>(a.q + (int64_t)e * C::SQUARE);
-#pragma unroll
-  for (int i = 0; i < C::SQUARE / 16 / SMALL_THREADS; ++i)
-    reinterpret_cast<uint4*>(b1)[i * SMALL_THREADS + tid] = q[i * SMALL_THREADS + tid];
+  copy_in<C::SQUARE>(b1, a.q + (int64_t)e * C::SQUARE, tid);
   const int ex = power_of(norm_of(a.sums, a.parts, e));
   const float ax = s.x * a.back[e];
   const int end = min(a.chunks, ((int)blockIdx.x + 1) * a.per);
