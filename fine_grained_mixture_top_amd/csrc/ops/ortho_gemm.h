@@ -69,7 +69,7 @@ struct Args {
 
 enum Epi { SYM, SPLIT, OUT };
 
-template <int BM, int BN, int WM, int WN, int PA, int PB>
+template <int BM, int BN, int WM, int WN, int BUFS, int PA, int PB>
 struct Cfg {
   static constexpr int W = WM * WN, NTH = 64 * W;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
@@ -78,7 +78,8 @@ struct Cfg {
   static constexpr int LA = WIDE || PA == 2 ? 128 : 64, LB = WIDE || PB == 2 ? 128 : 64;  // bytes of a line per stage
   static constexpr int IA = BM * LA / 1024 / W, IB = BN * LB / 1024 / W;                  // 1 KB loads per wave
   static constexpr int STAGE = BM * LA + BN * LB;
-  static constexpr int SMEM = 2 * STAGE;
+  static constexpr int SMEM = BUFS * STAGE;
+  static_assert(SMEM <= 160 * 1024 && (BUFS - 2) * (IA + IB) < 64, "LDS, and outstanding loads");
   static_assert(BM * LA % (1024 * W) == 0 && BN * LB % (1024 * W) == 0, "loads per wave");
 };
 
@@ -86,15 +87,27 @@ struct Cfg {
 // lanes that read a chunk of eight neighbouring lines hit eight different ones.
 template <int LINE> __device__ __forceinline__ int key(int r) { return LINE == 128 ? r & 7 : (r >> 1) & 3; }
 
+// waits until at most the newest min(N, n) stages of L loads each are outstanding
+template <int N, int L>
+__device__ __forceinline__ void wait_stages(int n) {
+  if constexpr (N > 0) {
+    if (n < N) {
+      wait_stages<N - 1, L>(n);
+      return;
+    }
+  }
+  wait_vm<N * L>();
+}
+
 // FINE: the two products with a lo, which are small, are summed apart and join the fp32
 // sums in one addition; a matrix instruction rounds its sum four times (eight products at
 // a time), so five roundings of a large sum take the place of twelve per 32 of the
 // reduction.  Error of five fp32 steps against 64 bits, without and with it: 2.0e-6 and
 // 1.5e-6 (1536 x 128; fp32 products 1.4e-6), 3.5e-6 and 2.3e-6 (720 x 1040; 2.4e-6); 4% of the time.
-template <int BM, int BN, int WM, int WN, int PA, int PB, bool FINE, Epi EPI, typename O>
+template <int BM, int BN, int WM, int WN, int BUFS, int PA, int PB, bool FINE, Epi EPI, typename O>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 k_ortho_gemm(Args g) {
-  using C = Cfg<BM, BN, WM, WN, PA, PB>;
+  using C = Cfg<BM, BN, WM, WN, BUFS, PA, PB>;
   constexpr int FM = C::FM, FN = C::FN;
   static_assert(!FINE || (PA == 2 && PB == 2), "products with a lo on both sides");
   extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -162,13 +175,18 @@ k_ortho_gemm(Args g) {
 #pragma unroll
   for (int x = 0; x < NB; ++x) slot_b[x] = ((h + 4 * x) ^ key<C::LB>(p)) * 16;
 
-  load(0, 0);
+  constexpr int L = C::IA + C::IB, AHEAD = BUFS - 1;
+#pragma unroll
+  for (int s = 0; s < AHEAD; ++s)
+    if (s < g.stages) load(s, s);
+  int buf = 0;
   for (int s = 0; s < g.stages; ++s) {
-    const int buf = s & 1;
-    wait_vm<0>();
-    lds_sync();  // the stage is there, and everybody is done with the other buffer
-    if (s + 1 < g.stages) load(s + 1, buf ^ 1);
+    // this stage is there when all but the loads of the stages behind it are
+    wait_stages<AHEAD - 1, L>(g.stages - 1 - s);
+    lds_sync();  // ... everybody's, and everybody is done with the buffer before it
+    if (s + AHEAD < g.stages) load(s + AHEAD, buf == 0 ? BUFS - 1 : buf - 1);
     const int at = buf * C::STAGE;
+    buf = buf + 1 == BUFS ? 0 : buf + 1;
     f16x8_v fb[FN][NB], fa[2][NA];
 #pragma unroll
     for (int x = 0; x < NA; ++x) fa[0][x] = lds_ld<f16x8_v>(la + at + slot_a[x]);

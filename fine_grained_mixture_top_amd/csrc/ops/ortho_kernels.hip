@@ -124,10 +124,10 @@ k_ortho_convert(Convert a) {
 }
 
 // ---- launches ----
-template <int BM, int BN, int WM, int WN, int PA, int PB, bool FINE, Epi EPI, typename O>
+template <int BM, int BN, int WM, int WN, int BUFS, int PA, int PB, bool FINE, Epi EPI, typename O>
 hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
-  using C = Cfg<BM, BN, WM, WN, PA, PB>;
-  auto* k = k_ortho_gemm<BM, BN, WM, WN, PA, PB, FINE, EPI, O>;
+  using C = Cfg<BM, BN, WM, WN, BUFS, PA, PB>;
+  auto* k = k_ortho_gemm<BM, BN, WM, WN, BUFS, PA, PB, FINE, EPI, O>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = allow_lds(k, C::SMEM, device(), done);
   if (e != hipSuccess) return e;
@@ -135,15 +135,26 @@ hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Tiles.  Few of them: a stage takes as long as its loads, so small tiles with three
+// stages ahead; many: large ones, which load least.  A whole call, us, with 64 x 64
+// tiles (four stage buffers) / 128 x 128 (two; with four 128 x 128 is no faster than either) /
+// 256 x 256:
+//   bf16   1 x 512 x 512 162 / 327 / 769          fp32   1 x 512 x 512 167 / 338 / 807
+//          4 x 1024 x 1024 525 / 571 / 1246              16 x 512 x 1024 523 / 505 / 1010
+//          64 x 256 x 1536 346 / 374 / 612               64 x 256 x 1536 901 / 913 / 1275
+//          24 x 720 x 1040 1045 / 890 / 1297             24 x 720 x 1040 1466 / 1197 / 1601
+//          32 x 1024 x 1024 - / 2657 / 2977              16 x 2048 x 2048 - / 8802 / 8868
+//          64 x 2048 x 2048 - / 32222 / 30367            64 x 2048 x 2048 - / 34278 / 32976
 template <int PA, int PB, bool FINE, Epi EPI, typename O>
 hipError_t gemm_by_size(const Args& a, hipStream_t st) {
   auto tiles = [&](int B) {
     const int64_t mt = div_up(a.ra, B), nt = div_up(a.rb, B);
     return a.batch * a.jobs * (EPI == SYM ? mt * (mt + 1) / 2 : mt * nt);
   };
-  const int64_t t256 = tiles(256);
-  if (t256 >= 512) return launch_gemm<256, 256, 2, 4, PA, PB, FINE, EPI, O>(a, t256, st);
-  return launch_gemm<128, 128, 2, 2, PA, PB, FINE, EPI, O>(a, tiles(128), st);
+  const int64_t t256 = tiles(256), t64 = tiles(64);
+  if (t256 >= 1024) return launch_gemm<256, 256, 2, 4, 2, PA, PB, FINE, EPI, O>(a, t256, st);
+  if (t64 <= 768) return launch_gemm<64, 64, 2, 2, 4, PA, PB, FINE, EPI, O>(a, t64, st);
+  return launch_gemm<128, 128, 2, 2, 2, PA, PB, FINE, EPI, O>(a, tiles(128), st);
 }
 
 // (fp32 updates are two parts throughout, and FINE)

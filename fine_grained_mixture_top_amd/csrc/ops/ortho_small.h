@@ -21,17 +21,25 @@ constexpr int SMALL_THREADS = 512;
 // line address of row r, plane c of a matrix of ROWS rows, and the slot of 16 bytes in it
 template <int ROWS> __device__ __forceinline__ int line_at(int c, int r) { return (c * ROWS + r) * 128; }
 
-// 4 numbers from column k on (a multiple of 4) of row r
+// Where the lanes of a wave find a piece of 16 x 16 at row R, column K (multiples of
+// 16, the same in all lanes) of a two-part matrix of ROWS rows: lane p + 16 h has four numbers
+// of row p from column 4 h on; turned (see turn4), of row 4 h + p % 4 from column
+// p / 4 * 4 on.  Slots of 16 bytes are xored with row % 8, the lo lies in the slot 4 further on:
+// all that depends on the lane is one offset, xored with 32 (odd half of a plane) and 64.
 template <int ROWS>
-__device__ __forceinline__ void put4(char* m, int r, int k, const f16x4_v hi, const f16x4_v lo) {
-  char* line = m + line_at<ROWS>(k >> 5, r);
-  const int c = (k & 31) >> 3, half = (k & 4) * 2;
-  *reinterpret_cast<f16x4_v*>(line + ((c ^ (r & 7)) * 16) + half) = hi;
-  *reinterpret_cast<f16x4_v*>(line + (((c + 4) ^ (r & 7)) * 16) + half) = lo;
-}
-template <int ROWS>
-__device__ __forceinline__ void put4(char* m, int r, int k, const f32x4_v v) {
-  f16x4_v hi, lo;
+struct Place {
+  uint32_t d, t;
+  __device__ __forceinline__ explicit Place(int lane) {
+    const int p = lane & 15, h = lane >> 4, tr = 4 * h + (p & 3);
+    d = p * 128 + (((h >> 1) ^ (p & 7)) * 16) + (h & 1) * 8;
+    t = tr * 128 + (((p >> 3) ^ (tr & 7)) * 16) + ((p >> 2) & 1) * 8;
+  }
+  static __device__ __forceinline__ uint32_t piece(int R, int K) { return ((K >> 5) * ROWS + R) * 128; }
+  __device__ __forceinline__ uint32_t direct(int R, int K) const { return piece(R, K) + (d ^ (K & 16) * 2); }
+  __device__ __forceinline__ uint32_t turned(int R, int K) const { return piece(R, K) + (t ^ (K & 16) * 2); }
+};
+
+__device__ __forceinline__ void split4(const f32x4_v v, f16x4_v& hi, f16x4_v& lo) {
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     _Float16 vh, vl;
@@ -39,34 +47,64 @@ __device__ __forceinline__ void put4(char* m, int r, int k, const f32x4_v v) {
     hi[x] = vh;
     lo[x] = vl;
   }
-  put4<ROWS>(m, r, k, hi, lo);
 }
-template <int ROWS>
-__device__ __forceinline__ f32x4_v get4(const char* m, int r, int k) {
-  const char* line = m + line_at<ROWS>(k >> 5, r);
-  const int c = (k & 31) >> 3, half = (k & 4) * 2;
-  const f16x4_v hi = *reinterpret_cast<const f16x4_v*>(line + ((c ^ (r & 7)) * 16) + half);
-  const f16x4_v lo = *reinterpret_cast<const f16x4_v*>(line + (((c + 4) ^ (r & 7)) * 16) + half);
+__device__ __forceinline__ void put(char* m, uint32_t at, const f16x4_v hi, const f16x4_v lo) {
+  *reinterpret_cast<f16x4_v*>(m + at) = hi;
+  *reinterpret_cast<f16x4_v*>(m + (at ^ 64)) = lo;
+}
+__device__ __forceinline__ f32x4_v get(const char* m, uint32_t at) {
+  const f16x4_v hi = *reinterpret_cast<const f16x4_v*>(m + at), lo = *reinterpret_cast<const f16x4_v*>(m + (at ^ 64));
   f32x4_v v;
 #pragma unroll
   for (int x = 0; x < 4; ++x) v[x] = (float)hi[x] + (float)lo[x];
   return v;
 }
-// one number
-template <int ROWS>
-__device__ __forceinline__ void put1(char* m, int r, int k, _Float16 hi, _Float16 lo) {
-  char* line = m + line_at<ROWS>(k >> 5, r);
-  const int c = (k & 31) >> 3, at = (k & 7) * 2;
-  *reinterpret_cast<_Float16*>(line + ((c ^ (r & 7)) * 16) + at) = hi;
-  *reinterpret_cast<_Float16*>(line + (((c + 4) ^ (r & 7)) * 16) + at) = lo;
+
+// Four neighbouring lanes hold four numbers each, a 4 x 4 block of 16-bit values by rows;
+// by columns afterwards.
+__device__ __forceinline__ f16x4_v turn4(const f16x4_v v, int lane) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  const u32x2_t d = __builtin_bit_cast(u32x2_t, v);
+  auto swap1 = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 15, 15, true); };  // lane ^ 1
+  auto swap2 = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 15, 15, true); };  // lane ^ 2
+  const uint32_t o0 = swap1(d[0]), o1 = swap1(d[1]);
+  // columns 0 and 2 of two rows in even lanes, 1 and 3 in odd ones
+  const uint32_t pick = lane & 1 ? 0x03020706u : 0x05040100u;
+  const uint32_t e0 = __builtin_amdgcn_perm(o0, d[0], pick), e1 = __builtin_amdgcn_perm(o1, d[1], pick);
+  const bool high = lane & 2;
+  const uint32_t got = swap2(high ? e0 : e1);
+  return __builtin_bit_cast(f16x4_v, high ? u32x2_t{got, e1} : u32x2_t{e0, got});
 }
 
-// acc = A B^T for the rows ra0 .. and rb0 .. of two matrices in LDS, over `planes` times 32
+// A piece on or below the diagonal of a symmetric matrix, and its mirror.  (Products of
+// matrices that commute are symmetric up to their rounding, and what is not would grow
+// with the steps: 63 x 65, five steps, error 3.7e-2 with both halves as computed.)
+template <int ROWS>
+__device__ __forceinline__ void put_mirrored(char* m, int R, int K, const f32x4_v v, const Place<ROWS>& at, int lane) {
+  f16x4_v hi, lo;
+  split4(v, hi, lo);
+  put(m, at.direct(R, K), hi, lo);
+  hi = turn4(hi, lane);
+  lo = turn4(lo, lane);
+  const uint32_t to = at.turned(K, R);
+  if (R > K) {
+    put(m, to, hi, lo);
+  } else {  // above the diagonal, over what the lines before put there (a wave's writes stay in order)
+    const int p = lane & 15, r = 4 * (lane >> 4) + (p & 3), c = p & ~3;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (c + x > r) {
+        *reinterpret_cast<_Float16*>(m + to + 2 * x) = hi[x];
+        *reinterpret_cast<_Float16*>(m + (to ^ 64) + 2 * x) = lo[x];
+      }
+  }
+}
+
+// acc = A B^T for the rows ra0 .. and rb0 .. of two matrices in LDS, over PLANES times 32
 // of the reduction.  ROWS_FIRST: a lane holds, of row p of A, four neighbouring rows of B;
 // else of row p of B four of A.
-template <int FM, int FN, int RA, int RB, int PA, int PB, bool FINE, bool ROWS_FIRST>
-__device__ __forceinline__ void product(f32x4_v (&acc)[FM][FN], const char* a, int ra0, const char* b, int rb0, int planes,
-                                        int lane) {
+template <int FM, int FN, int RA, int RB, int PLANES, int PA, int PB, bool FINE, bool ROWS_FIRST>
+__device__ __forceinline__ void product(f32x4_v (&acc)[FM][FN], const char* a, int ra0, const char* b, int rb0, int lane) {
   const int p = lane & 15, h = lane >> 4;
 #pragma unroll
   for (int j = 0; j < FM; ++j)
@@ -76,22 +114,23 @@ __device__ __forceinline__ void product(f32x4_v (&acc)[FM][FN], const char* a, i
     return ROWS_FIRST ? __builtin_amdgcn_mfma_f32_16x16x32_f16(y, x, c, 0, 0, 0)
                       : __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
   };
-  for (int c = 0; c < planes; ++c) {
+  // (what depends on the lane: one offset, and it xored with 64)
+  const uint32_t at = p * 128 + ((h ^ (p & 7)) * 16);
+  a += ra0 * 128;
+  b += rb0 * 128;
+#pragma unroll
+  for (int c = 0; c < PLANES; ++c) {
     f16x8_v fa[FM][PA], fb[FN][PB];
 #pragma unroll
     for (int j = 0; j < FM; ++j)
 #pragma unroll
-      for (int x = 0; x < PA; ++x) {
-        const int r = ra0 + 16 * j + p, slot = PA == 2 ? h + 4 * x : h + 4 * (c & 1);
-        fa[j][x] = *reinterpret_cast<const f16x8_v*>(a + line_at<RA>(PA == 2 ? c : c >> 1, r) + ((slot ^ (r & 7)) * 16));
-      }
+      for (int x = 0; x < PA; ++x)
+        fa[j][x] = *reinterpret_cast<const f16x8_v*>(a + (at ^ ((PA == 2 ? x : c & 1) * 64)) + line_at<RA>(PA == 2 ? c : c >> 1, 16 * j));
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
-      for (int x = 0; x < PB; ++x) {
-        const int r = rb0 + 16 * i + p, slot = PB == 2 ? h + 4 * x : h + 4 * (c & 1);
-        fb[i][x] = *reinterpret_cast<const f16x8_v*>(b + line_at<RB>(PB == 2 ? c : c >> 1, r) + ((slot ^ (r & 7)) * 16));
-      }
+      for (int x = 0; x < PB; ++x)
+        fb[i][x] = *reinterpret_cast<const f16x8_v*>(b + (at ^ ((PB == 2 ? x : c & 1) * 64)) + line_at<RB>(PB == 2 ? c : c >> 1, 16 * i));
 #pragma unroll
     for (int j = 0; j < FM; ++j)
 #pragma unroll
@@ -202,61 +241,14 @@ __device__ __forceinline__ void load_chunk(char* to, const Small& a, int e, int 
 template <int MP>
 __device__ __forceinline__ void put_square(char* to, const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], int w, int lane) {
   using C = SmallCfg<MP>;
-  const int r0 = (w >> 2) * (MP / 2) + (lane & 15), c0 = (w & 3) * (MP / 4) + 4 * (lane >> 4);
-#pragma unroll
-  for (int j = 0; j < C::FM; ++j)
-#pragma unroll
-    for (int i = 0; i < C::FN; ++i) put4<MP>(to, r0 + 16 * j, c0 + 16 * i, v[j][i]);
-}
-
-// Four neighbouring lanes hold four numbers each, a 4 x 4 block of 16-bit values by rows;
-// by columns afterwards.
-__device__ __forceinline__ f16x4_v turn4(const f16x4_v v, int lane) {
-  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-  const u32x2_t d = __builtin_bit_cast(u32x2_t, v);
-  auto swap1 = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 15, 15, true); };  // lane ^ 1
-  auto swap2 = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 15, 15, true); };  // lane ^ 2
-  const uint32_t o0 = swap1(d[0]), o1 = swap1(d[1]);
-  const bool odd = lane & 1, high = lane & 2;
-  // columns 0 and 2 of two rows in even lanes, 1 and 3 in odd ones
-  const uint32_t e0 = odd ? (o0 >> 16) | (d[0] & 0xffff0000u) : (d[0] & 0xffffu) | (o0 << 16);
-  const uint32_t e1 = odd ? (o1 >> 16) | (d[1] & 0xffff0000u) : (d[1] & 0xffffu) | (o1 << 16);
-  const uint32_t got = swap2(high ? e0 : e1);
-  return __builtin_bit_cast(f16x4_v, high ? u32x2_t{got, e1} : u32x2_t{e0, got});
-}
-
-// The lower half of a symmetric matrix, on both sides of the diagonal: products of
-// matrices that commute are symmetric up to their rounding, and what is not would
-// grow with the steps (63 x 65, five steps: error 3.7e-2 with both halves as computed).
-template <int MP>
-__device__ __forceinline__ void put_symmetric(char* to, const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], float scale,
-                                              int w, int lane) {
-  using C = SmallCfg<MP>;
-  const int p = lane & 15, h = lane >> 4;
+  const Place<MP> at(lane);
 #pragma unroll
   for (int j = 0; j < C::FM; ++j)
 #pragma unroll
     for (int i = 0; i < C::FN; ++i) {
-      const int R = (w >> 2) * (MP / 2) + 16 * j, K = (w & 3) * (MP / 4) + 16 * i;  // the piece's first row and column
-      if (R < K) continue;
-      const int r = R + p, k = K + 4 * h;
-      const f32x4_v u = v[j][i] * scale;
       f16x4_v hi, lo;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        _Float16 vh, vl;
-        split(u[x], vh, vl);
-        hi[x] = vh;
-        lo[x] = vl;
-      }
-      put4<MP>(to, r, k, hi, lo);
-      if (R > K) {
-        put4<MP>(to, k + (p & 3), R + (p & ~3), turn4(hi, lane), turn4(lo, lane));
-      } else {  // over what the lines above put there (a wave's LDS writes stay in order)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (k + x < r) put1<MP>(to, k + x, r, hi[x], lo[x]);
-      }
+      split4(v[j][i], hi, lo);
+      put(to, at.direct((w >> 2) * (MP / 2) + 16 * j, (w & 3) * (MP / 4) + 16 * i), hi, lo);
     }
 }
 
@@ -383,7 +375,7 @@ k_small_gram(Small a) {
     __syncthreads();
     load_chunk<T, P, MP, TALL, false>(smem, a, e, c, ex, tid);
     __syncthreads();
-    product<C::FM, C::FN, MP, MP, P, P, P == 2, true>(acc, smem, (w >> 2) * (MP / 2), smem, (w & 3) * (MP / 4), CHUNK / 32, lane);
+    product<C::FM, C::FN, MP, MP, CHUNK / 32, P, P, P == 2, true>(acc, smem, (w >> 2) * (MP / 2), smem, (w & 3) * (MP / 4), lane);
 #pragma unroll
     for (int j = 0; j < C::FM; ++j)
 #pragma unroll
@@ -422,22 +414,9 @@ k_small_reduce(ReduceArgs) {
   for (int s = 0; s < slices; ++s) v += p[(int64_t)s * (MP * MP / 4)];
   const float f = g->first ? (float)first_of(norm_of(g->a.sums, g->a.parts, e), g->a.eps) : g->a.back[e];
   v *= g->gram * f * f;
-  const int R = (w >> 2) * (MP / 2) + 16 * j, K = (w & 3) * (MP / 4) + 16 * i, r = R + (lane & 15), k = K + 4 * (lane >> 4);
+  const int R = (w >> 2) * (MP / 2) + 16 * j, K = (w & 3) * (MP / 4) + 16 * i;
   char* to = g->a.gram + (int64_t)e * C::SQUARE;
-  f16x4_v hi, lo;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    _Float16 vh, vl;
-    split(v[x], vh, vl);
-    hi[x] = vh;
-    lo[x] = vl;
-  }
-  if (R > K) put4<MP>(to, r, k, hi, lo);
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    if (R == K && k + x <= r) put1<MP>(to, r, k + x, hi[x], lo[x]);
-    if (k + x < r) put1<MP>(to, k + x, r, hi[x], lo[x]);
-  }
+  put_mirrored<MP>(to, R, K, v, Place<MP>(lane), lane);
 }
 
 // a matrix as it lies in LDS, from memory
@@ -454,11 +433,11 @@ __device__ __forceinline__ void copy_in(char* to, const char* from, int tid) {
 template <int MP>
 __device__ __forceinline__ void get_square(f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], const char* m, int w, int lane) {
   using C = SmallCfg<MP>;
+  const Place<MP> at(lane);
 #pragma unroll
   for (int j = 0; j < C::FM; ++j)
 #pragma unroll
-    for (int i = 0; i < C::FN; ++i)
-      v[j][i] = get4<MP>(m, (w >> 2) * (MP / 2) + 16 * j + (lane & 15), (w & 3) * (MP / 4) + 16 * i + 4 * (lane >> 4));
+    for (int i = 0; i < C::FN; ++i) v[j][i] = get(m, at.direct((w >> 2) * (MP / 2) + 16 * j, (w & 3) * (MP / 4) + 16 * i));
 }
 
 // A call's X = Q X, times alpha, at its place in o
@@ -511,7 +490,7 @@ k_small_step(StepArgs s) {
   copy_in<C::SQUARE>(b0, a.gram + (int64_t)e * C::SQUARE, tid);
   __syncthreads();
   get_square<MP>(A, b0, w, lane);
-  product<C::FM, C::FN, MP, MP, 2, 2, true, true>(P, b0, wr, b0, wc, MP / 32, lane);
+  product<C::FM, C::FN, MP, MP, MP / 32, 2, 2, true, true>(P, b0, wr, b0, wc, lane);
   polynomial<MP>(P, A, s.diag, s.beta, s.alpha, a.m, w, lane);
   put_square<MP>(b1, P, w, lane);
 
@@ -534,33 +513,28 @@ k_small_step(StepArgs s) {
     }
     __syncthreads();
     f32x4_v y[C::FM][C::XN];
-    product<C::FM, C::XN, MP, CHUNK, 2, 2, true, LAST && !TALL>(y, b1, wr, b0, (w & 3) * 32, MP / 32, lane);
+    product<C::FM, C::XN, MP, CHUNK, MP / 32, 2, 2, true, LAST && !TALL>(y, b1, wr, b0, (w & 3) * 32, lane);
     if constexpr (LAST) {
       write_out<float, MP, TALL, !TALL>(a, e, c, y, ax, w, lane);
     } else {
       __syncthreads();
       // X^T as it will be read next, and X over the old one; a lane holds, of row k = p,
       // four neighbouring m
+      const Place<CHUNK> xt(lane);
+      const Place<MP> x(lane);
 #pragma unroll
       for (int j = 0; j < C::FM; ++j)
 #pragma unroll
         for (int i = 0; i < C::XN; ++i) {
-          const int k = (w & 3) * 32 + 16 * i + (lane & 15), m = wr + 16 * j + 4 * (lane >> 4);
-          const f32x4_v v = y[j][i] * ax;
+          const int k = (w & 3) * 32 + 16 * i, m = wr + 16 * j;
           f16x4_v hi, lo;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            _Float16 vh, vl;
-            split(v[x], vh, vl);
-            hi[x] = vh;
-            lo[x] = vl;
-          }
-          put4<CHUNK>(image, k, m, hi, lo);
-          put4<MP>(b0, m + (lane & 3), k & ~3, turn4(hi, lane), turn4(lo, lane));
+          split4(y[j][i] * ax, hi, lo);
+          put(image, xt.direct(k, m), hi, lo);
+          put(b0, x.turned(m, k), turn4(hi, lane), turn4(lo, lane));
         }
       __syncthreads();
       f32x4_v acc[C::FM][C::FN];
-      product<C::FM, C::FN, MP, MP, 2, 2, true, true>(acc, b0, wr, b0, wc, CHUNK / 32, lane);
+      product<C::FM, C::FN, MP, MP, CHUNK / 32, 2, 2, true, true>(acc, b0, wr, b0, wc, lane);
 #pragma unroll
       for (int j = 0; j < C::FM; ++j)
 #pragma unroll
@@ -597,45 +571,53 @@ k_small_steps(StepsArgs) {
       for (int i = 0; i < C::FN; ++i) v[j][i] *= by;
   };
   auto times = [&](f32x4_v (&v)[C::FM][C::FN], const char* x, const char* y) {
-    product<C::FM, C::FN, MP, MP, 2, 2, false, true>(v, x, wr, y, wc, MP / 32, lane);
+    product<C::FM, C::FN, MP, MP, MP / 32, 2, 2, false, true>(v, x, wr, y, wc, lane);
+  };
+  const Place<MP> at(lane);
+  auto put_lower = [&](char* to, const f32x4_v (&v)[C::FM][C::FN], float scale) {
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i)
+        if (!above<MP>(j, i, w)) put_mirrored<MP>(to, wr + 16 * j, wc + 16 * i, v[j][i] * scale, at, lane);
   };
   copy_in<C::SQUARE>(b0, g->a.gram + (int64_t)e * C::SQUARE, tid);
   __syncthreads();
   get_square<MP>(A, b0, w, lane);
   const int steps = g->steps;
-  for (int i = 0; i < steps; ++i) {
-    const auto& s = g->s[i];
-    if (i > 0) {
+  for (int s = 0; s < steps; ++s) {
+    const float diag = g->s[s].diag, beta = g->s[s].beta, alpha = g->s[s].alpha;
+    if (s > 0) {
       __syncthreads();  // the buffers are free
-      put_symmetric<MP>(b0, A, 1.f, w, lane);
+      put_lower(b0, A, 1.f);
       __syncthreads();
     }
     times(P, b0, b0);
-    polynomial<MP>(P, A, s.diag, s.beta, s.alpha, m, w, lane);
-    put_symmetric<MP>(b1, P, 1.f, w, lane);
+    polynomial<MP>(P, A, diag, beta, alpha, m, w, lane);
+    put_lower(b1, P, 1.f);
     __syncthreads();
-    if (i + 1 < steps) {
+    if (s + 1 < steps) {
       times(A, b1, b0);  // T = P A
       __syncthreads();
-      put_symmetric<MP>(b0, A, s.t, w, lane);
+      put_lower(b0, A, g->s[s].t);
       __syncthreads();
       times(A, b0, b1);  // the next A = T P
-      scaled(A, s.next);
+      scaled(A, g->s[s].next);
     }
-    if (i == 0) {
+    if (s == 0) {
 #pragma unroll
       for (int j = 0; j < C::FM; ++j)
 #pragma unroll
-        for (int x = 0; x < C::FN; ++x) Q[j][x] = P[j][x];
+        for (int i = 0; i < C::FN; ++i) Q[j][i] = P[j][i];
     } else {
       __syncthreads();
-      put_symmetric<MP>(b0, Q, 1.f, w, lane);
+      put_lower(b0, Q, 1.f);
       __syncthreads();
       times(Q, b1, b0);
-      scaled(Q, s.q);
+      scaled(Q, g->s[s].q);
     }
   }
-  put_symmetric<MP>(g->a.q + (int64_t)e * C::SQUARE, Q, 1.f, w, lane);
+  put_lower(g->a.q + (int64_t)e * C::SQUARE, Q, 1.f);
 }
 
 // ---- o = Q X ----
@@ -661,7 +643,7 @@ k_small_apply(ApplyArgs s) {
     load_chunk<bf16_t, 1, MP, TALL, true>(b0, a, e, c, ex, tid);
     __syncthreads();
     f32x4_v y[C::FM][C::XN];
-    product<C::FM, C::XN, MP, CHUNK, 2, 1, false, !TALL>(y, b1, (w >> 2) * (MP / 2), b0, (w & 3) * 32, MP / 32, lane);
+    product<C::FM, C::XN, MP, CHUNK, MP / 32, 2, 1, false, !TALL>(y, b1, (w >> 2) * (MP / 2), b0, (w & 3) * 32, lane);
     write_out<bf16_t, MP, TALL, !TALL>(a, e, c, y, ax, w, lane);
   }
 }
