@@ -149,59 +149,80 @@ __device__ __forceinline__ void product(f32x4_v (&acc)[FM][FN], const char* a, i
   }
 }
 
-// A chunk of the update, times 2^ex, as a matrix in LDS.  The update's part is gr x gc
-// numbers (row stride ld) of GR x GC, zeros past them; TURN: its columns become the rows.
-template <typename T, int P, int GR, int GC, bool TURN>
-__device__ __forceinline__ void load_update(char* m, const T* g, int64_t ld, int gr, int gc, int ex, bool vec, int tid) {
-  constexpr int V = 8, ROWS = TURN ? GC : GR;
-  constexpr int TASKS = GR * GC / V / SMALL_THREADS;
+// A chunk of the update on its way into LDS: gr x gc numbers (row stride ld) of GR x GC,
+// zeros past them, 8 of a row per thread and task.  First all loads, then, times 2^ex, as a
+// matrix in P parts; TURN: its columns become the rows.  A wave takes whole rows, or to
+// turn them over 16 of them and 32 columns: 64 bytes of each (of whole rows, lanes would write
+// to the same banks 16 times over; the product of 128 x 1000 with Q 10.8 -> 8.0 us).
+template <typename T, int GR, int GC, bool TURN>
+struct Chunk {
+  static constexpr int V = 8, TASKS = GR * GC / V / SMALL_THREADS;
   float v[TASKS][V];
-#pragma unroll
-  for (int t = 0; t < TASKS; ++t) {
-    const int id = t * SMALL_THREADS + tid, r = id / (GC / V), c = id % (GC / V) * V;
-    const T* p = g + r * ld + c;
-    if (r < gr && c + V <= gc && vec) {
-      T x[V];
-      const uint4* u = reinterpret_cast<const uint4*>(p);
-      uint4 w[sizeof(T) * V / 16];
-#pragma unroll
-      for (int y = 0; y < (int)(sizeof(T) * V / 16); ++y) w[y] = u[y];
-      __builtin_memcpy(x, w, sizeof(x));
-#pragma unroll
-      for (int y = 0; y < V; ++y) v[t][y] = Elem<T>::to_f(x[y]);
+  static __device__ __forceinline__ void at(int t, int tid, int& r, int& c) {
+    const int id = t * SMALL_THREADS + tid;
+    if constexpr (TURN) {
+      const int tile = id >> 6, lane = id & 63;
+      r = tile / (GC / 32) * 16 + (lane & 15);
+      c = tile % (GC / 32) * 32 + (lane >> 4) * 8;
     } else {
-#pragma unroll
-      for (int y = 0; y < V; ++y) v[t][y] = r < gr && c + y < gc ? Elem<T>::to_f(p[y]) : 0.f;
+      r = id / (GC / V);
+      c = id % (GC / V) * V;
     }
   }
+  __device__ __forceinline__ void fetch(const T* g, int64_t ld, int gr, int gc, bool vec, int tid) {
 #pragma unroll
-  for (int t = 0; t < TASKS; ++t) {
-    const int id = t * SMALL_THREADS + tid, r = id / (GC / V), c = id % (GC / V) * V;
-    f16x8_v hi, lo;
+    for (int t = 0; t < TASKS; ++t) {
+      int r, c;
+      at(t, tid, r, c);
+      const T* p = g + r * ld + c;
+      if (r < gr && c + V <= gc && vec) {
+        T x[V];
+        const uint4* u = reinterpret_cast<const uint4*>(p);
+        uint4 w[sizeof(T) * V / 16];
 #pragma unroll
-    for (int y = 0; y < V; ++y) {
-      _Float16 vh, vl;
-      split(ldexpf(v[t][y], ex), vh, vl);
-      hi[y] = vh;
-      lo[y] = vl;
+        for (int y = 0; y < (int)(sizeof(T) * V / 16); ++y) w[y] = u[y];
+        __builtin_memcpy(x, w, sizeof(x));
+#pragma unroll
+        for (int y = 0; y < V; ++y) v[t][y] = Elem<T>::to_f(x[y]);
+      } else {
+#pragma unroll
+        for (int y = 0; y < V; ++y) v[t][y] = r < gr && c + y < gc ? Elem<T>::to_f(p[y]) : 0.f;
+      }
     }
-    if constexpr (TURN) {
-      // number k = r of the rows c .. c + 7
+  }
+  template <int P>
+  __device__ __forceinline__ void place(char* m, int ex, int tid) const {
+    constexpr int ROWS = TURN ? GC : GR;
+#pragma unroll
+    for (int t = 0; t < TASKS; ++t) {
+      int r, c;
+      at(t, tid, r, c);
+      f16x8_v hi, lo;
 #pragma unroll
       for (int y = 0; y < V; ++y) {
-        const int row = c + y, plane = P == 2 ? r >> 5 : r >> 6, slot = P == 2 ? (r & 31) >> 3 : (r & 63) >> 3;
-        char* line = m + line_at<ROWS>(plane, row) + (r & 7) * 2;
-        *reinterpret_cast<_Float16*>(line + ((slot ^ (row & 7)) * 16)) = hi[y];
-        if constexpr (P == 2) *reinterpret_cast<_Float16*>(line + (((slot + 4) ^ (row & 7)) * 16)) = lo[y];
+        _Float16 vh, vl;
+        split(ldexpf(v[t][y], ex), vh, vl);
+        hi[y] = vh;
+        lo[y] = vl;
       }
-    } else {
-      const int plane = P == 2 ? c >> 5 : c >> 6, slot = P == 2 ? (c & 31) >> 3 : (c & 63) >> 3;
-      char* line = m + line_at<ROWS>(plane, r);
-      *reinterpret_cast<f16x8_v*>(line + ((slot ^ (r & 7)) * 16)) = hi;
-      if constexpr (P == 2) *reinterpret_cast<f16x8_v*>(line + (((slot + 4) ^ (r & 7)) * 16)) = lo;
+      if constexpr (TURN) {
+        // number k = r of the rows c .. c + 7
+#pragma unroll
+        for (int y = 0; y < V; ++y) {
+          const int row = c + y, plane = P == 2 ? r >> 5 : r >> 6, slot = P == 2 ? (r & 31) >> 3 : (r & 63) >> 3;
+          char* line = m + line_at<ROWS>(plane, row) + (r & 7) * 2;
+          *reinterpret_cast<_Float16*>(line + ((slot ^ (row & 7)) * 16)) = hi[y];
+          if constexpr (P == 2) *reinterpret_cast<_Float16*>(line + (((slot + 4) ^ (row & 7)) * 16)) = lo[y];
+        }
+      } else {
+        const int plane = P == 2 ? c >> 5 : c >> 6, slot = P == 2 ? (c & 31) >> 3 : (c & 63) >> 3;
+        char* line = m + line_at<ROWS>(plane, r);
+        *reinterpret_cast<f16x8_v*>(line + ((slot ^ (r & 7)) * 16)) = hi;
+        if constexpr (P == 2) *reinterpret_cast<f16x8_v*>(line + (((slot + 4) ^ (r & 7)) * 16)) = lo;
+      }
     }
   }
-}
+};
 
 // A call's sizes, for matrices e = blockIdx.y
 struct Small {
@@ -229,14 +250,17 @@ template <int MP> struct SmallCfg {
   static constexpr int WIDE = MP * CHUNK * 4;
 };
 
-// a chunk of the update as X, m rows of 128, or as its transpose
-template <typename T, int P, int MP, bool TALL, bool TRANSPOSED>
-__device__ __forceinline__ void load_chunk(char* to, const Small& a, int e, int chunk, int ex, int tid) {
-  const int k0 = chunk * CHUNK, left = min(CHUNK, a.k - k0);
-  const T* g = (const T*)a.g + (int64_t)e * a.M * a.N;
-  if constexpr (TALL) load_update<T, P, CHUNK, MP, !TRANSPOSED>(to, g + (int64_t)k0 * a.N, a.N, left, a.m, ex, a.vec, tid);
-  else load_update<T, P, MP, CHUNK, TRANSPOSED>(to, g + k0, a.N, a.m, left, ex, a.vec, tid);
-}
+// a chunk of an update whose rows (TALL: columns) are X's, MP of them at most, as X, m
+// rows of 128, or TRANSPOSED
+template <typename T, int MP, bool TALL, bool TRANSPOSED>
+struct UpdateChunk : Chunk<T, TALL ? CHUNK : MP, TALL ? MP : CHUNK, TALL != TRANSPOSED> {
+  __device__ __forceinline__ void load(const Small& a, int e, int chunk, int tid) {
+    const int k0 = chunk * CHUNK, left = min(CHUNK, a.k - k0);
+    const T* g = (const T*)a.g + (int64_t)e * a.M * a.N;
+    if constexpr (TALL) this->fetch(g + (int64_t)k0 * a.N, a.N, left, a.m, a.vec, tid);
+    else this->fetch(g + k0, a.N, a.m, left, a.vec, tid);
+  }
+};
 
 template <int MP>
 __device__ __forceinline__ void put_square(char* to, const f32x4_v (&v)[SmallCfg<MP>::FM][SmallCfg<MP>::FN], int w, int lane) {
@@ -336,6 +360,7 @@ __device__ __forceinline__ void factors(const __attribute__((address_space(4))) 
   const float nan = __builtin_nanf("");
   const int lane = threadIdx.x & 63;
   if (lane == 0) a.back[e] = (float)first;
+  if (lane == 0 && a.groups == 1) a.on[e] = (float)power_of(norm);  // (no next group: the update's exponent)
   float most = norm == 0.0 ? 0.f : (float)(norm / (norm + (double)a.eps));  // of |X|
   int t = 0, c = 0;
   for (int i = 0; i + 1 < a.groups; ++i) {
@@ -363,8 +388,9 @@ k_small_gram(Small a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int e = blockIdx.y, slice = blockIdx.x;
-  const double norm = norm_of(a.sums, a.parts, e);
-  const int ex = power_of(norm);
+  UpdateChunk<T, MP, TALL, false> update;
+  update.load(a, e, slice * a.per, tid);
+  const int ex = power_of(norm_of(a.sums, a.parts, e));
   f32x4_v tot[C::FM][C::FN], acc[C::FM][C::FN];
 #pragma unroll
   for (int j = 0; j < C::FM; ++j)
@@ -372,8 +398,11 @@ k_small_gram(Small a) {
     for (int i = 0; i < C::FN; ++i) tot[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
   const int last = min(a.chunks, (slice + 1) * a.per);
   for (int c = slice * a.per; c < last; ++c) {
-    __syncthreads();
-    load_chunk<T, P, MP, TALL, false>(smem, a, e, c, ex, tid);
+    if (c > slice * a.per) {
+      update.load(a, e, c, tid);
+      __syncthreads();
+    }
+    update.template place<P>(smem, ex, tid);
     __syncthreads();
     product<C::FM, C::FN, MP, MP, CHUNK / 32, P, P, P == 2, true>(acc, smem, (w >> 2) * (MP / 2), smem, (w & 3) * (MP / 4), lane);
 #pragma unroll
@@ -507,7 +536,9 @@ k_small_step(StepArgs s) {
     __syncthreads();  // everybody is done with b0
     char* image = a.x + ((int64_t)e * a.chunks + c) * C::WIDE;
     if constexpr (FIRST) {
-      load_chunk<float, 2, MP, TALL, true>(b0, a, e, c, ex, tid);
+      UpdateChunk<float, MP, TALL, true> update;
+      update.load(a, e, c, tid);
+      update.template place<2>(b0, ex, tid);
     } else {
       copy_in<C::WIDE>(b0, image, tid);
     }
@@ -634,13 +665,18 @@ k_small_apply(ApplyArgs s) {
   const Small& a = s.a;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int e = blockIdx.y;
-  copy_in<C::SQUARE>(b1, a.q + (int64_t)e * C::SQUARE, tid);
-  const int ex = power_of(norm_of(a.sums, a.parts, e));
+  const int begin = blockIdx.x * a.per, end = min(a.chunks, begin + a.per);
+  UpdateChunk<bf16_t, MP, TALL, true> update;
+  update.load(a, e, begin, tid);
+  const int ex = (int)a.on[e];
   const float ax = s.x * a.back[e];
-  const int end = min(a.chunks, ((int)blockIdx.x + 1) * a.per);
-  for (int c = blockIdx.x * a.per; c < end; ++c) {
-    __syncthreads();
-    load_chunk<bf16_t, 1, MP, TALL, true>(b0, a, e, c, ex, tid);
+  copy_in<C::SQUARE>(b1, a.q + (int64_t)e * C::SQUARE, tid);
+  for (int c = begin; c < end; ++c) {
+    if (c > begin) {
+      update.load(a, e, c, tid);
+      __syncthreads();
+    }
+    update.template place<1>(b0, ex, tid);
     __syncthreads();
     f32x4_v y[C::FM][C::XN];
     product<C::FM, C::XN, MP, CHUNK, MP / 32, 2, 1, false, !TALL>(y, b1, (w >> 2) * (MP / 2), b0, (w & 3) * 32, lane);
