@@ -49,23 +49,48 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[V]) {
   *reinterpret_cast<W*>(p) = w;
 }
 
-// over the L lanes that hold a row
-__device__ __forceinline__ float row_sum(float v, int L) {
-  for (int s = 1; s < L; s <<= 1) v += __shfl_xor(v, s, 64);
-  return v;
+// The other value of a pair of lanes 2^K apart (K < 4), in lanes that are alike within 2^K:
+// moves between lanes of the vector unit.
+template <int K> __device__ __forceinline__ float partner(float v) {
+  const int i = __float_as_int(v);
+  if constexpr (K == 0) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0xB1, 15, 15, true));   // quad_perm 1 0 3 2
+  if constexpr (K == 1) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x4E, 15, 15, true));   // quad_perm 2 3 0 1
+  if constexpr (K == 2) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x141, 15, 15, true));  // mirror in 8 lanes
+  return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x140, 15, 15, true));                        // mirror in 16
 }
-__device__ __forceinline__ float row_max(float v, int L) {
-  // a NaN has to come through: fmaxf drops it, so it is turned into +inf, whose
-  // exponentials are NaN as well
-  v = v != v ? __builtin_inff() : v;
-  for (int s = 1; s < L; s <<= 1) v = fmaxf(v, __shfl_xor(v, s, 64));
-  return v;
+// f over the 2^log_l lanes that hold a row, U rows side by side
+template <int K = 0, int U, typename F>
+__device__ __forceinline__ void over_row(float (&v)[U], int log_l, F f) {
+  if (log_l > K) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if constexpr (K < 4) {
+        v[i] = f(v[i], partner<K>(v[i]));
+      } else {  // rows of 16 (halves) of one copy change places with those of another: both have a pair's two values
+        const int x = __float_as_int(v[i]);
+        const auto two = K == 4 ? __builtin_amdgcn_permlane16_swap(x, x, false, false)
+                                : __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        v[i] = f(__int_as_float((int)two[0]), __int_as_float((int)two[1]));
+      }
+    }
+    if constexpr (K < 5) over_row<K + 1>(v, log_l, f);
+  }
+}
+template <int U> __device__ __forceinline__ void row_sum(float (&v)[U], int log_l) {
+  over_row(v, log_l, [](float a, float b) { return a + b; });
+}
+// (a NaN has to come through: fmaxf drops it, so it counts as +inf, whose exponentials are
+// NaN as well)
+__device__ __forceinline__ float max_nan(float m, float v) { return v != v ? __builtin_inff() : fmaxf(m, v); }
+template <int U> __device__ __forceinline__ void row_max(float (&v)[U], int log_l) {
+  over_row(v, log_l, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // lines of the workspace: E sums of probabilities, E counts, lse^2, tokens
 __host__ __device__ inline int line_words(int E) { return 2 * E + 2; }
-// (behind them the final launch's sums: 16 of counts * load, and an arrival count)
-constexpr int TAIL_WORDS = 17;
+// (behind them the final launch's sums of counts * load, one a workgroup, and an arrival count)
+constexpr int FINAL_COLS = 16;
+constexpr int TAIL_WORDS = MAX_E / FINAL_COLS + 1;
 
 struct Fwd {
   BalanceArgs a;
@@ -113,9 +138,6 @@ k_balance(Fwd f) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const BalanceArgs& a = f.a;
   const int L = 1 << f.logL, rows = 64 >> f.logL;
-  for (int e = tid; e < a.E; e += 64 * W) hist[e] = 0;
-  __syncthreads();
-
   float acc[R][V];
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -125,9 +147,10 @@ k_balance(Fwd f) {
   int n = 0;
   const int64_t units = ((int64_t)a.T + rows - 1) / rows;
   const int64_t step = (int64_t)gridDim.x * W;
-  for (int64_t u0 = (int64_t)blockIdx.x * W + w; u0 < units; u0 += U * step) {
-    Unit<T, V, R> x[U];
-    int choice[U];
+  Unit<T, V, R> x[U];
+  int choice[U];
+  int64_t u0 = (int64_t)blockIdx.x * W + w;
+  auto load = [&] {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       x[i].load(f, min(u0 + i * step, units - 1), lane);
@@ -135,32 +158,42 @@ k_balance(Fwd f) {
       const int k = lane & (L - 1);
       choice[i] = k < a.K ? a.idx[(int64_t)x[i].t * a.K + k] : -1;
     }
+  };
+  if (u0 < units) load();
+  for (int e = tid; e < a.E; e += 64 * W) hist[e] = 0;
+  lds_sync();  // (the loads stay under way)
+  while (u0 < units) {
+    float m[U], s[U], p[U][R][V];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      float m = NEG_INF;
+      m[i] = NEG_INF;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int v = 0; v < V; ++v) m = (x[i].z[r][v] != x[i].z[r][v]) ? __builtin_inff() : fmaxf(m, x[i].z[r][v]);
-      m = row_max(m, L);
-      const bool counting = x[i].valid && m > NEG_INF;
-      float s = 0.f, p[R][V];
+        for (int v = 0; v < V; ++v) m[i] = max_nan(m[i], x[i].z[r][v]);
+    }
+    row_max(m, f.logL);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      s[i] = 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          p[r][v] = __expf(x[i].z[r][v] - m);
-          s += p[r][v];
+          p[i][r][v] = __expf(x[i].z[r][v] - m[i]);
+          s[i] += p[i][r][v];
         }
-      s = row_sum(s, L);
-      const float inv = 1.f / s;
-      if (counting) {
+    }
+    row_sum(s, f.logL);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+    for (int i = 0; i < U; ++i) {
+      const bool counting = x[i].valid && m[i] > NEG_INF;
+      const float inv = 1.f / s[i];
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[r][v] = fmaf(p[r][v], inv, acc[r][v]);
-      }
-      const float lse = counting ? m + __logf(s) : NEG_INF;
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[r][v] = counting ? fmaf(p[i][r][v], inv, acc[r][v]) : acc[r][v];
+      const float lse = counting ? m[i] + __logf(s[i]) : NEG_INF;
       const int j = lane & (L - 1);
       if (x[i].there && j == 0) a.lse[x[i].t] = lse;
       if (counting) {
@@ -175,6 +208,8 @@ k_balance(Fwd f) {
         }
       }
     }
+    u0 += U * step;
+    if (u0 < units) load();
   }
 
   // groups of the wave, then waves, in order
@@ -238,43 +273,58 @@ k_balance(Fwd f) {
   }
 }
 
-// The lines' sums: 64 columns per workgroup, 16 threads each; the workgroup that
-// arrives last adds up the balance loss.
+// The lines' sums: 16 columns per workgroup, 64 threads each, so that a thread's loads
+// are in flight together (64 columns with 16 threads each took 6.7 us at E = 128, this 4.8);
+// the workgroup that arrives last adds up the balance loss.
 __global__ void __launch_bounds__(1024)
 k_balance_final(Fwd f, int lines) {
-  __shared__ float sp[16][64];
-  __shared__ int sc[16][64];
+  __shared__ float sp[16][FINAL_COLS];
+  __shared__ int sc[16][FINAL_COLS];
   __shared__ float szw[16];
   __shared__ int snw[16];
-  __shared__ bool last;
   const BalanceArgs& a = f.a;
-  const int tid = threadIdx.x, c = tid & 63, s = tid >> 6;
-  const int e = blockIdx.x * 64 + c, words = line_words(a.E);
+  const int tid = threadIdx.x, c = tid & 15, s = tid >> 4, w = tid >> 6, lane = tid & 63;
+  const int e = blockIdx.x * FINAL_COLS + c, words = line_words(a.E);
   float p = 0.f, z = 0.f;
   int cnt = 0, n = 0;
   if (e < a.E) {
-#pragma unroll 8
-    for (int g = s; g < lines; g += 16) {
-      p += __uint_as_float(f.line[(int64_t)g * words + e]);
-      cnt += (int)f.line[(int64_t)g * words + a.E + e];
+    const uint32_t* from = f.line + e;
+    float pv[FWD_BLOCKS / 64];
+    int cv[FWD_BLOCKS / 64];
+#pragma unroll
+    for (int i = 0; i < FWD_BLOCKS / 64; ++i) {
+      const int g = min(s + 64 * i, lines - 1);
+      pv[i] = __uint_as_float(from[(int64_t)g * words]);
+      cv[i] = (int)from[(int64_t)g * words + a.E];
+    }
+#pragma unroll
+    for (int i = 0; i < FWD_BLOCKS / 64; ++i) {
+      p += s + 64 * i < lines ? pv[i] : 0.f;
+      cnt += s + 64 * i < lines ? cv[i] : 0;
     }
   }
   if (tid < lines) {  // (at most 512 lines)
     z = __uint_as_float(f.line[(int64_t)tid * words + 2 * a.E]);
     n = (int)f.line[(int64_t)tid * words + 2 * a.E + 1];
   }
-  sp[s][c] = p;
-  sc[s][c] = cnt;
+  for (int x = 16; x < 64; x <<= 1) {
+    p += __shfl_xor(p, x, 64);
+    cnt += __shfl_xor(cnt, x, 64);
+  }
   for (int x = 1; x < 64; x <<= 1) {
     z += __shfl_xor(z, x, 64);
     n += __shfl_xor(n, x, 64);
   }
-  if (c == 0) {
-    szw[s] = z;
-    snw[s] = n;
+  if (lane < FINAL_COLS) {
+    sp[w][c] = p;
+    sc[w][c] = cnt;
+  }
+  if (lane == 0) {
+    szw[w] = z;
+    snw[w] = n;
   }
   __syncthreads();
-  if (s > 0) return;
+  if (tid >= 16) return;
   p = z = 0.f;
   cnt = n = 0;
   for (int x = 0; x < 16; ++x) {
@@ -290,26 +340,20 @@ k_balance_final(Fwd f, int lines) {
     a.counts[e] = cnt;
     dot = (float)cnt * (p * per);
   }
-  dot = wave_sum(dot);
-  const float scale = per * ((float)a.E / (float)a.K);
-  if (c == 0) {
-    last = true;
-    if (gridDim.x > 1) {
-      __hip_atomic_store(&f.tail[blockIdx.x], __float_as_uint(dot), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = __hip_atomic_fetch_add(&f.tail[TAIL_WORDS - 1], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-             gridDim.x - 1;
-      if (last) {
-        dot = 0.f;
-        for (unsigned x = 0; x < gridDim.x; ++x)
-          dot += __uint_as_float(__hip_atomic_load(&f.tail[x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-      }
-    }
-    if (last) {
-      a.tokens[0] = n;
-      a.loss[0] = dot * scale;
-      a.loss[1] = z * per;
-    }
+  dot = sum16(dot);
+  if (c > 0) return;
+  if (gridDim.x > 1) {
+    __hip_atomic_store(&f.tail[blockIdx.x], __float_as_uint(dot), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__hip_atomic_fetch_add(&f.tail[TAIL_WORDS - 1], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) != gridDim.x - 1)
+      return;
+    dot = 0.f;
+#pragma unroll 8
+    for (unsigned x = 0; x < gridDim.x; ++x)
+      dot += __uint_as_float(__hip_atomic_load(&f.tail[x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
   }
+  a.tokens[0] = n;
+  a.loss[0] = dot * per * ((float)a.E / (float)a.K);
+  a.loss[1] = z * per;
 }
 
 struct Bwd {
@@ -323,25 +367,16 @@ k_balance_bwd(Bwd f) {
   constexpr int U = R * V <= 8 ? 2 : 1;
   const BalanceBwdArgs& a = f.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int L = 1 << f.logL, rows = 64 >> f.logL, j = lane & (L - 1), base = lane & ~(L - 1);
-  const int n = a.tokens[0];
-  const float per = n > 0 ? 1.f / (float)n : 0.f;
-  const float gb = a.d_loss[0] * (per * per * ((float)a.E / (float)a.K)), gz = a.d_loss[1] * 2.f * per;
-  float cf[R][V];  // what the balance loss gains by a probability
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = ((r << f.logL) + j) * V + v;
-      cf[r][v] = c < a.E ? gb * (float)a.counts[c] : 0.f;
-    }
+  const int L = 1 << f.logL, rows = 64 >> f.logL, j = lane & (L - 1);
+  __shared__ __attribute__((aligned(16))) int cols[GATES ? 4 * 64 * V * R : 1];
+  volatile int* const own = cols + (GATES ? w * 64 * V * R : 0);  // this wave's rows, as bits
   const int64_t units = ((int64_t)a.T + rows - 1) / rows;
   const int64_t step = (int64_t)gridDim.x * 4;
-  for (int64_t u0 = (int64_t)blockIdx.x * 4 + w; u0 < units; u0 += U * step) {
-    float z[U][R][V], lse[U];
-    int t[U], id[U];
-    float gt[U], dg[U];
-    bool there[U];
+  float z[U][R][V], lse[U], gt[U], dg[U];
+  int t[U], id[U];
+  bool there[U];
+  int64_t u0 = (int64_t)blockIdx.x * 4 + w;
+  auto load = [&] {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int64_t row = min(u0 + i * step, units - 1) * rows + (lane >> f.logL);
@@ -364,84 +399,132 @@ k_balance_bwd(Bwd f) {
         id[i] = a.idx[at];
         gt[i] = a.gate[at];
         dg[i] = a.d_gate[at];
+      }
+    }
+  };
+  if (u0 < units) load();
+  if constexpr (GATES)
+    for (int i = lane; i < 64 * V * R; i += 64) own[i] = 0;
+  const int n = a.tokens[0];
+  const float per = n > 0 ? 1.f / (float)n : 0.f;
+  const float gb = a.d_loss[0] * (per * per * ((float)a.E / (float)a.K)), gz = a.d_loss[1] * 2.f * per;
+  float cf[R][V];  // what the balance loss gains by a probability
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = ((r << f.logL) + j) * V + v;
+      cf[r][v] = c < a.E ? gb * (float)a.counts[c] : 0.f;
+    }
+  while (u0 < units) {
+    if constexpr (GATES) {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
         if (j >= a.K || (unsigned)id[i] >= (unsigned)a.E) {
           id[i] = -1;
           gt[i] = dg[i] = 0.f;
         }
+    }
+    bool counting[U], coarse[U], any = false;
+    float p[U][R][V], s[U], inner[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      counting[i] = lse[i] != NEG_INF;
+      // A large lse is too coarse a number for that (a row masked by its type's lowest
+      // value throughout has lse = -3.4e38 and equal p): those rows normalise again.
+      coarse[i] = counting[i] && fabsf(lse[i]) > 32.f;
+      any |= coarse[i];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p[i][r][v] = counting[i] ? __expf(z[i][r][v] - lse[i]) : 0.f;
+    }
+    if (__any(any)) {
+      float m[U], sum[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        m[i] = NEG_INF;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int v = 0; v < V; ++v) m[i] = max_nan(m[i], z[i][r][v]);
       }
+      row_max(m, f.logL);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        sum[i] = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int v = 0; v < V; ++v) sum[i] += __expf(z[i][r][v] - m[i]);
+      }
+      row_sum(sum, f.logL);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int v = 0; v < V; ++v) p[i][r][v] = coarse[i] ? __expf(z[i][r][v] - m[i]) / sum[i] : p[i][r][v];
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const bool counting = lse[i] != NEG_INF;
-      float p[R][V], s = 0.f;
+      s[i] = 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int v = 0; v < V; ++v) p[r][v] = counting ? __expf(z[i][r][v] - lse[i]) : 0.f;
-      // A large lse is too coarse a number for that (a row masked by its type's lowest
-      // value throughout has lse = -3.4e38 and equal p): those rows normalise again.
-      const bool coarse = counting && fabsf(lse[i]) > 32.f;
-      if (__any(coarse)) {
-        float m = NEG_INF, q[R][V], sum = 0.f;
+        for (int v = 0; v < V; ++v) s[i] = fmaf(p[i][r][v], cf[r][v], s[i]);
+    }
+    row_sum(s, f.logL);
+    if constexpr (GATES) {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int v = 0; v < V; ++v) m = fmaxf(m, z[i][r][v]);
-        m = row_max(m, L);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            q[r][v] = __expf(z[i][r][v] - m);
-            sum += q[r][v];
-          }
-        sum = row_sum(sum, L);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int v = 0; v < V; ++v) p[r][v] = coarse ? q[r][v] / sum : p[r][v];
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int v = 0; v < V; ++v) s = fmaf(p[r][v], cf[r][v], s);
-      s = row_sum(s, L);
-      const float add = counting ? gz * lse[i] - s : 0.f;
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int v = 0; v < V; ++v) p[r][v] *= cf[r][v] + add;
-      if constexpr (GATES) {
+      for (int i = 0; i < U; ++i) {
         // the choices lie across the row's lanes, L at a time
-        float inner = gt[i] * dg[i];
+        inner[i] = gt[i] * dg[i];
         for (int k = j + L; k < a.K; k += L) {
           const int64_t at = (int64_t)t[i] * a.K + k;
-          if ((unsigned)a.idx[at] < (unsigned)a.E) inner = fmaf(a.gate[at], a.d_gate[at], inner);
+          if ((unsigned)a.idx[at] < (unsigned)a.E) inner[i] = fmaf(a.gate[at], a.d_gate[at], inner[i]);
         }
-        inner = row_sum(inner, L);
-        for (int k0 = 0; k0 < a.K; k0 += L) {
-          int e = id[i];
-          float g = gt[i], d = dg[i];
-          if (k0 > 0) {
-            const int64_t at = (int64_t)t[i] * a.K + k0 + j;
-            e = k0 + j < a.K ? a.idx[at] : -1;
-            g = d = 0.f;
-            if ((unsigned)e < (unsigned)a.E) {
-              g = a.gate[at];
-              d = a.d_gate[at];
-            }
+      }
+      row_sum(inner, f.logL);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const float add = counting[i] ? gz * lse[i] - s[i] : 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p[i][r][v] *= cf[r][v] + add;
+      if constexpr (GATES) {
+        // A row's choices are few and lie in one lane each: they go to their columns through
+        // the row's words in LDS, zeros but for this.  (Every lane comparing its columns
+        // with every choice took 190 instructions a row in place of 80.)
+        // (volatile: other lanes of the wave read what one wrote, in order)
+        volatile int* const row = own + (lane >> f.logL << f.logL) * (V * R);
+        bool one = a.K <= L;
+        if (one) {  // an expert chosen twice?  (whose sum's order a write would not keep)
+          if (id[i] >= 0) row[id[i]] = j;
+          one = !__any(id[i] >= 0 && row[max(id[i], 0)] != j);
+        }
+        if (one) {
+          if (id[i] >= 0) row[id[i]] = __float_as_int(gt[i] * (dg[i] - inner[i]));
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const volatile int* from = row + ((r << f.logL) + j) * V;
+#pragma unroll
+            for (int v = 0; v < V; ++v) p[i][r][v] += __int_as_float(from[v]);
           }
-          const float val = g * (d - inner);
-          const int most = min(L, a.K - k0);
-          for (int k = 0; k < most; ++k) {
-            const int ek = __shfl(e, base + k, 64);
-            const float vk = __shfl(val, base + k, 64);
-            const int at = ek - j * V;  // its place among this lane's columns
+          if (id[i] >= 0) row[id[i]] = 0;
+        } else {
+          if (a.K <= L && id[i] >= 0) row[id[i]] = 0;
+          for (int k = 0; k < a.K; ++k) {
+            const int64_t at = (int64_t)t[i] * a.K + k;
+            const int e = a.idx[at];
+            const float val = (unsigned)e < (unsigned)a.E ? a.gate[at] * (a.d_gate[at] - inner[i]) : 0.f;
+            const int to = (unsigned)e < (unsigned)a.E ? e - j * V : -1;  // its place among this lane's columns
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
-              for (int v = 0; v < V; ++v)
-                if (at == (r << f.logL) * V + v) p[r][v] += vk;
+              for (int v = 0; v < V; ++v) p[i][r][v] += to == (r << f.logL) * V + v ? val : 0.f;
           }
         }
       }
@@ -450,10 +533,12 @@ k_balance_bwd(Bwd f) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const int c = ((r << f.logL) + j) * V;
-          if (c < a.E) store_vec<T, V>(o + c, p[r]);
+          if (c < a.E) store_vec<T, V>(o + c, p[i][r]);
         }
       }
     }
+    u0 += U * step;
+    if (u0 < units) load();
   }
 }
 
@@ -490,7 +575,8 @@ hipError_t by_shape(int E, int dtype, int V, F f) {
   return V == 8 ? by_vectors<bf16_t, 8>(E, f) : V == 4 ? by_vectors<bf16_t, 4>(E, f) : by_vectors<bf16_t, 1>(E, f);
 }
 
-// Few logits: one workgroup, one launch.
+// Few logits: one workgroup, one launch.  us a call, one workgroup / two launches: 512 x 32
+// 7.3 / 9.3, 512 x 48 11.4 / 9.7, 2048 x 16 11.1 / 9.1, 1024 x 64 19.5 / 10.1.
 bool one_block(int T, int E) { return (int64_t)T * E <= 16384; }
 
 }  // namespace
@@ -514,9 +600,9 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
       return hipGetLastError();
     }
     const int64_t units = ((int64_t)a.T + (64 >> log_l) - 1) / (64 >> log_l);
-    const int grid = (int)std::min<int64_t>(FWD_BLOCKS, (units + 3) / 4);
-    hipLaunchKernelGGL((k_balance<T, V, R, 4, false>), dim3(grid), dim3(256), 0, st, f);
-    hipLaunchKernelGGL(k_balance_final, dim3((a.E + 63) / 64), dim3(1024), 0, st, f, grid);
+    const int grid = (int)std::min<int64_t>(FWD_BLOCKS, (units + 7) / 8);
+    hipLaunchKernelGGL((k_balance<T, V, R, 8, false>), dim3(grid), dim3(512), 0, st, f);
+    hipLaunchKernelGGL(k_balance_final, dim3((a.E + FINAL_COLS - 1) / FINAL_COLS), dim3(1024), 0, st, f, grid);
     return hipGetLastError();
   });
 }
