@@ -105,8 +105,8 @@ hipError_t launch_mxfp4_mm(const PlanArgs& p, const Mxfp4Args& m, hipStream_t st
     if (used <= 4 * (int64_t)m.E) return launch_thin<1, 2>(m.out, a, used, st);
     return launch_thin<2, 4>(m.out, a, used, st);
   }
-  if (m.out == MOE_BF16) return launch_tile<128, 256, 2, 2, bf16_t>(a, used, st);
-  return launch_tile<128, 256, 2, 2, float>(a, used, st);
+  if (m.out == MOE_BF16) return launch_tile<128, 256, 1, 4, bf16_t>(a, used, st);
+  return launch_tile<128, 256, 1, 4, float>(a, used, st);
 }
 
 }  // namespace moe
