@@ -37,18 +37,31 @@ __device__ __forceinline__ bf16x8_v values(uint32_t w, uint32_t scale) {
   return bf16x8_v{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
 }
 
+// the value of lane p (of 0..15) in the lanes p, 16 + p, 32 + p and 48 + p
+__device__ __forceinline__ uint32_t from_first_row(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(a[0], a[0], false, false);
+  return b[0];
+}
+
 // ---------------------------------------------------------------------------
-// Few rows per expert (decode): the weights' bytes are the work, every touched
-// expert's are read once, straight into registers.  A workgroup takes 16 RT rows of a
-// segment and 16 FN columns; its four waves split the reduction (chunks of 256: wave w
-// takes w, w + 4, ...) and add up their sums in wave order.  A lane's 16 bytes of
-// codes are one block of 32 and have one scale.
+// Few rows per expert (decode): the weights' bytes are the work, every touched expert's
+// are read once, straight into registers, the next chunk's during this one's products.  A
+// workgroup takes 16 rows of a segment and 16 FN columns; its four waves split the
+// reduction (chunks of 256: wave w takes w, w + 4, ...) and add up their sums in wave
+// order.  A lane's 16 bytes of codes are one block of 32 and have one scale.
+//   Next to those bytes the L1 bounds it: one access per cycle, 16 bytes where
+// neighbouring lanes read different lines.  So the rows go through LDS, 512
+// contiguous bytes of each per chunk, and scales are read as 8 bytes per column by the
+// lanes 0..15, who tell the others (both straight into the lanes that use them: 16 rows
+// for each of 64 experts of 2048 x 2048 47 us in place of 40).
 // ---------------------------------------------------------------------------
-template <int RT, int FN, typename O>
+template <int FN, typename O>
 __global__ void __launch_bounds__(256)
 k_mxfp4_thin(Args g) {
-  constexpr int BN = 16 * FN, BM = 16 * RT;
-  __shared__ float part[3][RT][FN][64][4];
+  constexpr int W = 4, BN = 16 * FN, BM = 16, ROW = 512, ROWS = BM * ROW;
+  __shared__ __attribute__((aligned(1024))) char rows_lds[W][ROWS];
+  __shared__ float part[W - 1][FN][64][4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int NT = (g.N + BN - 1) / BN;
@@ -58,13 +71,9 @@ k_mxfp4_thin(Args g) {
 
   const int p = lane & 15, h = lane >> 4;
   const int kb = g.K / 32, chunks = (kb + 7) / 8;
-  // rows and columns past the end repeat the last one (their results are dropped)
-  int64_t row[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    row[r] = row0 + min(16 * r + p, rows - 1);
-    if (g.row_token) row[r] = g.row_token[row[r]];
-  }
+  int token = p;
+  if (g.row_token) token = g.row_token[row0 + min(p, rows - 1)];
+  // columns past the end repeat the last one (their results are dropped)
   const uint8_t *pq[FN], *ps[FN];
 #pragma unroll
   for (int i = 0; i < FN; ++i) {
@@ -72,95 +81,106 @@ k_mxfp4_thin(Args g) {
     pq[i] = g.q + n * (g.K / 2);
     ps[i] = g.s + n * kb;
   }
-  // Chunk k's loads: none under a condition; past the reduction they read the first
-  // block again, and the rows' values become zeros.
-  uint4 rq[2][FN], ra[2][RT][4];
-  uint32_t rs[2][FN];
+  struct Codes {
+    uint4 q[2][FN];
+    uint2 s[FN];
+  };
+  Codes cur, ahead;
   auto block = [&](int k, int c) { return 8 * k + 4 * c + h; };
-  auto load_q = [&](int k) {
+  // chunk k; past the reduction the first block's codes again, where the rows are zeros
+  auto load_q = [&](int k, Codes& d) {
+    if (lane < 16) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        if (8 * k + 8 <= kb) {
+          __builtin_memcpy(&d.s[i], ps[i] + 8 * k, 8);
+        } else {
+          uint32_t v[2] = {0, 0};
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            if (8 * k + y < kb) v[y >> 2] |= (uint32_t)ps[i][8 * k + y] << (8 * (y & 3));
+          d.s[i] = make_uint2(v[0], v[1]);
+        }
+      }
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int b = block(k, c) < kb ? block(k, c) : 0;
 #pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        rq[c][i] = *reinterpret_cast<const uint4*>(pq[i] + 16 * (int64_t)b);
-        rs[c][i] = ps[i][b];
-      }
+      for (int i = 0; i < FN; ++i) d.q[c][i] = *reinterpret_cast<const uint4*>(pq[i] + 16 * (int64_t)b);
     }
   };
-  load_q(w < chunks ? w : 0);  // (on the way while the tokens arrive)
+  load_q(w < chunks ? w : 0, cur);  // (on the way while the tokens arrive)
   __builtin_amdgcn_sched_barrier(0);
-  const bf16_t* pa[RT];
-  bool real[RT];
+  // Rows: lane l loads 16 bytes (unit l mod 32, xored with the row for the banks) of the
+  // rows l / 32, 2 + l / 32, ...; rows past the end and tokens that do not exist are zeros.
+  const int known = g.row_token ? g.a_rows : rows;
+  const __amdgpu_buffer_rsrc_t ra =
+      rsrc(g.row_token ? g.a : g.a + (int64_t)row0 * g.K, (uint32_t)known * (uint32_t)g.K * 2u);
+  uint32_t oa[ROWS / 1024];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    // a token that does not exist counts as zeros
-    real[r] = (uint64_t)row[r] < (uint64_t)g.a_rows;
-    pa[r] = g.a + (real[r] ? row[r] : 0) * g.K;
+  for (int i = 0; i < ROWS / 1024; ++i) {
+    const int r = 2 * i + (lane >> 5);
+    const uint32_t at = (uint32_t)__shfl(token, r, 64);
+    oa[i] = r < rows && at < (uint32_t)known ? at * (uint32_t)g.K * 2u + (((uint32_t)lane & 31u) ^ (r & 7)) * 16u : OOB;
   }
   auto load_a = [&](int k) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (what lay there has been read)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const bool there = block(k, c) < kb;
-      const int b = there ? block(k, c) : 0;
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint4 v = reinterpret_cast<const uint4*>(pa[r] + 32 * (int64_t)b)[x];
-          ra[c][r][x] = there && real[r] ? v : make_uint4(0, 0, 0, 0);
-        }
+    for (int i = 0; i < ROWS / 1024; ++i) {
+      const int unit = (lane & 31) ^ ((2 * i + (lane >> 5)) & 7);
+      load16_lds(ra, rows_lds[w] + 1024 * i, 32 * k + unit < 4 * kb ? oa[i] : OOB, (uint32_t)k * ROW);
     }
+    asm volatile("" ::: "memory");
   };
+  const char* const mine = rows_lds[w] + p * ROW;
 
-  f32x4_v acc[RT][FN];
+  f32x4_v acc[FN];
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int i = 0; i < FN; ++i) acc[r][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
-  for (int k = w; k < chunks; k += 4) {
-    if (k > w) load_q(k);
+  for (int i = 0; i < FN; ++i) acc[i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  for (int k = w; k < chunks; k += W) {
     load_a(k);
+    if (k + W < chunks) {
+      load_q(k + W, ahead);
+      wait_vm<3 * FN>();  // all but those
+    } else {
+      wait_vm<0>();
+    }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const bool there = block(k, c) < kb;
+      bf16x8_v a[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        a[x] = *reinterpret_cast<const bf16x8_v*>(mine + ((16 * c + 4 * h + x) ^ (p & 7)) * 16);
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
-        const uint32_t sc = there ? rs[c][i] : 127u;  // (zeros times a NaN would not be zeros)
-        const uint32_t words[4] = {rq[c][i].x, rq[c][i].y, rq[c][i].z, rq[c][i].w};
+        const uint32_t four = from_first_row(c ? cur.s[i].y : cur.s[i].x);
+        const uint32_t sc = there ? (four >> (8 * h)) & 255u : 127u;  // (zeros times a NaN would not be zeros)
+        const uint32_t words[4] = {cur.q[c][i].x, cur.q[c][i].y, cur.q[c][i].z, cur.q[c][i].w};
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const bf16x8_v b = values(words[x], sc);
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, __builtin_bit_cast(bf16x8_v, ra[c][r][x]), acc[r][i], 0, 0, 0);
-        }
+        for (int x = 0; x < 4; ++x)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values(words[x], sc), a[x], acc[i], 0, 0, 0);
       }
     }
+    cur = ahead;
   }
   if (w > 0)
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int i = 0; i < FN; ++i) *reinterpret_cast<f32x4_v*>(part[w - 1][r][i][lane]) = acc[r][i];
+    for (int i = 0; i < FN; ++i) *reinterpret_cast<f32x4_v*>(part[w - 1][i][lane]) = acc[i];
   __syncthreads();
-  if (w > 0) return;
+  if (w > 0 || p >= rows) return;
+  O* out = reinterpret_cast<O*>(g.c) + ((int64_t)row0 + p) * g.N;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int m = 16 * r + p;
-    if (m >= rows) continue;
-    O* out = reinterpret_cast<O*>(g.c) + ((int64_t)row0 + m) * g.N;
+  for (int i = 0; i < FN; ++i) {
+    f32x4_v v = acc[i];
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      f32x4_v v = acc[r][i];
-#pragma unroll
-      for (int x = 0; x < 3; ++x) v += *reinterpret_cast<const f32x4_v*>(part[x][r][i][lane]);
-      const int c = n0 + 16 * i + 4 * h;
-      if (c >= g.N) continue;
-      if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(out + c) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
-      else *reinterpret_cast<float4*>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
-    }
+    for (int x = 0; x < W - 1; ++x) v += *reinterpret_cast<const f32x4_v*>(part[x][i][lane]);
+    const int c = n0 + 16 * i + 4 * h;
+    if (c >= g.N) continue;
+    if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(out + c) = make_uint2(f2bf2(v[0], v[1]), f2bf2(v[2], v[3]));
+    else *reinterpret_cast<float4*>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -169,7 +189,9 @@ k_mxfp4_thin(Args g) {
 // reduction: 128 bytes of every row and 32 of every column's codes go straight into
 // LDS, three stages in turn.  Scales: 16 bytes of every column, eight stages' worth, go
 // there through registers, a thread per column (byte by byte into the lanes that use
-// them they were more than half of the loads, 1580 us in place of 1170 with 131072 rows, 64 experts of 2048 x 2048).
+// them they were more than half of the loads, 1580 us in place of 1170 with 131072 rows,
+// 64 experts of 2048 x 2048; 938 us today, 1170 TFLOP/s, where the clock gives way before
+// the matrix cores are full).
 // ---------------------------------------------------------------------------
 template <int BM, int BN, int WM, int WN>
 struct Cfg {

@@ -63,13 +63,16 @@ k_mxfp4_weights(const T* w, uint8_t* q, uint8_t* s, int K, int N) {
   s[at] = (uint8_t)code;
 }
 
-int64_t row_tiles(const f4::Args& a, int64_t used, int BM) { return div_up(used, BM) + std::min<int64_t>(a.E, used); }
+// at most so many tiles of BM rows have a row
+int64_t row_tiles(const f4::Args& a, int64_t used, int BM) {
+  return std::min(used, div_up(used, BM) + std::min<int64_t>(a.E, used));
+}
 
-template <int RT, int FN>
+template <int FN>
 hipError_t launch_thin(int out, const f4::Args& a, int64_t used, hipStream_t st) {
-  const int64_t tiles = row_tiles(a, used, 16 * RT) * div_up(a.N, 16 * FN);
-  if (out == MOE_BF16) hipLaunchKernelGGL((f4::k_mxfp4_thin<RT, FN, bf16_t>), dim3((unsigned)tiles), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((f4::k_mxfp4_thin<RT, FN, float>), dim3((unsigned)tiles), dim3(256), 0, st, a);
+  const dim3 grid((unsigned)(row_tiles(a, used, 16) * div_up(a.N, 16 * FN)));
+  if (out == MOE_BF16) hipLaunchKernelGGL((f4::k_mxfp4_thin<FN, bf16_t>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((f4::k_mxfp4_thin<FN, float>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -83,6 +86,11 @@ hipError_t launch_tile(const f4::Args& a, int64_t used, hipStream_t st) {
   const int64_t tiles = row_tiles(a, used, BM) * div_up(a.N, BN);
   hipLaunchKernelGGL(k, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(C::NTH), C::SMEM, st, a);
   return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN>
+hipError_t launch_tile(int out, const f4::Args& a, int64_t used, hipStream_t st) {
+  return out == MOE_BF16 ? launch_tile<BM, BN, WM, WN, bf16_t>(a, used, st) : launch_tile<BM, BN, WM, WN, float>(a, used, st);
 }
 
 }  // namespace
@@ -101,12 +109,25 @@ hipError_t launch_mxfp4_mm(const PlanArgs& p, const Mxfp4Args& m, hipStream_t st
   a.row_token = m.gather ? p.row_token : nullptr;
   a.a_rows = m.a_rows; a.rows = m.rows; a.E = m.E; a.K = m.K; a.N = m.N;
   const int64_t used = m.rows_used;
-  if (used <= 16 * (int64_t)m.E && row_tiles(a, used, 16) * div_up(a.N, 32) < (1 << 24)) {
-    if (used <= 4 * (int64_t)m.E) return launch_thin<1, 2>(m.out, a, used, st);
-    return launch_thin<2, 4>(m.out, a, used, st);
+  // Thin tiles read an expert's weights once per 16 rows; the others' time is at least
+  // their stages', however few they are.  So thin up to 16 rows per expert, and while
+  // there is little to compute.  Measured, thin and tiles of 64 (us):
+  //   64 experts of 2048 x 2048, 16 rows each 40 and 47, 24 54 and 49
+  //   128 experts of 1536 x 512, 16 rows each 20 and 28, 32 31 and 30
+  //   8 experts of 736 x 1040, 400 rows (416000) 8.2 and 12.6, 1600 (1664000) 23 and 14
+  //   one of 2048 x 2048, 256 rows (524288) 11 and 26, 1024 (2097152) 31 and 28
+  if (used <= 16 * (int64_t)a.E || used * a.N <= (1 << 20)) {
+    // under half a workgroup of 64 columns per CU: workgroups of 16 (one row, 7168 x 4096
+    // 8.4 us in place of 13.7; 64 of 2048 x 2048 7.9 in place of 7.5)
+    if (row_tiles(a, used, 16) * div_up(a.N, 64) < cu_count(device()) / 2) return launch_thin<1>(m.out, a, used, st);
+    return launch_thin<4>(m.out, a, used, st);
   }
-  if (m.out == MOE_BF16) return launch_tile<128, 256, 1, 4, bf16_t>(a, used, st);
-  return launch_tile<128, 256, 1, 4, float>(a, used, st);
+  // Rows of 64 or 128 (us): 64 experts of 2048 x 2048, 128 rows each 97 and 109, 512 286 and 275,
+  // 2048 1124 and 973; 128 experts of 1536 x 512, 256 rows each 68 and 73, 1024 228 and 204.
+  // Under four tiles of 128 per CU too: one of 2048 x 2048, 1024 rows 28 and 40, 8192 80 and 91.
+  if (used <= 256 * (int64_t)a.E || row_tiles(a, used, 128) * div_up(a.N, 256) <= 4 * cu_count(device()))
+    return launch_tile<64, 256, 1, 4>(m.out, a, used, st);
+  return launch_tile<128, 256, 1, 4>(m.out, a, used, st);
 }
 
 }  // namespace moe
