@@ -139,12 +139,12 @@ hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
 // stages ahead; many: large ones, which load least.  A whole call, us, with 64 x 64
 // tiles (four stage buffers) / 128 x 128 (two; with four 128 x 128 is no faster than either) /
 // 256 x 256:
-//   bf16   1 x 512 x 512 162 / 327 / 769          fp32   1 x 512 x 512 167 / 338 / 807
-//          4 x 1024 x 1024 525 / 571 / 1246              16 x 512 x 1024 523 / 505 / 1010
-//          64 x 256 x 1536 346 / 374 / 612               64 x 256 x 1536 901 / 913 / 1275
-//          24 x 720 x 1040 1045 / 890 / 1297             24 x 720 x 1040 1466 / 1197 / 1601
-//          32 x 1024 x 1024 - / 2657 / 2977              16 x 2048 x 2048 - / 8802 / 8868
-//          64 x 2048 x 2048 - / 32222 / 30367            64 x 2048 x 2048 - / 34278 / 32976
+//   bf16   1 x 512 x 512 156 / 302 / 629          fp32   1 x 512 x 512 164 / 318 / 685
+//          4 x 1024 x 1024 538 / 541 / 1075              16 x 512 x 1024 492 / 461 / 878
+//          64 x 256 x 1536 322 / 327 / 476               64 x 256 x 1536 853 / 827 / 1103
+//          24 x 720 x 1040 1034 / 823 / 1145             24 x 720 x 1040 1407 / 1099 / 1451
+//          32 x 1024 x 1024 - / 2574 / 2740              16 x 2048 x 2048 - / 8599 / 8579
+//          64 x 2048 x 2048 - / 30632 / 28640            64 x 2048 x 2048 - / 33275 / 31525
 template <int PA, int PB, bool FINE, Epi EPI, typename O>
 hipError_t gemm_by_size(const Args& a, hipStream_t st) {
   auto tiles = [&](int B) {

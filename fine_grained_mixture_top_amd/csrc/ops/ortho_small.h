@@ -60,22 +60,6 @@ __device__ __forceinline__ f32x4_v get(const char* m, uint32_t at) {
   return v;
 }
 
-// Four neighbouring lanes hold four numbers each, a 4 x 4 block of 16-bit values by rows;
-// by columns afterwards.
-__device__ __forceinline__ f16x4_v turn4(const f16x4_v v, int lane) {
-  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-  const u32x2_t d = __builtin_bit_cast(u32x2_t, v);
-  auto swap1 = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 15, 15, true); };  // lane ^ 1
-  auto swap2 = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 15, 15, true); };  // lane ^ 2
-  const uint32_t o0 = swap1(d[0]), o1 = swap1(d[1]);
-  // columns 0 and 2 of two rows in even lanes, 1 and 3 in odd ones
-  const uint32_t pick = lane & 1 ? 0x03020706u : 0x05040100u;
-  const uint32_t e0 = __builtin_amdgcn_perm(o0, d[0], pick), e1 = __builtin_amdgcn_perm(o1, d[1], pick);
-  const bool high = lane & 2;
-  const uint32_t got = swap2(high ? e0 : e1);
-  return __builtin_bit_cast(f16x4_v, high ? u32x2_t{got, e1} : u32x2_t{e0, got});
-}
-
 // A piece on or below the diagonal of a symmetric matrix, and its mirror.  (Products of
 // matrices that commute are symmetric up to their rounding, and what is not would grow
 // with the steps: 63 x 65, five steps, error 3.7e-2 with both halves as computed.)
