@@ -112,19 +112,20 @@ hipError_t launch_mxfp4_mm(const PlanArgs& p, const Mxfp4Args& m, hipStream_t st
   // Thin tiles read an expert's weights once per 16 rows; the others' time is at least
   // their stages', however few they are.  So thin up to 16 rows per expert, and while
   // there is little to compute.  Measured, thin and tiles of 64 (us):
-  //   64 experts of 2048 x 2048, 16 rows each 40 and 47, 24 54 and 49
-  //   128 experts of 1536 x 512, 16 rows each 20 and 28, 32 31 and 30
-  //   8 experts of 736 x 1040, 400 rows (416000) 8.2 and 12.6, 1600 (1664000) 23 and 14
-  //   one of 2048 x 2048, 256 rows (524288) 11 and 26, 1024 (2097152) 31 and 28
+  //   64 experts of 2048 x 2048, 16 rows each 42 and 47, 24 54 and 49
+  //   128 experts of 1536 x 512, 16 rows each 21 and 28, 32 32 and 29
+  //   8 experts of 736 x 1040, 400 rows (416000) 8.4 and 12.8, 1600 (1664000) 24 and 14
+  //   one of 2048 x 2048, 256 rows (524288) 10 and 25, 1024 (2097152) 28.5 and 25
   if (used <= 16 * (int64_t)a.E || used * a.N <= (1 << 20)) {
     // under half a workgroup of 64 columns per CU: workgroups of 16 (one row, 7168 x 4096
-    // 8.4 us in place of 13.7; 64 of 2048 x 2048 7.9 in place of 7.5)
+    // 8.6 us in place of 13.7; 64 of 2048 x 2048, where it is the other way, 8.0 and 7.9)
     if (row_tiles(a, used, 16) * div_up(a.N, 64) < cu_count(device()) / 2) return launch_thin<1>(m.out, a, used, st);
     return launch_thin<4>(m.out, a, used, st);
   }
-  // Rows of 64 or 128 (us): 64 experts of 2048 x 2048, 128 rows each 97 and 109, 512 286 and 275,
-  // 2048 1124 and 973; 128 experts of 1536 x 512, 256 rows each 68 and 73, 1024 228 and 204.
-  // Under four tiles of 128 per CU too: one of 2048 x 2048, 1024 rows 28 and 40, 8192 80 and 91.
+  // Tiles of 64 or 128 rows (us): 64 experts of 2048 x 2048, 128 rows each 92 and 100, 512 269
+  // and 254, 2048 1084 and 893; 128 experts of 1536 x 512, 256 rows each 63 and 67, 1024 208 and
+  // 193.  Up to four tiles of 128 per CU too: one of 2048 x 2048, 1024 rows 25 and 37, 8192 76
+  // and 88, 16384 132 and 135.
   if (used <= 256 * (int64_t)a.E || row_tiles(a, used, 128) * div_up(a.N, 256) <= 4 * cu_count(device()))
     return launch_tile<64, 256, 1, 4>(m.out, a, used, st);
   return launch_tile<128, 256, 1, 4>(m.out, a, used, st);
