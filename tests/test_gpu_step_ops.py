@@ -105,6 +105,25 @@ def test_balance(T, E, K, dtype, pad, masked, off):
     assert all(torch.equal(x, y) for x, y in zip(first, (b.counts, b.load, b.lse, b.loss)))
 
 
+@pytest.mark.parametrize("T,E,K", [(50, 12, 40), (20, 300, 200), (9, 5, 1024), (2500, 24, 33)])
+def test_balance_more_choices_than_lanes(T, E, K):
+    """Experts chosen many times by one token."""
+    g = gen(T)
+    z, idx = randn(g, T, E), torch.randint(-1, E + 1, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    b = ops.Balance(T, K, E)
+    ops.moe_balance(b, z, idx)
+    r = check_balance(b, z, idx, None)
+    d_loss, dz = torch.tensor([0.7, -0.3], device="cuda"), torch.empty_like(z)
+    gate, d_gate = torch.softmax(randn(g, T, K), 1), randn(g, T, K)
+    ops.moe_balance_bwd(b, z, d_loss, dz, idx, gate, d_gate)
+    want, bound = R.balance_bwd_ref(z, idx, r, d_loss, gate, d_gate)
+    # (up to K values join an element: rounding of every partial sum, none above the sum of magnitudes)
+    there = (idx >= 0) & (idx < E)
+    gd = torch.where(there, gate * d_gate.abs(), 0.0).double()
+    mag = torch.zeros_like(bound).scatter_add_(1, torch.where(there, idx, 0).long(), gd + gate.double() * gd.sum(1, keepdim=True))
+    R.within(dz, want, bound + K * 2.0 ** -23 * mag + want.abs() * 2.0 ** -24 + 1e-38, "dz")
+
+
 def test_balance_nothing_counts():
     b = ops.Balance(40, 2, 12)
     z = torch.full((40, 12), float("nan"), device="cuda")
@@ -498,6 +517,7 @@ MM = [  # T, K, E, align, drop, reduction, columns, result, gathered
     (1000, 2, 4, 1, 0.0, 224, 256, "f32", True), (129, 1, 1, 1, 0.0, 64, 272, "bf16", False), (4000, 3, 24, 1, 0.05, 512, 320, "bf16", True),
     (2500, 4, 1000, 1, 0.0, 128, 32, "bf16", True), (6000, 1, 2, 256, 0.0, 2048, 768, "f32", False), (50, 6, 1024, 1, 0.5, 64, 48, "f32", False),
     (700, 8, 64, 1, 0.0, 1056, 144, "bf16", True), (900, 8, 600, 1, 0.0, 96, 304, "bf16", True),
+    (9000, 1, 2, 1, 0.1, 160, 4112, "f32", True), (2300, 4, 2, 16, 0.0, 224, 4112, "bf16", False), (9100, 1, 1, 1, 0.0, 32, 4096, "bf16", False),
 ]
 
 
@@ -533,7 +553,7 @@ def test_mxfp4_mm_dense(rows, out):
     ops.moe_mxfp4_mm(None, torch.empty(0, 416, dtype=torch.bfloat16, device="cuda"), q, s, c[:0])
 
 
-@pytest.mark.parametrize("T", [4, 600])
+@pytest.mark.parametrize("T", [4, 600, 9000, 70000])
 def test_mxfp4_mm_keeps_what_is_not_finite_in_its_place(T):
     """NaN and infinity in a row stay in that row, a block without a number in its column and expert; scale
     codes from one end to the other; tokens that do not exist count as zeros."""
@@ -567,7 +587,7 @@ def test_mxfp4_mm_keeps_what_is_not_finite_in_its_place(T):
 def test_mxfp4_mm_captured_and_on_another_stream():
     """Decode through two products, captured: sort, product, product back; and a few hundred rows."""
     g = gen(31)
-    for T in (3, 500):
+    for T in (3, 500, 6000):
         E, K, d, n = 6, 2, 192, 96
         w1, w2 = quantized(weights(g, E, d, n)), quantized(weights(g, E, n, d))
         x, idx = randn(g, T, d, dtype=torch.bfloat16), torch.zeros(T, K, dtype=torch.int32, device="cuda")

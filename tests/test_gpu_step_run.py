@@ -1,0 +1,275 @@
+"""The operators of include/moe_step_ops.h as they are used together: steps of a
+small trained layer with MXFP4 experts, calls side by side on several streams, and
+tensors whose offsets pass 32 bits."""
+import pytest
+import torch
+
+from fine_grained_mixture_top_amd import ops
+
+import step_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def randn(g, *shape, dtype=torch.float32, std=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+class Layer:
+    """A router and experts of one product each: fp32 master weights, MXFP4 ones in the products, orthogonalised
+    updates, the router trained by its losses and its gates."""
+
+    def __init__(self, T, K, E, d, n, seed):
+        g = gen(seed)
+        self.T, self.K, self.E, self.d, self.n = T, K, E, d, n
+        self.router, self.w = randn(g, d, E, std=d ** -0.5), randn(g, E, d, n, std=d ** -0.5)
+        self.q = torch.empty(E, n, d // 2, dtype=torch.uint8, device="cuda")
+        self.s = torch.empty(E, n, d // 32, dtype=torch.uint8, device="cuda")
+        self.plan, self.bal = ops.Plan(T, K, E), ops.Balance(T, K, E)
+        self.ortho_r = ops.Ortho(1, d, E, dtype=torch.float32, scale=0.02)
+        self.ortho_w = ops.Ortho(E, d, n, dtype=torch.float32, scale=0.02)
+        self.d_loss = torch.tensor([0.01, 0.001], device="cuda")
+        cap, f = self.plan.cap, dict(device="cuda")
+        self.logits, self.dz = torch.empty(T, E, **f), torch.empty(T, E, **f)
+        self.gate, self.d_gate = torch.empty(T, K, **f), torch.empty(T, K, **f)
+        self.idx = torch.empty(T, K, dtype=torch.int32, **f)
+        self.y, self.dy, self.o = torch.zeros(cap, n, **f), torch.zeros(cap, n, **f), torch.empty(T, n, **f)
+        self.xp = torch.zeros(cap, d, dtype=torch.bfloat16, **f)
+        self.gw, self.uw = torch.empty_like(self.w), torch.empty_like(self.w)
+        self.gr, self.ur = torch.empty(1, d, E, **f), torch.empty(1, d, E, **f)
+
+    def forward(self, x, valid=None):
+        torch.mm(x.float(), self.router, out=self.logits)
+        self.logits[:, self.E - 1] = float("-inf")  # (an expert that is masked out: no rows, no gradient, no update)
+        best = torch.topk(self.logits, self.K, 1)
+        self.idx.copy_(best.indices)
+        self.gate.copy_(torch.softmax(best.values, 1))
+        if valid is not None:
+            self.idx.masked_fill_(~valid[:, None], -1)
+        ops.moe_sort(self.plan, self.idx)
+        ops.moe_balance(self.bal, self.logits, self.idx, valid)
+        ops.moe_mxfp4_quant_weights(self.w, self.q, self.s)
+        ops.moe_mxfp4_mm(self.plan, x, self.q, self.s, self.y, gather=True)
+        ops.moe_unpermute(self.plan, self.y, self.gate, self.o)
+
+    def backward(self, x, d_o, rows):
+        """rows: the rows of each expert, known to the caller."""
+        ops.moe_unpermute_bwd(self.plan, d_o, self.y, self.gate, self.dy, self.d_gate)
+        ops.moe_balance_bwd(self.bal, self.logits, self.d_loss, self.dz, self.idx, self.gate, self.d_gate)
+        torch.mm(x.float().t(), self.dz, out=self.gr[0])
+        ops.moe_permute(self.plan, x, self.xp)
+        for e, at in enumerate(rows):
+            torch.mm(self.xp[at].float().t(), self.dy[at], out=self.gw[e])
+        ops.moe_orthogonalize(self.ortho_r, self.gr, self.ur)
+        ops.moe_orthogonalize(self.ortho_w, self.gw, self.uw)
+        self.router -= self.ur[0]
+        self.w -= self.uw
+
+    def rows(self):
+        return [slice(o, o + c) for o, c in zip(self.plan.offsets.tolist(), self.plan.counts.tolist())]
+
+
+@pytest.mark.parametrize("T,K,E,d,n", [(96, 2, 5, 64, 48), (1500, 4, 12, 160, 112)])
+def test_steps_of_a_layer(T, K, E, d, n):
+    """Three steps; every stage of each against float64 from that stage's own inputs."""
+    g = gen(T)
+    layer = Layer(T, K, E, d, n, T + 1)
+    for step in range(3):
+        x, d_o = randn(g, T, d, dtype=torch.bfloat16), randn(g, T, n)
+        valid = torch.rand(T, generator=g, device="cuda") > 0.1
+        layer.forward(x, valid)
+        rows, token = layer.rows(), layer.plan.row_token.long()
+        # the choices, their losses
+        ref = R.balance_ref(layer.logits, layer.idx, valid)
+        assert layer.bal.counts.tolist() == ref["counts"].tolist() and int(layer.bal.tokens) == ref["n"]
+        assert layer.plan.counts.tolist() == ref["counts"].tolist()
+        steps = R.balance_steps(layer.logits) * 2.0 ** -23
+        R.within(layer.bal.load, ref["load"], ref["load"] * steps + 1e-38, "load")
+        # the experts
+        rq, rs = R.mxfp4_codes(layer.w)
+        assert torch.equal(layer.q, rq) and torch.equal(layer.s, rs)
+        y = torch.zeros(layer.plan.cap, n, dtype=torch.float64, device="cuda")
+        for e, at in enumerate(rows):
+            if at.stop > at.start:
+                w, a = R.mxfp4_values(layer.q[e], layer.s[e]), x[token[at]].double()
+                y[at] = a @ w.t()
+                R.within(layer.y[at], y[at], R.mxfp4_mm_bound(a, w, d, y[at], torch.float32), ("y", step, e))
+        # the gradients: fp32 sums of n, of the tokens
+        layer.backward(x, d_o, rows)
+        want, bound = R.balance_bwd_ref(layer.logits, layer.idx, ref, layer.d_loss, layer.gate, layer.d_gate)
+        R.within(layer.dz, want, bound + want.abs() * 2.0 ** -24 + 1e-38, ("dz", step))
+        # a choice's gate gradient is <d_o, y>
+        there = layer.idx >= 0
+        slot = torch.where(there, layer.plan.slot_row, 0).long()
+        dg = torch.where(there, (d_o.double()[:, None] * layer.y.double()[slot]).sum(2), 0.0)
+        mg = (d_o.double().abs()[:, None] * layer.y.double().abs()[slot]).sum(2)
+        R.within(layer.d_gate, dg, mg * (n + 8) * 2.0 ** -24 + 1e-38, ("d_gate", step))
+        # the updates, of the gradients as they are
+        for u, gw in ((layer.ur, layer.gr), (layer.uw, layer.gw)):
+            for e in range(gw.shape[0]):
+                want = R.ortho_ref(gw[e], 5, [R.QUINTIC] * 5, scale=0.02)
+                tol = R.ortho_tolerance(torch.float32, 5, [R.QUINTIC]) + 2.0 ** -24
+                assert float((u[e].double() - want).norm()) <= tol * float(want.norm()), (step, e)
+    # serving: single tokens through the weights of the last step
+    one = ops.Plan(1, K, E)
+    h = torch.zeros(one.cap, n, device="cuda")
+    for t in range(3):
+        ops.moe_sort(one, layer.idx[t:t + 1])
+        ops.moe_mxfp4_mm(one, x[t:t + 1], layer.q, layer.s, h, gather=True)
+        for k in range(K):
+            e, r = int(layer.idx[t, k]), int(one.slot_row[0, k])
+            if e >= 0:
+                w, a = R.mxfp4_values(layer.q[e], layer.s[e]), x[t:t + 1].double()
+                want = a @ w.t()
+                R.within(h[r:r + 1], want, R.mxfp4_mm_bound(a, w, d, want, torch.float32), (t, k))
+
+
+def test_gradient_of_the_losses_and_gates_against_differences():
+    """moe_balance_bwd with the gates of a real forward pass: central differences of the whole loss in float64, where
+    the choices do not change."""
+    T, K, E, d, n = 40, 2, 6, 64, 32
+    g = gen(3)
+    layer = Layer(T, K, E, d, n, 4)
+    x, d_o = randn(g, T, d, dtype=torch.bfloat16), randn(g, T, n)
+    layer.forward(x)
+    logits, idx, y = layer.logits.double(), layer.idx.long(), layer.y.double()
+    slot = layer.plan.slot_row.long()
+    layer.backward(x, d_o, layer.rows())
+    gb, gz = layer.d_loss.double().tolist()
+    f = layer.bal.counts.double()
+
+    def loss(z):
+        p = torch.softmax(z, 1)
+        gate = torch.softmax(z.gather(1, idx), 1)
+        o = (gate[..., None] * y[slot]).sum(1)
+        return (gb * E / (T * K) * (f * p.mean(0)).sum() + gz * (torch.logsumexp(z, 1) ** 2).mean() + (o * d_o.double()).sum())
+
+    h = 1e-4
+    for t in range(0, T, 7):
+        for e in range(E):
+            up, down = logits.clone(), logits.clone()
+            up[t, e] += h
+            down[t, e] -= h
+            want = float(loss(up) - loss(down)) / (2 * h)
+            # differences: h^2 / 6 of third derivatives, at most some units of the gates' part |d_o . y| < 100, and 1e-16 / h
+            # of a loss below 1e4; the kernel: 2^-16 of its terms, below 100 (balance_bwd_ref's bound is smaller)
+            assert abs(float(layer.dz[t, e]) - want) < 1e-6 + 2e-8 + 100 * 2.0 ** -16, (t, e)
+
+
+def test_calls_side_by_side():
+    """Handles of their own on three streams at once, many times: the results of one call after the other."""
+    g = gen(9)
+    T, E, K, d, n = 3000, 48, 4, 256, 320
+    z = randn(g, T, E)
+    idx = torch.topk(z, K, 1).indices.int()
+    gw = randn(g, 6, d, n, dtype=torch.bfloat16)
+    q = torch.randint(0, 256, (E, n, d // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.randint(118, 124, (E, n, d // 32), generator=g, device="cuda", dtype=torch.uint8)
+    x = randn(g, T, d, dtype=torch.bfloat16)
+    d_loss = torch.ones(2, device="cuda")
+
+    def handles():
+        plan = ops.Plan(T, K, E)
+        return (ops.Balance(T, K, E), torch.empty_like(z), ops.Ortho(6, d, n), torch.empty_like(gw), plan,
+                torch.zeros(plan.cap, n, dtype=torch.bfloat16, device="cuda"))
+
+    def run(h, streams):
+        b, dz, o, u, plan, c = h
+        ops.moe_balance(b, z, idx, stream=streams[0])
+        ops.moe_orthogonalize(o, gw, u, stream=streams[1])
+        ops.moe_sort(plan, idx, stream=streams[2])
+        ops.moe_balance_bwd(b, z, d_loss, dz, stream=streams[0])
+        ops.moe_mxfp4_mm(plan, x, q, s, c, gather=True, stream=streams[2])
+
+    want, sets = handles(), [handles() for _ in range(4)]
+    cur = torch.cuda.current_stream()
+    run(want, [cur] * 3)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    for i, h in enumerate(sets * 3):
+        run(h, [streams[(i % 4 + j) % 6] for j in range(3)])
+    torch.cuda.synchronize()
+    for h in sets:
+        for a, b in zip((h[0].loss, h[0].load, h[1], h[3], h[5]), (want[0].loss, want[0].load, want[1], want[3], want[5])):
+            assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+
+def test_balance_offsets_past_32_bits():
+    T, E, K = 2_200_000, 1024, 2
+    g = gen(1)
+    z = torch.empty(T, E, device="cuda").normal_(generator=g)
+    idx = torch.randint(0, E, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    b = ops.Balance(T, K, E)
+    ops.moe_balance(b, z, idx)
+    assert int(b.tokens) == T and torch.equal(b.counts.long(), torch.bincount(idx.flatten().long(), minlength=E))
+    ends = torch.cat([torch.arange(300), torch.arange(T // 2, T // 2 + 300), torch.arange(T - 300, T)]).cuda()
+    part = z[ends]
+    lse = torch.logsumexp(part.double(), 1)
+    R.within(b.lse[ends], lse, R.lse_bound(lse), "lse")
+    load = torch.zeros(E, dtype=torch.float64, device="cuda")
+    for at in range(0, T, 100_000):
+        load += torch.softmax(z[at:at + 100_000].double(), 1).sum(0)
+    load /= T
+    R.within(b.load, load, load * R.balance_steps(part) * 2.0 ** -23 * 2, "load")  # (twice: spread of `part` alone)
+    d_loss, dz = torch.tensor([1e9, 1e6], device="cuda"), torch.empty_like(z)
+    ops.moe_balance_bwd(b, z, d_loss, dz)
+    ref = dict(n=T, p=torch.softmax(part.double(), 1), counts=b.counts.long(), lse=lse,
+               counting=torch.ones(900, dtype=torch.bool, device="cuda"))
+    want, bound = R.balance_bwd_ref(part, idx[ends], ref, d_loss)
+    R.within(dz[ends], want, bound + want.abs() * 2.0 ** -24 + 1e-38, "dz")
+
+
+def test_orthogonalize_offsets_past_32_bits():
+    E, M, N = 520, 2048, 2080
+    w = torch.empty(E, M, N, dtype=torch.bfloat16, device="cuda").normal_(generator=gen(2))
+    o = torch.empty_like(w)
+    ops.moe_orthogonalize(ops.Ortho(E, M, N, steps=1), w, o)
+    tol = R.ortho_tolerance(w.dtype, 1, [R.QUINTIC]) + 2.0 ** -8
+    for e in (0, 503, 504, 505, E - 1):  # 504: past 2^31 numbers
+        want = R.ortho_ref(w[e], 1, [R.QUINTIC])
+        assert float((o[e].double() - want).norm()) <= tol * float(want.norm()), e
+
+
+@pytest.mark.parametrize("T", [3, 5000])
+def test_mxfp4_weights_past_32_bits(T):
+    """Codes past 2^32 bytes."""
+    E, d, N = 560, 4096, 4096
+    g = gen(T)
+    q = torch.randint(0, 256, (E, N, d // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.randint(118, 122, (E, N, d // 32), generator=g, device="cuda", dtype=torch.uint8)
+    idx = torch.tensor([0, 511, 512, 513, E - 1], device="cuda", dtype=torch.int32)[torch.arange(T, device="cuda") % 5].view(T, 1)
+    plan = ops.Plan(T, 1, E)
+    ops.moe_sort(plan, idx.contiguous())
+    x = randn(g, T, d, dtype=torch.bfloat16)
+    c = torch.zeros(plan.cap, N, device="cuda")
+    ops.moe_mxfp4_mm(plan, x, q, s, c, gather=True)
+    for t in (0, 1, 2, T - 2, T - 1):
+        e = int(idx[t])
+        w, a = R.mxfp4_values(q[e], s[e]), x[t:t + 1].double()
+        want = a @ w.t()
+        R.within(c[int(plan.slot_row[t, 0])][None], want, R.mxfp4_mm_bound(a, w, d, want, c.dtype), (t, e))
+
+
+def test_mxfp4_results_past_32_bits():
+    T, E, d, N = 560_000, 3, 32, 4096
+    g = gen(5)
+    q = torch.randint(0, 256, (E, N, d // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.randint(118, 122, (E, N, 1), generator=g, device="cuda", dtype=torch.uint8)
+    idx = torch.randint(0, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    plan = ops.Plan(T, 1, E)
+    ops.moe_sort(plan, idx)
+    x = randn(g, T, d, dtype=torch.bfloat16)
+    c = torch.zeros(plan.cap, N, dtype=torch.bfloat16, device="cuda")
+    ops.moe_mxfp4_mm(plan, x, q, s, c, gather=True)
+    offsets = plan.offsets.tolist()
+    for r in (0, offsets[1] - 1, offsets[1], 524287, 524288, 524289, T - 1):
+        e = sum(r >= o for o in offsets[1:E])
+        w, a = R.mxfp4_values(q[e], s[e]), x[int(plan.row_token[r])][None].double()
+        want = a @ w.t()
+        R.within(c[r][None], want, R.mxfp4_mm_bound(a, w, d, want, c.dtype), (r, e))
