@@ -116,17 +116,19 @@ __device__ __forceinline__ void wait_stages(int n) {
   wait_vm<N * L>();
 }
 
-// FINE: the two products with a lo, which are small, are summed apart and join the fp32
-// sums in one addition; a matrix instruction rounds its sum four times (eight products at
-// a time), so five roundings of a large sum take the place of twelve per 32 of the
-// reduction.  Error of five fp32 steps against 64 bits, without and with it: 2.0e-6 and
-// 1.5e-6 (1536 x 128; fp32 products 1.4e-6), 3.5e-6 and 2.3e-6 (720 x 1040; 2.4e-6); 4% of the time.
+// FINE: the two products with a lo, which are small, have sums of their own, added once at
+// the end; a matrix instruction rounds its sum four times (eight products at a time), so
+// four roundings of a large sum take the place of twelve per 32 of the reduction.  Error of
+// five fp32 steps of 720 x 1040 against 64 bits, without and with it: 3.5e-6 and 2.1e-6 (fp32
+// products 2.4e-6).  (The sums of every stage added
+// to the large ones instead: 2.3e-6, and vector instructions between the matrix ones, 1137 us in
+// place of 1069 for 24 of 720 x 1040.)
 template <int BM, int BN, int WM, int WN, int BUFS, int PA, int PB, bool FINE, Epi EPI, typename O>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 k_ortho_gemm(Args g) {
   using C = Cfg<BM, BN, WM, WN, BUFS, PA, PB>;
   constexpr int FM = C::FM, FN = C::FN;
-  static_assert(!FINE || (PA == 2 && PB == 2), "products with a lo on both sides");
+  static_assert(!FINE || (PA == 2 && PB == 2 && FM * FN <= 16), "products with a lo on both sides, registers");
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -182,6 +184,12 @@ k_ortho_gemm(Args g) {
   for (int j = 0; j < FM; ++j)
 #pragma unroll
     for (int i = 0; i < FN; ++i) acc[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  f32x4_v low[FINE ? FM : 1][FINE ? FN : 1];
+  if constexpr (FINE)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int i = 0; i < FN; ++i) low[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
   const int p = lane & 15, h = lane >> 4;
   constexpr int NA = C::LA / 64, NB = C::LB / 64;  // fragments of a line
   const lds_ptr_t la = (lds_ptr_t)smem + (wm * C::TM + p) * C::LA;
@@ -221,27 +229,28 @@ k_ortho_gemm(Args g) {
         for (int i = 0; i < FN; ++i)
           acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[i][xb], fa[j & 1][xa], acc[j][i], 0, 0, 0);
       };
+      mul(0, 0);
       if constexpr (FINE) {
-        f32x4_v d[FN];
 #pragma unroll
         for (int i = 0; i < FN; ++i)
-          d[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[i][1], fa[j & 1][0], f32x4_v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+          low[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[i][1], fa[j & 1][0], low[j][i], 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < FN; ++i) d[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[i][0], fa[j & 1][1], d[i], 0, 0, 0);
-        mul(0, 0);
-#pragma unroll
-        for (int i = 0; i < FN; ++i) acc[j][i] += d[i];
+        for (int i = 0; i < FN; ++i)
+          low[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[i][0], fa[j & 1][1], low[j][i], 0, 0, 0);
+      } else if constexpr (C::WIDE) {
+        mul(1, 1);  // the next 32 of the reduction
       } else {
-        mul(0, 0);
-        if constexpr (C::WIDE) {
-          mul(1, 1);  // the next 32 of the reduction
-        } else {
-          if constexpr (PB == 2) mul(0, 1);
-          if constexpr (PA == 2) mul(1, 0);
-        }
+        if constexpr (PB == 2) mul(0, 1);
+        if constexpr (PA == 2) mul(1, 0);
       }
     }
   }
+
+  if constexpr (FINE)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int i = 0; i < FN; ++i) acc[j][i] += low[j][i];
 
   // ---- results: a lane holds, of row p of a piece, the columns 4 h .. 4 h + 3 ----
   float alpha = job.alpha;

@@ -139,20 +139,23 @@ hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
 // stages ahead; many: large ones, which load least.  A whole call, us, with 64 x 64
 // tiles (four stage buffers) / 128 x 128 (two; with four 128 x 128 is no faster than either) /
 // 256 x 256:
-//   bf16   1 x 512 x 512 156 / 302 / 629          fp32   1 x 512 x 512 164 / 318 / 685
-//          4 x 1024 x 1024 538 / 541 / 1075              16 x 512 x 1024 492 / 461 / 878
-//          64 x 256 x 1536 322 / 327 / 476               64 x 256 x 1536 853 / 827 / 1103
-//          24 x 720 x 1040 1034 / 823 / 1145             24 x 720 x 1040 1407 / 1099 / 1451
-//          32 x 1024 x 1024 - / 2574 / 2740              16 x 2048 x 2048 - / 8599 / 8579
-//          64 x 2048 x 2048 - / 30632 / 28640            64 x 2048 x 2048 - / 33275 / 31525
+//   bf16   1 x 512 x 512 157 / 302 / 628          fp32   1 x 512 x 512 159 / 299 / 683
+//          4 x 1024 x 1024 528 / 533 / 1079              16 x 512 x 1024 476 / 447 / 882
+//          64 x 256 x 1536 327 / 339 / 482               64 x 256 x 1536 845 / 835 / 1127
+//          24 x 720 x 1040 1066 / 862 / 1155             24 x 720 x 1040 1362 / 1071 / 1456
+//          32 x 1024 x 1024 - / 2542 / 2811              16 x 2048 x 2048 - / 8079 / 8645
+//          64 x 2048 x 2048 - / 31176 / 29414            64 x 2048 x 2048 - / 31324 / 32475
+// (FINE's sums of two kinds do not fit the registers with 256 x 256: the fp32 figures there are
+// with one kind, the small sums added at every stage.)
 template <int PA, int PB, bool FINE, Epi EPI, typename O>
 hipError_t gemm_by_size(const Args& a, hipStream_t st) {
   auto tiles = [&](int B) {
     const int64_t mt = div_up(a.ra, B), nt = div_up(a.rb, B);
     return a.batch * a.jobs * (EPI == SYM ? mt * (mt + 1) / 2 : mt * nt);
   };
-  const int64_t t256 = tiles(256), t64 = tiles(64);
-  if (t256 >= 1024) return launch_gemm<256, 256, 2, 4, 2, PA, PB, FINE, EPI, O>(a, t256, st);
+  const int64_t t64 = tiles(64);
+  if constexpr (!FINE)
+    if (const int64_t t256 = tiles(256); t256 >= 1024) return launch_gemm<256, 256, 2, 4, 2, PA, PB, FINE, EPI, O>(a, t256, st);
   if (t64 <= 768) return launch_gemm<64, 64, 2, 2, 4, PA, PB, FINE, EPI, O>(a, t64, st);
   return launch_gemm<128, 128, 2, 2, 2, PA, PB, FINE, EPI, O>(a, tiles(128), st);
 }
