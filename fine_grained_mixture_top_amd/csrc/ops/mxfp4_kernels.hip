@@ -116,10 +116,12 @@ hipError_t launch_mxfp4_mm(const PlanArgs& p, const Mxfp4Args& m, hipStream_t st
   //   128 experts of 1536 x 512, 16 rows each 21 and 28, 32 32 and 29
   //   8 experts of 736 x 1040, 400 rows (416000) 8.4 and 12.8, 1600 (1664000) 24 and 14
   //   one of 2048 x 2048, 256 rows (524288) 10 and 25, 1024 (2097152) 28.5 and 25
-  if (used <= 16 * (int64_t)a.E || used * a.N <= (1 << 20)) {
+  // (a grid has fewer than 2^24 workgroups of 256)
+  const int64_t thin = row_tiles(a, used, 16) * div_up(a.N, 64);
+  if ((used <= 16 * (int64_t)a.E || used * a.N <= (1 << 20)) && thin < (1 << 24)) {
     // under half a workgroup of 64 columns per CU: workgroups of 16 (one row, 7168 x 4096
     // 8.6 us in place of 13.7; 64 of 2048 x 2048, where it is the other way, 8.0 and 7.9)
-    if (row_tiles(a, used, 16) * div_up(a.N, 64) < cu_count(device()) / 2) return launch_thin<1>(m.out, a, used, st);
+    if (thin < cu_count(device()) / 2) return launch_thin<1>(m.out, a, used, st);
     return launch_thin<4>(m.out, a, used, st);
   }
   // Tiles of 64 or 128 rows (us): 64 experts of 2048 x 2048, 128 rows each 92 and 100, 512 269

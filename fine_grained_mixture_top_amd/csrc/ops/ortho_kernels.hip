@@ -70,7 +70,7 @@ struct Convert {
   char* same;     // rows of g
   char* trans;    // columns of g
   int64_t ssame, strans;
-  float* back;    // [groups][gridDim.z]
+  float* back;    // [groups][gridDim.y]
 };
 
 // (a launch of its own, for more than one group)
@@ -84,10 +84,12 @@ template <typename T, int P>
 __global__ void __launch_bounds__(256)
 k_ortho_convert(Convert a) {
   __shared__ float tile[64][65];
-  const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tid = threadIdx.x;
+  // (both sides may have more tiles than a grid's second axis)
+  const int wide = (a.N + 63) / 64, e = blockIdx.y, tid = threadIdx.x;
+  const int r0 = (int)(blockIdx.x / (unsigned)wide) * 64, c0 = (int)(blockIdx.x % (unsigned)wide) * 64;
   const double norm = norm_of(a.sums, a.parts, e);
   const int ex = power_of(norm);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.back[e] = (float)first_of(norm, a.eps);
+  if (blockIdx.x == 0 && tid == 0) a.back[e] = (float)first_of(norm, a.eps);
   const T* g = (const T*)a.g + (int64_t)e * a.M * a.N;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -303,7 +305,7 @@ hipError_t prepare(const OrthoArgs& a, const Sizes& z, int e0, int nb, hipStream
     const Factors f = factors_of(a, z.groups, nb, sums, parts, c.back);
     hipLaunchKernelGGL(k_ortho_factors, dim3(nb), dim3(64), 0, st, f);
   }
-  hipLaunchKernelGGL((k_ortho_convert<T, P>), dim3((a.N + 63) / 64, (a.M + 63) / 64, nb), dim3(256), 0, st, c);
+  hipLaunchKernelGGL((k_ortho_convert<T, P>), dim3((a.N + 63) / 64 * ((a.M + 63) / 64), nb), dim3(256), 0, st, c);
   return hipGetLastError();
 }
 

@@ -94,7 +94,7 @@ int moe_balance_bwd(const moe_balance_desc* desc, const void* logits, const int3
  *   Precision.  With fp32 matrices every product is taken to about 2^-22 of its
  * factors and summed in fp32, as fp32 products are: results are as far from the
  * definition as those of fp32 products step by step (1.3e-6 to 3.2e-6 of the result's norm
- * for the coefficients above).  With bf16 matrices several steps share one product
+ * for the coefficients above and sides of thousands; sums over millions may add as much again).  With bf16 matrices several steps share one product
  * with X; that adds up to 4e-4 of the result's norm to its rounding's 1.7e-3.  The
  * polynomials' values on singular values 0 .. 1 have to stay below 2^40; a step sequence that
  * grows past that gives results that are not finite.

@@ -236,6 +236,42 @@ def test_orthogonalize_offsets_past_32_bits():
         assert float((o[e].double() - want).norm()) <= tol * float(want.norm()), e
 
 
+@pytest.mark.parametrize("M,N,dtype,steps", [(4_250_000, 50, torch.bfloat16, 6), (60, 4_250_000, torch.bfloat16, 6),
+                                             (4_150_000, 100, torch.float32, 2), (70, 4_150_000, torch.bfloat16, 2)])
+def test_orthogonalize_long_matrices(M, N, dtype, steps):
+    """More tiles on one side than a grid's second axis has workgroups: in groups of steps, and the small form."""
+    small, long = min(M, N), max(M, N)
+    # one number per line of the long side, a power of two: the sums over millions of products are exact
+    at = torch.arange(long, device="cuda")
+    x = torch.zeros(small, long, dtype=dtype, device="cuda")
+    sign = 1.0 - 2.0 * (torch.rand(long, generator=gen(small), device="cuda") < 0.5)
+    x[at % small, at] = (sign * 2.0 ** -(at % small % 4).float()).to(dtype)
+    w = (x if M < N else x.t()).contiguous()[None]
+    o = torch.empty_like(w)
+    ops.moe_orthogonalize(ops.Ortho(1, M, N, dtype=dtype, steps=steps), w, o)
+    rows = [x[i].double().square().sum() for i in range(small)]
+    norm = torch.stack(rows).sum().sqrt() + 1e-7
+    s = torch.stack(rows).sqrt() / norm  # the singular values: rows are orthogonal
+    f = torch.ones_like(s)
+    for a, b, c in [R.QUINTIC] * steps:
+        l = (s * f) ** 2
+        slope = (l * (b + 2 * c * l) / (a + l * (b + l * c))).abs().max()
+        f = f * (a + l * (b + l * c))
+    tol = R.ortho_tolerance(dtype, steps, [R.QUINTIC]) + R.HALF[dtype]
+    if dtype == torch.float32:
+        # The second step's numbers are no powers of two, and of a row all are alike, so that roundings do not cancel:
+        # a sixteenth of the line's sums of 128 join a sum one by one, each off by at most 2^-24 of it, which may then
+        # hold long / 2048 times 2^-24 of A's value too much; X's share of that is l p'(l) / p(l).  (ortho_tolerance
+        # counts a step's sums as 2^-22, for lengths of thousands.)
+        tol += float(slope) * (long / 2048 + 16) * 2.0 ** -24
+    got, off, size = o[0] if M < N else o[0].t(), 0.0, 0.0
+    for c in range(0, long, 500_000):
+        want = x[:, c:c + 500_000].double() * (f / norm)[:, None]
+        off += float((got[:, c:c + 500_000].double() - want).square().sum())
+        size += float(want.square().sum())
+    assert off ** 0.5 <= tol * size ** 0.5, (off ** 0.5 / size ** 0.5, tol)
+
+
 @pytest.mark.parametrize("T", [3, 5000])
 def test_mxfp4_weights_past_32_bits(T):
     """Codes past 2^32 bytes."""
