@@ -137,16 +137,25 @@ hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Tiles.  Few of them: a stage takes as long as its loads, so small tiles with three
-// stages ahead; many: large ones, which load least.  A whole call, us, with 64 x 64
-// tiles (four stage buffers) / 128 x 128 (two; with four 128 x 128 is no faster than either) /
-// 256 x 256:
-//   bf16   1 x 512 x 512 157 / 302 / 628          fp32   1 x 512 x 512 159 / 299 / 683
-//          4 x 1024 x 1024 528 / 533 / 1079              16 x 512 x 1024 476 / 447 / 882
-//          64 x 256 x 1536 327 / 339 / 482               64 x 256 x 1536 845 / 835 / 1127
-//          24 x 720 x 1040 1066 / 862 / 1155             24 x 720 x 1040 1362 / 1071 / 1456
-//          32 x 1024 x 1024 - / 2542 / 2811              16 x 2048 x 2048 - / 8079 / 8645
-//          64 x 2048 x 2048 - / 31176 / 29414            64 x 2048 x 2048 - / 31324 / 32475
+// Tiles.  Few of them: a stage takes as long as its loads, so tiles of 64 x 64 with three
+// stages ahead; while 128 x 128 fill no CU twice, one of those with eight waves and three
+// stages ahead for each; else two of them with four waves and one stage ahead; many:
+// 256 x 256, which load least.  A whole call, us, with one kind throughout, and by this rule:
+//                            64 x 64   128, 8 waves   128, 4 waves   256    rule
+//   bf16   1 x 512 x 512         157            249            302          156
+//          2 x 1024 x 1024       319            400            483          302
+//          4 x 1024 x 1024       519            491            548  1079    479
+//          64 x 256 x 1536       334            325            346   482    313
+//          128 x 256 x 1536                     632            587   661
+//          24 x 720 x 1040      1066            934            862  1155
+//          32 x 1024 x 1024                    2817           2542  2811
+//          64 x 2048 x 2048                   35750          31176 29414  29414
+//   fp32   1 x 512 x 512         158            248            299   683    160
+//          4 x 1024 x 1024       514            445            505  1188    445
+//          1 x 2048 x 2048       896            747            833          755
+//          64 x 256 x 1536       860            768            856  1127    743
+//          24 x 720 x 1040      1362           1182           1071  1456
+//          64 x 2048 x 2048                   36612          31324 32475
 // (FINE's sums of two kinds do not fit the registers with 256 x 256: the fp32 figures there are
 // with one kind, the small sums added at every stage.)
 template <int PA, int PB, bool FINE, Epi EPI, typename O>
@@ -158,8 +167,10 @@ hipError_t gemm_by_size(const Args& a, hipStream_t st) {
   const int64_t t64 = tiles(64);
   if constexpr (!FINE)
     if (const int64_t t256 = tiles(256); t256 >= 1024) return launch_gemm<256, 256, 2, 4, 2, PA, PB, FINE, EPI, O>(a, t256, st);
-  if (t64 <= 768) return launch_gemm<64, 64, 2, 2, 4, PA, PB, FINE, EPI, O>(a, t64, st);
-  return launch_gemm<128, 128, 2, 2, 2, PA, PB, FINE, EPI, O>(a, tiles(128), st);
+  const int64_t t128 = tiles(128), cus = cu_count(device());
+  if (t64 <= 2 * cus) return launch_gemm<64, 64, 2, 2, 4, PA, PB, FINE, EPI, O>(a, t64, st);
+  if (t128 <= cus) return launch_gemm<128, 128, 4, 2, 4, PA, PB, FINE, EPI, O>(a, t128, st);
+  return launch_gemm<128, 128, 2, 2, 2, PA, PB, FINE, EPI, O>(a, t128, st);
 }
 
 // (fp32 updates are two parts throughout, and FINE)
