@@ -138,24 +138,25 @@ hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
 }
 
 // Tiles.  Few of them: a stage takes as long as its loads, so tiles of 64 x 64 with three
-// stages ahead; while 128 x 128 fill no CU twice, one of those with eight waves and three
-// stages ahead for each; else two of them with four waves and one stage ahead; many:
-// 256 x 256, which load least.  A whole call, us, with one kind throughout, and by this rule:
-//                            64 x 64   128, 8 waves   128, 4 waves   256    rule
-//   bf16   1 x 512 x 512         157            249            302          156
+// stages ahead; while 128 x 128 fill no CU twice, one of those with three stages ahead for
+// each; else two of them with one stage ahead; many: 256 x 256, which load least.  128 x 128
+// have eight waves (four instead, two stage buffers: 24 x 720 x 1040 849 us in place of 809, in
+// fp32 1076 in place of 1035).  A whole call, us, with one kind throughout, and by this rule:
+//                            64 x 64   128, 3 ahead   128, 1 ahead   256    rule
+//   bf16   1 x 512 x 512         157            249            302   628    156
 //          2 x 1024 x 1024       319            400            483          302
-//          4 x 1024 x 1024       519            491            548  1079    479
-//          64 x 256 x 1536       334            325            346   482    313
-//          128 x 256 x 1536                     632            587   661
-//          24 x 720 x 1040      1066            934            862  1155
-//          32 x 1024 x 1024                    2817           2542  2811
-//          64 x 2048 x 2048                   35750          31176 29414  29414
+//          4 x 1024 x 1024       519            491            463  1079    453
+//          64 x 256 x 1536       334            325            303   482    301
+//          128 x 256 x 1536      573            584            539   661    541
+//          24 x 720 x 1040      1035            909            809  1155    815
+//          32 x 1024 x 1024     3199           2774           2484  2811   2475
+//          64 x 2048 x 2048                   35750          31175 29414  29034
 //   fp32   1 x 512 x 512         158            248            299   683    160
-//          4 x 1024 x 1024       514            445            505  1188    445
-//          1 x 2048 x 2048       896            747            833          755
-//          64 x 256 x 1536       860            768            856  1127    743
-//          24 x 720 x 1040      1362           1182           1071  1456
-//          64 x 2048 x 2048                   36612          31324 32475
+//          4 x 1024 x 1024       514            445            432  1188    429
+//          1 x 2048 x 2048       896            747            742          727
+//          64 x 256 x 1536       860            768            818  1127    723
+//          24 x 720 x 1040      1362           1182           1035  1456   1042
+//          64 x 2048 x 2048                   36612          31510 32475  31519
 // (FINE's sums of two kinds do not fit the registers with 256 x 256: the fp32 figures there are
 // with one kind, the small sums added at every stage.)
 template <int PA, int PB, bool FINE, Epi EPI, typename O>
@@ -170,7 +171,7 @@ hipError_t gemm_by_size(const Args& a, hipStream_t st) {
   const int64_t t128 = tiles(128), cus = cu_count(device());
   if (t64 <= 2 * cus) return launch_gemm<64, 64, 2, 2, 4, PA, PB, FINE, EPI, O>(a, t64, st);
   if (t128 <= cus) return launch_gemm<128, 128, 4, 2, 4, PA, PB, FINE, EPI, O>(a, t128, st);
-  return launch_gemm<128, 128, 2, 2, 2, PA, PB, FINE, EPI, O>(a, t128, st);
+  return launch_gemm<128, 128, 4, 2, 2, PA, PB, FINE, EPI, O>(a, t128, st);
 }
 
 // (fp32 updates are two parts throughout, and FINE)
