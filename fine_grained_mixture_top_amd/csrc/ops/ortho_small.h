@@ -364,7 +364,8 @@ __device__ __forceinline__ void factors(const __attribute__((address_space(4))) 
   }
 }
 
-// ---- X X^T of the update, slice by slice ----
+// ---- X X^T of the update, slice by slice (1536 x 128 in fp32 8.2 us: loads, then a
+// product per chunk) ----
 template <typename T, int P, int MP, bool TALL>
 __global__ void __launch_bounds__(SMALL_THREADS, 2)
 k_small_gram(Small a) {
@@ -483,7 +484,8 @@ __device__ __forceinline__ void write_out(const Small& a, int e, int chunk,
 }
 
 // ---- a step of fp32 updates: A from the slices' sums, P, and per chunk X = P X and the
-// next sums ----
+// next sums (1536 x 128 12.8 us: three products one after the other, 4.5 us of matrix
+// instructions, with their LDS writes and barriers between them) ----
 struct StepArgs {
   Small a;
   float diag, beta, alpha;  // P = diag I + beta A + alpha A^2
@@ -559,7 +561,8 @@ k_small_step(StepArgs s) {
   if constexpr (!LAST) write_part<MP>(a.part, a.slices, e, slice, tot, w, tid);
 }
 
-// ---- bf16 updates: all steps on the m x m matrices, a workgroup per update ----
+// ---- bf16 updates: all steps on the m x m matrices, a workgroup per update (five steps
+// 16.5 us up to 64 rows, 56 up to 128: a chain of 14 products on one CU) ----
 struct Recurrence {
   float diag, beta, alpha;  // P = diag I + beta A + alpha A^2
   float t, next, q;         // of T = P A, A = T P, Q = P Q
