@@ -50,6 +50,21 @@ __device__ __forceinline__ f16x4_v turn4(const f16x4_v v, int lane) {
   return __builtin_bit_cast(f16x4_v, high ? u32x2_v{got, e1} : u32x2_v{e0, got});
 }
 
+// A 16 x 16 piece on the diagonal of a symmetric matrix: lane p + 16 h has four numbers of row p
+// from column 4 h on, and gets those above the diagonal from the lanes that hold their mirror.
+__device__ __forceinline__ f16x4_v lower_mirrored(const f16x4_v v, int lane) {
+  const int p = lane & 15, h = lane >> 4;
+  const u32x2_v t = __builtin_bit_cast(u32x2_v, turn4(v, lane));  // row 4 h + p % 4 from column p / 4 * 4 on
+  const int from = ((p >> 2) * 16 + 4 * h + (p & 3)) * 4;
+  const u32x2_v row = {(uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)t[0]),
+                       (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)t[1])};
+  const f16x4_v m = __builtin_bit_cast(f16x4_v, row);
+  f16x4_v o;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) o[x] = 4 * h + x > p ? m[x] : v[x];
+  return o;
+}
+
 // bytes of a row of n numbers in `parts` parts
 __host__ __device__ inline int64_t pitch(int64_t n, int parts) { return (n + 63) / 64 * 128 * parts; }
 // byte of number i of a row of two parts (its lo is 64 bytes further on)
@@ -160,6 +175,10 @@ k_ortho_gemm(Args g) {
   }
   const int m0 = ti * BM, n0 = tj * BN;
 
+  // A symmetric product's tile on the diagonal, and a wave whose pieces all lie above it: it only
+  // loads (128 x 256 x 1536 619 -> 576 us; in tiles of 64 loads bound, 1 x 512 x 512 157.6 and 161.6).
+  const bool diagonal = EPI == SYM && ti == tj, above = BM > 64 && diagonal && wn * C::TN >= (wm + 1) * C::TM;
+
   // ---- loads ----
   const __amdgpu_buffer_rsrc_t ra = rsrc(job.a + e * g.sa, (uint32_t)(g.ra * (int64_t)g.pa));
   const __amdgpu_buffer_rsrc_t rb = rsrc(job.b + e * g.sb, (uint32_t)(g.rb * (int64_t)g.pb));
@@ -216,6 +235,7 @@ k_ortho_gemm(Args g) {
     if (s + AHEAD < g.stages) load(s + AHEAD, buf == 0 ? BUFS - 1 : buf - 1);
     const int at = buf * C::STAGE;
     buf = buf + 1 == BUFS ? 0 : buf + 1;
+    if (above) continue;
     f16x8_v fb[FN][NB], fa[2][NA];
 #pragma unroll
     for (int x = 0; x < NA; ++x) fa[0][x] = lds_ld<f16x8_v>(la + at + slot_a[x]);
@@ -309,8 +329,12 @@ k_ortho_gemm(Args g) {
       }
     }
   } else {
-    // c [ra][columns up to the padding] and, but for a diagonal tile, its transpose: a
-    // symmetric product's other half, or the next group's other layout.  Half of a wave's
+    // c [ra][columns up to the padding] and its transpose: a symmetric product's other half,
+    // or the next group's other layout.  Of a symmetric product's tile on the diagonal the
+    // pieces on and below it and the mirror of those below: a product of matrices that commute is
+    // symmetric up to its rounding only, and what is not symmetric would grow with the steps
+    // (bf16 updates of 256 x 1536 with one large direction, both halves as computed: error
+    // 6.4e-3 of the result's norm in place of 4.8e-4).  Half of a wave's
     // tile at a time goes through LDS, where lines have their final layout (slots of 16
     // bytes xored with line % 8), for lanes in a row to write whole lines: 8 bytes of
     // sixteen lines at a time, as the products leave them, one costs the L1 as much as a
@@ -327,6 +351,7 @@ k_ortho_gemm(Args g) {
       *reinterpret_cast<f16x4_v*>(mine + (at ^ 64)) = lo;
     };
     lds_sync();  // (all products' operands are read)
+    if (above) return;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int rh = r1 + half * (C::TM / 2);
@@ -372,6 +397,10 @@ k_ortho_gemm(Args g) {
             parts[x] = hi[x] = vh;
             parts[4 + x] = lo[x] = vl;
           }
+          if (diagonal && r1 + 16 * j == c1 + 16 * i) {
+            hi = lower_mirrored(hi, lane);
+            lo = lower_mirrored(lo, lane);
+          }
           put(to, hi, lo);
           acc[j][i] = __builtin_bit_cast(f32x4_v, parts);
         }
@@ -380,11 +409,11 @@ k_ortho_gemm(Args g) {
 #pragma unroll
       for (int k = 0; k < HALF / 1024; ++k) {
         const f16x8_v v = *reinterpret_cast<const f16x8_v*>(mine + at(k));
-        if (rh + line(k) < g.ra && c1 < cols) *reinterpret_cast<f16x8_v*>(out + where(k)) = v;
+        const int r = rh + line(k), c = c1 + (slot(k) >> 3) * 32 + (slot(k) & 3) * 8;
+        if (r < g.ra && c1 < cols && !(diagonal && (c >> 4) > (r >> 4))) *reinterpret_cast<f16x8_v*>(out + where(k)) = v;
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-    if (EPI == SYM && ti == tj) return;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int ch = c1 + half * (C::TN / 2);
@@ -403,7 +432,8 @@ k_ortho_gemm(Args g) {
       for (int k = 0; k < HALF / 1024; ++k) {
         const int l = (64 * k + lane) / (LT / 16), s = (64 * k + lane) % (LT / 16);
         const f16x8_v v = *reinterpret_cast<const f16x8_v*>(mine + l * LT + (s ^ (l & 7)) * 16);
-        if (ch + l < g.rb && r1 + (s >> 3) * 32 < rows)
+        const int r = ch + l, c = r1 + (s >> 3) * 32 + (s & 3) * 8;
+        if (r < g.rb && r1 + (s >> 3) * 32 < rows && !(diagonal && (r >> 4) >= (c >> 4)))
           *reinterpret_cast<f16x8_v*>(outt + (int64_t)(ch + l) * pt + r1 * 4 + s * 16) = v;
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
