@@ -109,6 +109,11 @@ struct Cfg {
   static constexpr int LA = WIDE || PA == 2 ? 128 : 64, LB = WIDE || PB == 2 ? 128 : 64;  // bytes of a line per stage
   static constexpr int IA = BM * LA / 1024 / W, IB = BN * LB / 1024 / W;                  // 1 KB loads per wave
   static constexpr int STAGE = BM * LA + BN * LB;
+  // X X^T of one part is summed in pieces of 512, so that a long sum is rounded once for each of
+  // those and not for every eight products: 129 x 50000, 317 -> 337 us, error 3.4e-3 -> 5.0e-4; 256 x 1536
+  // the same time, 4.8e-4 -> 3.0e-4 (but for 256 x 256 tiles, whose registers are full)
+  static constexpr bool PIECES = WIDE && FM * FN <= 16;
+  static constexpr int PIECE = 8;
   static constexpr int HALF = TM * TN * 2;  // bytes of half of a wave's results
   static constexpr int SMEM = BUFS * STAGE > W * HALF ? BUFS * STAGE : W * HALF;
   static_assert(SMEM <= 160 * 1024 && (BUFS - 2) * (IA + IB) < 64, "LDS, and outstanding loads");
@@ -207,8 +212,9 @@ k_ortho_gemm(Args g) {
   for (int j = 0; j < FM; ++j)
 #pragma unroll
     for (int i = 0; i < FN; ++i) acc[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
-  f32x4_v low[FINE ? FM : 1][FINE ? FN : 1];
-  if constexpr (FINE)
+  constexpr bool LOW = FINE || C::PIECES;  // the small products' sums, or those of the pieces before
+  f32x4_v low[LOW ? FM : 1][LOW ? FN : 1];
+  if constexpr (LOW)
 #pragma unroll
     for (int j = 0; j < FM; ++j)
 #pragma unroll
@@ -268,9 +274,18 @@ k_ortho_gemm(Args g) {
         if constexpr (PA == 2) mul(1, 0);
       }
     }
+    if constexpr (C::PIECES)
+      if (s % C::PIECE == C::PIECE - 1)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+#pragma unroll
+          for (int i = 0; i < FN; ++i) {
+            low[j][i] += acc[j][i];
+            acc[j][i] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+          }
   }
 
-  if constexpr (FINE)
+  if constexpr (LOW)
 #pragma unroll
     for (int j = 0; j < FM; ++j)
 #pragma unroll
@@ -334,7 +349,7 @@ k_ortho_gemm(Args g) {
     // pieces on and below it and the mirror of those below: a product of matrices that commute is
     // symmetric up to its rounding only, and what is not symmetric would grow with the steps
     // (bf16 updates of 256 x 1536 with one large direction, both halves as computed: error
-    // 6.4e-3 of the result's norm in place of 4.8e-4).  Half of a wave's
+    // 6.4e-3 of the result's norm in place of 3.0e-4).  Half of a wave's
     // tile at a time goes through LDS, where lines have their final layout (slots of 16
     // bytes xored with line % 8), for lanes in a row to write whole lines: 8 bytes of
     // sixteen lines at a time, as the products leave them, one costs the L1 as much as a

@@ -8,14 +8,17 @@
 //     A_1 = P A P,   Q = P_n ... P_1,   X_n = Q X_0
 // which needs one product with the m x k matrix for a group of steps, and half the
 // tiles of every product but that one.
-//   Rounding.  A singular value s enters A as s^2 beside the largest one's 1, and
-// every step multiplies a small one's share by a^2: what A's fp32 sums lost grows
-// with it, to (product of a)^2 2^-24 of a small direction's P.  Measured on m x k =
-// 64 x 64 to 512 x 512, gaussian, 1/i and low-rank spectra, five steps with a = 3.4445:
-// error of the result 1.3e-6 to 3.2e-6 with one step a group (products in fp32
-// throughout: 1.1e-6 to 3.4e-6), 1.4e-6 to 1.1e-5 with two and three, 1.4e-6 to 3.7e-4
-// with five.  So fp32 results take one step a group, and bf16 results, whose
-// rounding is 1.7e-3, as many as keep the product of the |a| at 512 or below.
+//   Rounding.  A singular value s enters A as s^2 beside the largest one's 1, so what A lost
+// (2^-23 of an element in its two parts, and its sums' roundings) stands beside s^2, grows by
+// a^2 with every step that A goes through, and each P loses |b| / a of it: see group_steps.
+// Error of bf16 results before their rounding, which is 1.7e-3 of their norm, five steps with
+// a = 3.4445 in one group, spectra gaussian / 1/i / one direction beside 3e-4:
+//     160 x 160     2e-5 / 1e-4 / 3.4e-4      129 x 50000   1e-6 / 8e-5 / 5.0e-4
+//     256 x 1536    2e-6 / 1.4e-4 / 3.0e-4    16 x 1000     3e-6 / 2e-6 / 7.0e-4
+//     2048 x 2048   1e-5 / 1.7e-4 / 2.1e-4    8 x 8000      1e-6 / 1e-6 / 9.1e-4
+// fp32 results with one step a group 1e-6 / 3e-6 / 2.6e-5 at most (products in fp32 throughout: 3e-6 /
+// 4e-6 / 4e-5).  So fp32 results take one
+// step a group, and bf16 results as many as add less than their rounding.
 #include <algorithm>
 #include <cmath>
 
@@ -161,6 +164,7 @@ hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
 //          64 x 2048 x 2048                   36612          31510 32475  31519
 // (FINE's sums of two kinds do not fit the registers with 256 x 256: the fp32 figures there are
 // with one kind, the small sums added at every stage.)
+constexpr int LONG = 6;  // sides from which on bf16 X X^T is summed in pieces throughout
 template <int PA, int PB, bool FINE, Epi EPI, typename O>
 hipError_t gemm_by_size(const Args& a, hipStream_t st) {
   auto tiles = [&](int B) {
@@ -168,8 +172,12 @@ hipError_t gemm_by_size(const Args& a, hipStream_t st) {
     return a.batch * a.jobs * (EPI == SYM ? mt * (mt + 1) / 2 : mt * nt);
   };
   const int64_t t64 = tiles(64);
-  if constexpr (!FINE)
-    if (const int64_t t256 = tiles(256); t256 >= 1024) return launch_gemm<256, 256, 2, 4, 2, PA, PB, FINE, EPI, O>(a, t256, st);
+  if constexpr (!FINE) {
+    // (not for X X^T whose sums are long: see lost)
+    const bool pieces = PA == 1 && PB == 1 && (int64_t)a.stages * 64 > LONG * (int64_t)a.ra;
+    const int64_t t256 = tiles(256);
+    if (t256 >= 1024 && !pieces) return launch_gemm<256, 256, 2, 4, 2, PA, PB, FINE, EPI, O>(a, t256, st);
+  }
   const int64_t t128 = tiles(128), cus = cu_count(device());
   if (t64 <= 2 * cus) return launch_gemm<64, 64, 2, 2, 4, PA, PB, FINE, EPI, O>(a, t64, st);
   if (t128 <= cus) return launch_gemm<128, 128, 4, 2, 4, PA, PB, FINE, EPI, O>(a, t128, st);
@@ -231,14 +239,32 @@ struct Sizes {
   int64_t x0, xt0, x1, xt1, mat, f, sums, total;
 };
 
-// How many steps from step s on form a group.
-int group_steps(const OrthoArgs& a, int s) {
+// What A = X X^T loses beside a small direction's share, in root mean square over m directions: an
+// element is off by 2^-25 sqrt(4 + sums) of itself, 2^-24 in its two parts and half a step for each
+// rounding of its sum (`sums`: their mean square, n roundings of a sum that grows evenly being n / 3);
+// elements of one large direction over all rows are about 1 / m.
+double lost(int m, double sums) { return std::ldexp(std::sqrt((4.0 + sums) * (m - 1)) / m, -25); }
+// ... products of any size: one sum over k, rounded once for eight products, or pieces of 512
+double lost(const OrthoArgs& a) {
+  const int m = std::min(a.M, a.N), k = std::max(a.M, a.N);
+  const double pieces = std::ceil(k / 512.0);
+  return lost(m, k <= (int64_t)LONG * m ? k / 24.0 : (64.0 / pieces + pieces) / 3.0);
+}
+
+// How many steps from step s on form a group: those whose P lose at most 1.5e-3 of the result
+// together, when a direction far above the others hides these from A.  X X^T of
+// long sides is summed in pieces for that: 129 x 50000 in one sum loses 3.4e-3, or takes 4 + 1
+// steps and 788 us; in pieces 5.0e-4, 337 us.)
+int group_steps(const OrthoArgs& a, int s, double lost) {
   if (a.dtype == MOE_F32) return 1;
-  double growth = 1.0;
+  double grown = 0.0, power = 1.0;
   int n = 0;
   while (s + n < a.steps) {
-    growth *= std::max(1.0, std::fabs((double)a.coef[3 * (s + n)]));
-    if (n > 0 && growth > 512.0) break;
+    const float* c = a.coef + 3 * (s + n);
+    const double up = std::max(1.0, std::fabs((double)c[0]));
+    grown += std::fabs((double)c[1]) / up * power;
+    power *= up * up;
+    if (n > 0 && lost * grown > 1.5e-3) break;
     ++n;
   }
   return n;
@@ -253,7 +279,7 @@ Sizes sizes(const OrthoArgs& a) {
   const int64_t mt = div_up(z.m, 256), tiles = mt * (mt + 1) / 2;
   const int64_t most = std::min<int64_t>(a.E, div_up(2304, tiles));
   z.nb = (int)div_up(a.E, div_up(a.E, most));
-  for (int s = 0; s < a.steps; s += group_steps(a, s)) ++z.groups;
+  for (int s = 0; s < a.steps; s += group_steps(a, s, lost(a))) ++z.groups;
   z.sx = z.m * pitch(z.k, 2);
   z.sxt = z.k * pitch(z.m, 2);
   z.sm = z.m * pitch(z.m, 2);
@@ -281,7 +307,7 @@ Factors factors_of(const OrthoArgs& a, int groups, int nb, const double* sums, i
   Factors f{};
   f.sums = sums; f.parts = parts; f.eps = a.eps;
   f.back = back; f.on = back + groups * nb; f.groups = groups;
-  for (int s = 0, i = 0; s < a.steps; s += f.steps[i], ++i) f.steps[i] = (uint8_t)group_steps(a, s);
+  for (int s = 0, i = 0; s < a.steps; s += f.steps[i], ++i) f.steps[i] = (uint8_t)(groups == 1 ? a.steps : group_steps(a, s, lost(a)));
   std::copy(a.coef, a.coef + 3 * a.steps, f.coef);
   return f;
 }
@@ -324,10 +350,6 @@ hipError_t prepare(const OrthoArgs& a, const Sizes& z, int e0, int nb, hipStream
 }
 
 // ---- the smaller side at most 128 (ortho_small.h) ----
-bool is_small(const OrthoArgs& a) {
-  return std::min(a.M, a.N) <= 128 && (a.dtype == MOE_F32 || group_steps(a, 0) == a.steps);
-}
-
 struct SmallSizes {
   int mp, chunks, nb, slices, per, groups;
   int64_t part, gram, x, q, f, sums, total;
@@ -360,6 +382,15 @@ SmallSizes small_sizes(const OrthoArgs& a) {
   z.sums = take(8 * (int64_t)z.nb * NORM_PARTS);
   z.total = at;
   return z;
+}
+
+// (bf16: all steps in one group.  Sums over a chunk's 16 roundings, over a slice's chunks, over slices)
+bool is_small(const OrthoArgs& a) {
+  const int m = std::min(a.M, a.N);
+  if (m > 128 || a.dtype == MOE_F32) return m <= 128;
+  const SmallSizes z = small_sizes(a);
+  const double sums = (16.0 / z.chunks + (double)z.per / z.slices + z.slices) / 3.0;
+  return group_steps(a, 0, lost(m, sums)) == a.steps;
 }
 
 template <typename K, typename A>
@@ -506,7 +537,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
 
     bool second = false;  // which of the later groups' buffers is free
     for (int s = 0; s < a.steps;) {
-      const int n = group_steps(a, s);
+      const int n = group_steps(a, s, lost(a));
       spec.begin();
       // mats in use: A, P, Q, T (any: a scratch)
       char *A = mats[0], *T = mats[1], *P = mats[2], *Q = nullptr, *spare[2] = {mats[3], mats[4]};

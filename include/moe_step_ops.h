@@ -94,8 +94,12 @@ int moe_balance_bwd(const moe_balance_desc* desc, const void* logits, const int3
  *   Precision.  With fp32 matrices every product is taken to about 2^-22 of its
  * factors and summed in fp32, as fp32 products are: results are as far from the
  * definition as those of fp32 products step by step (1.3e-6 to 3.2e-6 of the result's norm
- * for the coefficients above and sides of thousands; sums over millions may add as much again).  With bf16 matrices several steps share one product
- * with X; that adds up to 4e-4 of the result's norm to its rounding's 1.7e-3.  The
+ * for the coefficients above and sides of thousands, up to 2.6e-5 where one direction is far above all others, and
+ * fp32 products 4e-5 there; sums over millions may add as much again).  With bf16 matrices
+ * several steps share one product with X, as many as are expected to add at most 1.5e-3 of the result's norm to its
+ * rounding's 1.7e-3 when one direction is far above all others: measured 2e-4 to 5e-4 then for 100 rows (of the
+ * smaller side, rows of zeros not counted) or more, up to 1.2e-3 for two, and 2e-4 or less for singular values that
+ * fall like 1/i.  The
  * polynomials' values on singular values 0 .. 1 have to stay below 2^40; a step sequence that
  * grows past that gives results that are not finite.
  *   Limits: 1 <= E <= 1024, 1 <= steps <= 64, min(M, N) <= 16384, a padded matrix
