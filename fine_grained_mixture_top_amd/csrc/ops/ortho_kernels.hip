@@ -17,8 +17,8 @@
 //     256 x 1536    2e-6 / 1.4e-4 / 3.0e-4    16 x 1000     3e-6 / 2e-6 / 7.0e-4
 //     2048 x 2048   1e-5 / 1.7e-4 / 2.1e-4    8 x 8000      1e-6 / 1e-6 / 9.1e-4
 // fp32 results with one step a group 1e-6 / 3e-6 / 2.6e-5 at most (products in fp32 throughout: 3e-6 /
-// 4e-6 / 4e-5).  So fp32 results take one
-// step a group, and bf16 results as many as add less than their rounding.
+// 4e-6 / 4e-5).  So fp32 results take one step a group, and bf16 results as many as add less than
+// their rounding.
 #include <algorithm>
 #include <cmath>
 
@@ -235,7 +235,7 @@ int exponent_for(double most) {
 struct Sizes {
   int m, k, parts, nb;           // parts of the update; matrices at a time
   int64_t sx, sxt, sm;           // bytes of X, its transpose (two parts), an m x m matrix
-  int groups;
+  int groups, mats;              // m x m matrices
   int64_t x0, xt0, x1, xt1, mat, f, sums, total;
 };
 
@@ -293,10 +293,13 @@ Sizes sizes(const OrthoArgs& a) {
   z.xt0 = take(z.nb * z.sxt * z.parts / 2);
   if (z.groups > 1) {
     // X in two parts for the groups after the first, which one-part input leaves no place for
-    z.x1 = take(z.nb * z.sx * (z.parts == 1 ? 2 : 1));
-    z.xt1 = take(z.nb * z.sxt * (z.parts == 1 ? 2 : 1));
+    const int n = z.parts == 1 && z.groups > 2 ? 2 : 1;
+    z.x1 = take(z.nb * z.sx * n);
+    z.xt1 = take(z.nb * z.sxt * n);
   }
-  z.mat = take(5 * z.nb * z.sm);
+  // A and P; with more steps in a group T = P A and Q, the old one and the next
+  z.mats = z.groups == a.steps ? 2 : 5;
+  z.mat = take(z.mats * z.nb * z.sm);
   z.f = take(4 * z.nb * 2 * z.groups);
   z.sums = take(8 * (int64_t)z.nb * NORM_PARTS);
   z.total = at;
@@ -531,16 +534,16 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t st) {
     char *x = ws + z.x0, *xt = ws + z.xt0;
     int parts = z.parts, x_exp = 0;
     const float *back = (const float*)(ws + z.f), *on = back + z.groups * nb;
-    char* mats[5];
-    for (int i = 0; i < 5; ++i) mats[i] = ws + z.mat + i * nb * z.sm;
+    char* mats[5] = {};
+    for (int i = 0; i < z.mats; ++i) mats[i] = ws + z.mat + i * nb * z.sm;
     auto two = [](int n) { return (float)std::ldexp(1.0, n); };
 
     bool second = false;  // which of the later groups' buffers is free
     for (int s = 0; s < a.steps;) {
       const int n = group_steps(a, s, lost(a));
       spec.begin();
-      // mats in use: A, P, Q, T (any: a scratch)
-      char *A = mats[0], *T = mats[1], *P = mats[2], *Q = nullptr, *spare[2] = {mats[3], mats[4]};
+      // (T and the spare ones for more than one step)
+      char *A = mats[0], *P = mats[1], *T = mats[2], *Q = nullptr, *spare[2] = {mats[3], mats[4]};
       double lmax = 0.0;
       for (int i = 0; i < Spectrum::N; ++i) lmax = std::max(lmax, spec.l[i]);
       int ea = exponent_for(lmax), eq = 0;

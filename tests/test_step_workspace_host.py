@@ -1,0 +1,27 @@
+"""Workspaces of the operators in include/moe_step_ops.h (no GPU): what the forms need, and no more."""
+import ctypes
+
+import pytest
+import torch
+
+from fine_grained_mixture_top_amd import binding as B
+from fine_grained_mixture_top_amd import ops
+
+
+def ortho_bytes(E, M, N, dtype, steps):
+    c = (ctypes.c_float * (3 * steps))(*([3.4445, -4.775, 2.0315] * steps))
+    d = ops.MoeOrthoDesc(E, M, N, dtype, steps, 1e-7, 1.0, 0, 0, c, None)
+    return ops.lib().moe_orthogonalize_workspace_bytes(ctypes.byref(d))
+
+
+@pytest.mark.parametrize("dtype,steps,x,mats", [
+    (B.MOE_F32, 1, 2, 2),    # X and its transpose; A and P
+    (B.MOE_F32, 5, 4, 2),    # ... and the next ones
+    (B.MOE_BF16, 1, 1, 2),   # (one part is half of two)
+    (B.MOE_BF16, 5, 1, 5),   # one group: A, P, T, Q and the next Q
+    (B.MOE_BF16, 6, 3, 5),   # two groups: X in two parts after the first
+])
+def test_orthogonalize_workspace_is_what_the_steps_use(dtype, steps, x, mats):
+    matrix = 8 * 2048 * 2048 * 4
+    need = ortho_bytes(8, 2048, 2048, dtype, steps)
+    assert (x + mats) * matrix <= need <= (x + mats) * matrix + (1 << 20)
