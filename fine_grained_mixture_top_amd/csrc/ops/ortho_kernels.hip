@@ -275,7 +275,8 @@ Sizes sizes(const OrthoArgs& a) {
   z.m = std::min(a.M, a.N);
   z.k = std::max(a.M, a.N);
   z.parts = a.dtype == MOE_F32 ? 2 : 1;
-  // Matrices at a time: enough for nine rounds of 256 x 256 tiles over 256 CUs
+  // Matrices at a time: enough for nine rounds of 256 x 256 tiles over 256 CUs (whatever the long
+  // side: X X^T has no more tiles for it)
   const int64_t mt = div_up(z.m, 256), tiles = mt * (mt + 1) / 2;
   const int64_t most = std::min<int64_t>(a.E, div_up(2304, tiles));
   z.nb = (int)div_up(a.E, div_up(a.E, most));

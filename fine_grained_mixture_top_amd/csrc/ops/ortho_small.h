@@ -67,21 +67,12 @@ template <int ROWS>
 __device__ __forceinline__ void put_mirrored(char* m, int R, int K, const f32x4_v v, const Place<ROWS>& at, int lane) {
   f16x4_v hi, lo;
   split4(v, hi, lo);
-  put(m, at.direct(R, K), hi, lo);
-  hi = turn4(hi, lane);
-  lo = turn4(lo, lane);
-  const uint32_t to = at.turned(K, R);
-  if (R > K) {
-    put(m, to, hi, lo);
-  } else {  // above the diagonal, over what the lines before put there (a wave's writes stay in order)
-    const int p = lane & 15, r = 4 * (lane >> 4) + (p & 3), c = p & ~3;
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (c + x > r) {
-        *reinterpret_cast<_Float16*>(m + to + 2 * x) = hi[x];
-        *reinterpret_cast<_Float16*>(m + (to ^ 64) + 2 * x) = lo[x];
-      }
+  if (R == K) {  // (every number is written once: no order between the lanes' writes matters)
+    put(m, at.direct(R, K), lower_mirrored(hi, lane), lower_mirrored(lo, lane));
+    return;
   }
+  put(m, at.direct(R, K), hi, lo);
+  put(m, at.turned(K, R), turn4(hi, lane), turn4(lo, lane));
 }
 
 // acc = A B^T for the rows ra0 .. and rb0 .. of two matrices in LDS, over PLANES times 32
