@@ -581,13 +581,14 @@ hipError_t by_shape(int E, int dtype, int V, F f) {
 }
 
 // Few logits: one workgroup, one launch.  us a call, one workgroup / two launches: 512 x 32
-// 7.3 / 9.3, 512 x 48 11.4 / 9.7, 2048 x 16 11.1 / 9.1, 1024 x 64 19.5 / 10.1.
-bool one_block(int T, int E) { return (int64_t)T * E <= 16384; }
+// 7.3 / 9.3, 512 x 48 11.4 / 9.7, 2048 x 16 11.1 / 9.1, 1024 x 64 19.5 / 10.1.  Few choices too, as
+// its lanes count them: 512 x 32 with K = 128 21.7 / 11.4, 16384 x 1 with K = 1024 14003 / 447.
+bool one_block(int T, int E, int K) { return (int64_t)T * std::max(E, K) <= 16384; }
 
 }  // namespace
 
-size_t balance_ws_bytes(int T, int E) {
-  if (one_block(T, E)) return 0;
+size_t balance_ws_bytes(int T, int E, int K) {
+  if (one_block(T, E, K)) return 0;
   return 4 * ((size_t)FWD_BLOCKS * line_words(E) + TAIL_WORDS);
 }
 
@@ -600,7 +601,7 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
     constexpr int V = decltype(v)::value, R = decltype(r)::value;
     typedef decltype(t) T;
     f.logL = log_l;
-    if (one_block(a.T, a.E)) {
+    if (one_block(a.T, a.E, a.K)) {
       hipLaunchKernelGGL((k_balance<T, V, R, 8, true>), dim3(1), dim3(512), 0, st, f);
       return hipGetLastError();
     }

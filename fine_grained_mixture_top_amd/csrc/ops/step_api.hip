@@ -87,7 +87,7 @@ OrthoArgs ortho_args(const moe_ortho_desc* d, const void* g, void* o, void* ws) 
 extern "C" {
 
 size_t moe_balance_workspace_bytes(const moe_balance_desc* desc) {
-  return check_balance(desc) == MOE_OK ? up256(balance_ws_bytes(desc->T, desc->E)) : 0;
+  return check_balance(desc) == MOE_OK ? up256(balance_ws_bytes(desc->T, desc->E, desc->K)) : 0;
 }
 
 int moe_balance(const moe_balance_desc* desc, const void* logits, const int32_t* expert_idx, const uint8_t* valid,

@@ -25,7 +25,7 @@ struct BalanceArgs {
   float* loss;
   void* ws;
 };
-size_t balance_ws_bytes(int T, int E);
+size_t balance_ws_bytes(int T, int E, int K);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t st);
 
 struct BalanceBwdArgs {

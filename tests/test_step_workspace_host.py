@@ -2,7 +2,6 @@
 import ctypes
 
 import pytest
-import torch
 
 from fine_grained_mixture_top_amd import binding as B
 from fine_grained_mixture_top_amd import ops
@@ -25,3 +24,11 @@ def test_orthogonalize_workspace_is_what_the_steps_use(dtype, steps, x, mats):
     matrix = 8 * 2048 * 2048 * 4
     need = ortho_bytes(8, 2048, 2048, dtype, steps)
     assert (x + mats) * matrix <= need <= (x + mats) * matrix + (1 << 20)
+
+
+def test_balance_of_many_choices_is_not_one_workgroup():
+    """The form of one workgroup, which needs no workspace, is for few logits and few choices."""
+    need = lambda T, E, K: ops.lib().moe_balance_workspace_bytes(  # noqa: E731
+        ctypes.byref(ops.MoeBalanceDesc(T, E, K, B.MOE_F32, 0, 0, None)))
+    assert need(512, 32, 4) == need(16, 8, 1024) == need(0, 1024, 1024) == 0
+    assert need(16384, 1, 1024) > 0 and need(512, 32, 33) > 0 and need(512, 33, 4) > 0
