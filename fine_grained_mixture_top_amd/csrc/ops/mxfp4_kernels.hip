@@ -111,12 +111,17 @@ hipError_t launch_mxfp4_mm(const PlanArgs& p, const Mxfp4Args& m, hipStream_t st
   a.a_rows = m.a_rows; a.rows = m.rows; a.E = m.E; a.K = m.K; a.N = m.N;
   const int64_t used = m.rows_used;
   // Thin tiles read an expert's weights once per 16 rows; the others' time is at least
-  // their stages', however few they are.  So thin up to 16 rows per expert, and while
-  // there is little to compute.  Measured, thin and tiles of 64 (us):
+  // their stages', one after the other, however few they are.  So thin up to 16 rows per expert, and
+  // while there is little to compute.  Measured, thin and tiles of 64 (us):
   //   64 experts of 2048 x 2048, 16 rows each 42 and 47, 24 54 and 49
   //   128 experts of 1536 x 512, 16 rows each 21 and 28, 32 32 and 29
   //   8 experts of 736 x 1040, 400 rows (416000) 8.4 and 12.8, 1600 (1664000) 24 and 14
   //   one of 2048 x 2048, 256 rows (524288) 10 and 25, 1024 (2097152) 28.5 and 25
+  // The average and the rows times N decide as well where a few experts hold all rows, and whatever K:
+  //   128 experts of 1536 x 512, 2048 rows in 8 of them 17 and 27, in one 17 and 27
+  //   64 of 2048 x 2048, 1024 in 8 31 and 45, in one 30 and 43
+  //   256 of 7168 x 4096, 4096 in all 1071 and 1338, in 8 614 and 1065, in one 611 and 1051
+  //   one of K x 2048, 512 rows (1048576), K = 512 11 and 10, 2048 18 and 26, 7168 44 and 81
   // (a grid has fewer than 2^24 workgroups of 256)
   const int64_t thin = row_tiles(a, used, 16) * div_up(a.N, 64);
   if ((used <= 16 * (int64_t)a.E || used * a.N <= (1 << 20)) && thin < (1 << 24)) {
