@@ -64,10 +64,7 @@ k_mxfp4_weights(const T* w, uint8_t* q, uint8_t* s, int K, int N) {
   s[at] = (uint8_t)code;
 }
 
-// at most so many tiles of BM rows have a row
-int64_t row_tiles(const f4::Args& a, int64_t used, int BM) {
-  return std::min(used, div_up(used, BM) + std::min<int64_t>(a.E, used));
-}
+int64_t row_tiles(const f4::Args& a, int64_t used, int BM) { return mxfp4_row_tiles(used, a.E, BM); }
 
 template <int FN>
 hipError_t launch_thin(int out, const f4::Args& a, int64_t used, hipStream_t st) {
@@ -124,7 +121,7 @@ hipError_t launch_mxfp4_mm(const PlanArgs& p, const Mxfp4Args& m, hipStream_t st
   //   one of K x 2048, 512 rows (1048576), K = 512 11 and 10, 2048 18 and 26, 7168 44 and 81
   // (a grid has fewer than 2^24 workgroups of 256)
   const int64_t thin = row_tiles(a, used, 16) * div_up(a.N, 64);
-  if ((used <= 16 * (int64_t)a.E || used * a.N <= (1 << 20)) && thin < (1 << 24)) {
+  if ((used <= 16 * (int64_t)a.E || used * a.N <= (1 << 20)) && thin < MXFP4_MAX_TILES) {
     // under half a workgroup of 64 columns per CU: workgroups of 16 (one row, 7168 x 4096
     // 8.6 us in place of 13.7; 64 of 2048 x 2048, where it is the other way, 8.0 and 7.9)
     if (thin < cu_count(device()) / 2) return launch_thin<1>(m.out, a, used, st);
@@ -134,7 +131,8 @@ hipError_t launch_mxfp4_mm(const PlanArgs& p, const Mxfp4Args& m, hipStream_t st
   // and 254, 2048 1084 and 893; 128 experts of 1536 x 512, 256 rows each 63 and 67, 1024 208 and
   // 193.  Up to four tiles of 128 per CU too: one of 2048 x 2048, 1024 rows 25 and 37, 8192 76
   // and 88, 16384 132 and 135.
-  if (used <= 256 * (int64_t)a.E || row_tiles(a, used, 128) * div_up(a.N, 256) <= 4 * cu_count(device()))
+  if ((used <= 256 * (int64_t)a.E || row_tiles(a, used, 128) * div_up(a.N, 256) <= 4 * cu_count(device())) &&
+      row_tiles(a, used, 64) * div_up(a.N, 256) < MXFP4_MAX_TILES)
     return launch_tile<64, 256, 1, 4>(m.out, a, used, st);
   return launch_tile<128, 256, 1, 4>(m.out, a, used, st);
 }

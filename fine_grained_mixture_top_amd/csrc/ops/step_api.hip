@@ -165,6 +165,8 @@ int moe_mxfp4_mm(const moe_mm_desc* desc, const void* a, const void* q, const vo
   if ((int64_t)desc->N * desc->K >= INT32_MAX) return MOE_ESHAPE;
   if (gather && (int64_t)desc->a_rows * desc->K >= ((int64_t)1 << 30)) return MOE_ESHAPE;
   if (desc->rows == 0) return MOE_OK;
+  const int64_t used = desc->rows_used > 0 ? desc->rows_used : desc->rows;
+  if (mxfp4_row_tiles(used, desc->E, 128) * (((int64_t)desc->N + 255) / 256) >= MXFP4_MAX_TILES) return MOE_ESHAPE;
   if (desc->a_rows == 0) return MOE_EINVAL;  // rows of no token
   if (plan && (!plan->offsets || !plan->counts || (gather && !plan->row_token))) return MOE_EINVAL;
   if (!a || !q || !s || !c || !aligned(a, 16) || !aligned(q, 16) || !aligned(c, 16)) return MOE_EINVAL;
@@ -175,7 +177,7 @@ int moe_mxfp4_mm(const moe_mm_desc* desc, const void* a, const void* q, const vo
     p.row_token = plan->row_token;
   }
   const Mxfp4Args g{(const bf16_t*)a, (const uint8_t*)q, (const uint8_t*)s, c, desc->a_rows, desc->rows,
-                    desc->rows_used > 0 ? desc->rows_used : desc->rows, desc->E, desc->K, desc->N, desc->out, gather};
+                    (int)used, desc->E, desc->K, desc->N, desc->out, gather};
   return timed(desc->profile, stream, MOE_STEP_K_MXFP4_MM, [&](hipStream_t st) { return launch_mxfp4_mm(p, g, st); });
 }
 

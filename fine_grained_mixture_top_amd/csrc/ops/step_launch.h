@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../../include/moe_step_ops.h"
 #include "../device_common.h"
 #include "ops_launch.h"
@@ -64,6 +66,12 @@ struct Mxfp4Args {
   int out;
   bool gather;
 };
+// at most so many tiles of BM rows have a row
+inline int64_t mxfp4_row_tiles(int64_t used, int E, int BM) {
+  return std::min(used, (used + BM - 1) / BM + std::min<int64_t>(E, used));
+}
+// tiles of a launch, workgroups of 256 in whole eights (a grid has fewer than 2^32 threads)
+constexpr int64_t MXFP4_MAX_TILES = (1 << 24) - 8;
 hipError_t launch_mxfp4_weights(int dtype, int E, int K, int N, const void* w, uint8_t* q, uint8_t* s, hipStream_t st);
 hipError_t launch_mxfp4_mm(const PlanArgs& p, const Mxfp4Args& m, hipStream_t st);
 

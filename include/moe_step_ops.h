@@ -147,7 +147,8 @@ int moe_mxfp4_quant_weights(int dtype, int E, int K, int N, const void* w, void*
  * per expert add up in another order, so a row's result may depend, within fp32's rounding,
  * on the sizes of the call.  The same call gives the same bits.
  *   Limits: K a multiple of 32, N of 16, each at most 2^20, E <= 1024, N * K below 2^31, with
- * MOE_MM_GATHER a_rows * K below 2^30 (MOE_ESHAPE; larger ones go through moe_permute).
+ * MOE_MM_GATHER a_rows * K below 2^30 (MOE_ESHAPE; larger ones go through moe_permute),
+ * (ceil(rows / 128) + E) ceil(N / 256) below 2^24 - 8 (rows_used in place of rows where given).
  * a, q and c 16-byte aligned.
  */
 int moe_mxfp4_mm(const moe_mm_desc* desc, const void* a, const void* q, const void* s, const moe_plan* plan, void* c,

@@ -1,4 +1,4 @@
-"""Workspaces of the operators in include/moe_step_ops.h (no GPU): what the forms need, and no more."""
+"""Workspaces and limits of the operators in include/moe_step_ops.h (no GPU): what the forms need, and no more."""
 import ctypes
 
 import pytest
@@ -32,3 +32,12 @@ def test_balance_of_many_choices_is_not_one_workgroup():
         ctypes.byref(ops.MoeBalanceDesc(T, E, K, B.MOE_F32, 0, 0, None)))
     assert need(512, 32, 4) == need(16, 8, 1024) == need(0, 1024, 1024) == 0
     assert need(16384, 1, 1024) > 0 and need(512, 32, 33) > 0 and need(512, 33, 4) > 0
+
+
+def test_mxfp4_mm_refuses_more_tiles_than_a_launch_has():
+    P = 4096
+    mm = lambda rows, N: ops.lib().moe_mxfp4_mm(  # noqa: E731
+        ctypes.byref(ops.MoeMmDesc(rows, rows, 0, 1, 32, N, B.MOE_BF16, 0, 0, None)), P, P, P, None, None, None)
+    most = ((1 << 24) - 8 - 2) * 128
+    assert mm(2 ** 31 - 1, 16) == mm(most + 1, 256) == mm(most // 4096 + 129, 1 << 20) == B.MOE_ESHAPE
+    assert mm(most, 16) == mm(most // 2 - 128, 512) == B.MOE_EINVAL  # (no result's address: past the sizes' check)
