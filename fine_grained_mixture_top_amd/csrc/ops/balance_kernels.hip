@@ -444,7 +444,8 @@ k_balance_bwd(Bwd f) {
 #pragma unroll
         for (int v = 0; v < V; ++v) p[i][r][v] = counting[i] ? __expf(z[i][r][v] - lse[i]) : 0.f;
     }
-    if (__any(any)) {
+    const bool some = __any(any);
+    if (some) {
       float m[U], sum[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
@@ -494,11 +495,21 @@ k_balance_bwd(Bwd f) {
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const float add = counting[i] ? gz * lse[i] - s[i] : 0.f;
+      // (with few tokens, gz lse may pass fp32's range where p gz lse does not: logits at their type's ends)
+      const float far = gz * lse[i], add = counting[i] ? far - s[i] : 0.f;
+      const bool huge = coarse[i] && fabsf(far) == __builtin_inff();
+      if (some && __any(huge)) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int v = 0; v < V; ++v) p[i][r][v] *= cf[r][v] + add;
+          for (int v = 0; v < V; ++v)
+            p[i][r][v] = huge ? fmaf(p[i][r][v], cf[r][v] - s[i], p[i][r][v] * lse[i] * gz) : p[i][r][v] * (cf[r][v] + add);
+      } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int v = 0; v < V; ++v) p[i][r][v] *= cf[r][v] + add;
+      }
       if constexpr (GATES) {
         // A row's choices are few and lie in one lane each: they go to their columns through
         // the row's words in LDS, zeros but for this.  (Every lane comparing its columns
