@@ -137,9 +137,9 @@ __device__ __forceinline__ void wait_stages(int n) {
 }
 
 // A tile's stages go through BUFS buffers, loaded straight into LDS; matrix instructions
-// bound large calls (64 symmetric products of 2048 x 2048 in two parts 1535 us, 1210
+// bound large calls (64 symmetric products of 2048 x 2048 in two parts 1542 us, 1200
 // TFLOP/s, where the card's power holds the clock down), loads and results small ones
-// (128 of 256 x 256 23 us, of which the instructions are 7).
+// (128 of 256 x 256 21 us, of which the instructions are 5).
 //   FINE: the two products with a lo, which are small, have sums of their own, added once at
 // the end; a matrix instruction rounds its sum four times (eight products at a time), so
 // four roundings of a large sum take the place of twelve per 32 of the reduction.  Error of

@@ -148,22 +148,23 @@ hipError_t launch_gemm(const Args& a, int64_t tiles, hipStream_t st) {
 // have eight waves (four instead, two stage buffers: 24 x 720 x 1040 849 us in place of 809, in
 // fp32 1076 in place of 1035).  A whole call, us, with one kind throughout, and by this rule:
 //                            64 x 64   128, 3 ahead   128, 1 ahead   256    rule
-//   bf16   1 x 512 x 512         157            249            302   628    156
-//          2 x 1024 x 1024       319            400            483          302
-//          4 x 1024 x 1024       519            491            463  1079    453
-//          64 x 256 x 1536       334            325            303   482    301
-//          128 x 256 x 1536      573            584            539   661    541
-//          24 x 720 x 1040      1035            909            809  1155    815
-//          32 x 1024 x 1024     3199           2774           2484  2811   2475
-//          64 x 2048 x 2048                   35750          31175 29414  29034
-//   fp32   1 x 512 x 512         158            248            299   683    160
-//          4 x 1024 x 1024       514            445            432  1188    429
-//          1 x 2048 x 2048       896            747            742          727
-//          64 x 256 x 1536       860            768            818  1127    723
-//          24 x 720 x 1040      1362           1182           1035  1456   1042
-//          64 x 2048 x 2048                   36612          31510 32475  31519
-// (FINE's sums of two kinds do not fit the registers with 256 x 256: the fp32 figures there are
-// with one kind, the small sums added at every stage.)
+//   bf16   1 x 512 x 512         158            258            255   648    158
+//          2 x 1024 x 1024       309            412            414  1088    295
+//          4 x 1024 x 1024       509            487            461  1096    458
+//          64 x 256 x 1536       330            321            308   555    307
+//          128 x 256 x 1536      596            625            533   702    534
+//          24 x 720 x 1040      1021            919            777  1146    773
+//          32 x 1024 x 1024     3148           2764           2477  2715   2479
+//          64 x 2048 x 2048                   35009          30439 28395  28336
+//          342 x 300 x 4000                    4056           3544  4661   4532
+//   fp32   1 x 512 x 512         159            252            251          159
+//          4 x 1024 x 1024       503            435            430          435
+//          1 x 2048 x 2048       877            733            741          733
+//          64 x 256 x 1536       841            759            815          724
+//          24 x 720 x 1040      1370           1161           1014         1020
+//          64 x 2048 x 2048                   35412          30616        30702
+// (The rule counts tiles, not what of them lies outside: 300 rows fill 256 x 256 worst.  FINE's
+// sums of two kinds do not fit the registers with 256 x 256.)
 constexpr int LONG = 6;  // sides from which on bf16 X X^T is summed in pieces throughout
 template <int PA, int PB, bool FINE, Epi EPI, typename O>
 hipError_t gemm_by_size(const Args& a, hipStream_t st) {
