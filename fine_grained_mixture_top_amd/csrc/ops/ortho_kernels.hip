@@ -258,14 +258,16 @@ double lost(const OrthoArgs& a) {
 // steps and 788 us; in pieces 5.0e-4, 337 us.)
 int group_steps(const OrthoArgs& a, int s, double lost) {
   if (a.dtype == MOE_F32) return 1;
-  double grown = 0.0, power = 1.0;
+  double grown = 0.0, power = 1.0;  // of A's error; of a small direction
   int n = 0;
   while (s + n < a.steps) {
     const float* c = a.coef + 3 * (s + n);
     const double up = std::max(1.0, std::fabs((double)c[0]));
-    grown += std::fabs((double)c[1]) / up * power;
-    power *= up * up;
-    if (n > 0 && lost * grown > 1.5e-3) break;
+    // (without a b, P loses by c once A has grown)
+    grown += std::max(std::fabs((double)c[1]), std::fabs((double)c[2])) / up * power * power;
+    power *= up;
+    // (and Q, which holds a small direction's growth beside the large ones' near 1, keeps its bits)
+    if (n > 0 && (lost * grown > 1.5e-3 || power > 512.0)) break;
     ++n;
   }
   return n;

@@ -108,3 +108,24 @@ def test_steep_spectra_in_fp32(E, M, N):
         ref = R.ortho_ref(w[e], 5, [R.QUINTIC] * 5)
         tol = R.ortho_tolerance(torch.float32, 5, [R.QUINTIC]) + R.HALF[torch.float32]
         assert float((o[e].double() - ref).norm()) <= tol * float(ref.norm()), KINDS[e]
+
+
+CUBELESS = (1.25, 0.0, -0.25)  # s (5 - s^4) / 4: rises to 1 and stays there
+
+
+@pytest.mark.parametrize("E,M,N,coef,steps", [
+    (1, 1, 40, R.SMOOTH, 64), (3, 500, 1, R.SMOOTH, 40), (1, 2, 300, R.SMOOTH, 40), (1, 30, 100, CUBELESS, 64),
+    (1, 140, 200, CUBELESS, 64), (1, 140, 200, R.SMOOTH, 40), (30, 300, 170, CUBELESS, 40),
+])
+def test_many_steps(E, M, N, coef, steps):
+    """Steps without end, in groups that neither lose more nor hold a larger Q than a few do: the singular values
+    are 1 in the end, and more steps only mend what the ones before lost.  One dominant direction, which what
+    the last groups add is not seen behind: each may add 1.5e-3, and three of those are a bound."""
+    g = torch.Generator("cuda").manual_seed(M + N + steps)
+    w = torch.stack([steep("one", M, N, g) for _ in range(E)])
+    o = torch.empty_like(w)
+    ops.moe_orthogonalize(ops.Ortho(E, M, N, steps=steps, coef=coef), w, o)
+    for e in range(E):
+        ref = R.ortho_ref(w[e], steps, [coef] * steps)
+        off = float((o[e].double() - ref).norm())
+        assert off <= (R.HALF[o.dtype] + 3 * 1.5e-3) * float(ref.norm()), (e, off / float(ref.norm()))
